@@ -452,6 +452,160 @@ TPMLP_API uint64_t tpattn_launch_count(const tpattn_ctx* ctx);
 TPMLP_API const char* tpattn_last_error(const tpattn_ctx* ctx);
 TPMLP_API void tpattn_destroy(tpattn_ctx* ctx);
 
+/* ---------------------------------------------------------------- queries and keys: norm and rotation
+ * What a decoder's attention does between the packed projection and the
+ * scores: the RMS norm of every query and key head over its head_dim values
+ * (optional), then the position rotation, in one pass over the rows.
+ *
+ *     y = x * rsqrt(mean(x^2) + eps) * w                 (with norm weights)
+ *     (z1, z2) = (y1 cos a - y2 sin a, y2 cos a + y1 sin a),  a = position * inv_freq[j]
+ *
+ * for the rot_dim / 2 pairs j of a head: values (j, j + rot_dim/2), or
+ * (2j, 2j + 1) when interleaved; values from rot_dim on pass unrotated.  A row
+ * is n_heads query heads followed by n_kv_heads key heads of head_dim values
+ * (the first columns of a packed [Q | K | V] row, or rows of either alone with
+ * the other count 0).  Calls without a context run on the current device;
+ * their errors are in tpmlp_last_error(NULL). */
+
+/* The rotation, a host structure without device memory: inv_freq as turns per
+ * position, 64-bit fractions of a turn, so that angles are exact at any 32-bit
+ * position.  Filled by tpattn_rotary_init; may be copied. */
+#define TPATTN_MAX_ROT_DIM 256
+typedef struct {
+  int32_t rot_dim;     /* a multiple of 16, at most head_dim; 0: no rotation */
+  int32_t interleaved; /* 0: pairs (j, j + rot_dim/2); 1: pairs (2j, 2j + 1) */
+  uint64_t turn[TPATTN_MAX_ROT_DIM / 2];
+} tpattn_rotary;
+/* inv_freq: rot_dim / 2 finite host doubles, radians per position, at most
+ * 2^20 in magnitude.  TPMLP_ERR_SHAPE for a bad rot_dim, TPMLP_ERR_ARG for
+ * NULL or a bad frequency. */
+TPMLP_API tpmlp_status tpattn_rotary_init(tpattn_rotary* r, int32_t rot_dim, int32_t interleaved,
+                                          const double* inv_freq);
+
+typedef struct {
+  int64_t rows;
+  int32_t n_heads, n_kv_heads; /* either may be 0 */
+  int32_t head_dim;            /* 64, 128, 192 or 256 */
+  int32_t dtype;               /* TPMLP_F32 or TPMLP_BF16: rows and norm weights */
+  const int32_t* positions;    /* device [rows], any int32; NULL: row % seq */
+  int64_t seq;                 /* with positions NULL: rows of a sequence, 0: position = row */
+  const void* q_norm_w;        /* device [head_dim] or NULL: no norm of the queries */
+  const void* k_norm_w;        /* device [head_dim] or NULL: no norm of the keys */
+  float eps;                   /* finite, >= 0 */
+  int32_t reserved;            /* 0 */
+} tpattn_qk_desc;
+
+/* out = rotated (normed) rows of x.  ld_x, ld_out: row strides in elements,
+ * multiples of 8.  `rot` NULL: no rotation.  out may be x itself with the same
+ * stride (in place); otherwise the two must not overlap.  Columns behind the
+ * (n_heads + n_kv_heads) * head_dim first are neither read nor written. */
+TPMLP_API tpmlp_status tpattn_qk_rope_forward(const tpattn_qk_desc* desc, const tpattn_rotary* rot, const void* x,
+                                              int64_t ld_x, void* out, int64_t ld_out, void* cuda_stream);
+
+/* Device scratch of the backward (the weight gradients' partial sums). */
+TPMLP_API size_t tpattn_qk_rope_workspace_bytes(int32_t head_dim);
+
+/* dx: gradient of the rows x (the forward's input, which must be kept when
+ * there are norm weights; x is not read otherwise and may be NULL), given dout
+ * of the forward's output.  dx may be dout itself with the same stride.
+ * dq_norm_w, dk_norm_w: float [head_dim], overwritten, exactly where the
+ * forward had that weight (else NULL); they are summed in a fixed order.
+ * workspace: tpattn_qk_rope_workspace_bytes, 16-byte aligned, needed with norm
+ * weights; it needs no initial contents and is free again after the call's
+ * kernels. */
+TPMLP_API tpmlp_status tpattn_qk_rope_backward(const tpattn_qk_desc* desc, const tpattn_rotary* rot, const void* x,
+                                               int64_t ld_x, const void* dout, int64_t ld_dout, void* dx,
+                                               int64_t ld_dx, float* dq_norm_w, float* dk_norm_w, void* workspace,
+                                               size_t workspace_bytes, void* cuda_stream);
+
+/* ---------------------------------------------------------------- paged key/value cache
+ * Answering with a trained attention sublayer: keys and values of the tokens
+ * so far live in pages of page_size tokens, and a block table names each
+ * sequence's pages in order.  tpkv_append norms and rotates new tokens' queries
+ * and keys and stores keys and values; tpkv_decode is the attention of one new
+ * token per sequence over the cache.
+ *
+ * The cache is caller-owned device memory: k and v, element
+ * (page, head, slot, c) at page * stride_page + head * stride_head +
+ * slot * stride_slot + c, so [pages, n_kv, page_size, d] and
+ * [pages, page_size, n_kv, d] both fit.  bf16, or E4M3 codes with an inverse
+ * scale per key head (value = code * inv_scale).
+ *
+ * Device-side arguments are checked where they are read: a page outside
+ * [0, num_pages) or a length above the table's capacity is never followed;
+ * tpkv_sync then returns TPMLP_ERR_ARG, the affected token is not stored, and
+ * the affected output of a decode is unspecified.  A context's calls share its
+ * workspace: launches (graph replays included) that may overlap on the GPU
+ * need contexts of their own. */
+typedef struct tpkv_ctx tpkv_ctx;
+typedef enum { TPKV_BF16 = 0, TPKV_E4M3 = 1 } tpkv_cache_dtype;
+typedef struct {
+  int64_t num_pages;  /* >= 1 */
+  int32_t page_size;  /* tokens of a page: a multiple of 8, at most 65536 */
+  int32_t max_batch;  /* largest batch of a call */
+  int32_t n_heads;    /* query heads, a multiple of n_kv_heads */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* 64, 128, 192 or 256 */
+  int32_t cache_dtype; /* tpkv_cache_dtype */
+  int32_t reserved;   /* 0 */
+} tpkv_config;
+
+TPMLP_API size_t tpkv_workspace_bytes(const tpkv_config* cfg);
+TPMLP_API tpmlp_status tpkv_create(const tpkv_config* cfg, void* cuda_stream, tpkv_ctx** out);
+/* As tpmlp_bind_workspace (tpkv_workspace_bytes, 256-byte aligned). */
+TPMLP_API tpmlp_status tpkv_bind_workspace(tpkv_ctx* ctx, void* dev, size_t bytes);
+TPMLP_API tpmlp_status tpkv_set_stream(tpkv_ctx* ctx, void* cuda_stream);
+/* The cache, strides in elements, each a multiple of 16 bytes and positive;
+ * k and v 16-byte aligned.  k_inv_scale, v_inv_scale: device float
+ * [n_kv_heads], positive, or NULL (1); NULL for a bf16 cache. */
+TPMLP_API tpmlp_status tpkv_bind_cache(tpkv_ctx* ctx, void* k, void* v, int64_t stride_page, int64_t stride_head,
+                                       int64_t stride_slot, const float* k_inv_scale, const float* v_inv_scale);
+/* What tpkv_append does to queries and keys: rotation (copied; NULL: none) and
+ * norm weights (bf16 [head_dim], each may be NULL; kept by pointer). */
+TPMLP_API tpmlp_status tpkv_set_rotary(tpkv_ctx* ctx, const tpattn_rotary* rot, const void* q_norm_w,
+                                       const void* k_norm_w, float eps);
+
+/* Append new tokens.  qkv: bf16 packed rows [rows, (n_heads + 2 n_kv) d] with
+ * row stride ld_qkv (a multiple of 8).  Which row is whose:
+ *  cu_rows NULL: rows / batch rows for each sequence in order; new_lens
+ *    (device [batch], or NULL: all) counts how many of them are tokens, the
+ *    rest being padding;
+ *  cu_rows (device [batch + 1], ascending): sequence b has the rows
+ *    [cu_rows[b], cu_rows[b+1]); rows outside belong to nobody.  new_lens NULL.
+ * The i-th row of sequence b has position past_lens[b] + i (past_lens: device
+ * [batch]; negative: an inactive sequence) and goes to page
+ * block_table[b, position / page_size], slot position % page_size.
+ * block_table: device int32 [batch, max_pages], row stride ld_table.
+ * q_out: bf16 [rows, n_heads d], row stride ld_q: the normed and rotated
+ * queries, or NULL.  transform 0 stores keys (and copies queries) as they are,
+ * for rows that are normed and rotated already.  Rows of padding, of nobody or
+ * of inactive sequences leave cache and q_out as they were.  E4M3:
+ * code = round-to-nearest-even(value / inv_scale), saturated to +-448. */
+TPMLP_API tpmlp_status tpkv_append(tpkv_ctx* ctx, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,
+                                   const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
+                                   const int32_t* block_table, int64_t ld_table, int32_t max_pages, int32_t transform,
+                                   void* q_out, int64_t ld_q);
+
+/* Attention of one token per sequence: over tokens t < n_b = lens[b] + len_add
+ * of sequence b (n_b <= 0: none) and, with window > 0, t >= n_b - window or
+ * t < sinks.
+ *  q bf16 [batch, n_heads d] (row stride ld_q) -> out bf16 [batch, n_heads d]
+ *  (row stride ld_out; may be q), lse float [batch, n_heads] or NULL: the
+ *  natural log of the sum of exp(scale q.k); a sequence without visible tokens
+ *  gets out 0 and lse -inf.  len_add 1 attends to a token just appended with
+ *  past_lens = lens.  Nothing behind a sequence's last visible token, in
+ *  pages or table, influences the result.  Repeated calls give the same bits. */
+TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, int64_t ld_q, const int32_t* lens,
+                                   int32_t len_add, const int32_t* block_table, int64_t ld_table, int32_t max_pages,
+                                   float scale, int32_t window, int32_t sinks, void* out, int64_t ld_out, float* lse);
+
+/* Wait for the context's stream, then report as tpmlp_sync does, and
+ * TPMLP_ERR_ARG for a page or length outside the cache (the word is cleared). */
+TPMLP_API tpmlp_status tpkv_sync(tpkv_ctx* ctx);
+TPMLP_API uint64_t tpkv_launch_count(const tpkv_ctx* ctx);
+TPMLP_API const char* tpkv_last_error(const tpkv_ctx* ctx);
+TPMLP_API void tpkv_destroy(tpkv_ctx* ctx);
+
 /* Loss and loss gradient without any device allocation or workspace.
  *
  * The method itself has no such call: this entry point exists for callers that

@@ -18,4 +18,5 @@ from .tpmlp import (  # noqa: F401
     ERR_TIMEOUT, ERR_UNSUPPORTED, F32, GELU, LIB_PATH, SWIGLU, TPMLP, TPAttn, AdamWParams, Config, ParamSet, TPMLPError,
     fp8_gemm, fp8_quantize, kernel_names, lib,
     make_config, tpmlp_create, tpmlp_workspace_bytes,
+    Rotary, TPKV, qk_norm_rope, qk_norm_rope_backward,
 )

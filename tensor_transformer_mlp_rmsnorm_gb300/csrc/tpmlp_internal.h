@@ -12,6 +12,7 @@ namespace tpmlp {
 
 // Device status word bits (written by kernels, read by tpmlp_sync).
 constexpr uint32_t STATUS_TIMEOUT = 1u;
+constexpr uint32_t STATUS_BAD_INDEX = 2u;  // a page or length outside the cache (the cache context only)
 
 // C[M, N] = sum over the contraction segments of A(m, k) B(k, n).
 //  A K-major : A(m,k) = a[m * lda + k]  (tensor [M, K_extent])

@@ -68,6 +68,30 @@ class Config(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+MAX_ROT_DIM = 256
+
+
+class RotarySpec(ctypes.Structure):
+    """tpattn_rotary."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("turn", ctypes.c_uint64 * (MAX_ROT_DIM // 2))]
+
+
+class QkDesc(ctypes.Structure):
+    """tpattn_qk_desc."""
+    _fields_ = [("rows", ctypes.c_int64), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                ("seq", ctypes.c_int64), ("q_norm_w", ctypes.c_void_p), ("k_norm_w", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class KvConfig(ctypes.Structure):
+    """tpkv_config."""
+    _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("max_batch", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _vp, _i32, _i64, _u32, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
 _fp = ctypes.c_void_p  # float* (device)
 _SIGNATURES = {
@@ -120,6 +144,23 @@ _SIGNATURES = {
     "tpattn_launch_count": (ctypes.c_uint64, [_vp]),
     "tpattn_last_error": (ctypes.c_char_p, [_vp]),
     "tpattn_destroy": (None, [_vp]),
+    "tpattn_rotary_init": (_i32, [ctypes.POINTER(RotarySpec), _i32, _i32, ctypes.POINTER(ctypes.c_double)]),
+    "tpattn_qk_rope_forward": (_i32, [ctypes.POINTER(QkDesc), ctypes.POINTER(RotarySpec), _vp, _i64, _vp, _i64, _vp]),
+    "tpattn_qk_rope_workspace_bytes": (ctypes.c_size_t, [_i32]),
+    "tpattn_qk_rope_backward": (_i32, [ctypes.POINTER(QkDesc), ctypes.POINTER(RotarySpec), _vp, _i64, _vp, _i64, _vp,
+                                       _i64, _fp, _fp, _vp, ctypes.c_size_t, _vp]),
+    "tpkv_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvConfig)]),
+    "tpkv_create": (_i32, [ctypes.POINTER(KvConfig), _vp, ctypes.POINTER(_vp)]),
+    "tpkv_bind_workspace": (_i32, [_vp, _vp, ctypes.c_size_t]),
+    "tpkv_set_stream": (_i32, [_vp, _vp]),
+    "tpkv_bind_cache": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _fp, _fp]),
+    "tpkv_set_rotary": (_i32, [_vp, ctypes.POINTER(RotarySpec), _vp, _vp, _f32]),
+    "tpkv_append": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _i64]),
+    "tpkv_decode": (_i32, [_vp, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _i32, _f32, _i32, _i32, _vp, _i64, _fp]),
+    "tpkv_sync": (_i32, [_vp]),
+    "tpkv_launch_count": (ctypes.c_uint64, [_vp]),
+    "tpkv_last_error": (ctypes.c_char_p, [_vp]),
+    "tpkv_destroy": (None, [_vp]),
     "tpmlp_fp8_quantize": (_i32, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _fp, _vp, _vp]),
     "tpmlp_fp8_gemm": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _fp, _fp, _fp, _i64, _vp, _vp]),
 }
@@ -606,3 +647,235 @@ class TPAttn:
 
     def launch_count(self) -> int:
         return int(lib().tpattn_launch_count(self.ctx))
+
+
+class Rotary:
+    """Position rotation of query and key heads (tpattn_rotary): the first ``rot_dim`` values of a head, as
+    pairs (j, j + rot_dim/2), or (2j, 2j + 1) when ``interleaved``; pair j turns by ``inv_freq[j]`` radians per
+    position, ``theta ** (-2 j / rot_dim)`` unless given.  Holds no device memory."""
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, inv_freq=None, interleaved: bool = False):
+        freq = [theta ** (-2.0 * j / rot_dim) for j in range(rot_dim // 2)] if inv_freq is None else list(inv_freq)
+        if len(freq) != rot_dim // 2:
+            raise TPMLPError(ERR_ARG, "inv_freq needs rot_dim / 2 values")
+        self.spec = RotarySpec()
+        _check(lib().tpattn_rotary_init(ctypes.byref(self.spec), rot_dim, int(bool(interleaved)),
+                                        (ctypes.c_double * max(len(freq), 1))(*freq)))
+        self.ref = ctypes.byref(self.spec)
+        self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
+
+
+def _stream_of(device, stream):
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _rows(t, width: int, dtype, name: str, device=None, rows=None):
+    """Pointer and row stride of a 2-D tensor whose rows hold `width` contiguous values."""
+    if (t.dtype is not dtype or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1)
+            or t.shape[1] < width or (rows is not None and t.shape[0] != rows)
+            or (device is not None and t.device != device)):
+        raise TPMLPError(ERR_ARG, f"{name}: need {dtype} rows of at least {width} contiguous values"
+                                  + (f", {rows} of them," if rows is not None else "") + " on the call's CUDA device, "
+                                  f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vec(t, n: int, dtype, name: str, device):
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise TPMLPError(ERR_ARG, f"{name}: need contiguous {dtype} ({n},) on {device}, got {t.dtype} "
+                                  f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _qk_desc(x, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps) -> QkDesc:
+    dt = BF16 if x.dtype is torch.bfloat16 else F32 if x.dtype is torch.float32 else None
+    if dt is None:
+        raise TPMLPError(ERR_UNSUPPORTED, "rows must be float32 or bfloat16")
+    n = x.shape[0]
+    return QkDesc(n, n_heads, n_kv_heads, head_dim, dt, _vec(positions, n, torch.int32, "positions", x.device), seq,
+                  _vec(q_norm_w, head_dim, x.dtype, "q_norm_w", x.device),
+                  _vec(k_norm_w, head_dim, x.dtype, "k_norm_w", x.device), eps, 0)
+
+
+def qk_norm_rope(x, n_heads: int, n_kv_heads: int, head_dim: int, rotary: Rotary | None = None, positions=None,
+                 seq: int = 0, q_norm_w=None, k_norm_w=None, eps: float = 1e-6, out=None, stream=None):
+    """RMS norm (where a weight is given) and position rotation of the query and key heads at the start of each
+    row of x (tpattn_qk_rope_forward); out may be x.  Positions: int32 per row, or row % seq (seq 0: the row)."""
+    width = (n_heads + n_kv_heads) * head_dim
+    xp, ldx = _rows(x, width, x.dtype, "x")
+    if out is None:
+        out = torch.empty(x.shape[0], width, dtype=x.dtype, device=x.device)
+    op, ldo = _rows(out, width, x.dtype, "out", x.device, x.shape[0])
+    d = _qk_desc(x, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
+    with torch.cuda.device(x.device):
+        _check(lib().tpattn_qk_rope_forward(ctypes.byref(d), rotary.ref if rotary is not None else None, xp, ldx, op,
+                                            ldo, _stream_of(x.device, stream)))
+    return out
+
+
+def qk_norm_rope_backward(dout, x, n_heads: int, n_kv_heads: int, head_dim: int, rotary: Rotary | None = None,
+                          positions=None, seq: int = 0, q_norm_w=None, k_norm_w=None, eps: float = 1e-6, dx=None,
+                          dq_norm_w=None, dk_norm_w=None, workspace=None, stream=None):
+    """Backward of qk_norm_rope: (dx, dq_norm_w, dk_norm_w), the weights' gradients in float32 (None without the
+    weight).  x: the forward's input (only read with norm weights, else it may be None); dx may be dout."""
+    width = (n_heads + n_kv_heads) * head_dim
+    n, dev, norm = dout.shape[0], dout.device, q_norm_w is not None or k_norm_w is not None
+    gp, ldg = _rows(dout, width, dout.dtype, "dout")
+    xp, ldx = _rows(x, width, dout.dtype, "x", dev, n) if norm else (None, 0)
+    if dx is None:
+        dx = torch.empty(n, width, dtype=dout.dtype, device=dev)
+    dp, ldd = _rows(dx, width, dout.dtype, "dx", dev, n)
+    f32 = torch.float32
+    if q_norm_w is not None and dq_norm_w is None:
+        dq_norm_w = torch.empty(head_dim, dtype=f32, device=dev)
+    if k_norm_w is not None and dk_norm_w is None:
+        dk_norm_w = torch.empty(head_dim, dtype=f32, device=dev)
+    nbytes = lib().tpattn_qk_rope_workspace_bytes(head_dim) if norm else 0
+    if norm and workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    if norm and (workspace.device != dev or not workspace.is_contiguous()):
+        raise TPMLPError(ERR_ARG, "workspace must be contiguous on the call's device")
+    wbytes = workspace.numel() * workspace.element_size() if norm else 0
+    d = _qk_desc(dout, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
+    with torch.cuda.device(dev):
+        _check(lib().tpattn_qk_rope_backward(
+            ctypes.byref(d), rotary.ref if rotary is not None else None, xp, ldx, gp, ldg, dp, ldd,
+            _vec(dq_norm_w, head_dim, f32, "dq_norm_w", dev), _vec(dk_norm_w, head_dim, f32, "dk_norm_w", dev),
+            workspace.data_ptr() if norm else None, wbytes, _stream_of(dev, stream)))
+    return dx, dq_norm_w, dk_norm_w
+
+
+class TPKV:
+    """A paged key/value cache (tpkv_*): append new tokens, attend with one token per sequence.
+
+    ``k_cache`` and ``v_cache``: [pages, n_kv_heads, page_size, head_dim], bfloat16 or float8_e4m3fn, with the same
+    strides, the last one 1 (a [pages, page_size, n_kv_heads, head_dim] tensor is passed transposed).  E4M3 codes
+    stand for code * inv_scale of their head.  The cache stays the caller's; the context's scratch is a torch
+    tensor.  Calls run on ``stream``, or on torch's current stream at each call where it is None; calls that may
+    overlap on the GPU need a TPKV each."""
+
+    def __init__(self, k_cache, v_cache, n_heads: int, max_batch: int = 1024, k_inv_scale=None, v_inv_scale=None,
+                 stream=None):
+        if k_cache.dim() != 4 or not k_cache.is_cuda:
+            raise TPMLPError(ERR_ARG, "k_cache must be a CUDA tensor [pages, n_kv_heads, page_size, head_dim]")
+        kinds = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+        if k_cache.dtype not in kinds:
+            raise TPMLPError(ERR_UNSUPPORTED, "the cache must be bfloat16 or float8_e4m3fn")
+        if (v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or v_cache.device != k_cache.device
+                or v_cache.stride() != k_cache.stride() or k_cache.stride(3) != 1):
+            raise TPMLPError(ERR_ARG, "k_cache and v_cache must agree in type, shape, device and strides, the last 1")
+        self.device = dev = k_cache.device
+        pages, nkv, page, d = k_cache.shape
+        self.cfg = KvConfig(pages, page, max_batch, n_heads, nkv, d, kinds[k_cache.dtype], 0)
+        self.nq, self.nkv, self.d, self.page_size = n_heads, nkv, d, page
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self._scales = (k_inv_scale, v_inv_scale)
+        self._norm = (None, None)
+        self._fixed = stream
+        self._stream = _stream_of(dev, stream)
+        ctx = ctypes.c_void_p()
+        with torch.cuda.device(dev):
+            self._ck(lib().tpkv_create(ctypes.byref(self.cfg), self._stream, ctypes.byref(ctx)))
+            self.ctx = ctx
+            nbytes = int(lib().tpkv_workspace_bytes(ctypes.byref(self.cfg)))
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        self._ck(lib().tpkv_bind_workspace(ctx, self.workspace.data_ptr(), nbytes))
+        f32 = torch.float32
+        self._ck(lib().tpkv_bind_cache(ctx, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
+                                       _vec(k_inv_scale, nkv, f32, "k_inv_scale", dev),
+                                       _vec(v_inv_scale, nkv, f32, "v_inv_scale", dev)))
+
+    def _ck(self, status: int):
+        if status != OK:
+            ctx = getattr(self, "ctx", None)
+            msg = lib().tpkv_last_error(ctx).decode(errors="replace")
+            raise TPMLPError(status, msg or lib().tpmlp_status_string(status).decode())
+
+    def close(self):
+        if getattr(self, "ctx", None):
+            lib().tpkv_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def set_stream(self, stream):
+        """Run later calls on `stream` (None: torch's current stream at each call)."""
+        self._fixed = stream
+
+    def _enter(self):
+        s = _stream_of(self.device, self._fixed)
+        if s != self._stream:
+            self._ck(lib().tpkv_set_stream(self.ctx, s))
+            self._stream = s
+
+    def set_rotary(self, rotary: Rotary | None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6):
+        """What append does to queries and keys: norm where a bf16 weight is given, then the rotation."""
+        b = torch.bfloat16
+        self._ck(lib().tpkv_set_rotary(self.ctx, rotary.ref if rotary is not None else None,
+                                       _vec(q_norm_w, self.d, b, "q_norm_w", self.device),
+                                       _vec(k_norm_w, self.d, b, "k_norm_w", self.device), float(eps)))
+        self._norm = (q_norm_w, k_norm_w)  # the context keeps their pointers
+
+    def _table(self, t, batch: int):
+        if (t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != batch or t.device != self.device
+                or (t.shape[1] > 1 and t.stride(1) != 1)):
+            raise TPMLPError(ERR_ARG, f"block_table: need int32 [{batch}, pages] on {self.device}, got {t.dtype} "
+                                      f"{tuple(t.shape)} on {t.device}")
+        return t.data_ptr(), max(t.stride(0), t.shape[1]), t.shape[1]
+
+    def append(self, qkv, past_lens, block_table, cu_rows=None, new_lens=None, q_out=None, transform: bool = True,
+               with_queries: bool = True):
+        """Store the keys and values of packed rows [Q | K | V] behind each sequence's ``past_lens`` tokens and
+        return the normed and rotated queries [rows, n_heads * d] (None without ``with_queries``); see tpkv_append."""
+        dev, i32, batch = self.device, torch.int32, past_lens.shape[0]
+        n = qkv.shape[0]
+        xp, ldx = _rows(qkv, (self.nq + 2 * self.nkv) * self.d, torch.bfloat16, "qkv", dev)
+        width = self.nq * self.d
+        if q_out is None and with_queries:
+            # rows that are nobody's are left as they were: give them a value where there may be any
+            new = torch.empty if cu_rows is None and new_lens is None else torch.zeros
+            q_out = new(n, width, dtype=torch.bfloat16, device=dev)
+        op, ldo = _rows(q_out, width, torch.bfloat16, "q_out", dev, n) if q_out is not None else (None, 0)
+        tp, ldt, pages = self._table(block_table, batch)
+        self._enter()
+        self._ck(lib().tpkv_append(self.ctx, n, batch, xp, ldx, _vec(cu_rows, batch + 1, i32, "cu_rows", dev),
+                                   _vec(new_lens, batch, i32, "new_lens", dev),
+                                   _vec(past_lens, batch, i32, "past_lens", dev), tp, ldt, pages,
+                                   1 if transform else 0, op, ldo))
+        return q_out
+
+    def decode(self, q, lens, block_table, scale: float | None = None, window: int = 0, sinks: int = 0, out=None,
+               lse=None, return_lse: bool = False, len_add: int = 0):
+        """Attention of one token per sequence over its first ``lens + len_add`` cached tokens; with a window, over
+        its last ``window`` tokens and first ``sinks``.  scale: 1 / sqrt(head_dim) unless given.  Returns out
+        [batch, n_heads * d], with ``return_lse`` or ``lse`` (out, lse float32 [batch, n_heads]); see tpkv_decode."""
+        dev, batch, width = self.device, q.shape[0], self.nq * self.d
+        qp, ldq = _rows(q, width, torch.bfloat16, "q", dev)
+        if out is None:
+            out = torch.empty(batch, width, dtype=torch.bfloat16, device=dev)
+        op, ldo = _rows(out, width, torch.bfloat16, "out", dev, batch)
+        if lse is None and return_lse:
+            lse = torch.empty(batch, self.nq, dtype=torch.float32, device=dev)
+        if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (batch, self.nq)
+                                or lse.device != dev or not lse.is_contiguous()):
+            raise TPMLPError(ERR_ARG, f"lse: need contiguous float32 {(batch, self.nq)} on {dev}")
+        tp, ldt, pages = self._table(block_table, batch)
+        self._enter()
+        self._ck(lib().tpkv_decode(self.ctx, batch, qp, ldq, _vec(lens, batch, torch.int32, "lens", dev), len_add, tp,
+                                   ldt, pages, self.d ** -0.5 if scale is None else scale, window, sinks, op, ldo,
+                                   lse.data_ptr() if lse is not None else None))
+        return out if lse is None else (out, lse)
+
+    def sync(self):
+        """Wait for the stream; raises where a page or length lay outside the cache."""
+        self._enter()
+        self._ck(lib().tpkv_sync(self.ctx))
+
+    def launch_count(self) -> int:
+        return int(lib().tpkv_launch_count(self.ctx))
