@@ -274,8 +274,8 @@ tpmlp_status tpkv_create(const tpkv_config* cfg, void* stream, tpkv_ctx** out) {
   c->stream = static_cast<cudaStream_t>(stream);
   c->device = dev;
   c->num_sms = sms;
-  c->box_tokens = 64;
-  while (cfg->page_size % c->box_tokens) c->box_tokens /= 2;
+  c->box_tokens = kv_decode_tile(cfg->head_dim, cfg->cache_dtype == TPKV_E4M3);
+  while (cfg->page_size % c->box_tokens) c->box_tokens /= 2;  // ends at 8 at the latest
   c->workers = kv_decode_workers(cfg->head_dim, cfg->n_heads / cfg->n_kv_heads, sms);
   if (c->workers > KV_MAX_WORKERS) c->workers = KV_MAX_WORKERS;
   *out = c;
@@ -455,7 +455,7 @@ tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void*
     a.eps = c->eps;
   }
   a.batch = batch;
-  a.rows_per_seq = rows / batch;
+  a.rows_per_seq = (int)(rows / batch);
   a.cu_rows = cu_rows;
   a.new_lens = new_lens;
   a.past_lens = past_lens;

@@ -44,16 +44,20 @@
 namespace tpmlp {
 namespace {
 
-constexpr int TK = 64;          // tokens of a tile
-constexpr int NCW = 4;          // computing warps (16 tokens of a tile each)
+constexpr int NCW = 4;          // computing warps
 constexpr int NTHR = 32 * (NCW + 1);
 constexpr int RING_BYTES = 96 * 1024;
 constexpr int JOIN_GROUP = 16;  // partials one CTA joins at a time
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 100000000ull;
 
+// Every computing warp works on every tile, so each waits for every use of a
+// slot: a barrier's one-bit phase is never asked about two rounds ahead.
 template <int D, bool F8>
 struct Ring {
-  static constexpr int SLOT = TK * D * (F8 ? 1 : 2);  // one operand of a tile
+  static constexpr int ROW = D * (F8 ? 1 : 2);
+  static constexpr int BLOCK = ROW % 128 == 0 ? 128 : 64;  // bytes of a row that lie together (the swizzle's width)
+  static constexpr int TK = ROW <= 128 ? 128 : 64;  // tokens of a tile
+  static constexpr int SLOT = TK * ROW;             // one operand of a tile
   static constexpr int N = RING_BYTES / SLOT;
 };
 
@@ -123,6 +127,7 @@ __device__ __forceinline__ bool bar_compute_any(bool v) {
 
 // Visible tokens of a sequence, as ranges of tiles: [0, sink_tiles) and
 // [win_tile, ...), tile j of the sequence's list being tile(j).
+template <int TK>
 struct Seq {
   int len;         // tokens attended
   int lo;          // first token of the window (0 without one)
@@ -136,8 +141,9 @@ struct Seq {
   }
   __device__ __forceinline__ bool sees(int t) const { return t < len && (t >= lo || t < sinks); }
 };
-__device__ __forceinline__ Seq make_seq(const DecodeArgs& a, int b, bool report) {
-  Seq s;
+template <int TK>
+__device__ __forceinline__ Seq<TK> make_seq(const DecodeArgs& a, int b, bool report) {
+  Seq<TK> s;
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
   int64_t n = (int64_t)a.lens[b] + a.len_add;
   if (n > cap) {
@@ -155,10 +161,11 @@ __device__ __forceinline__ Seq make_seq(const DecodeArgs& a, int b, bool report)
 }
 
 // A worker's place in the list of all (sequence, key head chunk, tile).
+template <int TK>
 struct Cursor {
   int64_t pos, end, base;  // tile index, end of the worker's range, first tile of sequence b
   int b;
-  Seq s;
+  Seq<TK> s;
 };
 
 template <int D, bool F8, int HT>
@@ -166,11 +173,14 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
     kv_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   using R = Ring<D, F8>;
+  constexpr int TK = R::TK;
+  constexpr int KW = TK / NCW;      // tokens of a tile that a warp works on
+  constexpr int KT = KW / 16;       // as m-tiles
   constexpr int NT = HT / 8;        // n-tiles of 8 heads
   constexpr int KS = D / 16;        // k-steps of Q K^T
   constexpr int MT = D / 16;        // m-tiles of V^T P^T
-  constexpr int NBLK = D / 64;      // 64-column blocks of a row in shared memory
-  constexpr int ROWB = F8 ? 64 : 128;  // bytes of a block's row
+  constexpr int ROWB = R::BLOCK;        // bytes of a block's row
+  constexpr int NBLK = R::ROW / ROWB;   // blocks of a row in shared memory
   extern __shared__ __align__(1024) uint8_t ring_raw[];
   __shared__ __align__(8) uint64_t full[R::N], empty[R::N];
   __shared__ int s_abort;
@@ -180,9 +190,9 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
   __shared__ int s_last;
   __shared__ float s_m[NCW][HT], s_l[NCW][HT];
   __shared__ float s_mx[HT], s_inv[HT];
-  __shared__ float s_w[32][HT];
+  __shared__ float s_w[32][HT], s_s[32][HT];
   constexpr int OD = 512 / HT;  // columns of O joined at a time: 8 KB, so that two CTAs fit an SM
-  __shared__ float s_o[NCW][HT * (OD + 4)];
+  __shared__ __align__(16) float s_o[NCW][HT * (OD + 4)];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
   const int per = (a.batch + NTHR - 1) / NTHR;
   const int b_lo = min(tid * per, a.batch), b_hi = min(b_lo + per, a.batch);
   int64_t sum = 0;
-  for (int b = b_lo; b < b_hi; ++b) sum += make_seq(a, b, blockIdx.x == 0).tiles;
+  for (int b = b_lo; b < b_hi; ++b) sum += make_seq<TK>(a, b, blockIdx.x == 0).tiles;
   int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -220,16 +230,18 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
   }
   const int nhc = a.nkv * a.chunks;
   const int64_t T = total * nhc;
-  const int64_t G = T < a.workers ? T : a.workers;  // every worker below G has a tile
+  // two tiles a worker where there are few: fewer partial results to join
+  const int64_t want = (T + 1) / 2;
+  const int64_t G = want < a.workers ? want : a.workers;
   if ((int64_t)blockIdx.x >= G) return;
-  Cursor c;
+  Cursor<TK> c;
   c.pos = (int64_t)blockIdx.x * T / G;
   c.end = ((int64_t)blockIdx.x + 1) * T / G;
   if (c.pos >= before * nhc && c.pos < (before + sum) * nhc) {
     int64_t base = before * nhc;
     int b = b_lo;
     for (;;) {
-      const int64_t next = base + (int64_t)make_seq(a, b, false).tiles * nhc;
+      const int64_t next = base + (int64_t)make_seq<TK>(a, b, false).tiles * nhc;
       if (c.pos < next) break;
       base = next;
       ++b;
@@ -240,87 +252,102 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
   __syncthreads();
   c.b = s_b;
   c.base = s_base;
-  c.s = make_seq(a, c.b, false);
+  c.s = make_seq<TK>(a, c.b, false);
 
   if (warp == NCW) {
     // ------------------------------------------------------------ producer
-    // Lane i of the first TK / box_tokens lanes fetches box i of each tile.
-    const int nbox = TK / a.box_tokens;
+    // A batch is up to 32 boxes of consecutive tiles of one (sequence, key
+    // head), a lane each: the next batch's table entries are read while this
+    // one's are fetched, so no tile waits for its page's number.
+    const int nbox = TK / a.box_tokens, per_batch = 32 / nbox;
+    const int my_tile = lane / nbox, my_box = lane % nbox;
     const int box_bytes = a.box_tokens * D * (F8 ? 1 : 2);
-    auto box_page = [&](int j, int& slot) -> int {  // page of this lane's box in tile j, -1: not needed
-      const int t = c.s.tile(j) * TK + lane * a.box_tokens;
-      slot = 0;
-      if (lane >= nbox || t >= c.s.len || !(t + a.box_tokens > c.s.lo || t < c.s.sinks)) return -1;
-      const int pi = t / a.page_size;
-      slot = t - pi * a.page_size;
-      const int page = a.table[(int64_t)c.b * a.ld_table + pi];
-      if (page < 0 || page >= a.num_pages) {
-        atomicOr(a.status, STATUS_BAD_INDEX);
-        return 0;
-      }
-      return page;
-    };
-    uint32_t n = 0;  // ring uses so far
-    bool ok = true;
     int64_t rel = c.pos - c.base;
     int hc = (int)(rel / c.s.tiles), j = (int)(rel - (int64_t)hc * c.s.tiles);
-    int slot, page = box_page(j, slot);
-    while (ok && c.pos < c.end) {
-      const int g = hc / a.chunks;
-      const int cur_page = page, cur_slot = slot;
-      // the next tile's page, read while this tile's buffers are waited for
-      ++c.pos;
-      ++j;
-      if (c.pos < c.end) {
-        if (j == c.s.tiles) {
-          j = 0;
-          if (++hc == nhc) {
-            hc = 0;
-            c.base += (int64_t)c.s.tiles * nhc;
-            c.s = make_seq(a, ++c.b, false);
-          }
+    struct Batch {
+      int count, head, page, slot;  // tiles, key head; this lane's page (-1: not needed) and first slot in it
+    };
+    auto next_batch = [&]() -> Batch {
+      Batch r{0, 0, -1, 0};
+      if (c.pos >= c.end) return r;
+      r.count = (int)min((int64_t)min(per_batch, c.s.tiles - j), c.end - c.pos);
+      r.head = hc / a.chunks;
+      const int t = c.s.tile(j + my_tile) * TK + my_box * a.box_tokens;
+      if (my_tile < r.count && t < c.s.len && (t + a.box_tokens > c.s.lo || t < c.s.sinks)) {
+        const int pi = t / a.page_size;
+        r.slot = t - pi * a.page_size;
+        r.page = a.table[(int64_t)c.b * a.ld_table + pi];
+        if (r.page < 0 || r.page >= a.num_pages) {
+          atomicOr(a.status, STATUS_BAD_INDEX);
+          r.page = 0;
         }
-        page = box_page(j, slot);
       }
-      const unsigned need = __ballot_sync(0xffffffffu, cur_page >= 0);
-      const uint32_t bytes = (uint32_t)__popc(need) * box_bytes;
+      c.pos += r.count;
+      j += r.count;
+      if (c.pos < c.end && j == c.s.tiles) {
+        j = 0;
+        if (++hc == nhc) {
+          hc = 0;
+          c.base += (int64_t)c.s.tiles * nhc;
+          c.s = make_seq<TK>(a, ++c.b, false);
+        }
+      }
+      return r;
+    };
+    uint32_t n = 0;  // fetches issued: K and V of tile 0, 1, ...
+    bool ok = true;
+    Batch cur = next_batch();
+    while (ok && cur.count > 0) {
+      const Batch nxt = next_batch();
+      const unsigned need = __ballot_sync(0xffffffffu, cur.page >= 0);
+      for (int i = 0; ok && i < cur.count; ++i) {
+        const unsigned mine = (need >> (i * nbox)) & (nbox == 32 ? 0xffffffffu : (1u << nbox) - 1);
+        const uint32_t bytes = (uint32_t)__popc(mine) * box_bytes;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++n) {
-        const uint32_t sl = n % R::N, round = n / R::N;
-        ok = round == 0 || mbar_wait(&empty[sl], (round - 1) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[sl], bytes);
-        __syncwarp();
-        if (cur_page >= 0)
-          tma_load_5d(ring_s + sl * R::SLOT + lane * box_bytes, kv ? &vmap : &kmap, &full[sl], cur_slot, g, cur_page);
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t sl = n % R::N, round = n / R::N;
+          ok = round == 0 || mbar_wait(&empty[sl], (round - 1) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[sl], bytes);
+          __syncwarp();
+          if (my_tile == i && cur.page >= 0)
+            tma_load_5d(ring_s + sl * R::SLOT + my_box * box_bytes, kv ? &vmap : &kmap, &full[sl], cur.slot, cur.head,
+                        cur.page);
+          ++n;
+        }
       }
+      cur = nxt;
     }
     // the CTA does not end before its copies have landed, whatever the others did
     int no_abort = 0;
-    const uint32_t first = n > (uint32_t)R::N ? n - R::N : 0;
-    for (uint32_t i = first; i < n; ++i)
+    for (uint32_t i = n > (uint32_t)R::N ? n - R::N : 0; i < n; ++i)
       mbar_wait(&full[i % R::N], (i / R::N) & 1, &no_abort, a.status, STATUS_TIMEOUT, DRAIN_NS);
     return;
   }
 
   // -------------------------------------------------------------- computing warps
   const int g8 = lane >> 2, c4 = lane & 3;  // row group and column pair of the mma fragments
-  const int key_a = warp * 16 + g8;         // this lane's tokens of a tile: key_a, key_a + 8
-  // shared-memory address parts of the lane's ldmatrix rows
+  // shared-memory address parts of the lane's ldmatrix rows: token 16 y + key of the warp's
   const int bt = a.box_tokens;
-  const uint32_t blk = (uint32_t)bt * ROWB;  // bytes from one 64-column block to the next
-  auto row_base = [&](int key) -> uint32_t { return (uint32_t)(key / bt) * (bt * ROWB * NBLK) + (key % bt) * ROWB; };
-  const int k_key = warp * 16 + (lane & 15);  // K: matrices (keys 0-7, 8-15) x 2 chunks
+  const uint32_t blk = (uint32_t)bt * ROWB;  // bytes from one block to the next
+  auto row_base = [&](int key) -> uint32_t { return (uint32_t)(key / bt) * (blk * NBLK) + (key % bt) * ROWB; };
+  const int k_key = lane & 15;  // K: matrices (keys 0-7, 8-15) x 2 chunks
   // V: the same with E4M3; bf16 (2 chunks) x (keys 0-7, 8-15)
-  const int v_key = F8 ? k_key : warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-  const uint32_t k_row = row_base(k_key), v_row = row_base(v_key);
-  const uint32_t k_sw = F8 ? (k_key >> 1) & 3 : k_key & 7, v_sw = F8 ? (v_key >> 1) & 3 : v_key & 7;
-  const uint32_t k_half = lane >> 4;                         // chunk of the pair
+  const int v_key = F8 ? k_key : (lane & 7) + ((lane >> 4) << 3);
+  uint32_t k_row[KT], v_row[KT];
+#pragma unroll
+  for (int y = 0; y < KT; ++y) {
+    k_row[y] = row_base(warp * KW + 16 * y + k_key);
+    v_row[y] = row_base(warp * KW + 16 * y + v_key);
+  }
+  const uint32_t k_sw = ROWB == 64 ? (k_key >> 1) & 3 : k_key & 7, v_sw = ROWB == 64 ? (v_key >> 1) & 3 : v_key & 7;
+  const uint32_t k_half = lane >> 4;  // chunk of the pair
   const uint32_t v_half = F8 ? lane >> 4 : (lane >> 3) & 1;
-  constexpr int CPB = ROWB / 16;  // 16-byte chunks of a block's row: 8 (bf16), 4 (E4M3)
-  auto chunk_addr = [&](uint32_t row, uint32_t sw, int chunk) -> uint32_t {
-    return row + (uint32_t)(chunk / CPB) * blk + ((((uint32_t)(chunk % CPB)) ^ sw) << 4);
+  constexpr int CPB = ROWB / 16;  // 16-byte chunks of a block's row
+  // offset of 16-byte chunk 2 pair + half within a token's row
+  auto chunk_off = [&](int pair, uint32_t half, uint32_t sw) -> uint32_t {
+    return (uint32_t)(2 * pair / CPB) * blk + ((((uint32_t)(2 * pair % CPB) + half) ^ sw) << 4);
   };
 
   uint32_t qf[NT][KS][2];
@@ -328,7 +355,7 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
   float o[MT][NT][4];
   float m[NT][2], l[NT][2];
 
-  uint32_t n = 0;
+  uint32_t n = 0;  // ring uses so far
   bool ok = true;
   int64_t rel = c.pos - c.base;
   int hc = (int)(rel / c.s.tiles), j = (int)(rel - (int64_t)hc * c.s.tiles);
@@ -387,56 +414,69 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
     }
 
     for (; ok && c.pos < seg_end; ++c.pos, ++j) {
-      const int t0 = c.s.tile(j) * TK;
-      const bool whole = c.s.whole(t0);
+      const int tile0 = c.s.tile(j) * TK, t0 = tile0 + warp * KW;
+      const bool whole = c.s.whole(tile0);
       // ---- S^T = K Q^T
-      uint32_t sl = n % R::N, par = (n / R::N) & 1;
-      ++n;
-      ok = mbar_wait(&full[sl], par, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
+      uint32_t sl = n % R::N;
+      ok = mbar_wait(&full[sl], (n / R::N) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      float sc[NT][4];
+      float sc[KT][NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
+      for (int y = 0; y < KT; ++y)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sc[y][t][0] = sc[y][t][1] = sc[y][t][2] = sc[y][t][3] = 0.0f;
       const uint32_t kb = ring_s + sl * R::SLOT;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        if (F8) {
-          if (k & 1) continue;
+      for (int k = 0; k < (F8 ? KS / 2 : KS); ++k) {
+        const uint32_t off = kb + chunk_off(k, k_half, k_sw);
+#pragma unroll
+        for (int y = 0; y < KT; ++y) {
           uint32_t r[4];
-          ldsm4(kb + chunk_addr(k_row, k_sw, k + k_half), r);
+          ldsm4(off + k_row[y], r);
+          if (F8) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {  // chunk k + x
-            const uint32_t af[4] = {f16x2_of_e4m3x2(r[2 * x]), f16x2_of_e4m3x2(r[2 * x + 1]),
-                                    f16x2_of_e4m3x2(r[2 * x] >> 16), f16x2_of_e4m3x2(r[2 * x + 1] >> 16)};
+            for (int x = 0; x < 2; ++x) {  // chunk 2k + x
+              const uint32_t af[4] = {f16x2_of_e4m3x2(r[2 * x]), f16x2_of_e4m3x2(r[2 * x + 1]),
+                                      f16x2_of_e4m3x2(r[2 * x] >> 16), f16x2_of_e4m3x2(r[2 * x + 1] >> 16)};
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<true>(sc[t], af, qf[t][k + x][0], qf[t][k + x][1]);
+              for (int t = 0; t < NT; ++t) mma16816<true>(sc[y][t], af, qf[t][(2 * k + x) % KS][0], qf[t][(2 * k + x) % KS][1]);
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816<false>(sc[y][t], r, qf[t][k][0], qf[t][k][1]);
           }
-        } else {
-          uint32_t r[4];
-          ldsm4(kb + chunk_addr(k_row, k_sw, 2 * k + k_half), r);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816<false>(sc[t], r, qf[t][k][0], qf[t][k][1]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[sl]);
       // ---- softmax
-      bool see[2] = {true, true};
+#pragma unroll
+      for (int y = 0; y < KT; ++y)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[y][t][e] *= qs[t][e & 1];
       if (!whole) {
-        see[0] = c.s.sees(t0 + key_a);
-        see[1] = c.s.sees(t0 + key_a + 8);
+#pragma unroll
+        for (int y = 0; y < KT; ++y)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (!c.s.sees(t0 + 16 * y + 8 * x + g8)) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t) sc[y][t][2 * x] = sc[y][t][2 * x + 1] = -INFINITY;
+            }
       }
-      uint32_t pf[NT][2], pl[NT][2];
+      uint32_t pf[KT][NT][2], pl[KT][NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x0 = see[0] ? sc[t][e] * qs[t][e] : -INFINITY;
-          float x1 = see[1] ? sc[t][2 + e] * qs[t][e] : -INFINITY;
-          float mx = fmaxf(x0, x1);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < KT; ++y) mx = fmax3(mx, sc[y][t][e], sc[y][t][2 + e]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -444,11 +484,14 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
           const float mu = mn == -INFINITY ? 0.0f : mn;  // nothing visible yet
           alpha[e] = ex2_fast(m[t][e] - mu);             // m = -inf: 0
           m[t][e] = mn;
-          x0 = ex2_fast(x0 - mu);
-          x1 = ex2_fast(x1 - mu);
-          l[t][e] = fmaf(l[t][e], alpha[e], x0 + x1);
-          sc[t][e] = x0;
-          sc[t][2 + e] = x1;
+          float sum = 0.0f;
+#pragma unroll
+          for (int y = 0; y < KT; ++y) {
+            sc[y][t][e] = ex2_fast(sc[y][t][e] - mu);
+            sc[y][t][2 + e] = ex2_fast(sc[y][t][2 + e] - mu);
+            sum += sc[y][t][e] + sc[y][t][2 + e];
+          }
+          l[t][e] = fmaf(l[t][e], alpha[e], sum);
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
@@ -460,72 +503,75 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
           }
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float p0 = sc[t][2 * x], p1 = sc[t][2 * x + 1];
-          if (F8) {
-            pf[t][x] = movm(pack_f16(p0, p1));
-          } else {
-            const uint32_t hi = pack_bf16(p0, p1);
-            pf[t][x] = movm(hi);
-            pl[t][x] = movm(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi)));
+        for (int y = 0; y < KT; ++y)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float p0 = sc[y][t][2 * x], p1 = sc[y][t][2 * x + 1];
+            if (F8) {
+              pf[y][t][x] = movm(pack_f16(p0, p1));
+            } else {
+              const uint32_t hi = pack_bf16(p0, p1);
+              pf[y][t][x] = movm(hi);
+              pl[y][t][x] = movm(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi)));
+            }
           }
-        }
       }
       // ---- O^T += V^T P^T
-      sl = n % R::N;
-      par = (n / R::N) & 1;
       ++n;
-      ok = mbar_wait(&full[sl], par, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
+      sl = n % R::N;
+      ok = mbar_wait(&full[sl], (n / R::N) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t vb = ring_s + sl * R::SLOT;
-      uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;  // values of unseen tokens, NaN maybe, become 0
-      if (!whole) {
-        const int t = t0 + warp * 16 + 2 * c4;
-        mk0 = (c.s.sees(t) ? 0xffffu : 0u) | (c.s.sees(t + 1) ? 0xffff0000u : 0u);
-        mk1 = (c.s.sees(t + 8) ? 0xffffu : 0u) | (c.s.sees(t + 9) ? 0xffff0000u : 0u);
-      }
-      if (F8) {
 #pragma unroll
-        for (int i = 0; i < MT / 2; ++i) {  // 32 columns: matrices (keys 0-7, 8-15) x chunks (2i, 2i + 1)
-          uint32_t r[4];
-          ldsm4t(vb + chunk_addr(v_row, v_sw, 2 * i + v_half), r);
-          uint32_t ev[4], od[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t s = __byte_perm(r[x], 0, 0x3120);
-            const uint32_t mk = x & 1 ? mk1 : mk0;
-            ev[x] = f16x2_of_e4m3x2(s) & mk;
-            od[x] = f16x2_of_e4m3x2(s >> 16) & mk;
-          }
-          const uint32_t ea[4] = {ev[0], ev[2], ev[1], ev[3]}, oa[4] = {od[0], od[2], od[1], od[3]};
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma16816<true>(o[2 * i][t], ea, pf[t][0], pf[t][1]);
-            mma16816<true>(o[2 * i + 1][t], oa, pf[t][0], pf[t][1]);
-          }
+      for (int y = 0; y < KT; ++y) {
+        uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;  // values of unseen tokens, NaN maybe, become 0
+        if (!whole) {
+          const int t = t0 + 16 * y + 2 * c4;
+          mk0 = (c.s.sees(t) ? 0xffffu : 0u) | (c.s.sees(t + 1) ? 0xffff0000u : 0u);
+          mk1 = (c.s.sees(t + 8) ? 0xffffu : 0u) | (c.s.sees(t + 9) ? 0xffff0000u : 0u);
         }
-      } else {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {  // 16 columns: matrices (chunks 2i, 2i + 1) x (keys 0-7, 8-15)
+        for (int i = 0; i < (F8 ? MT / 2 : MT); ++i) {
           uint32_t r[4];
-          ldsm4t(vb + chunk_addr(v_row, v_sw, 2 * i + v_half), r);
-          if (!whole) {
-            r[0] &= mk0;
-            r[1] &= mk0;
-            r[2] &= mk1;
-            r[3] &= mk1;
-          }
+          ldsm4t(vb + v_row[y] + chunk_off(i, v_half, v_sw), r);
+          if (F8) {  // 32 columns: matrices (keys 0-7, 8-15) x chunks (2i, 2i + 1)
+            uint32_t ev[4], od[4];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma16816<false>(o[i][t], r, pf[t][0], pf[t][1]);
-            mma16816<false>(o[i][t], r, pl[t][0], pl[t][1]);
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t s = __byte_perm(r[x], 0, 0x3120);
+              ev[x] = f16x2_of_e4m3x2(s);
+              od[x] = f16x2_of_e4m3x2(s >> 16);
+              if (!whole) {
+                ev[x] &= x & 1 ? mk1 : mk0;
+                od[x] &= x & 1 ? mk1 : mk0;
+              }
+            }
+            const uint32_t ea[4] = {ev[0], ev[2], ev[1], ev[3]}, oa[4] = {od[0], od[2], od[1], od[3]};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma16816<true>(o[(2 * i) % MT][t], ea, pf[y][t][0], pf[y][t][1]);
+              mma16816<true>(o[(2 * i + 1) % MT][t], oa, pf[y][t][0], pf[y][t][1]);
+            }
+          } else {  // 16 columns: matrices (chunks 2i, 2i + 1) x (keys 0-7, 8-15)
+            if (!whole) {
+              r[0] &= mk0;
+              r[1] &= mk0;
+              r[2] &= mk1;
+              r[3] &= mk1;
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma16816<false>(o[i][t], r, pf[y][t][0], pf[y][t][1]);
+              mma16816<false>(o[i][t], r, pl[y][t][0], pl[y][t][1]);
+            }
           }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[sl]);
+      ++n;
     }
 
     // ---- join the four warps: common maximum, then the sums in warp order
@@ -642,15 +688,20 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
         };
         const bool final_level = ngroups == 1 || level == 1;
         if (!final_level && cnt == 1) continue;  // a group of one stands for itself
+        for (int x = tid; x < cnt * HT; x += NCW * 32) {
+          const float* pp = part_of(x / HT) + (size_t)HT * D + x % HT;
+          s_w[x / HT][x % HT] = __ldcg(pp);
+          s_s[x / HT][x % HT] = __ldcg(pp + HT);
+        }
+        bar_compute();
         if (tid < HT) {
           float mx = -INFINITY;
-          for (int i = 0; i < cnt; ++i) mx = fmaxf(mx, __ldcg(part_of(i) + (size_t)HT * D + tid));
+          for (int i = 0; i < cnt; ++i) mx = fmaxf(mx, s_w[i][tid]);
           float s = 0.0f;
           for (int i = 0; i < cnt; ++i) {
-            const float* pp = part_of(i) + (size_t)HT * D + tid;
-            const float w = mx == -INFINITY ? 0.0f : ex2_fast(__ldcg(pp) - mx);
+            const float w = mx == -INFINITY ? 0.0f : ex2_fast(s_w[i][tid] - mx);
             s_w[i][tid] = w;
-            s += w * __ldcg(pp + HT);
+            s += w * s_s[i][tid];
           }
           s_mx[tid] = mx;
           s_inv[tid] = final_level ? (s > 0.0f ? vscale / s : (s == s ? 0.0f : s)) : s;
@@ -658,21 +709,30 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
         }
         bar_compute();
         float* lead = part_of(0);
-        for (int x = tid; x < HT * D / 2; x += NCW * 32) {
-          const int h = 2 * x / D, col = 2 * x % D;
-          float2 v = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-          for (int i = 0; i < cnt; ++i) {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(part_of(i) + 2 * (size_t)x));
-            const float w = s_w[i][h];
-            v.x = fmaf(w, y.x, v.x);
-            v.y = fmaf(w, y.y, v.y);
+        for (int x = tid; x < HT * D / 4; x += NCW * 32) {
+          const int h = 4 * x / D, col = 4 * x % D;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int i0 = 0; i0 < cnt; i0 += 8) {
+            float4 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < cnt) y[i] = __ldcg(reinterpret_cast<const float4*>(part_of(i0 + i)) + x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < cnt) {
+                const float w = s_w[i0 + i][h];
+                v.x = fmaf(w, y[i].x, v.x);
+                v.y = fmaf(w, y[i].y, v.y);
+                v.z = fmaf(w, y[i].z, v.z);
+                v.w = fmaf(w, y[i].w, v.w);
+              }
           }
           if (final_level) {
+            const float r = s_inv[h];
             if (h < heads)
-              *reinterpret_cast<uint32_t*>(out + (int64_t)h * D + col) = pack_bf16(v.x * s_inv[h], v.y * s_inv[h]);
+              *reinterpret_cast<uint2*>(out + (int64_t)h * D + col) = make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
           } else {
-            __stcg(reinterpret_cast<float2*>(lead + 2 * (size_t)x), v);
+            __stcg(reinterpret_cast<float4*>(lead) + x, v);
           }
         }
         if (!final_level && tid < HT) {
@@ -689,7 +749,7 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
       if (++hc == nhc) {
         hc = 0;
         c.base += (int64_t)c.s.tiles * nhc;
-        c.s = make_seq(a, ++c.b, false);
+        c.s = make_seq<TK>(a, ++c.b, false);
       }
     }
   }
@@ -714,6 +774,8 @@ cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& km, const CUtensorM
 
 }  // namespace
 
+int kv_decode_tile(int d, bool e4m3) { return d * (e4m3 ? 1 : 2) <= 128 ? 128 : 64; }  // Ring::TK
+
 int kv_decode_workers(int d, int hpg, int num_sms) {
   const int ht = kv_decode_head_tile(hpg);
   return (d * ht >= 4096 || (d == 192 && ht == 16) ? 1 : 2) * num_sms;
@@ -724,14 +786,15 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, bool e4m3, int d, int page_
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const uint64_t e = e4m3 ? 1 : 2;
-  // {64 columns, slot, 64-column block, key head, page}: a box of all blocks
-  // lands as blocks of [box_tokens][64] one behind the other
-  cuuint64_t dims[5] = {64, (cuuint64_t)page_size, (cuuint64_t)d / 64, (cuuint64_t)nkv, (cuuint64_t)num_pages};
-  cuuint64_t strides[4] = {(cuuint64_t)stride_slot * e, 64 * e, (cuuint64_t)stride_head * e, (cuuint64_t)stride_page * e};
-  cuuint32_t box[5] = {64, (cuuint32_t)box_tokens, (cuuint32_t)d / 64, 1, 1};
+  // {block of columns, slot, block, key head, page}: a box of all blocks lands
+  // as [box_tokens][block] one behind the other (Ring::BLOCK bytes a block's row)
+  const uint64_t row = d * e, blk = row % 128 == 0 ? 128 : 64;
+  cuuint64_t dims[5] = {blk / e, (cuuint64_t)page_size, row / blk, (cuuint64_t)nkv, (cuuint64_t)num_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)stride_slot * e, blk, (cuuint64_t)stride_head * e, (cuuint64_t)stride_page * e};
+  cuuint32_t box[5] = {(cuuint32_t)(blk / e), (cuuint32_t)box_tokens, (cuuint32_t)(row / blk), 1, 1};
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, blk == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

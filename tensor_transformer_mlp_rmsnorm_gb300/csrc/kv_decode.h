@@ -28,7 +28,7 @@ struct DecodeArgs {
   float scale_log2;  // softmax scale * log2(e)
   int window, sinks;  // window 0: no limit
   const float *k_inv_scale, *v_inv_scale;  // E4M3: [nkv] or null
-  int box_tokens;  // tokens a TMA box holds: 8, 16, 32 or 64, dividing page_size
+  int box_tokens;  // tokens a TMA box holds: 8 to 128, dividing page_size and the tile
   int workers;     // CTAs the work is divided over
   float* part;     // partial results, 2 per worker (kv_decode_part_floats)
   uint32_t* counters;  // 3 per worker, zero between launches
@@ -37,6 +37,8 @@ struct DecodeArgs {
 
 // Query heads worked on together: the smallest tile that holds a key head's.
 inline int kv_decode_head_tile(int hpg) { return hpg <= 8 ? 8 : 16; }
+// Tokens of a tile.
+int kv_decode_tile(int d, bool e4m3);
 // CTAs the kernel runs with for this head size.
 int kv_decode_workers(int d, int hpg, int num_sms);
 inline size_t kv_decode_part_floats(int d, int hpg) {

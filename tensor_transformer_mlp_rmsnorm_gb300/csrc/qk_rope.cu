@@ -33,7 +33,16 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int ROPE_UNROLL = 4;
+#ifndef P_RU
+#define P_RU 2
+#define P_RB 3
+#define P_BU 2
+#define P_BB 2
+#endif
+constexpr int ROPE_UNROLL = P_RU;   // heads a lane group has in flight
+constexpr int ROWS_BLOCKS = P_RB;
+constexpr int BWD_UNROLL = P_BU;
+constexpr int BWD_BLOCKS = P_BB;
 
 // 8 consecutive elements as loaded.
 template <typename T>
@@ -87,6 +96,13 @@ struct HeadLanes {
     for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
+  static __device__ __forceinline__ void sum2(float& v, float& y) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+  }
 };
 
 // The two chunks of unit u: partners 8u + i and rot/2 + 8u + i for pairs
@@ -120,11 +136,12 @@ __device__ __forceinline__ void rotate16(float* a, float* b, const float* cs, co
 }
 
 // Cosine and sine of position * turn: one frequency a lane, left in shared memory.
+template <int D>
 __device__ __forceinline__ void row_angles(const uint64_t* turn, int nfreq, int pos, float2* cs_warp) {
   const int lane = threadIdx.x & 31;
   __syncwarp();  // the previous row's readers are done
 #pragma unroll
-  for (int k = 0; k < ROPE_MAX_PAIRS / 32; ++k) {
+  for (int k = 0; k < D / 64; ++k) {
     const int f = lane + 32 * k;
     if (f < nfreq) {
       const uint64_t ph = turn[k] * (uint64_t)(int64_t)pos;  // turns mod 1
@@ -136,9 +153,10 @@ __device__ __forceinline__ void row_angles(const uint64_t* turn, int nfreq, int 
   __syncwarp();
 }
 
+template <int D>
 __device__ __forceinline__ void load_turns(const RopeFreqs& fr, uint64_t* turn) {
 #pragma unroll
-  for (int k = 0; k < ROPE_MAX_PAIRS / 32; ++k) {
+  for (int k = 0; k < D / 64; ++k) {
     const int f = (threadIdx.x & 31) + 32 * k;
     turn[k] = f < fr.rot / 2 ? fr.turn[f] : 0;
   }
@@ -181,9 +199,37 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int r
   return cu[lo] <= r && r < cu[lo + 1] ? lo : -1;
 }
 
+// An append row's position, and where its key and value go in the cache
+// (elements; negative: nowhere).
+__device__ __forceinline__ int append_place(const RopeArgs& a, int64_t row, int64_t& slot_off) {
+  slot_off = -1;
+  int b, at;
+  if (a.cu_rows) {
+    b = find_sequence(a.cu_rows, a.batch, (int)row);
+    if (b < 0) return 0;
+    at = (int)row - a.cu_rows[b];
+  } else {
+    b = (int)row / a.rows_per_seq;
+    at = (int)row - b * a.rows_per_seq;
+    if (a.new_lens && at >= a.new_lens[b]) return 0;
+  }
+  const int past = a.past_lens[b];
+  if (past < 0) return 0;  // an inactive sequence
+  const uint32_t p = (uint32_t)past + (uint32_t)at;
+  const uint32_t pi = p / (uint32_t)a.page_size;
+  int page = -1;
+  if (pi < (uint32_t)a.max_pages) page = a.table[(int64_t)b * a.ld_table + pi];
+  if (page < 0 || page >= a.num_pages) {  // nowhere to store: reported, not written
+    if ((threadIdx.x & 31) == 0) atomicOr(a.status, STATUS_BAD_INDEX);
+    return 0;
+  }
+  slot_off = (int64_t)page * a.stride_page + (int64_t)(p - pi * a.page_size) * a.stride_slot;
+  return (int)p;
+}
+
 // KIND 0: rows to rows (RopeArgs); 1, 2: append to a bf16 or E4M3 cache.
 template <typename T, int D, int KIND>
-__global__ void __launch_bounds__(THREADS) rope_rows_kernel(const __grid_constant__ RopeArgs a,
+__global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const __grid_constant__ RopeArgs a,
                                                             const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
   __shared__ __align__(16) float2 s_cs[WARPS][ROPE_MAX_PAIRS];
@@ -194,46 +240,19 @@ __global__ void __launch_bounds__(THREADS) rope_rows_kernel(const __grid_constan
   const int rot = fr.rot;
   int oa, ob;
   unit_offsets(active ? u : 0, rot, il, oa, ob);
-  uint64_t turn[ROPE_MAX_PAIRS / 32];
-  load_turns(fr, turn);
+  uint64_t turn[D / 64];
+  load_turns<D>(fr, turn);
   const int h_end = a.nq + a.nkv + (KIND ? a.nkv : 0);
   const int h_begin = KIND && !a.out ? a.nq : 0;  // an append without a query output skips the queries
   const int64_t items = a.rows * a.splits, stride = (int64_t)gridDim.x * WARPS;
   for (int64_t it = (int64_t)blockIdx.x * WARPS + warp; it < items; it += stride) {
     const int64_t row = it / a.splits;
     const int split = (int)(it - row * a.splits);
-    int pos;
-    int64_t slot_off = 0;
-    if (KIND) {
-      int b, at;
-      if (a.cu_rows) {
-        b = row <= 0x7fffffff ? find_sequence(a.cu_rows, a.batch, (int)row) : -1;
-        if (b < 0) continue;
-        at = (int)row - a.cu_rows[b];
-      } else {
-        b = (int)(row / a.rows_per_seq);
-        at = (int)(row - (int64_t)b * a.rows_per_seq);
-        if (a.new_lens && at >= a.new_lens[b]) continue;
-      }
-      const int past = a.past_lens[b];
-      if (past < 0) continue;  // an inactive sequence
-      const int64_t p64 = (int64_t)past + at;
-      const int64_t pi = p64 / a.page_size;
-      int page = -1;
-      if (pi < a.max_pages) page = a.table[(int64_t)b * a.ld_table + pi];
-      if (page < 0 || page >= a.num_pages) {  // nowhere to store: reported, not written
-        if (lane == 0) atomicOr(a.status, STATUS_BAD_INDEX);
-        continue;
-      }
-      pos = (int)p64;
-      slot_off = (int64_t)page * a.stride_page + (p64 - pi * a.page_size) * a.stride_slot;
-    } else {
-      pos = a.pos ? a.pos[row] : (int)(a.seq > 0 ? row % a.seq : row);
-    }
     const T* in = static_cast<const T*>(a.in) + row * a.ld_in;
     const int hstep = a.splits * HL::GROUPS;
     float cs[8], sn[8];
-    bool have_angles = false;
+    int64_t slot_off = 0;
+    bool placed = false;
     for (int h0 = h_begin + split * HL::GROUPS + group; h0 - group < h_end; h0 += ROPE_UNROLL * hstep) {
       Raw8<T> xa[ROPE_UNROLL], xb[ROPE_UNROLL];
 #pragma unroll
@@ -248,10 +267,12 @@ __global__ void __launch_bounds__(THREADS) rope_rows_kernel(const __grid_constan
           xb[k].set(z);
         }
       }
-      if (!have_angles) {  // behind the first loads, which they do not wait for
-        if (rot) row_angles(turn, rot / 2, pos, s_cs[warp]);
+      if (!placed) {  // behind the first loads, which do not wait for it
+        const int pos = KIND ? append_place(a, row, slot_off) : a.pos ? a.pos[row] : (int)(a.seq > 0 ? row % a.seq : row);
+        if (KIND && slot_off < 0) break;
+        if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
         unit_angles(s_cs[warp], u, rot, 1.0f, cs, sn);
-        have_angles = true;
+        placed = true;
       }
 #pragma unroll
       for (int k = 0; k < ROPE_UNROLL; ++k) {
@@ -324,15 +345,14 @@ __global__ void __launch_bounds__(THREADS) rope_rows_kernel(const __grid_constan
   }
 }
 
-// Backward.  The query heads and the key heads of a row are taken one after the
-// other so that each lane adds its 16 columns of the two weight gradients in
-// registers; blocks leave their sums as partials, added in a fixed order by
+// Backward.  All rows' query heads are taken first, then their key heads, so
+// that a lane holds its 16 columns of one weight gradient at a time in registers; blocks leave their sums as partials, added in a fixed order by
 // rope_dw_kernel, so the gradients are the same every run.
 template <typename T, int D>
-__global__ void __launch_bounds__(THREADS) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a,
+__global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a,
                                                            const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
-  constexpr int UN = 2;
+  constexpr int UN = BWD_UNROLL;
   __shared__ __align__(16) float2 s_cs[WARPS][ROPE_MAX_PAIRS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = lane % HL::LANES, group = lane / HL::LANES;
@@ -341,24 +361,23 @@ __global__ void __launch_bounds__(THREADS) rope_bwd_kernel(const __grid_constant
   const int rot = fr.rot;
   int oa, ob;
   unit_offsets(active ? u : 0, rot, il, oa, ob);
-  uint64_t turn[ROPE_MAX_PAIRS / 32];
-  load_turns(fr, turn);
-  float acc[2][16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.0f;
+  uint64_t turn[D / 64];
+  load_turns<D>(fr, turn);
+  __shared__ float s_dw[WARPS][2][D];
   const int64_t items = a.rows * a.splits, stride = (int64_t)gridDim.x * WARPS;
-  for (int64_t it = (int64_t)blockIdx.x * WARPS + warp; it < items; it += stride) {
-    const int64_t row = it / a.splits;
-    const int split = (int)(it - row * a.splits);
-    const int pos = a.pos ? a.pos[row] : (int)(a.seq > 0 ? row % a.seq : row);
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int h_begin = part ? a.nq : 0, h_end = part ? a.nq + a.nkv : a.nq;
+    const T* w = static_cast<const T*>(part ? a.k_norm_w : a.q_norm_w);
     const int hstep = a.splits * HL::GROUPS;
-    float cs[8], sn[8];
-    if (rot) row_angles(turn, rot / 2, pos, s_cs[warp]);
-    unit_angles(s_cs[warp], u, rot, -1.0f, cs, sn);
+    float acc[16];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int h_begin = part ? a.nq : 0, h_end = part ? a.nq + a.nkv : a.nq;
-      const T* w = static_cast<const T*>(part ? a.k_norm_w : a.q_norm_w);
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (int64_t it = (int64_t)blockIdx.x * WARPS + warp; it < items; it += stride) {
+      const int64_t row = it / a.splits;
+      const int split = (int)(it - row * a.splits);
+      float cs[8], sn[8];
+      bool placed = false;
       for (int h0 = h_begin + split * HL::GROUPS + group; h0 - group < h_end; h0 += UN * hstep) {
         Raw8<T> ga[UN], gb[UN], xa[UN], xb[UN];
 #pragma unroll
@@ -380,6 +399,12 @@ __global__ void __launch_bounds__(THREADS) rope_bwd_kernel(const __grid_constant
             }
           }
         }
+        if (!placed) {  // behind the first loads, which do not wait for it
+          const int pos = a.pos ? a.pos[row] : (int)(a.seq > 0 ? row % a.seq : row);
+          if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
+          unit_angles(s_cs[warp], u, rot, -1.0f, cs, sn);
+          placed = true;
+        }
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
           const int h = h0 + k * hstep;
@@ -392,32 +417,28 @@ __global__ void __launch_bounds__(THREADS) rope_bwd_kernel(const __grid_constant
             float va[8], vb[8];
             xa[k].get(va);
             xb[k].get(vb);
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
-            ss = HL::sum(ss);
-            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
             float wa[8], wb[8];
             Raw8<T> wr;
             wr.load(w + oa);
             wr.get(wa);
             wr.load(w + ob);
             wr.get(wb);
-            float dot = 0.0f;
+            // both sums at once: sum x^2 and sum w g x = mean(w g xh) d / r
+            float ss = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              va[i] *= r;  // xh
-              vb[i] *= r;
-              const float ta = fa[i] * va[i], tb = fb[i] * vb[i];  // g xh
-              acc[part][i] += ta;
-              acc[part][8 + i] += tb;
-              dot = fmaf(wa[i], ta, fmaf(wb[i], tb, dot));
+              ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
+              dot = fmaf(wa[i] * fa[i], va[i], fmaf(wb[i] * fb[i], vb[i], dot));
             }
-            dot = HL::sum(dot) * (1.0f / D);
+            HL::sum2(ss, dot);
+            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+            const float c = dot * (1.0f / D) * r * r * r;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              fa[i] = r * (wa[i] * fa[i] - va[i] * dot);
-              fb[i] = r * (wb[i] * fb[i] - vb[i] * dot);
+              acc[i] = fmaf(fa[i], va[i] * r, acc[i]);
+              acc[8 + i] = fmaf(fb[i], vb[i] * r, acc[8 + i]);
+              fa[i] = fmaf(r * wa[i], fa[i], -c * va[i]);
+              fb[i] = fmaf(r * wb[i], fb[i], -c * vb[i]);
             }
           }
           if (!active || h >= h_end) continue;
@@ -429,21 +450,18 @@ __global__ void __launch_bounds__(THREADS) rope_bwd_kernel(const __grid_constant
         }
       }
     }
-  }
-  if (!a.part) return;
-  // lanes of the same unit, then the warps of the block in order
-  __shared__ float s_dw[WARPS][2][D];
-#pragma unroll
-  for (int part = 0; part < 2; ++part)
+    // lanes of the same unit
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float v = acc[part][i];
+      float v = acc[i];
 #pragma unroll
       for (int o = HL::LANES; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (active && group == 0) s_dw[warp][part][(i < 8 ? oa : ob - 8) + i] = v;
     }
+  }
+  if (!a.part) return;
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += THREADS) {
+  for (int c = threadIdx.x; c < 2 * D; c += THREADS) {  // the warps of the block in order
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) v += (&s_dw[k][0][0])[c];

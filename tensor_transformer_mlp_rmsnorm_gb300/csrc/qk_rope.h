@@ -34,7 +34,7 @@ struct RopeArgs {
   int splits;
   // append
   int batch;
-  int64_t rows_per_seq;
+  int rows_per_seq;
   const int32_t *cu_rows, *new_lens, *past_lens, *table;
   int64_t ld_table;
   int max_pages;  // pages of a sequence that the table holds

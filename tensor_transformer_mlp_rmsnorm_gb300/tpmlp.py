@@ -665,53 +665,90 @@ class Rotary:
         self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
 
 
-def _stream_of(device, stream):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+_BF, _F32T, _I32T = torch.bfloat16, torch.float32, torch.int32
+# the raw handle of torch's current stream on a device, without a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(t, width: int, dtype, name: str, device=None, rows=None):
-    """Pointer and row stride of a 2-D tensor whose rows hold `width` contiguous values."""
-    if (t.dtype is not dtype or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1)
-            or t.shape[1] < width or (rows is not None and t.shape[0] != rows)
-            or (device is not None and t.device != device)):
-        raise TPMLPError(ERR_ARG, f"{name}: need {dtype} rows of at least {width} contiguous values"
-                                  + (f", {rows} of them," if rows is not None else "") + " on the call's CUDA device, "
-                                  f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _stream_of(device, index: int, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
-def _vec(t, n: int, dtype, name: str, device):
+def _bad(t, name: str, want: str):
+    return TPMLPError(ERR_ARG, f"{name}: need {want}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
+                               f"{t.device}")
+
+
+def _rows(t, width: int, dtype, name: str, index: int, rows: int = -1):
+    """Pointer, row count and row stride of a 2-D tensor on CUDA device `index` whose rows hold at least `width`
+    contiguous values."""
+    shape = t.shape
+    if len(shape) == 2 and t.dtype is dtype and t.get_device() == index and shape[1] >= width:
+        n = shape[0]
+        ld, inner = t.stride()
+        if (rows < 0 or n == rows) and (inner == 1 or shape[1] == 1):
+            return t.data_ptr(), n, ld if n > 1 and ld != 0 else max(ld, shape[1])
+    raise _bad(t, name, f"{'' if rows < 0 else f'{rows} '}{dtype} rows of at least {width} contiguous values on "
+                        f"cuda:{index}")
+
+
+def _vec(t, n: int, dtype, name: str, index: int):
     if t is None:
         return None
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise TPMLPError(ERR_ARG, f"{name}: need contiguous {dtype} ({n},) on {device}, got {t.dtype} "
-                                  f"{tuple(t.shape)} on {t.device}")
+    shape = t.shape
+    if (len(shape) != 1 or t.dtype is not dtype or shape[0] != n or t.get_device() != index
+            or (n > 1 and t.stride(0) != 1)):
+        raise _bad(t, name, f"contiguous {dtype} ({n},) on cuda:{index}")
     return t.data_ptr()
 
 
-def _qk_desc(x, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps) -> QkDesc:
-    dt = BF16 if x.dtype is torch.bfloat16 else F32 if x.dtype is torch.float32 else None
+class _on:
+    """The device `index` made current while a call without a context runs, where it is not."""
+
+    def __init__(self, index: int):
+        self.dev = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.dev is not None:
+            self.dev.__enter__()
+
+    def __exit__(self, *exc):
+        if self.dev is not None:
+            self.dev.__exit__(*exc)
+
+
+def _qk_desc(n, dtype, index, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps) -> QkDesc:
+    dt = BF16 if dtype is _BF else F32 if dtype is _F32T else None
     if dt is None:
         raise TPMLPError(ERR_UNSUPPORTED, "rows must be float32 or bfloat16")
-    n = x.shape[0]
-    return QkDesc(n, n_heads, n_kv_heads, head_dim, dt, _vec(positions, n, torch.int32, "positions", x.device), seq,
-                  _vec(q_norm_w, head_dim, x.dtype, "q_norm_w", x.device),
-                  _vec(k_norm_w, head_dim, x.dtype, "k_norm_w", x.device), eps, 0)
+    return QkDesc(n, n_heads, n_kv_heads, head_dim, dt, _vec(positions, n, _I32T, "positions", index), seq,
+                  _vec(q_norm_w, head_dim, dtype, "q_norm_w", index),
+                  _vec(k_norm_w, head_dim, dtype, "k_norm_w", index), eps, 0)
+
+
+def _cuda_index(t, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise TPMLPError(ERR_ARG, f"{name} must be a CUDA tensor")
+    return index
 
 
 def qk_norm_rope(x, n_heads: int, n_kv_heads: int, head_dim: int, rotary: Rotary | None = None, positions=None,
                  seq: int = 0, q_norm_w=None, k_norm_w=None, eps: float = 1e-6, out=None, stream=None):
     """RMS norm (where a weight is given) and position rotation of the query and key heads at the start of each
-    row of x (tpattn_qk_rope_forward); out may be x.  Positions: int32 per row, or row % seq (seq 0: the row)."""
-    width = (n_heads + n_kv_heads) * head_dim
-    xp, ldx = _rows(x, width, x.dtype, "x")
+    row of x (tpattn_qk_rope_forward); out may be x.  Positions: int32 per row, or row % seq (seq 0: the row).
+    Runs on `stream`, torch's current stream where it is None."""
+    width, dtype, index = (n_heads + n_kv_heads) * head_dim, x.dtype, _cuda_index(x, "x")
+    xp, n, ldx = _rows(x, width, dtype, "x", index)
     if out is None:
-        out = torch.empty(x.shape[0], width, dtype=x.dtype, device=x.device)
-    op, ldo = _rows(out, width, x.dtype, "out", x.device, x.shape[0])
-    d = _qk_desc(x, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
-    with torch.cuda.device(x.device):
-        _check(lib().tpattn_qk_rope_forward(ctypes.byref(d), rotary.ref if rotary is not None else None, xp, ldx, op,
-                                            ldo, _stream_of(x.device, stream)))
+        out = x.new_empty((n, width))
+    op, _, ldo = _rows(out, width, dtype, "out", index, n)
+    d = _qk_desc(n, dtype, index, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
+    with _on(index):
+        _check(lib().tpattn_qk_rope_forward(d, rotary.spec if rotary is not None else None, xp, ldx, op, ldo,
+                                            _stream_of(x.device, index, stream)))
     return out
 
 
@@ -720,30 +757,37 @@ def qk_norm_rope_backward(dout, x, n_heads: int, n_kv_heads: int, head_dim: int,
                           dq_norm_w=None, dk_norm_w=None, workspace=None, stream=None):
     """Backward of qk_norm_rope: (dx, dq_norm_w, dk_norm_w), the weights' gradients in float32 (None without the
     weight).  x: the forward's input (only read with norm weights, else it may be None); dx may be dout."""
-    width = (n_heads + n_kv_heads) * head_dim
-    n, dev, norm = dout.shape[0], dout.device, q_norm_w is not None or k_norm_w is not None
-    gp, ldg = _rows(dout, width, dout.dtype, "dout")
-    xp, ldx = _rows(x, width, dout.dtype, "x", dev, n) if norm else (None, 0)
+    width, dtype, index = (n_heads + n_kv_heads) * head_dim, dout.dtype, _cuda_index(dout, "dout")
+    norm = q_norm_w is not None or k_norm_w is not None
+    gp, n, ldg = _rows(dout, width, dtype, "dout", index)
+    xp, _, ldx = _rows(x, width, dtype, "x", index, n) if norm else (None, n, 0)
     if dx is None:
-        dx = torch.empty(n, width, dtype=dout.dtype, device=dev)
-    dp, ldd = _rows(dx, width, dout.dtype, "dx", dev, n)
-    f32 = torch.float32
-    if q_norm_w is not None and dq_norm_w is None:
-        dq_norm_w = torch.empty(head_dim, dtype=f32, device=dev)
-    if k_norm_w is not None and dk_norm_w is None:
-        dk_norm_w = torch.empty(head_dim, dtype=f32, device=dev)
-    nbytes = lib().tpattn_qk_rope_workspace_bytes(head_dim) if norm else 0
-    if norm and workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    if norm and (workspace.device != dev or not workspace.is_contiguous()):
-        raise TPMLPError(ERR_ARG, "workspace must be contiguous on the call's device")
-    wbytes = workspace.numel() * workspace.element_size() if norm else 0
-    d = _qk_desc(dout, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
-    with torch.cuda.device(dev):
+        dx = dout.new_empty((n, width))
+    dp, _, ldd = _rows(dx, width, dtype, "dx", index, n)
+    wp, wbytes = None, 0
+    if norm:
+        # without given ones, the two gradients and the scratch come from one allocation
+        need = lib().tpattn_qk_rope_workspace_bytes(head_dim)
+        own = workspace is None or (q_norm_w is not None and dq_norm_w is None) or (
+            k_norm_w is not None and dk_norm_w is None)
+        if own:
+            buf = torch.empty(2 * head_dim + (need // 4 if workspace is None else 0), dtype=_F32T, device=dout.device)
+            if q_norm_w is not None and dq_norm_w is None:
+                dq_norm_w = buf[:head_dim]
+            if k_norm_w is not None and dk_norm_w is None:
+                dk_norm_w = buf[head_dim: 2 * head_dim]
+        if workspace is None:
+            wp, wbytes = buf.data_ptr() + 8 * head_dim, need
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            raise _bad(workspace, "workspace", f"a contiguous tensor on cuda:{index}")
+        else:
+            wp, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    d = _qk_desc(n, dtype, index, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
+    with _on(index):
         _check(lib().tpattn_qk_rope_backward(
-            ctypes.byref(d), rotary.ref if rotary is not None else None, xp, ldx, gp, ldg, dp, ldd,
-            _vec(dq_norm_w, head_dim, f32, "dq_norm_w", dev), _vec(dk_norm_w, head_dim, f32, "dk_norm_w", dev),
-            workspace.data_ptr() if norm else None, wbytes, _stream_of(dev, stream)))
+            d, rotary.spec if rotary is not None else None, xp, ldx, gp, ldg, dp, ldd,
+            _vec(dq_norm_w, head_dim, _F32T, "dq_norm_w", index), _vec(dk_norm_w, head_dim, _F32T, "dk_norm_w", index),
+            wp, wbytes, _stream_of(dout.device, index, stream)))
     return dx, dq_norm_w, dk_norm_w
 
 
@@ -758,7 +802,7 @@ class TPKV:
 
     def __init__(self, k_cache, v_cache, n_heads: int, max_batch: int = 1024, k_inv_scale=None, v_inv_scale=None,
                  stream=None):
-        if k_cache.dim() != 4 or not k_cache.is_cuda:
+        if k_cache.dim() != 4 or k_cache.get_device() < 0:
             raise TPMLPError(ERR_ARG, "k_cache must be a CUDA tensor [pages, n_kv_heads, page_size, head_dim]")
         kinds = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
         if k_cache.dtype not in kinds:
@@ -773,8 +817,9 @@ class TPKV:
         self.k_cache, self.v_cache = k_cache, v_cache
         self._scales = (k_inv_scale, v_inv_scale)
         self._norm = (None, None)
+        self.index = k_cache.get_device()
         self._fixed = stream
-        self._stream = _stream_of(dev, stream)
+        self._stream = _stream_of(dev, self.index, stream)
         ctx = ctypes.c_void_p()
         with torch.cuda.device(dev):
             self._ck(lib().tpkv_create(ctypes.byref(self.cfg), self._stream, ctypes.byref(ctx)))
@@ -784,8 +829,8 @@ class TPKV:
         self._ck(lib().tpkv_bind_workspace(ctx, self.workspace.data_ptr(), nbytes))
         f32 = torch.float32
         self._ck(lib().tpkv_bind_cache(ctx, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
-                                       _vec(k_inv_scale, nkv, f32, "k_inv_scale", dev),
-                                       _vec(v_inv_scale, nkv, f32, "v_inv_scale", dev)))
+                                       _vec(k_inv_scale, nkv, f32, "k_inv_scale", self.index),
+                                       _vec(v_inv_scale, nkv, f32, "v_inv_scale", self.index)))
 
     def _ck(self, status: int):
         if status != OK:
@@ -809,45 +854,43 @@ class TPKV:
         self._fixed = stream
 
     def _enter(self):
-        s = _stream_of(self.device, self._fixed)
+        s = _stream_of(self.device, self.index, self._fixed)
         if s != self._stream:
             self._ck(lib().tpkv_set_stream(self.ctx, s))
             self._stream = s
 
     def set_rotary(self, rotary: Rotary | None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6):
         """What append does to queries and keys: norm where a bf16 weight is given, then the rotation."""
-        b = torch.bfloat16
         self._ck(lib().tpkv_set_rotary(self.ctx, rotary.ref if rotary is not None else None,
-                                       _vec(q_norm_w, self.d, b, "q_norm_w", self.device),
-                                       _vec(k_norm_w, self.d, b, "k_norm_w", self.device), float(eps)))
+                                       _vec(q_norm_w, self.d, _BF, "q_norm_w", self.index),
+                                       _vec(k_norm_w, self.d, _BF, "k_norm_w", self.index), float(eps)))
         self._norm = (q_norm_w, k_norm_w)  # the context keeps their pointers
 
     def _table(self, t, batch: int):
-        if (t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != batch or t.device != self.device
-                or (t.shape[1] > 1 and t.stride(1) != 1)):
-            raise TPMLPError(ERR_ARG, f"block_table: need int32 [{batch}, pages] on {self.device}, got {t.dtype} "
-                                      f"{tuple(t.shape)} on {t.device}")
-        return t.data_ptr(), max(t.stride(0), t.shape[1]), t.shape[1]
+        shape = t.shape
+        if (len(shape) != 2 or t.dtype is not _I32T or shape[0] != batch or t.get_device() != self.index
+                or (shape[1] > 1 and t.stride(1) != 1)):
+            raise _bad(t, "block_table", f"int32 [{batch}, pages] on cuda:{self.index}")
+        return t.data_ptr(), max(t.stride(0), shape[1]), shape[1]
 
     def append(self, qkv, past_lens, block_table, cu_rows=None, new_lens=None, q_out=None, transform: bool = True,
                with_queries: bool = True):
         """Store the keys and values of packed rows [Q | K | V] behind each sequence's ``past_lens`` tokens and
-        return the normed and rotated queries [rows, n_heads * d] (None without ``with_queries``); see tpkv_append."""
-        dev, i32, batch = self.device, torch.int32, past_lens.shape[0]
-        n = qkv.shape[0]
-        xp, ldx = _rows(qkv, (self.nq + 2 * self.nkv) * self.d, torch.bfloat16, "qkv", dev)
-        width = self.nq * self.d
+        return the normed and rotated queries [rows, n_heads * d] (None without ``with_queries``); see tpkv_append.
+        Rows that are no sequence's leave ``q_out`` as it was (undefined where it is made here)."""
+        index, batch, width = self.index, past_lens.shape[0], self.nq * self.d
+        xp, n, ldx = _rows(qkv, width + 2 * self.nkv * self.d, _BF, "qkv", index)
         if q_out is None and with_queries:
-            # rows that are nobody's are left as they were: give them a value where there may be any
-            new = torch.empty if cu_rows is None and new_lens is None else torch.zeros
-            q_out = new(n, width, dtype=torch.bfloat16, device=dev)
-        op, ldo = _rows(q_out, width, torch.bfloat16, "q_out", dev, n) if q_out is not None else (None, 0)
+            q_out = qkv.new_empty((n, width))
+        op, _, ldo = _rows(q_out, width, _BF, "q_out", index, n) if q_out is not None else (None, n, 0)
         tp, ldt, pages = self._table(block_table, batch)
         self._enter()
-        self._ck(lib().tpkv_append(self.ctx, n, batch, xp, ldx, _vec(cu_rows, batch + 1, i32, "cu_rows", dev),
-                                   _vec(new_lens, batch, i32, "new_lens", dev),
-                                   _vec(past_lens, batch, i32, "past_lens", dev), tp, ldt, pages,
-                                   1 if transform else 0, op, ldo))
+        status = lib().tpkv_append(self.ctx, n, batch, xp, ldx, _vec(cu_rows, batch + 1, _I32T, "cu_rows", index),
+                                   _vec(new_lens, batch, _I32T, "new_lens", index),
+                                   _vec(past_lens, batch, _I32T, "past_lens", index), tp, ldt, pages,
+                                   1 if transform else 0, op, ldo)
+        if status:
+            self._ck(status)
         return q_out
 
     def decode(self, q, lens, block_table, scale: float | None = None, window: int = 0, sinks: int = 0, out=None,
@@ -855,21 +898,24 @@ class TPKV:
         """Attention of one token per sequence over its first ``lens + len_add`` cached tokens; with a window, over
         its last ``window`` tokens and first ``sinks``.  scale: 1 / sqrt(head_dim) unless given.  Returns out
         [batch, n_heads * d], with ``return_lse`` or ``lse`` (out, lse float32 [batch, n_heads]); see tpkv_decode."""
-        dev, batch, width = self.device, q.shape[0], self.nq * self.d
-        qp, ldq = _rows(q, width, torch.bfloat16, "q", dev)
+        index, width = self.index, self.nq * self.d
+        qp, batch, ldq = _rows(q, width, _BF, "q", index)
         if out is None:
-            out = torch.empty(batch, width, dtype=torch.bfloat16, device=dev)
-        op, ldo = _rows(out, width, torch.bfloat16, "out", dev, batch)
-        if lse is None and return_lse:
-            lse = torch.empty(batch, self.nq, dtype=torch.float32, device=dev)
-        if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (batch, self.nq)
-                                or lse.device != dev or not lse.is_contiguous()):
-            raise TPMLPError(ERR_ARG, f"lse: need contiguous float32 {(batch, self.nq)} on {dev}")
+            out = q.new_empty((batch, width))
+        op, _, ldo = _rows(out, width, _BF, "out", index, batch)
+        if lse is None:
+            if return_lse:
+                lse = torch.empty((batch, self.nq), dtype=_F32T, device=self.device)
+        elif (lse.dtype is not _F32T or tuple(lse.shape) != (batch, self.nq) or lse.get_device() != index
+                or not lse.is_contiguous()):
+            raise _bad(lse, "lse", f"contiguous float32 {(batch, self.nq)} on cuda:{index}")
         tp, ldt, pages = self._table(block_table, batch)
         self._enter()
-        self._ck(lib().tpkv_decode(self.ctx, batch, qp, ldq, _vec(lens, batch, torch.int32, "lens", dev), len_add, tp,
+        status = lib().tpkv_decode(self.ctx, batch, qp, ldq, _vec(lens, batch, _I32T, "lens", index), len_add, tp,
                                    ldt, pages, self.d ** -0.5 if scale is None else scale, window, sinks, op, ldo,
-                                   lse.data_ptr() if lse is not None else None))
+                                   lse.data_ptr() if lse is not None else None)
+        if status:
+            self._ck(status)
         return out if lse is None else (out, lse)
 
     def sync(self):
