@@ -276,7 +276,7 @@ tpmlp_status tpkv_create(const tpkv_config* cfg, void* stream, tpkv_ctx** out) {
   c->num_sms = sms;
   c->box_tokens = kv_decode_tile(cfg->head_dim, cfg->cache_dtype == TPKV_E4M3);
   while (cfg->page_size % c->box_tokens) c->box_tokens /= 2;  // ends at 8 at the latest
-  c->workers = kv_decode_workers(cfg->head_dim, cfg->n_heads / cfg->n_kv_heads, sms);
+  c->workers = kv_decode_workers(sms);
   if (c->workers > KV_MAX_WORKERS) c->workers = KV_MAX_WORKERS;
   *out = c;
   return TPMLP_OK;

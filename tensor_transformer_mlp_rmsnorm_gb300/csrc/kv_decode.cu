@@ -41,24 +41,38 @@
 #include "tma_maps.cuh"
 #include "f32x2.cuh"
 
+#ifndef P_T
+#define P_T 128
+#endif
 namespace tpmlp {
 namespace {
 
-constexpr int NCW = 4;          // computing warps
-constexpr int NTHR = 32 * (NCW + 1);
-constexpr int RING_BYTES = 96 * 1024;
-constexpr int JOIN_GROUP = 16;  // partials one CTA joins at a time
+constexpr int NCW = 4;           // computing warps
+constexpr int NTHR = 256;        // a warpgroup that computes and one whose first warp fetches
+// Registers a thread: 128 at launch (two CTAs an SM); the computing warpgroup
+// takes what the other gives up, 200 + 56 = 2 x 128.
+constexpr int COMPUTE_REGS = 200, FETCH_REGS = 56;
+constexpr int JOIN_MAX = 24;     // partials one CTA joins at a time: the square root of the most CTAs
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 100000000ull;
 
-// Every computing warp works on every tile, so each waits for every use of a
-// slot: a barrier's one-bit phase is never asked about two rounds ahead.
-template <int D, bool F8>
-struct Ring {
-  static constexpr int ROW = D * (F8 ? 1 : 2);
+// Shape of the kernel for heads of D values, F8: E4M3 cache, HG: groups of 8
+// query heads.  A warp works on one head group and its share of a tile's
+// tokens, so its registers do not grow with the heads; NCW / HG warps share a
+// head group's tokens.
+template <int D, bool F8, int HG>
+struct Cfg {
+  static constexpr int HT = 8 * HG;                        // query heads of a CTA
+  static constexpr int RING_BYTES = 96 * 1024;             // two CTAs an SM
+  static constexpr int ROW = D * (F8 ? 1 : 2);             // bytes of a token's key or value
   static constexpr int BLOCK = ROW % 128 == 0 ? 128 : 64;  // bytes of a row that lie together (the swizzle's width)
-  static constexpr int TK = ROW <= 128 ? 128 : 64;  // tokens of a tile
-  static constexpr int SLOT = TK * ROW;             // one operand of a tile
+  static constexpr int TK = ROW <= P_T ? 128 : 64;         // tokens of a tile
+  static constexpr int SLOT = TK * ROW;                    // one operand of a tile
+  // Every computing warp works on every tile, so each waits for every use of a
+  // slot: a barrier's one-bit phase is never asked about two rounds ahead.
   static constexpr int N = RING_BYTES / SLOT;
+  static constexpr int KG = NCW / HG;                      // warps that share a tile's tokens
+  static constexpr int KW = TK / KG;                       // tokens of a tile that a warp works on
+  static constexpr int OD = 64;                            // columns of O joined at a time
 };
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c1, int c3,
@@ -84,18 +98,18 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
 template <bool F16>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Transpose of an 8x8 tile of 16-bit values spread over the warp.
 __device__ __forceinline__ uint32_t movm(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t lo16) {
@@ -168,31 +182,181 @@ struct Cursor {
   Seq<TK> s;
 };
 
-template <int D, bool F8, int HT>
-__global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16)) ? 1 : 2)
+// Joins the partial results of one (sequence, key head chunk) whose tiles
+// several CTAs had; called by the computing warps of each of them with their
+// partial written.
+struct JoinArgs {
+  float* part;
+  uint32_t *ctr_first, *ctr_last;  // arrival counts of the groups and of their leaders
+  __nv_bfloat16* out;
+  float* lse;
+  int w_first, nparts, p_me, heads;
+  float vscale;
+};
+template <int D, int HT>
+__device__ __forceinline__ void join_parts(const JoinArgs a, float* s_o, float* s_mx, float* s_inv, volatile int* s_last) {
+  const int tid = threadIdx.x;
+  const size_t part_sz = (size_t)HT * (D + 2);
+  // ---- the last CTA to arrive joins: groups of about sqrt(parts), then the groups' leaders
+  int group = a.nparts;
+  if (a.nparts > 8)
+    for (group = 3; group * group < a.nparts;) ++group;
+  const int ngroups = (a.nparts + group - 1) / group;
+  float* s_w = s_o;                  // [JOIN_MAX][HT] maxima, then weights
+  float* s_s = s_o + JOIN_MAX * HT;  // sums
+  for (int level = 0; level < 2; ++level) {
+    const int p0 = level == 0 ? a.p_me / group * group : 0;
+    const int pstep = level == 0 ? 1 : group;
+    const int cnt = level == 0 ? min(group, a.nparts - p0) : ngroups;
+    uint32_t* ctr = level == 0 ? a.ctr_first + 2 * (a.w_first + p0) + (p0 == 0) : a.ctr_last + a.w_first;
+    if (cnt > 1) {
+      bar_compute();
+      if (tid == 0) {
+        // the fences order the whole CTA's partial before the count and
+        // the others' partials behind it (the barriers carry them)
+        __threadfence();
+        const uint32_t old = atomicAdd(ctr, 1u);
+        __threadfence();
+        *s_last = old == (uint32_t)cnt - 1;
+        if (old == (uint32_t)cnt - 1) *ctr = 0;  // ready for the next launch
+      }
+      bar_compute();
+      if (!*s_last) break;
+    }
+    auto part_of = [&](int i) -> float* {
+      const int p = p0 + i * pstep;
+      return a.part + (size_t)(2 * (a.w_first + p) + (p == 0)) * part_sz;
+    };
+    const bool final_level = ngroups == 1 || level == 1;
+    if (!final_level && cnt == 1) continue;  // a group of one stands for itself
+    for (int x = tid; x < cnt * HT; x += NCW * 32) {
+      const float* pp = part_of(x / HT) + (size_t)HT * D + x % HT;
+      s_w[x] = __ldcg(pp);
+      s_s[x] = __ldcg(pp + HT);
+    }
+    bar_compute();
+    if (tid < HT) {
+      float mx = -INFINITY;
+      for (int i = 0; i < cnt; ++i) mx = fmaxf(mx, s_w[i * HT + tid]);
+      float s = 0.0f;
+      for (int i = 0; i < cnt; ++i) {
+        const float w = mx == -INFINITY ? 0.0f : ex2_fast(s_w[i * HT + tid] - mx);
+        s_w[i * HT + tid] = w;
+        s += w * s_s[i * HT + tid];
+      }
+      s_mx[tid] = mx;
+      s_inv[tid] = final_level ? (s > 0.0f ? a.vscale / s : (s == s ? 0.0f : s)) : s;
+      if (final_level && a.lse && tid < a.heads) a.lse[tid] = s == 0.0f ? -INFINITY : (mx + log2f(s)) * 0.69314718055994531f;
+    }
+    bar_compute();
+    float* lead = part_of(0);
+    // all of a thread's loads of eight parts in flight at once
+    constexpr int V = HT * D / 4 / (NCW * 32) >= 2 ? 2 : 1;  // float4 of a part that a thread adds up at a time
+    for (int x0 = tid; x0 < HT * D / 4; x0 += V * NCW * 32) {
+      float4 v[V];
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i0 = 0; i0 < cnt; i0 += 8) {
+        float4 y[8][V];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < cnt) {
+            const float4* pp = reinterpret_cast<const float4*>(part_of(i0 + i)) + x0;
+#pragma unroll
+            for (int q = 0; q < V; ++q) y[i][q] = __ldcg(pp + q * NCW * 32);
+          }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < cnt) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+              const float w = s_w[(i0 + i) * HT + 4 * (x0 + q * NCW * 32) / D];
+              v[q].x = fmaf(w, y[i][q].x, v[q].x);
+              v[q].y = fmaf(w, y[i][q].y, v[q].y);
+              v[q].z = fmaf(w, y[i][q].z, v[q].z);
+              v[q].w = fmaf(w, y[i][q].w, v[q].w);
+            }
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const int x = x0 + q * NCW * 32, h = 4 * x / D, col = 4 * x % D;
+        if (final_level) {
+          const float r = s_inv[h];
+          if (h < a.heads)
+            *reinterpret_cast<uint2*>(a.out + (int64_t)h * D + col) =
+                make_uint2(pack_bf16(v[q].x * r, v[q].y * r), pack_bf16(v[q].z * r, v[q].w * r));
+        } else {
+          __stcg(reinterpret_cast<float4*>(lead) + x, v[q]);
+        }
+      }
+    }
+    if (!final_level && tid < HT) {
+      __stcg(lead + (size_t)HT * D + tid, s_mx[tid]);
+      __stcg(lead + (size_t)HT * D + HT + tid, s_inv[tid]);
+    }
+    bar_compute();
+    if (final_level) break;
+  }
+}
+
+// The segment the computing warps are at, kept in shared memory by one of
+// their threads so that it costs the main loop no registers.
+template <int TK>
+struct Walk {
+  Cursor<TK> c;
+  int64_t T, G;
+  int hc, j;   // key head chunk; first tile in the sequence's list
+  int ntiles;  // tiles of the segment, 0 behind the last one
+  int direct;  // the segment is the whole (sequence, key head chunk)
+  int64_t item0, item1;
+  __device__ __forceinline__ void set() {
+    if (c.pos >= c.end) {
+      ntiles = 0;
+      return;
+    }
+    item0 = c.base + (int64_t)hc * c.s.tiles;
+    item1 = item0 + c.s.tiles;
+    const int64_t seg_end = item1 < c.end ? item1 : c.end;
+    ntiles = (int)(seg_end - c.pos);
+    direct = c.pos == item0 && seg_end == item1;
+  }
+  __device__ __forceinline__ void next(const DecodeArgs& a, int nhc) {
+    j += ntiles;
+    c.pos += ntiles;
+    if (c.pos < c.end && j == c.s.tiles) {
+      j = 0;
+      if (++hc == nhc) {
+        hc = 0;
+        c.base += (int64_t)c.s.tiles * nhc;
+        c.s = make_seq<TK>(a, ++c.b, false);
+      }
+    }
+    set();
+  }
+};
+
+template <int D, bool F8, int HG>
+__global__ void __launch_bounds__(NTHR, 2)
     kv_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
-  using R = Ring<D, F8>;
-  constexpr int TK = R::TK;
-  constexpr int KW = TK / NCW;      // tokens of a tile that a warp works on
-  constexpr int KT = KW / 16;       // as m-tiles
-  constexpr int NT = HT / 8;        // n-tiles of 8 heads
-  constexpr int KS = D / 16;        // k-steps of Q K^T
-  constexpr int MT = D / 16;        // m-tiles of V^T P^T
-  constexpr int ROWB = R::BLOCK;        // bytes of a block's row
-  constexpr int NBLK = R::ROW / ROWB;   // blocks of a row in shared memory
+  using R = Cfg<D, F8, HG>;
+  constexpr int TK = R::TK, KW = R::KW, KG = R::KG, HT = R::HT, OD = R::OD;
+  constexpr int KT = KW / 16;          // a warp's tokens of a tile as m-tiles
+  constexpr int KS = D / 16;           // k-steps of Q K^T
+  constexpr int MT = D / 16;           // m-tiles of V^T P^T
+  constexpr int ROWB = R::BLOCK;       // bytes of a block's row
+  constexpr int NBLK = R::ROW / ROWB;  // blocks of a row in shared memory
   extern __shared__ __align__(1024) uint8_t ring_raw[];
   __shared__ __align__(8) uint64_t full[R::N], empty[R::N];
-  __shared__ int s_abort;
-  __shared__ int64_t s_scan[NTHR / 32 + 1];
-  __shared__ int64_t s_base;
-  __shared__ int s_b;
-  __shared__ int s_last;
-  __shared__ float s_m[NCW][HT], s_l[NCW][HT];
+  __shared__ int s_abort, s_b, s_last;
+  __shared__ Walk<TK> s_walk;
+  __shared__ int64_t s_scan[NTHR / 32], s_base;
+  __shared__ float s_m[KG][HT], s_l[KG][HT];
   __shared__ float s_mx[HT], s_inv[HT];
-  __shared__ float s_w[32][HT], s_s[32][HT];
-  constexpr int OD = 512 / HT;  // columns of O joined at a time: 8 KB, so that two CTAs fit an SM
-  __shared__ __align__(16) float s_o[NCW][HT * (OD + 4)];
+  // the warps' outputs of OD columns, [KG][HT][OD + 4]; the join's weights [JOIN_MAX][HT] and sums behind them
+  constexpr int S_O = KG * HT * (OD + 4), S_W = 2 * JOIN_MAX * HT;
+  __shared__ __align__(16) float s_o[S_O > S_W ? S_O : S_W];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
@@ -254,8 +418,23 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
   c.base = s_base;
   c.s = make_seq<TK>(a, c.b, false);
 
-  if (warp == NCW) {
+  if (tid == 0) {
+    const int64_t rel = c.pos - c.base;
+    Walk<TK> w;
+    w.c = c;
+    w.T = T;
+    w.G = G;
+    w.hc = (int)(rel / c.s.tiles);
+    w.j = (int)(rel - (int64_t)w.hc * c.s.tiles);
+    w.set();
+    s_walk = w;
+  }
+  __syncthreads();
+
+  if (warp >= NCW) {
     // ------------------------------------------------------------ producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FETCH_REGS));
+    if (warp > NCW) return;
     // A batch is up to 32 boxes of consecutive tiles of one (sequence, key
     // head), a lane each: the next batch's table entries are read while this
     // one's are fetched, so no tile waits for its page's number.
@@ -327,59 +506,56 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
   }
 
   // -------------------------------------------------------------- computing warps
-  const int g8 = lane >> 2, c4 = lane & 3;  // row group and column pair of the mma fragments
-  // shared-memory address parts of the lane's ldmatrix rows: token 16 y + key of the warp's
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(COMPUTE_REGS));
+  const int hgrp = warp % HG, kgrp = warp / HG;  // the warp's head group and token share
+  const int g8 = lane >> 2, c4 = lane & 3;       // row group and column pair of the mma fragments
+  // Shared-memory offsets of the lane's ldmatrix rows (token 16 y + key of the
+  // warp's share) with the swizzled chunk of the first pair; chunk pair p of a
+  // block is that offset xor 32 p, as rows and blocks are multiples of 64 bytes
+  // and chunk numbers differ in their upper bits only.
   const int bt = a.box_tokens;
   const uint32_t blk = (uint32_t)bt * ROWB;  // bytes from one block to the next
-  auto row_base = [&](int key) -> uint32_t { return (uint32_t)(key / bt) * (blk * NBLK) + (key % bt) * ROWB; };
+  const int bt_log2 = __ffs(bt) - 1;
+  auto row_base = [&](int key) -> uint32_t {
+    return (uint32_t)(key >> bt_log2) * (blk * NBLK) + (key & (bt - 1)) * ROWB;
+  };
   const int k_key = lane & 15;  // K: matrices (keys 0-7, 8-15) x 2 chunks
   // V: the same with E4M3; bf16 (2 chunks) x (keys 0-7, 8-15)
   const int v_key = F8 ? k_key : (lane & 7) + ((lane >> 4) << 3);
-  uint32_t k_row[KT], v_row[KT];
+  const uint32_t k_ch = (lane >> 4) ^ (ROWB == 64 ? (k_key >> 1) & 3 : k_key & 7);
+  const uint32_t v_ch = (F8 ? lane >> 4 : (lane >> 3) & 1) ^ (ROWB == 64 ? (v_key >> 1) & 3 : v_key & 7);
+  uint32_t k_off[KT], v_off[KT];
 #pragma unroll
   for (int y = 0; y < KT; ++y) {
-    k_row[y] = row_base(warp * KW + 16 * y + k_key);
-    v_row[y] = row_base(warp * KW + 16 * y + v_key);
+    k_off[y] = row_base(kgrp * KW + 16 * y + k_key) + (k_ch << 4);
+    v_off[y] = row_base(kgrp * KW + 16 * y + v_key) + (v_ch << 4);
   }
-  const uint32_t k_sw = ROWB == 64 ? (k_key >> 1) & 3 : k_key & 7, v_sw = ROWB == 64 ? (v_key >> 1) & 3 : v_key & 7;
-  const uint32_t k_half = lane >> 4;  // chunk of the pair
-  const uint32_t v_half = F8 ? lane >> 4 : (lane >> 3) & 1;
-  constexpr int CPB = ROWB / 16;  // 16-byte chunks of a block's row
-  // offset of 16-byte chunk 2 pair + half within a token's row
-  auto chunk_off = [&](int pair, uint32_t half, uint32_t sw) -> uint32_t {
-    return (uint32_t)(2 * pair / CPB) * blk + ((((uint32_t)(2 * pair % CPB) + half) ^ sw) << 4);
-  };
+  constexpr int PPB = ROWB / 32;  // chunk pairs of a block's row
 
-  uint32_t qf[NT][KS][2];
-  float qs[NT][2];  // log2-domain scale of this lane's two score columns
-  float o[MT][NT][4];
-  float m[NT][2], l[NT][2];
-
-  uint32_t n = 0;  // ring uses so far
+  uint32_t nu = 0;  // ring uses so far
   bool ok = true;
-  int64_t rel = c.pos - c.base;
-  int hc = (int)(rel / c.s.tiles), j = (int)(rel - (int64_t)hc * c.s.tiles);
 
-  while (ok && c.pos < c.end) {
+  for (;;) {
     // ---- one segment: the worker's tiles of (sequence b, key head g, chunk)
-    const int g = hc / a.chunks, h0 = (hc - g * a.chunks) * HT;
-    const int heads = min(HT, a.hpg - h0);
-    const int64_t item0 = c.base + (int64_t)hc * c.s.tiles, item1 = item0 + c.s.tiles;
-    const int64_t seg_end = item1 < c.end ? item1 : c.end;
-    const int64_t seg_begin = c.pos;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)c.b * a.ld_q + (int64_t)(g * a.hpg + h0) * D;
-    const float kscale = a.scale_log2 * (F8 && a.k_inv_scale ? a.k_inv_scale[g] : 1.0f);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int h = t * 8 + g8;
+    const int ntiles = s_walk.ntiles, j = s_walk.j;
+    if (ntiles == 0) break;
+    const Seq<TK> seq = s_walk.c.s;
+    uint32_t qf[KS][2];
+    float qs[2];  // log2-domain scale of this lane's two score columns
+    {
+      const int hc = s_walk.hc, g = hc / a.chunks, h0 = (hc - g * a.chunks) * HT, heads = min(HT, a.hpg - h0);
+      const float kscale = a.scale_log2 * (F8 && a.k_inv_scale ? a.k_inv_scale[g] : 1.0f);
+      const int h = hgrp * 8 + g8;
+      const __nv_bfloat16* q =
+          static_cast<const __nv_bfloat16*>(a.q) + (int64_t)s_walk.c.b * a.ld_q + (int64_t)(g * a.hpg + h0 + h) * D;
       if (F8) {
         float mx = 0.0f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint2 v = make_uint2(0, 0);
-          if (h < heads) v = *reinterpret_cast<const uint2*>(q + (int64_t)h * D + 16 * k + 4 * c4);
-          qf[t][k][0] = v.x;
-          qf[t][k][1] = v.y;
+          if (h < heads) v = *reinterpret_cast<const uint2*>(q + 16 * k + 4 * c4);
+          qf[k][0] = v.x;
+          qf[k][1] = v.y;
           mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf_lo(v.x)), fabsf(bf_hi(v.x))), fmaxf(fabsf(bf_lo(v.y)), fabsf(bf_hi(v.y)))));
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -392,149 +568,150 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) qf[t][k][i] = pack_f16(bf_lo(qf[t][k][i]) * inv, bf_hi(qf[t][k][i]) * inv);
-        qs[t][0] = kscale * __shfl_sync(0xffffffffu, mul, 8 * c4);
-        qs[t][1] = kscale * __shfl_sync(0xffffffffu, mul, 8 * c4 + 4);
+          for (int i = 0; i < 2; ++i) qf[k][i] = pack_f16(bf_lo(qf[k][i]) * inv, bf_hi(qf[k][i]) * inv);
+        qs[0] = kscale * __shfl_sync(0xffffffffu, mul, 8 * c4);
+        qs[1] = kscale * __shfl_sync(0xffffffffu, mul, 8 * c4 + 4);
       } else {
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            qf[t][k][i] = 0;
-            if (h < heads) qf[t][k][i] = *reinterpret_cast<const uint32_t*>(q + (int64_t)h * D + 16 * k + 8 * i + 2 * c4);
+            qf[k][i] = 0;
+            if (h < heads) qf[k][i] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * c4);
           }
-        qs[t][0] = qs[t][1] = kscale;
+        qs[0] = qs[1] = kscale;
       }
-      m[t][0] = m[t][1] = -INFINITY;
-      l[t][0] = l[t][1] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][t][e] = 0.0f;
     }
+    float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
 
-    for (; ok && c.pos < seg_end; ++c.pos, ++j) {
-      const int tile0 = c.s.tile(j) * TK, t0 = tile0 + warp * KW;
-      const bool whole = c.s.whole(tile0);
+    for (int it = 0; it < ntiles; ++it) {
+      const int tile0 = seq.tile(j + it) * TK, t0 = tile0 + kgrp * KW;
+      const bool whole = seq.whole(tile0);
       // ---- S^T = K Q^T
-      uint32_t sl = n % R::N;
-      ok = mbar_wait(&full[sl], (n / R::N) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
+      uint32_t sl = nu % R::N;
+      ok = mbar_wait(&full[sl], (nu / R::N) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      float sc[KT][NT][4];
+      float sc[KT][4];
 #pragma unroll
-      for (int y = 0; y < KT; ++y)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) sc[y][t][0] = sc[y][t][1] = sc[y][t][2] = sc[y][t][3] = 0.0f;
+      for (int y = 0; y < KT; ++y) sc[y][0] = sc[y][1] = sc[y][2] = sc[y][3] = 0.0f;
       const uint32_t kb = ring_s + sl * R::SLOT;
 #pragma unroll
       for (int k = 0; k < (F8 ? KS / 2 : KS); ++k) {
-        const uint32_t off = kb + chunk_off(k, k_half, k_sw);
 #pragma unroll
         for (int y = 0; y < KT; ++y) {
           uint32_t r[4];
-          ldsm4(off + k_row[y], r);
+          ldsm4(kb + (k / PPB) * blk + (k_off[y] ^ (32 * (k % PPB))), r);
           if (F8) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {  // chunk 2k + x
               const uint32_t af[4] = {f16x2_of_e4m3x2(r[2 * x]), f16x2_of_e4m3x2(r[2 * x + 1]),
                                       f16x2_of_e4m3x2(r[2 * x] >> 16), f16x2_of_e4m3x2(r[2 * x + 1] >> 16)};
-#pragma unroll
-              for (int t = 0; t < NT; ++t) mma16816<true>(sc[y][t], af, qf[t][(2 * k + x) % KS][0], qf[t][(2 * k + x) % KS][1]);
+              mma16816<true>(sc[y], af, qf[(2 * k + x) % KS][0], qf[(2 * k + x) % KS][1]);
             }
           } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<false>(sc[y][t], r, qf[t][k][0], qf[t][k][1]);
+            mma16816<false>(sc[y], r, qf[k][0], qf[k][1]);
           }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[sl]);
+      ++nu;
       // ---- softmax
 #pragma unroll
       for (int y = 0; y < KT; ++y)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[y][t][e] *= qs[t][e & 1];
+        for (int e = 0; e < 4; ++e) sc[y][e] *= qs[e & 1];
       if (!whole) {
 #pragma unroll
         for (int y = 0; y < KT; ++y)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (!c.s.sees(t0 + 16 * y + 8 * x + g8)) {
-#pragma unroll
-              for (int t = 0; t < NT; ++t) sc[y][t][2 * x] = sc[y][t][2 * x + 1] = -INFINITY;
-            }
+            if (!seq.sees(t0 + 16 * y + 8 * x + g8)) sc[y][2 * x] = sc[y][2 * x + 1] = -INFINITY;
       }
-      uint32_t pf[KT][NT][2], pl[KT][NT][2];
+      float mx[2] = {-INFINITY, -INFINITY}, alpha[2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float alpha[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < KT; ++y) mx = fmax3(mx, sc[y][t][e], sc[y][t][2 + e]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m[t][e], mx);
-          const float mu = mn == -INFINITY ? 0.0f : mn;  // nothing visible yet
-          alpha[e] = ex2_fast(m[t][e] - mu);             // m = -inf: 0
-          m[t][e] = mn;
-          float sum = 0.0f;
-#pragma unroll
-          for (int y = 0; y < KT; ++y) {
-            sc[y][t][e] = ex2_fast(sc[y][t][e] - mu);
-            sc[y][t][2 + e] = ex2_fast(sc[y][t][2 + e] - mu);
-            sum += sc[y][t][e] + sc[y][t][2 + e];
-          }
-          l[t][e] = fmaf(l[t][e], alpha[e], sum);
-        }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[i][t][0] *= alpha[0];
-            o[i][t][1] *= alpha[1];
-            o[i][t][2] *= alpha[0];
-            o[i][t][3] *= alpha[1];
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < KT; ++y)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float p0 = sc[y][t][2 * x], p1 = sc[y][t][2 * x + 1];
-            if (F8) {
-              pf[y][t][x] = movm(pack_f16(p0, p1));
-            } else {
-              const uint32_t hi = pack_bf16(p0, p1);
-              pf[y][t][x] = movm(hi);
-              pl[y][t][x] = movm(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi)));
-            }
-          }
+      for (int y = 0; y < KT; ++y) {
+        mx[0] = fmax3(mx[0], sc[y][0], sc[y][2]);
+        mx[1] = fmax3(mx[1], sc[y][1], sc[y][3]);
       }
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], x));
+        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], x));
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(m[e], mx[e]);
+        const float mu = mn == -INFINITY ? 0.0f : mn;  // nothing visible yet
+        alpha[e] = ex2_fast(m[e] - mu);                // m = -inf: 0
+        m[e] = mn;
+        float add = 0.0f;
+#pragma unroll
+        for (int y = 0; y < KT; ++y) {
+          sc[y][e] = ex2_fast(sc[y][e] - mu);
+          sc[y][2 + e] = ex2_fast(sc[y][2 + e] - mu);
+          add += sc[y][e] + sc[y][2 + e];
+        }
+        l[e] = fmaf(l[e], alpha[e], add);
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[1];
+          o[i][2] *= alpha[0];
+          o[i][3] *= alpha[1];
+        }
+      }
+      uint32_t pf[KT][2], pl[KT][2];
+#pragma unroll
+      for (int y = 0; y < KT; ++y)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float p0 = sc[y][2 * x], p1 = sc[y][2 * x + 1];
+          if (F8) {
+            pf[y][x] = movm(pack_f16(p0, p1));
+          } else {
+            const uint32_t hi = pack_bf16(p0, p1);
+            pf[y][x] = movm(hi);
+            pl[y][x] = movm(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi)));
+          }
+        }
       // ---- O^T += V^T P^T
-      ++n;
-      sl = n % R::N;
-      ok = mbar_wait(&full[sl], (n / R::N) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
+      sl = nu % R::N;
+      ok = mbar_wait(&full[sl], (nu / R::N) & 1, abort_flag, a.status, STATUS_TIMEOUT, WAIT_NS);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t vb = ring_s + sl * R::SLOT;
+      if (!whole) {
+        // Values of hidden tokens, NaN maybe, are made 0 where they lie (0 x NaN
+        // would reach the sum): each warp clears those of its own tokens.
+        constexpr int CH = R::ROW / 16;  // 16-byte chunks of a token
+        for (int t = lane; t < KW; t += 32) {
+          if (seq.sees(t0 + t)) continue;
+          const uint32_t row = vb + row_base(kgrp * KW + t);
+          for (int x = 0; x < CH; ++x) {
+            const int ch = (x + lane) % CH;  // lanes start at different banks
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + (ch / (ROWB / 16)) * blk +
+                                                                         (ch % (ROWB / 16)) * 16),
+                         "r"(0)
+                         : "memory");
+          }
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int y = 0; y < KT; ++y) {
-        uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;  // values of unseen tokens, NaN maybe, become 0
-        if (!whole) {
-          const int t = t0 + 16 * y + 2 * c4;
-          mk0 = (c.s.sees(t) ? 0xffffu : 0u) | (c.s.sees(t + 1) ? 0xffff0000u : 0u);
-          mk1 = (c.s.sees(t + 8) ? 0xffffu : 0u) | (c.s.sees(t + 9) ? 0xffff0000u : 0u);
-        }
 #pragma unroll
         for (int i = 0; i < (F8 ? MT / 2 : MT); ++i) {
           uint32_t r[4];
-          ldsm4t(vb + v_row[y] + chunk_off(i, v_half, v_sw), r);
+          ldsm4t(vb + (i / PPB) * blk + (v_off[y] ^ (32 * (i % PPB))), r);
           if (F8) {  // 32 columns: matrices (keys 0-7, 8-15) x chunks (2i, 2i + 1)
             uint32_t ev[4], od[4];
 #pragma unroll
@@ -542,81 +719,59 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
               const uint32_t s = __byte_perm(r[x], 0, 0x3120);
               ev[x] = f16x2_of_e4m3x2(s);
               od[x] = f16x2_of_e4m3x2(s >> 16);
-              if (!whole) {
-                ev[x] &= x & 1 ? mk1 : mk0;
-                od[x] &= x & 1 ? mk1 : mk0;
-              }
             }
             const uint32_t ea[4] = {ev[0], ev[2], ev[1], ev[3]}, oa[4] = {od[0], od[2], od[1], od[3]};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma16816<true>(o[(2 * i) % MT][t], ea, pf[y][t][0], pf[y][t][1]);
-              mma16816<true>(o[(2 * i + 1) % MT][t], oa, pf[y][t][0], pf[y][t][1]);
-            }
+            mma16816<true>(o[(2 * i) % MT], ea, pf[y][0], pf[y][1]);
+            mma16816<true>(o[(2 * i + 1) % MT], oa, pf[y][0], pf[y][1]);
           } else {  // 16 columns: matrices (chunks 2i, 2i + 1) x (keys 0-7, 8-15)
-            if (!whole) {
-              r[0] &= mk0;
-              r[1] &= mk0;
-              r[2] &= mk1;
-              r[3] &= mk1;
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma16816<false>(o[i][t], r, pf[y][t][0], pf[y][t][1]);
-              mma16816<false>(o[i][t], r, pl[y][t][0], pl[y][t][1]);
-            }
+            mma16816<false>(o[i], r, pf[y][0], pf[y][1]);
+            mma16816<false>(o[i], r, pl[y][0], pl[y][1]);
           }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[sl]);
-      ++n;
+      ++nu;
     }
 
-    // ---- join the four warps: common maximum, then the sums in warp order
+    // ---- join the warps that share a head group: common maximum, then the sums in warp order
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = l[t][e];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (g8 == 0) {
-          s_m[warp][t * 8 + 2 * c4 + e] = m[t][e];
-          s_l[warp][t * 8 + 2 * c4 + e] = v;
-        }
+    for (int e = 0; e < 2; ++e) {
+      float v = l[e];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      if (g8 == 0) {
+        s_m[kgrp][hgrp * 8 + 2 * c4 + e] = m[e];
+        s_l[kgrp][hgrp * 8 + 2 * c4 + e] = v;
       }
+    }
     if (bar_compute_any(!ok)) return;  // a wait gave up: all four warps leave together
-    const bool direct = seg_begin == item0 && seg_end == item1;
-    const int64_t w_first = direct ? blockIdx.x : ((item0 + 1) * G + T - 1) / T - 1;
-    const int64_t w_last = direct ? blockIdx.x : (item1 * G + T - 1) / T - 1;
-    const int nparts = (int)(w_last - w_first + 1);
-    const int p_me = (int)(blockIdx.x - w_first);
     const size_t part_sz = (size_t)HT * (D + 2);
-    float* my_part = a.part + (size_t)(2 * blockIdx.x + (p_me == 0)) * part_sz;
+    const bool direct = s_walk.direct;
+    const int hc = s_walk.hc, g = hc / a.chunks, h0 = (hc - g * a.chunks) * HT, heads = min(HT, a.hpg - h0), b = s_walk.c.b;
+    const int64_t w_first = direct ? blockIdx.x : ((s_walk.item0 + 1) * s_walk.G + s_walk.T - 1) / s_walk.T - 1;
+    float* my_part = a.part + (size_t)(2 * blockIdx.x + (blockIdx.x == w_first)) * part_sz;
     const float vscale = F8 && a.v_inv_scale ? a.v_inv_scale[g] : 1.0f;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (int64_t)c.b * a.ld_out + (int64_t)(g * a.hpg + h0) * D;
-    float* lse = a.lse ? a.lse + (int64_t)c.b * a.nq + g * a.hpg + h0 : nullptr;
-    float al[NT][2];
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (int64_t)b * a.ld_out + (int64_t)(g * a.hpg + h0) * D;
+    float* lse = a.lse ? a.lse + (int64_t)b * a.nq + g * a.hpg + h0 : nullptr;
+    float al[2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int e = 0; e < 2; ++e) {
+      const int h = hgrp * 8 + 2 * c4 + e;
+      float mx = s_m[0][h];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = t * 8 + 2 * c4 + e;
-        float mx = s_m[0][h];
-#pragma unroll
-        for (int w = 1; w < NCW; ++w) mx = fmaxf(mx, s_m[w][h]);
-        al[t][e] = mx == -INFINITY ? 0.0f : ex2_fast(m[t][e] - mx);
-      }
+      for (int w = 1; w < KG; ++w) mx = fmaxf(mx, s_m[w][h]);
+      al[e] = mx == -INFINITY ? 0.0f : ex2_fast(m[e] - mx);
+    }
     if (tid < HT) {
       float mx = s_m[0][tid];
 #pragma unroll
-      for (int w = 1; w < NCW; ++w) mx = fmaxf(mx, s_m[w][tid]);
+      for (int w = 1; w < KG; ++w) mx = fmaxf(mx, s_m[w][tid]);
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) s += mx == -INFINITY ? 0.0f : s_l[w][tid] * ex2_fast(s_m[w][tid] - mx);
+      for (int w = 0; w < KG; ++w) s += mx == -INFINITY ? 0.0f : s_l[w][tid] * ex2_fast(s_m[w][tid] - mx);
       if (direct) {
         s_inv[tid] = s > 0.0f ? vscale / s : (s == s ? 0.0f : s);
         if (lse && tid < heads) lse[tid] = s == 0.0f ? -INFINITY : (mx + log2f(s)) * 0.69314718055994531f;
@@ -630,156 +785,86 @@ __global__ void __launch_bounds__(NTHR, (D * HT >= 4096 || (D == 192 && HT == 16
     for (int ps = 0; ps < D / OD; ++ps) {
 #pragma unroll
       for (int ii = 0; ii < IP; ++ii) {
-        const int i = ps * IP + ii;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = g8 + (e >> 1) * 8, h = t * 8 + 2 * c4 + (e & 1);
-            // column of the m-tile's row, within the columns joined now
-            const int col = F8 ? 32 * (ii / 2) + 16 * (e >> 1) + 2 * g8 + (ii & 1) : 16 * ii + row;
-            s_o[warp][h * (OD + 4) + col] = o[i][t][e] * al[t][e & 1];
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int h = hgrp * 8 + 2 * c4 + (e & 1);
+          // column of the m-tile's row, within the columns joined now
+          const int col = F8 ? 32 * (ii / 2) + 16 * (e >> 1) + 2 * g8 + (ii & 1) : 16 * ii + g8 + 8 * (e >> 1);
+          s_o[(kgrp * HT + h) * (OD + 4) + col] = o[ps * IP + ii][e] * al[e & 1];
+        }
       }
       bar_compute();
-      for (int x = tid; x < HT * OD / 2; x += NCW * 32) {
-        const int h = x / (OD / 2), col = 2 * (x % (OD / 2));
-        float2 v = *reinterpret_cast<const float2*>(&s_o[0][h * (OD + 4) + col]);
+      for (int x = tid; x < HT * OD / 4; x += NCW * 32) {
+        const int h = x / (OD / 4), col = 4 * (x % (OD / 4));
+        float4 v = *reinterpret_cast<const float4*>(&s_o[h * (OD + 4) + col]);
 #pragma unroll
-        for (int w = 1; w < NCW; ++w) {
-          const float2 y = *reinterpret_cast<const float2*>(&s_o[w][h * (OD + 4) + col]);
+        for (int w = 1; w < KG; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(&s_o[(w * HT + h) * (OD + 4) + col]);
           v.x += y.x;
           v.y += y.y;
+          v.z += y.z;
+          v.w += y.w;
         }
         if (direct) {
+          const float r = s_inv[h];
           if (h < heads)
-            *reinterpret_cast<uint32_t*>(out + (int64_t)h * D + ps * OD + col) = pack_bf16(v.x * s_inv[h], v.y * s_inv[h]);
+            *reinterpret_cast<uint2*>(out + (int64_t)h * D + ps * OD + col) =
+                make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
         } else {
-          __stcg(reinterpret_cast<float2*>(my_part + (size_t)h * D + ps * OD + col), v);
+          __stcg(reinterpret_cast<float4*>(my_part + (size_t)h * D + ps * OD + col), v);
         }
       }
       bar_compute();
     }
 
     if (!direct) {
-      // ---- the last CTA to arrive joins: groups of JOIN_GROUP, then the groups' leaders
-      for (int level = 0; level < 2; ++level) {
-        const int ngroups = (nparts + JOIN_GROUP - 1) / JOIN_GROUP;
-        const int p0 = level == 0 ? p_me / JOIN_GROUP * JOIN_GROUP : 0;
-        const int pstep = level == 0 ? 1 : JOIN_GROUP;
-        const int cnt = level == 0 ? min(JOIN_GROUP, nparts - p0) : ngroups;
-        const int64_t w_lead = w_first + p0;
-        uint32_t* ctr = a.counters + (level == 0 ? 2 * w_lead + (p0 == 0) : 2 * (int64_t)a.workers + w_first);
-        if (cnt > 1) {
-          __threadfence();
-          bar_compute();
-          if (tid == 0) {
-            const uint32_t old = atomicAdd(ctr, 1u);
-            s_last = old == (uint32_t)cnt - 1;
-            if (old == (uint32_t)cnt - 1) *ctr = 0;  // ready for the next launch
-          }
-          bar_compute();
-          if (!s_last) break;
-          __threadfence();
-        }
-        auto part_of = [&](int i) -> float* {
-          const int p = p0 + i * pstep;
-          return a.part + (size_t)(2 * (w_first + p) + (p == 0)) * part_sz;
-        };
-        const bool final_level = ngroups == 1 || level == 1;
-        if (!final_level && cnt == 1) continue;  // a group of one stands for itself
-        for (int x = tid; x < cnt * HT; x += NCW * 32) {
-          const float* pp = part_of(x / HT) + (size_t)HT * D + x % HT;
-          s_w[x / HT][x % HT] = __ldcg(pp);
-          s_s[x / HT][x % HT] = __ldcg(pp + HT);
-        }
-        bar_compute();
-        if (tid < HT) {
-          float mx = -INFINITY;
-          for (int i = 0; i < cnt; ++i) mx = fmaxf(mx, s_w[i][tid]);
-          float s = 0.0f;
-          for (int i = 0; i < cnt; ++i) {
-            const float w = mx == -INFINITY ? 0.0f : ex2_fast(s_w[i][tid] - mx);
-            s_w[i][tid] = w;
-            s += w * s_s[i][tid];
-          }
-          s_mx[tid] = mx;
-          s_inv[tid] = final_level ? (s > 0.0f ? vscale / s : (s == s ? 0.0f : s)) : s;
-          if (final_level && lse && tid < heads) lse[tid] = s == 0.0f ? -INFINITY : (mx + log2f(s)) * 0.69314718055994531f;
-        }
-        bar_compute();
-        float* lead = part_of(0);
-        for (int x = tid; x < HT * D / 4; x += NCW * 32) {
-          const int h = 4 * x / D, col = 4 * x % D;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int i0 = 0; i0 < cnt; i0 += 8) {
-            float4 y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i0 + i < cnt) y[i] = __ldcg(reinterpret_cast<const float4*>(part_of(i0 + i)) + x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i0 + i < cnt) {
-                const float w = s_w[i0 + i][h];
-                v.x = fmaf(w, y[i].x, v.x);
-                v.y = fmaf(w, y[i].y, v.y);
-                v.z = fmaf(w, y[i].z, v.z);
-                v.w = fmaf(w, y[i].w, v.w);
-              }
-          }
-          if (final_level) {
-            const float r = s_inv[h];
-            if (h < heads)
-              *reinterpret_cast<uint2*>(out + (int64_t)h * D + col) = make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
-          } else {
-            __stcg(reinterpret_cast<float4*>(lead) + x, v);
-          }
-        }
-        if (!final_level && tid < HT) {
-          __stcg(lead + (size_t)HT * D + tid, s_mx[tid]);
-          __stcg(lead + (size_t)HT * D + HT + tid, s_inv[tid]);
-        }
-        bar_compute();
-        if (final_level) break;
-      }
+      JoinArgs ja;
+      ja.part = a.part;
+      ja.ctr_first = a.counters;
+      ja.ctr_last = a.counters + 2 * (int64_t)a.workers;
+      ja.out = out;
+      ja.lse = lse;
+      ja.w_first = (int)w_first;
+      ja.nparts = (int)((s_walk.item1 * s_walk.G + s_walk.T - 1) / s_walk.T - w_first);
+      ja.p_me = (int)(blockIdx.x - w_first);
+      ja.heads = heads;
+      ja.vscale = vscale;
+      join_parts<D, HT>(ja, s_o, s_mx, s_inv, &s_last);
     }
-    // ---- next segment
-    if (c.pos < c.end && j == c.s.tiles) {
-      j = 0;
-      if (++hc == nhc) {
-        hc = 0;
-        c.base += (int64_t)c.s.tiles * nhc;
-        c.s = make_seq<TK>(a, ++c.b, false);
-      }
-    }
+    if (tid == 0) s_walk.next(a, nhc);
+    bar_compute();
   }
 }
 
-template <int D, bool F8, int HT>
+template <int D, bool F8, int HG>
 cudaError_t launch_one(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
-  constexpr int smem = Ring<D, F8>::N * Ring<D, F8>::SLOT + 1024;
-  static const cudaError_t attr = cudaFuncSetAttribute(kv_decode_kernel<D, F8, HT>,
+  constexpr int smem = Cfg<D, F8, HG>::N * Cfg<D, F8, HG>::SLOT + 1024;
+  static const cudaError_t attr = cudaFuncSetAttribute(kv_decode_kernel<D, F8, HG>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (attr != cudaSuccess) return attr;
-  kv_decode_kernel<D, F8, HT><<<a.workers, NTHR, smem, st>>>(a, km, vm);
+  kv_decode_kernel<D, F8, HG><<<a.workers, NTHR, smem, st>>>(a, km, vm);
   return cudaGetLastError();
+}
+
+template <int D, bool F8>
+cudaError_t launch_h(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  switch (kv_decode_head_tile(a.hpg)) {
+    case 8: return launch_one<D, F8, 1>(a, km, vm, st);
+    case 16: return launch_one<D, F8, 2>(a, km, vm, st);
+    default: return launch_one<D, F8, 4>(a, km, vm, st);
+  }
 }
 
 template <int D>
 cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, bool e4m3, cudaStream_t st) {
-  const bool wide = kv_decode_head_tile(a.hpg) == 16;
-  if (e4m3) return wide ? launch_one<D, true, 16>(a, km, vm, st) : launch_one<D, true, 8>(a, km, vm, st);
-  return wide ? launch_one<D, false, 16>(a, km, vm, st) : launch_one<D, false, 8>(a, km, vm, st);
+  return e4m3 ? launch_h<D, true>(a, km, vm, st) : launch_h<D, false>(a, km, vm, st);
 }
 
 }  // namespace
 
-int kv_decode_tile(int d, bool e4m3) { return d * (e4m3 ? 1 : 2) <= 128 ? 128 : 64; }  // Ring::TK
+int kv_decode_tile(int d, bool e4m3) { return d * (e4m3 ? 1 : 2) <= P_T ? 128 : 64; }  // Cfg::TK
 
-int kv_decode_workers(int d, int hpg, int num_sms) {
-  const int ht = kv_decode_head_tile(hpg);
-  return (d * ht >= 4096 || (d == 192 && ht == 16) ? 1 : 2) * num_sms;
-}
+int kv_decode_workers(int num_sms) { return 2 * num_sms; }
 
 bool make_cache_map(CUtensorMap* m, const void* ptr, bool e4m3, int d, int page_size, int nkv, int64_t num_pages,
                     int64_t stride_page, int64_t stride_head, int64_t stride_slot, int box_tokens) {

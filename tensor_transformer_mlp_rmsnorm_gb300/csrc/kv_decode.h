@@ -35,12 +35,12 @@ struct DecodeArgs {
   uint32_t* status;
 };
 
-// Query heads worked on together: the smallest tile that holds a key head's.
-inline int kv_decode_head_tile(int hpg) { return hpg <= 8 ? 8 : 16; }
+// Query heads worked on together: the smallest tile that holds a key head's, at most 32.
+inline int kv_decode_head_tile(int hpg) { return hpg <= 8 ? 8 : hpg <= 16 ? 16 : 32; }
 // Tokens of a tile.
 int kv_decode_tile(int d, bool e4m3);
-// CTAs the kernel runs with for this head size.
-int kv_decode_workers(int d, int hpg, int num_sms);
+// CTAs the kernel runs with.
+int kv_decode_workers(int num_sms);
 inline size_t kv_decode_part_floats(int d, int hpg) {
   return (size_t)kv_decode_head_tile(hpg) * (d + 2);
 }
