@@ -36,14 +36,12 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "allow_smem.h"
 #include "kv_decode.h"
 #include "ptx_sm103.cuh"
 #include "tma_maps.cuh"
 #include "f32x2.cuh"
 
-#ifndef P_T
-#define P_T 128
-#endif
 namespace tpmlp {
 namespace {
 
@@ -65,7 +63,7 @@ struct Cfg {
   static constexpr int RING_BYTES = 96 * 1024;             // two CTAs an SM
   static constexpr int ROW = D * (F8 ? 1 : 2);             // bytes of a token's key or value
   static constexpr int BLOCK = ROW % 128 == 0 ? 128 : 64;  // bytes of a row that lie together (the swizzle's width)
-  static constexpr int TK = ROW <= P_T ? 128 : 64;         // tokens of a tile
+  static constexpr int TK = ROW <= 128 ? 128 : 64;         // tokens of a tile
   static constexpr int SLOT = TK * ROW;                    // one operand of a tile
   // Every computing warp works on every tile, so each waits for every use of a
   // slot: a barrier's one-bit phase is never asked about two rounds ahead.
@@ -839,9 +837,8 @@ __global__ void __launch_bounds__(NTHR, 2)
 template <int D, bool F8, int HG>
 cudaError_t launch_one(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   constexpr int smem = Cfg<D, F8, HG>::N * Cfg<D, F8, HG>::SLOT + 1024;
-  static const cudaError_t attr = cudaFuncSetAttribute(kv_decode_kernel<D, F8, HG>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (attr != cudaSuccess) return attr;
+  const cudaError_t e = allow_smem<kv_decode_kernel<D, F8, HG>>(smem);
+  if (e != cudaSuccess) return e;
   kv_decode_kernel<D, F8, HG><<<a.workers, NTHR, smem, st>>>(a, km, vm);
   return cudaGetLastError();
 }
@@ -862,7 +859,7 @@ cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& km, const CUtensorM
 
 }  // namespace
 
-int kv_decode_tile(int d, bool e4m3) { return d * (e4m3 ? 1 : 2) <= P_T ? 128 : 64; }  // Cfg::TK
+int kv_decode_tile(int d, bool e4m3) { return d * (e4m3 ? 1 : 2) <= 128 ? 128 : 64; }  // Cfg::TK
 
 int kv_decode_workers(int num_sms) { return 2 * num_sms; }
 

@@ -18,13 +18,16 @@
 // What bounds it: memory (about 8 flops a byte are far below the f32 rate).
 // A head belongs to d / 16 lanes; a lane holds two 16-byte (bf16) chunks whose
 // values are each other's rotation partners, so the rotation needs no shuffle
-// and the norm three or four.  A warp works on one row at a time (four heads
-// at d = 128), takes the row's sines and cosines once, shared through shared
-// memory, and loads ROPE_UNROLL heads a lane group ahead of their arithmetic.
+// and the norm three or four.  A warp walks rows, four heads at a time at
+// d = 128, and takes a row's sines and cosines once.  Loads run several steps
+// ahead, across rows, through a queue in shared memory (cp.async): each lane
+// reads back only what it copied itself, so nothing but its own copies is
+// waited for, and no registers are held by loads in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "allow_smem.h"
 #include "qk_rope.h"
 #include "vec.cuh"
 
@@ -33,16 +36,26 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-#ifndef P_RU
-#define P_RU 2
-#define P_RB 3
-#define P_BU 2
-#define P_BB 2
-#endif
-constexpr int ROPE_UNROLL = P_RU;   // heads a lane group has in flight
-constexpr int ROWS_BLOCKS = P_RB;
-constexpr int BWD_UNROLL = P_BU;
-constexpr int BWD_BLOCKS = P_BB;
+
+// Steps that a lane's loads run ahead, and blocks of an SM: what fits shared
+// memory (64 KB of queue a block forward, 96 KB backward) and the registers.
+template <typename T>
+struct Ahead {
+  static constexpr int CHUNK = 8 * sizeof(T) / 16;              // 16-byte pieces of 8 values
+  static constexpr int ROWS = sizeof(T) == 2 ? 8 : 4;           // forward and append: 2 chunks a step
+  static constexpr int BWD = sizeof(T) == 2 ? 6 : 3;            // backward: 4 chunks a step
+};
+constexpr int ROWS_BLOCKS = 3, BWD_BLOCKS = 2;
+
+__device__ __forceinline__ void cp_async16(void* smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(g)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // 8 consecutive elements as loaded.
 template <typename T>
@@ -73,6 +86,45 @@ struct Raw8<float> {
   __device__ void set(const float* f) {
     a = make_float4(f[0], f[1], f[2], f[3]);
     b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// A lane's queue slot: chunk c of a step lies 32 lanes x 16 bytes apart, so a
+// warp's accesses are contiguous.
+template <typename T>
+__device__ __forceinline__ void queue_load(uint4* slot, int c, const T* g) {
+#pragma unroll
+  for (int i = 0; i < Ahead<T>::CHUNK; ++i)
+    cp_async16(slot + (c * Ahead<T>::CHUNK + i) * 32, reinterpret_cast<const uint4*>(g) + i);
+}
+__device__ __forceinline__ void queue_get(const uint4* slot, int c, Raw8<__nv_bfloat16>& r) { r.v = slot[c * 32]; }
+__device__ __forceinline__ void queue_get(const uint4* slot, int c, Raw8<float>& r) {
+  r.a = *reinterpret_cast<const float4*>(slot + 2 * c * 32);
+  r.b = *reinterpret_cast<const float4*>(slot + (2 * c + 1) * 32);
+}
+
+// A warp's walk over (row, heads): rows of its items in turn, in each the
+// heads group, group + step, ... of [begin, end).
+struct Steps {
+  int64_t it, items, stride;
+  int splits, begin, end, step, groups;
+  int64_t row;
+  int h;  // the first lane group's head
+  __device__ __forceinline__ void enter() {
+    while (it < items) {
+      row = splits == 1 ? it : it / splits;
+      h = begin + (splits == 1 ? 0 : (int)(it - row * splits) * groups);
+      if (h < end) return;
+      it += stride;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return it < items; }
+  __device__ __forceinline__ void next() {
+    h += step;
+    if (h >= end) {
+      it += stride;
+      enter();
+    }
   }
 };
 
@@ -230,9 +282,11 @@ __device__ __forceinline__ int append_place(const RopeArgs& a, int64_t row, int6
 // KIND 0: rows to rows (RopeArgs); 1, 2: append to a bf16 or E4M3 cache.
 template <typename T, int D, int KIND>
 __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const __grid_constant__ RopeArgs a,
-                                                            const __grid_constant__ RopeFreqs fr) {
+                                                                         const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
-  __shared__ __align__(16) float2 s_cs[WARPS][ROPE_MAX_PAIRS];
+  constexpr int S = Ahead<T>::ROWS, STEP = 2 * Ahead<T>::CHUNK * 32;  // a step's uint4 of a warp
+  extern __shared__ __align__(16) uint4 s_queue[];
+  __shared__ __align__(16) float2 s_cs[WARPS][D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = lane % HL::LANES, group = lane / HL::LANES;
   const bool active = u < HL::UNITS;
@@ -242,107 +296,125 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
   unit_offsets(active ? u : 0, rot, il, oa, ob);
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
-  const int h_end = a.nq + a.nkv + (KIND ? a.nkv : 0);
-  const int h_begin = KIND && !a.out ? a.nq : 0;  // an append without a query output skips the queries
-  const int64_t items = a.rows * a.splits, stride = (int64_t)gridDim.x * WARPS;
-  for (int64_t it = (int64_t)blockIdx.x * WARPS + warp; it < items; it += stride) {
-    const int64_t row = it / a.splits;
-    const int split = (int)(it - row * a.splits);
-    const T* in = static_cast<const T*>(a.in) + row * a.ld_in;
-    const int hstep = a.splits * HL::GROUPS;
-    float cs[8], sn[8];
-    int64_t slot_off = 0;
-    bool placed = false;
-    for (int h0 = h_begin + split * HL::GROUPS + group; h0 - group < h_end; h0 += ROPE_UNROLL * hstep) {
-      Raw8<T> xa[ROPE_UNROLL], xb[ROPE_UNROLL];
-#pragma unroll
-      for (int k = 0; k < ROPE_UNROLL; ++k) {
-        const int h = h0 + k * hstep;
-        if (active && h < h_end) {
-          xa[k].load(in + (int64_t)h * D + oa);
-          xb[k].load(in + (int64_t)h * D + ob);
-        } else {
-          const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          xa[k].set(z);
-          xb[k].set(z);
-        }
+  uint4* queue = s_queue + warp * S * STEP + lane;
+
+  Steps ld;  // the step to load next
+  ld.it = (int64_t)blockIdx.x * WARPS + warp;
+  ld.items = a.rows * a.splits;
+  ld.stride = (int64_t)gridDim.x * WARPS;
+  ld.splits = a.splits;
+  ld.begin = KIND && !a.out ? a.nq : 0;  // an append without a query output skips the queries
+  ld.end = a.nq + a.nkv + (KIND ? a.nkv : 0);
+  ld.groups = HL::GROUPS;
+  ld.step = a.splits * HL::GROUPS;
+  ld.enter();
+  Steps st = ld;  // the step to work on
+  auto load = [&](int slot) {
+    if (ld.more()) {
+      const int h = ld.h + group;
+      if (active && h < ld.end) {
+        const T* in = static_cast<const T*>(a.in) + ld.row * a.ld_in + (int64_t)h * D;
+        queue_load<T>(queue + slot * STEP, 0, in + oa);
+        queue_load<T>(queue + slot * STEP, 1, in + ob);
       }
-      if (!placed) {  // behind the first loads, which do not wait for it
-        const int pos = KIND ? append_place(a, row, slot_off) : a.pos ? a.pos[row] : (int)(a.seq > 0 ? row % a.seq : row);
-        if (KIND && slot_off < 0) break;
+      ld.next();
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) load(i);
+  int slot = 0;
+  int64_t cur_it = -1, slot_off = 0;
+  float cs[8], sn[8];
+  for (; st.more(); st.next(), slot = slot + 1 == S ? 0 : slot + 1) {
+    load(slot == 0 ? S - 1 : slot - 1);
+    if (st.it != cur_it) {  // a new row
+      cur_it = st.it;
+      slot_off = 0;
+      const int pos = KIND ? append_place(a, st.row, slot_off)
+                           : a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
+      if (slot_off >= 0) {
         if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
         unit_angles(s_cs[warp], u, rot, 1.0f, cs, sn);
-        placed = true;
       }
+    }
+    cp_wait<S - 1>();
+    if (KIND && slot_off < 0) continue;  // a row that is nobody's
+    const int h = st.h + group;
+    const bool work = active && h < st.end;
+    const bool is_q = h < a.nq, is_v = KIND && h >= a.nq + a.nkv;
+    Raw8<T> xa, xb;
+    float fa[8], fb[8];
+    if (work) {
+      queue_get(queue + slot * STEP, 0, xa);
+      queue_get(queue + slot * STEP, 1, xb);
+    } else {
+      const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      xa.set(z);
+      xb.set(z);
+    }
+    xa.get(fa);
+    xb.get(fb);
+    if (norm) {
+      float ss = 0.0f;
 #pragma unroll
-      for (int k = 0; k < ROPE_UNROLL; ++k) {
-        const int h = h0 + k * hstep;
-        if (h - group >= h_end) break;  // the same for the whole warp
-        const bool is_q = h < a.nq, is_v = KIND && h >= a.nq + a.nkv;
-        float fa[8], fb[8];
-        xa[k].get(fa);
-        xb[k].get(fb);
-        if (norm) {
-          float ss = 0.0f;
+      for (int i = 0; i < 8; ++i) ss = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], ss));
+      ss = HL::sum(ss);
+      const T* w = static_cast<const T*>(is_q ? a.q_norm_w : a.k_norm_w);
+      if (work && !is_v && w) {
+        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+        Raw8<T> wr;
+        float wf[8];
+        wr.load(w + oa);
+        wr.get(wf);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], ss));
-          ss = HL::sum(ss);
-          const T* w = static_cast<const T*>(is_q ? a.q_norm_w : a.k_norm_w);
-          if (active && h < h_end && !is_v && w) {
-            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-            Raw8<T> wr;
-            float wf[8];
-            wr.load(w + oa);
-            wr.get(wf);
+        for (int i = 0; i < 8; ++i) fa[i] *= r * wf[i];
+        wr.load(w + ob);
+        wr.get(wf);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fa[i] *= r * wf[i];
-            wr.load(w + ob);
-            wr.get(wf);
+        for (int i = 0; i < 8; ++i) fb[i] *= r * wf[i];
+      }
+    }
+    if (!work) continue;
+    if (!is_v) rotate16(fa, fb, cs, sn, il);
+    if (KIND == 0 || is_q) {
+      if (KIND == 0 && a.save) {  // the values before the norm, for the backward pass
+        T* sv = static_cast<T*>(a.save) + st.row * a.ld_save + (int64_t)h * D;
+        xa.store(sv + oa);
+        xb.store(sv + ob);
+      }
+      T* out = static_cast<T*>(a.out) + st.row * a.ld_out + (int64_t)h * D;
+      xa.set(fa);
+      xb.set(fb);
+      xa.store(out + oa);
+      xb.store(out + ob);
+    } else {
+      const int g = is_v ? h - a.nq - a.nkv : h - a.nq;
+      const int64_t off = slot_off + g * a.stride_head;
+      if (KIND == 1) {
+        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + off;
+        Raw8<__nv_bfloat16> t;
+        t.set(fa);
+        t.store(c + oa);
+        t.set(fb);
+        t.store(c + ob);
+      } else {
+        uint8_t* c = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + off;
+        const float* isc = is_v ? a.v_inv_scale : a.k_inv_scale;
+        if (isc) {
+          const float sc = isc[g];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fb[i] *= r * wf[i];
+          for (int i = 0; i < 8; ++i) {
+            fa[i] = __fdiv_rn(fa[i], sc);
+            fb[i] = __fdiv_rn(fb[i], sc);
           }
         }
-        if (!active || h >= h_end) continue;
-        if (!is_v) rotate16(fa, fb, cs, sn, il);
-        if (KIND == 0 || is_q) {
-          if (KIND == 0 && a.save) {  // the values before the norm, for the backward pass
-            T* sv = static_cast<T*>(a.save) + row * a.ld_save + (int64_t)h * D;
-            xa[k].store(sv + oa);
-            xb[k].store(sv + ob);
-          }
-          T* out = static_cast<T*>(a.out) + row * a.ld_out + (int64_t)h * D;
-          xa[k].set(fa);
-          xb[k].set(fb);
-          xa[k].store(out + oa);
-          xb[k].store(out + ob);
-        } else {
-          const int g = is_v ? h - a.nq - a.nkv : h - a.nq;
-          const int64_t off = slot_off + g * a.stride_head;
-          if (KIND == 1) {
-            __nv_bfloat16* c = static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + off;
-            Raw8<__nv_bfloat16> t;
-            t.set(fa);
-            t.store(c + oa);
-            t.set(fb);
-            t.store(c + ob);
-          } else {
-            uint8_t* c = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + off;
-            const float* isc = is_v ? a.v_inv_scale : a.k_inv_scale;
-            const float sc = isc ? isc[g] : 1.0f;
-            if (isc) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                fa[i] = __fdiv_rn(fa[i], sc);
-                fb[i] = __fdiv_rn(fb[i], sc);
-              }
-            }
-            *reinterpret_cast<uint2*>(c + oa) = e4m3x8(fa);
-            *reinterpret_cast<uint2*>(c + ob) = e4m3x8(fb);
-          }
-        }
+        *reinterpret_cast<uint2*>(c + oa) = e4m3x8(fa);
+        *reinterpret_cast<uint2*>(c + ob) = e4m3x8(fb);
       }
     }
   }
+  cp_wait<0>();
 }
 
 // Backward.  All rows' query heads are taken first, then their key heads, so
@@ -350,10 +422,12 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
 // rope_dw_kernel, so the gradients are the same every run.
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a,
-                                                           const __grid_constant__ RopeFreqs fr) {
+                                                                       const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
-  constexpr int UN = BWD_UNROLL;
-  __shared__ __align__(16) float2 s_cs[WARPS][ROPE_MAX_PAIRS];
+  constexpr int S = Ahead<T>::BWD, STEP = 4 * Ahead<T>::CHUNK * 32;
+  extern __shared__ __align__(16) uint4 s_queue[];
+  __shared__ __align__(16) float2 s_cs[WARPS][D / 2];
+  __shared__ float s_dw[WARPS][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = lane % HL::LANES, group = lane / HL::LANES;
   const bool active = u < HL::UNITS;
@@ -363,109 +437,127 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
   unit_offsets(active ? u : 0, rot, il, oa, ob);
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
-  __shared__ float s_dw[WARPS][2][D];
-  const int64_t items = a.rows * a.splits, stride = (int64_t)gridDim.x * WARPS;
+  uint4* queue = s_queue + warp * S * STEP + lane;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
-    const int h_begin = part ? a.nq : 0, h_end = part ? a.nq + a.nkv : a.nq;
     const T* w = static_cast<const T*>(part ? a.k_norm_w : a.q_norm_w);
-    const int hstep = a.splits * HL::GROUPS;
-    float acc[16];
+    float acc[16], cs[8], sn[8];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    for (int64_t it = (int64_t)blockIdx.x * WARPS + warp; it < items; it += stride) {
-      const int64_t row = it / a.splits;
-      const int split = (int)(it - row * a.splits);
-      float cs[8], sn[8];
-      bool placed = false;
-      for (int h0 = h_begin + split * HL::GROUPS + group; h0 - group < h_end; h0 += UN * hstep) {
-        Raw8<T> ga[UN], gb[UN], xa[UN], xb[UN];
-#pragma unroll
-        for (int k = 0; k < UN; ++k) {
-          const int h = h0 + k * hstep;
-          const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          ga[k].set(z);
-          gb[k].set(z);
-          xa[k].set(z);
-          xb[k].set(z);
-          if (active && h < h_end) {
-            const T* g = static_cast<const T*>(a.dout) + row * a.ld_dout + (int64_t)h * D;
-            ga[k].load(g + oa);
-            gb[k].load(g + ob);
-            if (w) {
-              const T* x = static_cast<const T*>(a.x) + row * a.ld_x + (int64_t)h * D;
-              xa[k].load(x + oa);
-              xb[k].load(x + ob);
-            }
-          }
-        }
-        if (!placed) {  // behind the first loads, which do not wait for it
-          const int pos = a.pos ? a.pos[row] : (int)(a.seq > 0 ? row % a.seq : row);
-          if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
-          unit_angles(s_cs[warp], u, rot, -1.0f, cs, sn);
-          placed = true;
-        }
-#pragma unroll
-        for (int k = 0; k < UN; ++k) {
-          const int h = h0 + k * hstep;
-          if (h - group >= h_end) break;  // the same for the whole warp
-          float fa[8], fb[8];
-          ga[k].get(fa);
-          gb[k].get(fb);
-          rotate16(fa, fb, cs, sn, il);
+    Steps ld;  // the step to load next
+    ld.it = (int64_t)blockIdx.x * WARPS + warp;
+    ld.items = a.rows * a.splits;
+    ld.stride = (int64_t)gridDim.x * WARPS;
+    ld.splits = a.splits;
+    ld.begin = part ? a.nq : 0;
+    ld.end = part ? a.nq + a.nkv : a.nq;
+    ld.groups = HL::GROUPS;
+    ld.step = a.splits * HL::GROUPS;
+    ld.enter();
+    Steps st = ld;  // the step to work on
+    auto load = [&](int slot) {
+      if (ld.more()) {
+        const int h = ld.h + group;
+        if (active && h < ld.end) {
+          const T* g = static_cast<const T*>(a.dout) + ld.row * a.ld_dout + (int64_t)h * D;
+          uint4* q = queue + slot * STEP;
+          queue_load<T>(q, 0, g + oa);
+          queue_load<T>(q, 1, g + ob);
           if (w) {
-            float va[8], vb[8];
-            xa[k].get(va);
-            xb[k].get(vb);
-            float wa[8], wb[8];
-            Raw8<T> wr;
-            wr.load(w + oa);
-            wr.get(wa);
-            wr.load(w + ob);
-            wr.get(wb);
-            // both sums at once: sum x^2 and sum w g x = mean(w g xh) d / r
-            float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
-              dot = fmaf(wa[i] * fa[i], va[i], fmaf(wb[i] * fb[i], vb[i], dot));
-            }
-            HL::sum2(ss, dot);
-            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-            const float c = dot * (1.0f / D) * r * r * r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[i] = fmaf(fa[i], va[i] * r, acc[i]);
-              acc[8 + i] = fmaf(fb[i], vb[i] * r, acc[8 + i]);
-              fa[i] = fmaf(r * wa[i], fa[i], -c * va[i]);
-              fb[i] = fmaf(r * wb[i], fb[i], -c * vb[i]);
-            }
+            const T* x = static_cast<const T*>(a.x) + ld.row * a.ld_x + (int64_t)h * D;
+            queue_load<T>(q, 2, x + oa);
+            queue_load<T>(q, 3, x + ob);
           }
-          if (!active || h >= h_end) continue;
-          T* dx = static_cast<T*>(a.dx) + row * a.ld_dx + (int64_t)h * D;
-          ga[k].set(fa);
-          gb[k].set(fb);
-          ga[k].store(dx + oa);
-          gb[k].store(dx + ob);
+        }
+        ld.next();
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) load(i);
+    int slot = 0;
+    int64_t cur_it = -1;
+    for (; st.more(); st.next(), slot = slot + 1 == S ? 0 : slot + 1) {
+      load(slot == 0 ? S - 1 : slot - 1);
+      if (st.it != cur_it) {  // a new row
+        cur_it = st.it;
+        const int pos = a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
+        if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
+        unit_angles(s_cs[warp], u, rot, -1.0f, cs, sn);
+      }
+      cp_wait<S - 1>();
+      const int h = st.h + group;
+      const bool work = active && h < st.end;
+      const uint4* q = queue + slot * STEP;
+      const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      Raw8<T> ra, rb;
+      float fa[8], fb[8];
+      ra.set(z);
+      rb.set(z);
+      if (work) {
+        queue_get(q, 0, ra);
+        queue_get(q, 1, rb);
+      }
+      ra.get(fa);
+      rb.get(fb);
+      rotate16(fa, fb, cs, sn, il);
+      if (w) {
+        float va[8], vb[8], wa[8], wb[8];
+        ra.set(z);
+        rb.set(z);
+        if (work) {
+          queue_get(q, 2, ra);
+          queue_get(q, 3, rb);
+        }
+        ra.get(va);
+        rb.get(vb);
+        ra.load(w + oa);
+        ra.get(wa);
+        rb.load(w + ob);
+        rb.get(wb);
+        // both sums at once: sum x^2 and sum w g x = mean(w g xh) d / r
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
+          dot = fmaf(wa[i] * fa[i], va[i], fmaf(wb[i] * fb[i], vb[i], dot));
+        }
+        HL::sum2(ss, dot);
+        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+        const float c = dot * (1.0f / D) * r * r * r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[i] = fmaf(fa[i], va[i] * r, acc[i]);
+          acc[8 + i] = fmaf(fb[i], vb[i] * r, acc[8 + i]);
+          fa[i] = fmaf(r * wa[i], fa[i], -c * va[i]);
+          fb[i] = fmaf(r * wb[i], fb[i], -c * vb[i]);
         }
       }
+      if (!work) continue;
+      T* dx = static_cast<T*>(a.dx) + st.row * a.ld_dx + (int64_t)h * D;
+      ra.set(fa);
+      rb.set(fb);
+      ra.store(dx + oa);
+      rb.store(dx + ob);
     }
-    // lanes of the same unit
+    cp_wait<0>();
+    if (!a.part) continue;
+    // lanes of the same unit, then the warps of the block in order
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float v = acc[i];
 #pragma unroll
       for (int o = HL::LANES; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (active && group == 0) s_dw[warp][part][(i < 8 ? oa : ob - 8) + i] = v;
+      if (active && group == 0) s_dw[warp][(i < 8 ? oa : ob - 8) + i] = v;
     }
-  }
-  if (!a.part) return;
-  __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += THREADS) {  // the warps of the block in order
-    float v = 0.0f;
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += THREADS) {
+      float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < WARPS; ++k) v += (&s_dw[k][0][0])[c];
-    a.part[(int64_t)blockIdx.x * 2 * D + c] = v;
+      for (int k = 0; k < WARPS; ++k) v += s_dw[k][c];
+      a.part[((int64_t)blockIdx.x * 2 + part) * D + c] = v;
+    }
   }
 }
 
@@ -496,6 +588,19 @@ int head_splits(int64_t rows, int heads, int groups, int num_sms) {
   return (int)(want < 1 ? 1 : want > most ? most : want);
 }
 
+template <typename T>
+constexpr int ROWS_QUEUE = WARPS * Ahead<T>::ROWS * 2 * Ahead<T>::CHUNK * 32 * 16;
+template <typename T>
+constexpr int BWD_QUEUE = WARPS * Ahead<T>::BWD * 4 * Ahead<T>::CHUNK * 32 * 16;
+
+template <auto K, typename A>
+cudaError_t launch_kernel(int64_t blocks, int queue, cudaStream_t st, const A& a, const RopeFreqs& fr) {
+  const cudaError_t e = allow_smem<K>(queue);
+  if (e != cudaSuccess) return e;
+  K<<<(unsigned)blocks, THREADS, queue, st>>>(a, fr);
+  return cudaGetLastError();
+}
+
 template <int KIND, typename T>
 cudaError_t launch_rows(RopeArgs a, const RopeFreqs& fr, int d, int num_sms, cudaStream_t st) {
   const int heads = (KIND && !a.out ? 0 : a.nq) + a.nkv + (KIND ? a.nkv : 0);
@@ -503,15 +608,14 @@ cudaError_t launch_rows(RopeArgs a, const RopeFreqs& fr, int d, int num_sms, cud
   a.splits = head_splits(a.rows, heads, groups, num_sms);
   const int64_t items = a.rows * a.splits;
   int64_t blocks = (items + WARPS - 1) / WARPS;
-  if (blocks > 16LL * num_sms) blocks = 16LL * num_sms;
+  if (blocks > (int64_t)ROWS_BLOCKS * num_sms) blocks = (int64_t)ROWS_BLOCKS * num_sms;  // one wave
   switch (d) {
-    case 64: rope_rows_kernel<T, 64, KIND><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
-    case 128: rope_rows_kernel<T, 128, KIND><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
-    case 192: rope_rows_kernel<T, 192, KIND><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
-    case 256: rope_rows_kernel<T, 256, KIND><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
+    case 64: return launch_kernel<rope_rows_kernel<T, 64, KIND>>(blocks, ROWS_QUEUE<T>, st, a, fr);
+    case 128: return launch_kernel<rope_rows_kernel<T, 128, KIND>>(blocks, ROWS_QUEUE<T>, st, a, fr);
+    case 192: return launch_kernel<rope_rows_kernel<T, 192, KIND>>(blocks, ROWS_QUEUE<T>, st, a, fr);
+    case 256: return launch_kernel<rope_rows_kernel<T, 256, KIND>>(blocks, ROWS_QUEUE<T>, st, a, fr);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 template <typename T>
@@ -520,17 +624,16 @@ cudaError_t launch_bwd(RopeBwdArgs a, const RopeFreqs& fr, int d, int num_sms, c
   a.splits = head_splits(a.rows, a.nq + a.nkv, groups, num_sms);
   const int64_t items = a.rows * a.splits;
   int64_t blocks = (items + WARPS - 1) / WARPS;
-  if (blocks > 4LL * num_sms) blocks = 4LL * num_sms;
+  if (blocks > (int64_t)BWD_BLOCKS * num_sms) blocks = (int64_t)BWD_BLOCKS * num_sms;  // one wave
   if (blocks > ROPE_MAX_PARTS) blocks = ROPE_MAX_PARTS;
   *blocks_out = (int)blocks;
   switch (d) {
-    case 64: rope_bwd_kernel<T, 64><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
-    case 128: rope_bwd_kernel<T, 128><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
-    case 192: rope_bwd_kernel<T, 192><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
-    case 256: rope_bwd_kernel<T, 256><<<(unsigned)blocks, THREADS, 0, st>>>(a, fr); break;
+    case 64: return launch_kernel<rope_bwd_kernel<T, 64>>(blocks, BWD_QUEUE<T>, st, a, fr);
+    case 128: return launch_kernel<rope_bwd_kernel<T, 128>>(blocks, BWD_QUEUE<T>, st, a, fr);
+    case 192: return launch_kernel<rope_bwd_kernel<T, 192>>(blocks, BWD_QUEUE<T>, st, a, fr);
+    case 256: return launch_kernel<rope_bwd_kernel<T, 256>>(blocks, BWD_QUEUE<T>, st, a, fr);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -766,22 +766,19 @@ def qk_norm_rope_backward(dout, x, n_heads: int, n_kv_heads: int, head_dim: int,
     dp, _, ldd = _rows(dx, width, dtype, "dx", index, n)
     wp, wbytes = None, 0
     if norm:
-        # without given ones, the two gradients and the scratch come from one allocation
         need = lib().tpattn_qk_rope_workspace_bytes(head_dim)
-        own = workspace is None or (q_norm_w is not None and dq_norm_w is None) or (
-            k_norm_w is not None and dk_norm_w is None)
-        if own:
-            buf = torch.empty(2 * head_dim + (need // 4 if workspace is None else 0), dtype=_F32T, device=dout.device)
-            if q_norm_w is not None and dq_norm_w is None:
-                dq_norm_w = buf[:head_dim]
-            if k_norm_w is not None and dk_norm_w is None:
-                dk_norm_w = buf[head_dim: 2 * head_dim]
-        if workspace is None:
-            wp, wbytes = buf.data_ptr() + 8 * head_dim, need
-        elif workspace.get_device() != index or not workspace.is_contiguous():
-            raise _bad(workspace, "workspace", f"a contiguous tensor on cuda:{index}")
-        else:
+        if workspace is not None:
+            if workspace.get_device() != index or not workspace.is_contiguous():
+                raise _bad(workspace, "workspace", f"a contiguous tensor on cuda:{index}")
             wp, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        no_dq, no_dk = q_norm_w is not None and dq_norm_w is None, k_norm_w is not None and dk_norm_w is None
+        if workspace is None or no_dq or no_dk:
+            # one allocation for what was not given: every torch call here costs more than the launch
+            parts = torch.empty(2 * head_dim + (0 if wp else need // 4), dtype=_F32T,
+                                device=dout.device).split_with_sizes((head_dim, head_dim, 0 if wp else need // 4))
+            dq_norm_w, dk_norm_w = parts[0] if no_dq else dq_norm_w, parts[1] if no_dk else dk_norm_w
+            if wp is None:
+                wp, wbytes = parts[2].data_ptr(), need
     d = _qk_desc(n, dtype, index, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
     with _on(index):
         _check(lib().tpattn_qk_rope_backward(
