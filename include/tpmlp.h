@@ -599,6 +599,50 @@ TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, 
                                    int32_t len_add, const int32_t* block_table, int64_t ld_table, int32_t max_pages,
                                    float scale, int32_t window, int32_t sinks, void* out, int64_t ld_out, float* lse);
 
+/* ---- the attention sublayer with rotation, norms and a cache */
+
+/* The attention sublayer's rotation and per-head norms: queries and keys of
+ * position row % seq, as tpattn_qk_rope_forward.  Norm weights (bf16
+ * [head_dim]) are parameters: backward writes their gradients (float
+ * [head_dim]) and tpattn_sgd_step, tpattn_adamw_step and the update in
+ * backward update them with the others, without decay, through the masters
+ * where given. */
+typedef struct {
+  const tpattn_rotary* rot; /* copied; NULL: no rotation */
+  void *q_norm_w, *k_norm_w; /* both or neither */
+  float *dq_norm_w, *dk_norm_w; /* with norm weights */
+  float *master_q, *master_k;   /* both or neither */
+  float *m_q, *m_k, *v_q, *v_k; /* AdamW moments: all or none; tpattn_adamw_step needs them with norm weights */
+  float eps;
+  int32_t reserved; /* 0 */
+} tpattn_qk_params;
+/* Bytes of the extra workspace that norm weights need (the query and key rows
+ * before the norms, partial sums); 0 if `cfg` is invalid. */
+TPMLP_API size_t tpattn_qk_workspace_bytes(const tpattn_config* cfg);
+/* Turn rotation and norms on for later forwards and decodes (all tensors by
+ * pointer, the caller keeps them), or off with params NULL.  workspace:
+ * 256-byte aligned, needed with norm weights.  Requires a new forward. */
+TPMLP_API tpmlp_status tpattn_set_qk(tpattn_ctx* ctx, const tpattn_qk_params* params, void* workspace, size_t bytes);
+
+/* Store the keys and values of the last forward's prompts in a cache: sequence
+ * b's first new_lens[b] tokens (device [batch]; NULL: all seq) at positions
+ * 0, 1, ...  The cache's heads must be the sublayer's (TPMLP_ERR_SHAPE).  Runs
+ * on the attention context's stream; cache errors are reported by tpkv_sync. */
+TPMLP_API tpmlp_status tpattn_append_kv(tpattn_ctx* ctx, tpkv_ctx* kv, const int32_t* new_lens,
+                                        const int32_t* block_table, int64_t ld_table, int32_t max_pages);
+
+/* The sublayer for one new token of each of `batch` sequences (x, y [batch, H];
+ * batch <= max_tokens): pre-norm, projection, rotation and norms as set by
+ * tpattn_set_qk, append at position past_lens[b], attention over the
+ * past_lens[b] + 1 tokens (window and sinks as in tpkv_decode), output
+ * projection, bias and residual.  A sequence with past_lens[b] < 0 is inactive:
+ * nothing is stored and its attention output is 0.  Overwrites the workspace
+ * of the last forward, whose backward is then TPMLP_ERR_ORDER. */
+TPMLP_API tpmlp_status tpattn_decode(tpattn_ctx* ctx, tpkv_ctx* kv, int32_t batch, const void* x, const void* norm_w,
+                                     const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
+                                     const int32_t* past_lens, const int32_t* block_table, int64_t ld_table,
+                                     int32_t max_pages, int32_t window, int32_t sinks, void* y);
+
 /* Wait for the context's stream, then report as tpmlp_sync does, and
  * TPMLP_ERR_ARG for a page or length outside the cache (the word is cleared). */
 TPMLP_API tpmlp_status tpkv_sync(tpkv_ctx* ctx);

@@ -14,6 +14,8 @@
 //             f all-reduce) -> rmsnorm_bwd_residual -> colsum_finalize
 //   sgd     : sgd_update
 //   adamw   : grad_sqnorm -> adamw_update
+//   with tpattn_set_qk: qk_rope behind gemm_qkv, qk_rope_bwd before gemm_dgrad_norm
+//   decode  : rmsnorm_fwd -> gemm_qkv -> kv_append -> kv_decode -> gemm_out_proj
 // Fused path (head_dim 128, seq % 128 == 0; the default): gemm_scores ->
 // softmax_fwd -> gemm_pv become flash_attn_fwd (Z and each row's log-sum-exp),
 // and gemm_dp .. group_sum become flash_bwd_prep (D = rowsum(dZ o Z), dQ
@@ -31,6 +33,7 @@
 #include <vector>
 
 #include "../../include/tpmlp.h"
+#include "kv_ctx.h"
 #include "tpmlp_internal.h"
 
 using namespace tpmlp;
@@ -63,6 +66,10 @@ enum AttnKernel {
   A_FLASH_DQ_CAST,
   A_GRAD_NORM,
   A_ADAMW,
+  A_QK_ROPE,
+  A_QK_ROPE_BWD,
+  A_KV_APPEND,
+  A_KV_DECODE,
   A_COUNT
 };
 const char* const kAttnNames[A_COUNT] = {
@@ -71,7 +78,7 @@ const char* const kAttnNames[A_COUNT] = {
     "group_sum",       "softmax_bwd",     "gemm_dq",         "gemm_dk",          "gemm_wgrad_qkv",
     "gemm_dgrad_norm", "rmsnorm_bwd_residual", "colsum_finalize", "sgd_update",
     "flash_attn_fwd",  "flash_bwd_prep",  "flash_attn_bwd",  "flash_dq_cast",   "grad_sqnorm",
-    "adamw_update"};
+    "adamw_update",   "qk_rope",         "qk_rope_bwd",     "kv_append",       "kv_decode"};
 
 constexpr int MAX_PARTS = 1024;
 thread_local std::string g_attn_err;
@@ -163,6 +170,13 @@ struct tpattn_ctx {
   float *m_norm_w = nullptr, *m_w_qkv = nullptr, *m_w_o = nullptr, *m_b_o = nullptr;
   tpattn_param_set adam_m{}, adam_v{};
   bool adam_bound = false;
+  // tpattn_set_qk: rotation and per-head norms, the rows before them (for
+  // backward) and scratch in a workspace of their own
+  bool qk_on = false;
+  tpattn_qk_params qk{};
+  RopeFreqs qk_freqs{};
+  uint8_t* qk_ws = nullptr;
+  size_t qk_rows_off = 0, qk_part_off = 0;
   bool timing = false;
   struct Rec {
     int id;
@@ -533,6 +547,23 @@ tpmlp_status tpattn_forward(tpattn_ctx* c, int64_t batch, int64_t seq, const voi
   g.ep.out0 = qkv;
   g.ep.ld_out0 = W;
   ATTN_TRY(c->gemm(A_GEMM_QKV, g));
+  if (c->qk_on) {  // in place; the rows before the norms are kept for backward
+    RopeArgs r{};
+    r.in = qkv;
+    r.ld_in = W;
+    r.out = qkv;
+    r.ld_out = W;
+    if (c->qk.q_norm_w) r.save = c->qk_ws + c->qk_rows_off;
+    r.ld_save = (int64_t)(nq + nkv) * d;
+    r.rows = N;
+    r.nq = nq;
+    r.nkv = nkv;
+    r.q_norm_w = c->qk.q_norm_w;
+    r.k_norm_w = c->qk.k_norm_w;
+    r.eps = c->qk.eps;
+    r.seq = S;
+    ATTN_TRY(c->run(A_QK_ROPE, [&] { return launch_qk_rope(1, d, r, c->qk_freqs, c->num_sms, c->stream); }));
+  }
   if (c->fwd_fused) {
     ATTN_TRY(c->run(A_FLASH_FWD, [&] {
       return launch_flash_attn_fwd(qkv, B, S, nq, nkv, d, z, c->wsp<float>(c->L.lse2), c->wsp<uint32_t>(c->L.status),
@@ -582,6 +613,10 @@ static tpmlp_status attn_run_sgd(tpattn_ctx* c, float lr, bool matrices) {
     a.seg[a.nseg++] = SgdSeg{c->m_w_o, c->g_w_o, const_cast<void*>(c->w_o), H * Zc};
   }
   a.seg[a.nseg++] = SgdSeg{c->m_b_o, c->g_b_o, const_cast<void*>(c->b_o), H};
+  if (c->qk_on && c->qk.q_norm_w) {
+    a.seg[a.nseg++] = SgdSeg{c->qk.master_q, c->qk.dq_norm_w, c->qk.q_norm_w, d};
+    a.seg[a.nseg++] = SgdSeg{c->qk.master_k, c->qk.dk_norm_w, c->qk.k_norm_w, d};
+  }
   return c->run(A_SGD, [&] { return launch_sgd(1, a, c->num_sms, c->stream); });
 }
 
@@ -668,6 +703,26 @@ tpmlp_status tpattn_backward(tpattn_ctx* c, const void* dy, void* dx, float* dno
                     [&] { return launch_flash_dq_cast(dq_acc, dqkv, N, Zc, W, c->num_sms, c->stream); }));
   } else {
     ATTN_TRY(attn_core_bwd_unfused(c, B, S, qkv, dz, dqkv, dp, pr, dkv));
+  }
+  if (c->qk_on) {  // dqkv's query and key columns, in place
+    RopeBwdArgs r{};
+    r.x = c->qk_ws + c->qk_rows_off;
+    r.ld_x = (int64_t)(nq + nkv) * d;
+    r.dout = dqkv;
+    r.ld_dout = W;
+    r.dx = dqkv;
+    r.ld_dx = W;
+    r.rows = N;
+    r.nq = nq;
+    r.nkv = nkv;
+    r.q_norm_w = c->qk.q_norm_w;
+    r.k_norm_w = c->qk.k_norm_w;
+    r.eps = c->qk.eps;
+    r.seq = S;
+    if (c->qk.q_norm_w) r.part = reinterpret_cast<float*>(c->qk_ws + c->qk_part_off);
+    ATTN_TRY(c->run(A_QK_ROPE_BWD, [&] {
+      return launch_qk_rope_bwd(1, d, r, c->qk_freqs, c->num_sms, c->stream, c->qk.dq_norm_w, c->qk.dk_norm_w);
+    }));
   }
   // dN = dqkv W_qkv: every head's contribution summed on chip (the f all-reduce);
   // it runs before the QKV weight gradient, which may update W_qkv
@@ -795,6 +850,8 @@ tpmlp_status tpattn_adamw_step(tpattn_ctx* c, const tpmlp_adamw_params* hp, floa
   if (!c->bwd_done) return c->fail(TPMLP_ERR_ORDER, "adamw_step before backward");
   if (c->upd_done) return c->fail(TPMLP_ERR_ORDER, "the last backward already applied the update");
   if (!c->adam_bound) return c->fail(TPMLP_ERR_ARG, "AdamW moments are not bound");
+  if (c->qk_on && c->qk.q_norm_w && !c->qk.m_q)
+    return c->fail(TPMLP_ERR_ARG, "AdamW moments of the query and key norm weights are not set");
   if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay) || !std::isfinite(hp->max_grad_norm) ||
       !(hp->beta1 >= 0.f && hp->beta1 < 1.f) || !(hp->beta2 >= 0.f && hp->beta2 < 1.f) ||
       !(hp->eps >= 0.f && std::isfinite(hp->eps)) || hp->step < 1)
@@ -823,9 +880,167 @@ tpmlp_status tpattn_adamw_step(tpattn_ctx* c, const tpmlp_adamw_params* hp, floa
   a.seg[a.nseg++] = AdamSeg{c->m_w_qkv, c->g_w_qkv, const_cast<void*>(c->w_qkv), M.w_qkv, V.w_qkv, W * H, lr_wd};
   a.seg[a.nseg++] = AdamSeg{c->m_w_o, c->g_w_o, const_cast<void*>(c->w_o), M.w_o, V.w_o, H * Zc, lr_wd};
   a.seg[a.nseg++] = AdamSeg{c->m_b_o, c->g_b_o, const_cast<void*>(c->b_o), M.b_o, V.b_o, H, 0.0f};
+  if (c->qk_on && c->qk.q_norm_w) {
+    const tpattn_qk_params& q = c->qk;
+    a.seg[a.nseg++] = AdamSeg{q.master_q, q.dq_norm_w, q.q_norm_w, q.m_q, q.v_q, d, 0.0f};
+    a.seg[a.nseg++] = AdamSeg{q.master_k, q.dk_norm_w, q.k_norm_w, q.m_k, q.v_k, d, 0.0f};
+  }
   const int nb = adam_blocks(a, c->num_sms);
   ATTN_TRY(c->run(A_GRAD_NORM, [&] { return launch_grad_sqnorm(a, nb, c->stream); }));
   return c->run(A_ADAMW, [&] { return launch_adamw(1, a, nb, c->stream); });
+}
+
+namespace {
+// The workspace of tpattn_set_qk: the query and key rows before the norms, and
+// the partial sums of the norm weights' gradients.
+size_t qk_rows_bytes(const tpattn_config& c) {
+  return al256((size_t)c.max_tokens * (size_t)(c.n_heads + c.n_kv_heads) * (size_t)c.head_dim * 2);
+}
+}  // namespace
+
+size_t tpattn_qk_workspace_bytes(const tpattn_config* cfg) {
+  if (attn_config_error(cfg, nullptr)) return 0;
+  return qk_rows_bytes(*cfg) + al256((size_t)ROPE_MAX_PARTS * 2 * cfg->head_dim * sizeof(float));
+}
+
+tpmlp_status tpattn_set_qk(tpattn_ctx* c, const tpattn_qk_params* p, void* ws, size_t bytes) {
+  if (!c) return TPMLP_ERR_ARG;
+  if (!p) {
+    c->qk_on = false;
+    c->fwd_done = c->bwd_done = false;
+    return TPMLP_OK;
+  }
+  if (p->reserved != 0) return c->fail(TPMLP_ERR_ARG, "reserved must be 0");
+  if (const char* m = rotary_error(p->rot, c->cfg.head_dim)) return c->fail(TPMLP_ERR_SHAPE, m);
+  if (!p->q_norm_w != !p->k_norm_w) return c->fail(TPMLP_ERR_ARG, "norm weights of queries and keys, or neither");
+  const bool norm = p->q_norm_w != nullptr;
+  if (!(p->eps >= 0.0f) || !std::isfinite(p->eps)) return c->fail(TPMLP_ERR_ARG, "eps must be finite and >= 0");
+  if (norm && (!p->dq_norm_w || !p->dk_norm_w)) return c->fail(TPMLP_ERR_ARG, "norm weights need gradient tensors");
+  if (!p->master_q != !p->master_k) return c->fail(TPMLP_ERR_ARG, "set both masters or neither");
+  if (!p->m_q != !p->m_k || !p->m_q != !p->v_q || !p->m_q != !p->v_k)
+    return c->fail(TPMLP_ERR_ARG, "set all four moments or none");
+  for (const void* q : {(const void*)p->q_norm_w, (const void*)p->k_norm_w, (const void*)p->dq_norm_w,
+                        (const void*)p->dk_norm_w, (const void*)p->master_q, (const void*)p->master_k,
+                        (const void*)p->m_q, (const void*)p->m_k, (const void*)p->v_q, (const void*)p->v_k})
+    if (!a16(q)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
+  if (norm) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+      return c->fail(TPMLP_ERR_ARG, "workspace must be 256-byte aligned");
+    if (bytes < tpattn_qk_workspace_bytes(&c->cfg)) return c->fail(TPMLP_ERR_ARG, "workspace too small");
+  }
+  c->qk = *p;
+  c->qk.rot = nullptr;  // copied
+  c->qk_freqs = freqs_of(p->rot);
+  c->qk_ws = static_cast<uint8_t*>(ws);
+  c->qk_rows_off = 0;
+  c->qk_part_off = qk_rows_bytes(c->cfg);
+  c->qk_on = true;
+  c->fwd_done = c->bwd_done = false;
+  return TPMLP_OK;
+}
+
+static tpmlp_status attn_check_kv(tpattn_ctx* c, const tpkv_ctx* kv) {
+  if (!kv) return c->fail(TPMLP_ERR_ARG, "cache context is NULL");
+  if (kv->cfg.n_heads != c->cfg.n_heads || kv->cfg.n_kv_heads != c->cfg.n_kv_heads ||
+      kv->cfg.head_dim != c->cfg.head_dim)
+    return c->fail(TPMLP_ERR_SHAPE, "the cache's heads are not the sublayer's");
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != kv->device)
+    return c->fail(TPMLP_ERR_ARG, "the cache is not on the current device");
+  return TPMLP_OK;
+}
+
+tpmlp_status tpattn_append_kv(tpattn_ctx* c, tpkv_ctx* kv, const int32_t* new_lens, const int32_t* table,
+                              int64_t ld_table, int32_t max_pages) {
+  if (!c) return TPMLP_ERR_ARG;
+  ATTN_TRY(attn_check_kv(c, kv));
+  if (!c->fwd_done) return c->fail(TPMLP_ERR_ORDER, "append_kv before forward");
+  const tpattn_config& cf = c->cfg;
+  const int64_t rows = c->batch * c->seq, W = (int64_t)(cf.n_heads + 2 * cf.n_kv_heads) * cf.head_dim;
+  if (reinterpret_cast<uintptr_t>(new_lens) & 3u) return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
+  tpmlp_status s = kv_check_call(kv, c->batch, table, table, ld_table, max_pages);
+  if (s != TPMLP_OK) return c->fail(s, kv->err);
+  s = TPMLP_OK;
+  const tpmlp_status r = c->run(A_KV_APPEND, [&] {
+    s = kv_run_append(kv, rows, (int32_t)c->batch, c->wsp<void>(c->L.qkv), W, nullptr, new_lens, nullptr, table, ld_table,
+                      max_pages, QkTransform{}, nullptr, 0, c->stream);
+    return cudaSuccess;
+  });
+  return s != TPMLP_OK ? c->fail(s, kv->err) : r;
+}
+
+tpmlp_status tpattn_decode(tpattn_ctx* c, tpkv_ctx* kv, int32_t batch, const void* x, const void* norm_w,
+                           const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
+                           const int32_t* past_lens, const int32_t* table, int64_t ld_table, int32_t max_pages,
+                           int32_t window, int32_t sinks, void* y) {
+  if (!c) return TPMLP_ERR_ARG;
+  if (!c->ws) return c->fail(TPMLP_ERR_ORDER, "no workspace bound");
+  ATTN_TRY(attn_check_kv(c, kv));
+  const tpattn_config& cf = c->cfg;
+  if (batch < 1 || batch > cf.max_tokens) return c->fail(TPMLP_ERR_SHAPE, "batch must be within max_tokens");
+  if (t < 1 || t > cf.max_t || cf.n_kv_heads % t != 0) return c->fail(TPMLP_ERR_SHAPE, "t must divide n_kv_heads");
+  if (!x || !norm_w || !w_qkv || !w_o || !b_o || !y) return c->fail(TPMLP_ERR_ARG, "NULL tensor");
+  for (const void* p : {x, norm_w, w_qkv, w_o, b_o, (const void*)y})
+    if (!a16(p)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return c->fail(TPMLP_ERR_ARG, "eps must be finite and >= 0");
+  if (window < 0 || sinks < 0) return c->fail(TPMLP_ERR_ARG, "window and sinks must be >= 0");
+  tpmlp_status s = kv_check_call(kv, batch, past_lens, table, ld_table, max_pages);
+  if (s != TPMLP_OK) return c->fail(s, kv->err);
+  const int N = batch, H = (int)cf.hidden, d = cf.head_dim, nq = cf.n_heads, nkv = cf.n_kv_heads;
+  const int W = (nq + 2 * nkv) * d, Zc = nq * d;
+  c->fwd_done = c->bwd_done = false;  // the workspace of the last forward is overwritten
+  void* nrm = c->wsp<void>(c->L.nrm);
+  void* qkv = c->wsp<void>(c->L.qkv);
+  void* z = c->wsp<void>(c->L.z);
+  ATTN_TRY(c->run(A_RMSNORM_FWD, [&] {
+    return launch_rmsnorm_fwd(1, x, norm_w, eps, nrm, c->wsp<float>(c->L.rstd), N, H, c->stream);
+  }));
+  GemmDesc g;
+  g.M = N;
+  g.N = W;
+  g.k_extent = H;
+  g.a = nrm;
+  g.lda = H;
+  g.b = w_qkv;
+  g.ldb = H;
+  g.b_rows = W;
+  g.kseg[1] = H;
+  g.epi = EPI_STORE_BF16;
+  g.ep.out0 = qkv;
+  g.ep.ld_out0 = W;
+  ATTN_TRY(c->gemm(A_GEMM_QKV, g));
+  QkTransform tr;
+  if (c->qk_on) tr = {&c->qk_freqs, c->qk.q_norm_w, c->qk.k_norm_w, c->qk.eps};
+  tpmlp_status r = c->run(A_KV_APPEND, [&] {  // the queries in place
+    s = kv_run_append(kv, N, N, qkv, W, nullptr, nullptr, past_lens, table, ld_table, max_pages, tr, qkv, W, c->stream);
+    return cudaSuccess;
+  });
+  if (s != TPMLP_OK) return c->fail(s, kv->err);
+  ATTN_TRY(r);
+  r = c->run(A_KV_DECODE, [&] {
+    s = kv_run_decode(kv, N, qkv, W, past_lens, 1, table, ld_table, max_pages, 1.0f / std::sqrt((float)d), window, sinks, z,
+                      Zc, nullptr, c->stream);
+    return cudaSuccess;
+  });
+  if (s != TPMLP_OK) return c->fail(s, kv->err);
+  ATTN_TRY(r);
+  GemmDesc o;
+  o.M = N;
+  o.N = H;
+  o.k_extent = Zc;
+  o.a = z;
+  o.lda = Zc;
+  o.b = w_o;
+  o.ldb = Zc;
+  o.b_rows = H;
+  o.kseg[1] = Zc;
+  o.epi = EPI_DOWN_RESID;
+  o.ep.out0 = y;
+  o.ep.ld_out0 = H;
+  o.ep.in0 = x;
+  o.ep.ld_in0 = H;
+  o.ep.vec = b_o;
+  return c->gemm(A_GEMM_OUT, o);
 }
 
 tpmlp_status tpattn_sync(tpattn_ctx* c) {

@@ -9,6 +9,28 @@
 #include "../../include/tpmlp.h"
 #include "kv_ctx.h"
 
+namespace tpmlp {
+
+// Null if `r` is a rotation that heads of d values can take.
+const char* rotary_error(const tpattn_rotary* r, int d) {
+  if (!r) return nullptr;
+  if (r->rot_dim < 0 || r->rot_dim % 16 != 0 || r->rot_dim > d) return "rot_dim must be a multiple of 16 within head_dim";
+  if (r->interleaved != 0 && r->interleaved != 1) return "interleaved must be 0 or 1";
+  return nullptr;
+}
+
+RopeFreqs freqs_of(const tpattn_rotary* r) {
+  RopeFreqs f{};
+  if (r) {
+    f.rot = r->rot_dim;
+    f.interleaved = r->interleaved;
+    for (int i = 0; i < r->rot_dim / 2; ++i) f.turn[i] = r->turn[i];
+  }
+  return f;
+}
+
+}  // namespace tpmlp
+
 using namespace tpmlp;
 
 namespace {
@@ -46,14 +68,6 @@ tpmlp_status current_sms(int* sms) {
   return TPMLP_OK;
 }
 
-// Null if `r` is a rotation that heads of d values can take.
-const char* rotary_error(const tpattn_rotary* r, int d) {
-  if (!r) return nullptr;
-  if (r->rot_dim < 0 || r->rot_dim % 16 != 0 || r->rot_dim > d) return "rot_dim must be a multiple of 16 within head_dim";
-  if (r->interleaved != 0 && r->interleaved != 1) return "interleaved must be 0 or 1";
-  return nullptr;
-}
-
 // Checks of both directions of the row call.
 tpmlp_status check_desc(const tpattn_qk_desc* q, const tpattn_rotary* rot) {
   if (!q) return bad(TPMLP_ERR_ARG, "descriptor is NULL");
@@ -79,16 +93,6 @@ tpmlp_status check_rows(const char* what_null, const void* p, int64_t ld, int64_
   if (!p && !empty) return bad(TPMLP_ERR_ARG, what_null);
   if (!a16(p)) return bad(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
   return TPMLP_OK;
-}
-
-RopeFreqs freqs_of(const tpattn_rotary* r) {
-  RopeFreqs f{};
-  if (r) {
-    f.rot = r->rot_dim;
-    f.interleaved = r->interleaved;
-    for (int i = 0; i < r->rot_dim / 2; ++i) f.turn[i] = r->turn[i];
-  }
-  return f;
 }
 
 #define KV_TRY(expr)                \
@@ -372,8 +376,10 @@ tpmlp_status tpkv_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q
   if (rows == 0 || batch == 0) return TPMLP_OK;
   if (!qkv) return c->fail(TPMLP_ERR_ARG, "qkv is NULL");
   if (!a16(qkv) || !a16(q_out)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
-  return kv_run_append(c, rows, batch, qkv, ld_qkv, cu_rows, new_lens, past_lens, table, ld_table, max_pages,
-                       transform, q_out, ld_q, c->stream);
+  QkTransform tr;
+  if (transform) tr = {&c->freqs, c->q_norm_w, c->k_norm_w, c->eps};
+  return kv_run_append(c, rows, batch, qkv, ld_qkv, cu_rows, new_lens, past_lens, table, ld_table, max_pages, tr,
+                       q_out, ld_q, c->stream);
 }
 
 tpmlp_status tpkv_decode(tpkv_ctx* c, int32_t batch, const void* q, int64_t ld_q, const int32_t* lens, int32_t len_add,
@@ -438,8 +444,8 @@ tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, cons
 
 tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,
                            const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
-                           const int32_t* table, int64_t ld_table, int32_t max_pages, int32_t transform, void* q_out,
-                           int64_t ld_q, cudaStream_t st) {
+                           const int32_t* table, int64_t ld_table, int32_t max_pages, const QkTransform& tr,
+                           void* q_out, int64_t ld_q, cudaStream_t st) {
   const tpkv_config& cf = c->cfg;
   RopeArgs a{};
   a.in = qkv;
@@ -449,11 +455,9 @@ tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void*
   a.rows = rows;
   a.nq = cf.n_heads;
   a.nkv = cf.n_kv_heads;
-  if (transform) {
-    a.q_norm_w = c->q_norm_w;
-    a.k_norm_w = c->k_norm_w;
-    a.eps = c->eps;
-  }
+  a.q_norm_w = tr.q_norm_w;
+  a.k_norm_w = tr.k_norm_w;
+  a.eps = tr.eps;
   a.batch = batch;
   a.rows_per_seq = (int)(rows / batch);
   a.cu_rows = cu_rows;
@@ -474,7 +478,7 @@ tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void*
   a.status = c->status;
   OnDevice on(c->device);
   const cudaError_t e = launch_kv_append(cf.cache_dtype == TPKV_E4M3, cf.head_dim, a,
-                                         transform ? c->freqs : RopeFreqs{}, c->num_sms, st);
+                                         tr.freqs ? *tr.freqs : RopeFreqs{}, c->num_sms, st);
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
   ++c->launches;
   return TPMLP_OK;

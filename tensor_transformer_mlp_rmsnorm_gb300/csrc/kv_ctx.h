@@ -36,14 +36,23 @@ struct tpkv_ctx {
 
 namespace tpmlp {
 
+// What is done to queries and keys on the way (nothing by default).
+struct QkTransform {
+  const RopeFreqs* freqs = nullptr;
+  const void *q_norm_w = nullptr, *k_norm_w = nullptr;
+  float eps = 0.0f;
+};
+const char* rotary_error(const tpattn_rotary* r, int d);
+RopeFreqs freqs_of(const tpattn_rotary* r);
+
 // Checks that every cache call makes; the caller has checked its own tensors
-// before the two launches below.
+// before the two launches below.  past_lens null: all 0.
 tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, const int32_t* table, int64_t ld_table,
                            int32_t max_pages);
 tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,
                            const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
-                           const int32_t* table, int64_t ld_table, int32_t max_pages, int32_t transform, void* q_out,
-                           int64_t ld_q, cudaStream_t st);
+                           const int32_t* table, int64_t ld_table, int32_t max_pages, const QkTransform& tr,
+                           void* q_out, int64_t ld_q, cudaStream_t st);
 tpmlp_status kv_run_decode(tpkv_ctx* c, int32_t batch, const void* q, int64_t ld_q, const int32_t* lens,
                            int32_t len_add, const int32_t* table, int64_t ld_table, int32_t max_pages, float scale,
                            int32_t window, int32_t sinks, void* out, int64_t ld_out, float* lse, cudaStream_t st);

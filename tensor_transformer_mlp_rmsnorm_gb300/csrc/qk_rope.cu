@@ -214,23 +214,16 @@ __device__ __forceinline__ void load_turns(const RopeFreqs& fr, uint64_t* turn) 
   }
 }
 
-// Eight angles of unit u (identity where the unit lies behind the rotated part).
-__device__ __forceinline__ void unit_angles(const float2* cs_warp, int u, int rot, float sign, float* cs, float* sn) {
-  if (u < rot / 16) {
+// The eight angles of unit u, which lies in the rotated part; sign -1 for the
+// inverse rotation.
+__device__ __forceinline__ void unit_angles(const float2* cs_warp, int u, float sign, float* cs, float* sn) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 t = reinterpret_cast<const float4*>(cs_warp)[4 * u + i];
-      cs[2 * i] = t.x;
-      sn[2 * i] = sign * t.y;
-      cs[2 * i + 1] = t.z;
-      sn[2 * i + 1] = sign * t.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = 1.0f;
-      sn[i] = 0.0f;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float4 t = reinterpret_cast<const float4*>(cs_warp)[4 * u + i];
+    cs[2 * i] = t.x;
+    sn[2 * i] = sign * t.y;
+    cs[2 * i + 1] = t.z;
+    sn[2 * i + 1] = sign * t.w;
   }
 }
 
@@ -265,7 +258,7 @@ __device__ __forceinline__ int append_place(const RopeArgs& a, int64_t row, int6
     at = (int)row - b * a.rows_per_seq;
     if (a.new_lens && at >= a.new_lens[b]) return 0;
   }
-  const int past = a.past_lens[b];
+  const int past = a.past_lens ? a.past_lens[b] : 0;
   if (past < 0) return 0;  // an inactive sequence
   const uint32_t p = (uint32_t)past + (uint32_t)at;
   const uint32_t pi = p / (uint32_t)a.page_size;
@@ -292,6 +285,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
   const bool active = u < HL::UNITS;
   const bool il = fr.interleaved != 0, norm = a.q_norm_w != nullptr || a.k_norm_w != nullptr;
   const int rot = fr.rot;
+  const bool turns = u < rot / 16;  // the others pass, whatever lies beside them
   int oa, ob;
   unit_offsets(active ? u : 0, rot, il, oa, ob);
   uint64_t turn[D / 64];
@@ -335,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
                            : a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
       if (slot_off >= 0) {
         if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
-        unit_angles(s_cs[warp], u, rot, 1.0f, cs, sn);
+        if (turns) unit_angles(s_cs[warp], u, 1.0f, cs, sn);
       }
     }
     cp_wait<S - 1>();
@@ -376,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
       }
     }
     if (!work) continue;
-    if (!is_v) rotate16(fa, fb, cs, sn, il);
+    if (!is_v && turns) rotate16(fa, fb, cs, sn, il);
     if (KIND == 0 || is_q) {
       if (KIND == 0 && a.save) {  // the values before the norm, for the backward pass
         T* sv = static_cast<T*>(a.save) + st.row * a.ld_save + (int64_t)h * D;
@@ -433,6 +427,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
   const bool active = u < HL::UNITS;
   const bool il = fr.interleaved != 0;
   const int rot = fr.rot;
+  const bool turns = u < rot / 16;  // the others pass, whatever lies beside them
   int oa, ob;
   unit_offsets(active ? u : 0, rot, il, oa, ob);
   uint64_t turn[D / 64];
@@ -483,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
         cur_it = st.it;
         const int pos = a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
         if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
-        unit_angles(s_cs[warp], u, rot, -1.0f, cs, sn);
+        if (turns) unit_angles(s_cs[warp], u, -1.0f, cs, sn);
       }
       cp_wait<S - 1>();
       const int h = st.h + group;
@@ -500,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
       }
       ra.get(fa);
       rb.get(fb);
-      rotate16(fa, fb, cs, sn, il);
+      if (turns) rotate16(fa, fb, cs, sn, il);
       if (w) {
         float va[8], vb[8], wa[8], wb[8];
         ra.set(z);

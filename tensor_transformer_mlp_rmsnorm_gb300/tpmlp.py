@@ -85,6 +85,13 @@ class QkDesc(ctypes.Structure):
                 ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class QkParams(ctypes.Structure):
+    """tpattn_qk_params."""
+    _fields_ = [("rot", ctypes.POINTER(RotarySpec))] + [
+        (n, ctypes.c_void_p) for n in ("q_norm_w", "k_norm_w", "dq_norm_w", "dk_norm_w", "master_q", "master_k", "m_q",
+                                       "m_k", "v_q", "v_k")] + [("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 class KvConfig(ctypes.Structure):
     """tpkv_config."""
     _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("max_batch", ctypes.c_int32),
@@ -149,6 +156,10 @@ _SIGNATURES = {
     "tpattn_qk_rope_workspace_bytes": (ctypes.c_size_t, [_i32]),
     "tpattn_qk_rope_backward": (_i32, [ctypes.POINTER(QkDesc), ctypes.POINTER(RotarySpec), _vp, _i64, _vp, _i64, _vp,
                                        _i64, _fp, _fp, _vp, ctypes.c_size_t, _vp]),
+    "tpattn_qk_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AttnConfig)]),
+    "tpattn_set_qk": (_i32, [_vp, ctypes.POINTER(QkParams), _vp, ctypes.c_size_t]),
+    "tpattn_append_kv": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32]),
+    "tpattn_decode": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp]),
     "tpkv_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvConfig)]),
     "tpkv_create": (_i32, [ctypes.POINTER(KvConfig), _vp, ctypes.POINTER(_vp)]),
     "tpkv_bind_workspace": (_i32, [_vp, _vp, ctypes.c_size_t]),
@@ -543,6 +554,7 @@ class TPAttn:
         self._fwd_tensors = (x, norm_w, w_qkv, w_o, b_o)
         self.params = (norm_w, w_qkv, w_o, b_o)
         self.tokens = n
+        self._batch = batch
         return y
 
     def new_grads(self):
@@ -623,6 +635,59 @@ class TPAttn:
         _acheck(lib().tpattn_adamw_step(self.ctx, ctypes.byref(hp),
                                         self._t(grad_norm, (1,), torch.float32, "grad_norm")), self.ctx)
         return grad_norm
+
+    def set_qk(self, rotary: Rotary | None = None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6, masters=None,
+               moments=None):
+        """Rotate queries and keys by position (row % seq) in later forwards and decodes, after the RMS norm of each
+        head where bf16 weights are given (tpattn_set_qk).  masters: fp32 (q, k); moments: fp32 AdamW (m_q, m_k, v_q,
+        v_k).  Returns the weights' gradient tensors {"q_norm_w", "k_norm_w"} that backward fills (empty without)."""
+        d, i = self.d, self.device.index
+        p = QkParams()
+        p.rot = ctypes.pointer(rotary.spec) if rotary is not None else None
+        p.q_norm_w, p.k_norm_w = _vec(q_norm_w, d, _BF, "q_norm_w", i), _vec(k_norm_w, d, _BF, "k_norm_w", i)
+        norm = q_norm_w is not None
+        grads = {k: torch.zeros(d, dtype=_F32T, device=self.device) for k in ("q_norm_w", "k_norm_w")} if norm else {}
+        if norm:
+            p.dq_norm_w, p.dk_norm_w = grads["q_norm_w"].data_ptr(), grads["k_norm_w"].data_ptr()
+        for names, given in ((("master_q", "master_k"), masters), (("m_q", "m_k", "v_q", "v_k"), moments)):
+            for name, t in zip(names, given or ()):
+                setattr(p, name, _vec(t, d, _F32T, name, i))
+        p.eps = float(eps)
+        nbytes = int(lib().tpattn_qk_workspace_bytes(ctypes.byref(self.cfg))) if norm else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if norm else None
+        _acheck(lib().tpattn_set_qk(self.ctx, ctypes.byref(p), _ptr(ws), nbytes), self.ctx)
+        self._qk = (rotary, q_norm_w, k_norm_w, masters, moments, grads, ws)  # the context keeps their pointers
+        return grads
+
+    def clear_qk(self):
+        """Later forwards and decodes neither rotate nor norm."""
+        _acheck(lib().tpattn_set_qk(self.ctx, None, None, 0), self.ctx)
+        self._qk = None
+
+    def append_kv(self, kv: TPKV, block_table, new_lens=None):
+        """Store the last forward's keys and values in a cache, the first new_lens[b] of each sequence (or all)."""
+        batch = block_table.shape[0]
+        if self.tokens is not None and (batch < 1 or self.tokens % batch or batch != self._batch):
+            raise TPMLPError(ERR_SHAPE, "block_table needs a row for each sequence of the last forward")
+        tp, ldt, pages = kv._table(block_table, batch)
+        _acheck(lib().tpattn_append_kv(self.ctx, kv.ctx, _vec(new_lens, batch, _I32T, "new_lens", self.device.index),
+                                       tp, ldt, pages), self.ctx)
+
+    def decode(self, kv: TPKV, x, norm_w, w_qkv, w_o, b_o, eps: float, t: int, past_lens, block_table, window: int = 0,
+               sinks: int = 0, y=None):
+        """The sublayer for one new token per sequence, appended to the cache at position past_lens[b]
+        (tpattn_decode); returns y [batch, H]."""
+        n = x.shape[0]
+        y = torch.empty_like(x) if y is None else y
+        tp, ldt, pages = kv._table(block_table, n)
+        _acheck(lib().tpattn_decode(self.ctx, kv.ctx, n, self._t(x, (n, self.H), name="x"),
+                                    self._t(norm_w, (self.H,), name="norm_w"),
+                                    self._t(w_qkv, (self.W, self.H), name="w_qkv"),
+                                    self._t(w_o, (self.H, self.nq * self.d), name="w_o"),
+                                    self._t(b_o, (self.H,), name="b_o"), float(eps), int(t),
+                                    _vec(past_lens, n, _I32T, "past_lens", self.device.index), tp, ldt, pages, window,
+                                    sinks, self._t(y, (n, self.H), name="y")), self.ctx)
+        return y
 
     def sync(self):
         _acheck(lib().tpattn_sync(self.ctx), self.ctx)
