@@ -43,7 +43,8 @@ template <typename T>
 struct Ahead {
   static constexpr int CHUNK = 8 * sizeof(T) / 16;              // 16-byte pieces of 8 values
   static constexpr int ROWS = sizeof(T) == 2 ? 8 : 4;           // forward and append: 2 chunks a step
-  static constexpr int BWD = sizeof(T) == 2 ? 6 : 3;            // backward: 4 chunks a step
+  // backward: 4 chunks a step; heads of 256 values leave room for one step less
+  static constexpr __host__ __device__ int bwd(int d) { return (sizeof(T) == 2 ? 6 : 3) - (d == 256 ? 1 : 0); }
 };
 constexpr int ROWS_BLOCKS = 3, BWD_BLOCKS = 2;
 
@@ -63,6 +64,7 @@ struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 v;
+  __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ void get(float* f) const { Vec<__nv_bfloat16>::load(reinterpret_cast<const __nv_bfloat16*>(&v), f); }
@@ -71,6 +73,7 @@ struct Raw8<__nv_bfloat16> {
 template <>
 struct Raw8<float> {
   float4 a, b;
+  __device__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
   __device__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -103,30 +106,44 @@ __device__ __forceinline__ void queue_get(const uint4* slot, int c, Raw8<float>&
   r.b = *reinterpret_cast<const float4*>(slot + (2 * c + 1) * 32);
 }
 
-// A warp's walk over (row, heads): rows of its items in turn, in each the
-// heads group, group + step, ... of [begin, end).
-struct Steps {
-  int64_t it, items, stride;
-  int splits, begin, end, step, groups;
-  int64_t row;
-  int h;  // the first lane group's head
-  __device__ __forceinline__ void enter() {
-    while (it < items) {
-      row = splits == 1 ? it : it / splits;
-      h = begin + (splits == 1 ? 0 : (int)(it - row * splits) * groups);
-      if (h < end) return;
-      it += stride;
+// A warp's items are (row, share of its heads).  `left` steps remain of the
+// current row, `h` is this lane's head: all row arithmetic happens once a row.
+struct Walk {
+  int64_t it, row;
+  int left, h;
+};
+struct Items {
+  int64_t count, stride;
+  int splits, begin, end, step, groups, group;
+  // Moves `w` to its item w.it or the first behind it that has heads; false at the end.
+  __device__ __forceinline__ bool enter(Walk& w) const {
+    for (; w.it < count; w.it += stride) {
+      w.row = splits == 1 ? w.it : w.it / splits;
+      const int h = begin + (splits == 1 ? 0 : (int)(w.it - w.row * splits) * groups);
+      if (h < end) {
+        w.left = (end - h + step - 1) / step;
+        w.h = h + group;
+        return true;
+      }
     }
-  }
-  __device__ __forceinline__ bool more() const { return it < items; }
-  __device__ __forceinline__ void next() {
-    h += step;
-    if (h >= end) {
-      it += stride;
-      enter();
-    }
+    w.left = 0;
+    return false;
   }
 };
+
+// The norm weights of queries and keys as floats in shared memory.
+template <typename T, int D>
+__device__ __forceinline__ void stage_weights(float (&s_w)[2][D], const void* qw, const void* kw) {
+  for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
+    const T* w = static_cast<const T*>(i < D ? qw : kw);
+    (&s_w[0][0])[i] = w ? (float)w[i < D ? i : i - D] : 1.0f;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void load8(const float* p, float* f) {
+  Vec<float>::load(p, f);
+  Vec<float>::load(p + 4, f + 4);
+}
 
 // E4M3 code of v: round to nearest even, saturated to +-448 (NaN stays NaN).
 __device__ __forceinline__ uint2 e4m3x8(const float* f) {
@@ -285,128 +302,138 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
   const bool active = u < HL::UNITS;
   const bool il = fr.interleaved != 0, norm = a.q_norm_w != nullptr || a.k_norm_w != nullptr;
   const int rot = fr.rot;
-  const bool turns = u < rot / 16;  // the others pass, whatever lies beside them
+  // lanes behind the rotated part pass their values, whatever lies beside them;
+  // `whole` spares the warp the question where there are none (6% of the forward)
+  const bool turns = u < rot / 16, whole = HL::UNITS == HL::LANES && rot == D;
   int oa, ob;
   unit_offsets(active ? u : 0, rot, il, oa, ob);
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
-  uint4* queue = s_queue + warp * S * STEP + lane;
+  uint4* const queue = s_queue + warp * S * STEP + lane;
+  __shared__ __align__(16) float s_w[2][D];
 
-  Steps ld;  // the step to load next
+  Items items;
+  items.count = a.rows * a.splits;
+  items.stride = (int64_t)gridDim.x * WARPS;
+  items.splits = a.splits;
+  items.begin = KIND && !a.out ? a.nq : 0;  // an append without a query output skips the queries
+  items.end = a.nq + a.nkv + (KIND ? a.nkv : 0);
+  items.groups = HL::GROUPS;
+  items.group = group;
+  items.step = a.splits * HL::GROUPS;
+  const int end = active ? items.end : 0;  // lanes without a unit never have work
+  Walk ld, st;
   ld.it = (int64_t)blockIdx.x * WARPS + warp;
-  ld.items = a.rows * a.splits;
-  ld.stride = (int64_t)gridDim.x * WARPS;
-  ld.splits = a.splits;
-  ld.begin = KIND && !a.out ? a.nq : 0;  // an append without a query output skips the queries
-  ld.end = a.nq + a.nkv + (KIND ? a.nkv : 0);
-  ld.groups = HL::GROUPS;
-  ld.step = a.splits * HL::GROUPS;
-  ld.enter();
-  Steps st = ld;  // the step to work on
-  auto load = [&](int slot) {
-    if (ld.more()) {
-      const int h = ld.h + group;
-      if (active && h < ld.end) {
-        const T* in = static_cast<const T*>(a.in) + ld.row * a.ld_in + (int64_t)h * D;
-        queue_load<T>(queue + slot * STEP, 0, in + oa);
-        queue_load<T>(queue + slot * STEP, 1, in + ob);
+  bool more = items.enter(ld);
+  st = ld;
+  const T* src = static_cast<const T*>(a.in) + ld.row * a.ld_in;
+  auto load = [&](uint4* slot) {
+    if (ld.left > 0) {
+      if (ld.h < end) {
+        queue_load<T>(slot, 0, src + (ld.h * D + oa));
+        queue_load<T>(slot, 1, src + (ld.h * D + ob));
       }
-      ld.next();
+      ld.h += items.step;
+      if (--ld.left == 0) {
+        ld.it += items.stride;
+        if (items.enter(ld)) src = static_cast<const T*>(a.in) + ld.row * a.ld_in;
+      }
     }
     cp_commit();
   };
+  if (more) {
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) load(i);
-  int slot = 0;
-  int64_t cur_it = -1, slot_off = 0;
+    for (int i = 0; i < S - 1; ++i) load(queue + i * STEP);
+  }
+  if (norm) stage_weights<T, D>(s_w, a.q_norm_w, a.k_norm_w);  // behind the first loads
+  uint4 *slot = queue, *fill = queue + (S - 1) * STEP;
   float cs[8], sn[8];
-  for (; st.more(); st.next(), slot = slot + 1 == S ? 0 : slot + 1) {
-    load(slot == 0 ? S - 1 : slot - 1);
-    if (st.it != cur_it) {  // a new row
-      cur_it = st.it;
-      slot_off = 0;
-      const int pos = KIND ? append_place(a, st.row, slot_off)
-                           : a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
-      if (slot_off >= 0) {
-        if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
-        if (turns) unit_angles(s_cs[warp], u, 1.0f, cs, sn);
+  while (more) {
+    // ---- a row
+    int64_t slot_off = 0;
+    const int pos =
+        KIND ? append_place(a, st.row, slot_off) : a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
+    if (slot_off >= 0) {
+      if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
+      if (turns) unit_angles(s_cs[warp], u, 1.0f, cs, sn);
+    }
+    T* const out = static_cast<T*>(a.out) + st.row * a.ld_out;
+    for (; st.left > 0; --st.left, st.h += items.step) {
+      load(fill);
+      cp_wait<S - 1>();
+      const uint4* now = slot;
+      fill = slot;
+      slot = slot == queue + (S - 1) * STEP ? queue : slot + STEP;
+      if (KIND && slot_off < 0) continue;  // a row that is nobody's
+      const int h = st.h;
+      const bool work = h < end;
+      const bool is_q = h < a.nq, is_v = KIND && h >= a.nq + a.nkv;
+      Raw8<T> xa, xb;
+      float fa[8], fb[8];
+      xa.zero();
+      xb.zero();
+      if (work) {
+        queue_get(now, 0, xa);
+        queue_get(now, 1, xb);
       }
-    }
-    cp_wait<S - 1>();
-    if (KIND && slot_off < 0) continue;  // a row that is nobody's
-    const int h = st.h + group;
-    const bool work = active && h < st.end;
-    const bool is_q = h < a.nq, is_v = KIND && h >= a.nq + a.nkv;
-    Raw8<T> xa, xb;
-    float fa[8], fb[8];
-    if (work) {
-      queue_get(queue + slot * STEP, 0, xa);
-      queue_get(queue + slot * STEP, 1, xb);
-    } else {
-      const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      xa.set(z);
-      xb.set(z);
-    }
-    xa.get(fa);
-    xb.get(fb);
-    if (norm) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], ss));
-      ss = HL::sum(ss);
-      const T* w = static_cast<const T*>(is_q ? a.q_norm_w : a.k_norm_w);
-      if (work && !is_v && w) {
-        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-        Raw8<T> wr;
-        float wf[8];
-        wr.load(w + oa);
-        wr.get(wf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fa[i] *= r * wf[i];
-        wr.load(w + ob);
-        wr.get(wf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fb[i] *= r * wf[i];
-      }
-    }
-    if (!work) continue;
-    if (!is_v && turns) rotate16(fa, fb, cs, sn, il);
-    if (KIND == 0 || is_q) {
-      if (KIND == 0 && a.save) {  // the values before the norm, for the backward pass
-        T* sv = static_cast<T*>(a.save) + st.row * a.ld_save + (int64_t)h * D;
+      if (KIND == 0 && a.save && work) {  // the values before the norm, for the backward pass
+        T* sv = static_cast<T*>(a.save) + st.row * a.ld_save + h * D;
         xa.store(sv + oa);
         xb.store(sv + ob);
       }
-      T* out = static_cast<T*>(a.out) + st.row * a.ld_out + (int64_t)h * D;
-      xa.set(fa);
-      xb.set(fb);
-      xa.store(out + oa);
-      xb.store(out + ob);
-    } else {
-      const int g = is_v ? h - a.nq - a.nkv : h - a.nq;
-      const int64_t off = slot_off + g * a.stride_head;
-      if (KIND == 1) {
-        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + off;
-        Raw8<__nv_bfloat16> t;
-        t.set(fa);
-        t.store(c + oa);
-        t.set(fb);
-        t.store(c + ob);
-      } else {
-        uint8_t* c = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + off;
-        const float* isc = is_v ? a.v_inv_scale : a.k_inv_scale;
-        if (isc) {
-          const float sc = isc[g];
+      xa.get(fa);
+      xb.get(fb);
+      if (norm) {
+        float ss = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            fa[i] = __fdiv_rn(fa[i], sc);
-            fb[i] = __fdiv_rn(fb[i], sc);
-          }
+        for (int i = 0; i < 8; ++i) ss = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], ss));
+        ss = HL::sum(ss);
+        if (is_q ? a.q_norm_w != nullptr : !is_v && a.k_norm_w != nullptr) {
+          const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+          float wf[8];
+          load8(&s_w[is_q ? 0 : 1][oa], wf);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fa[i] *= r * wf[i];
+          load8(&s_w[is_q ? 0 : 1][ob], wf);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fb[i] *= r * wf[i];
         }
-        *reinterpret_cast<uint2*>(c + oa) = e4m3x8(fa);
-        *reinterpret_cast<uint2*>(c + ob) = e4m3x8(fb);
+      }
+      if (!work) continue;
+      if (!is_v && (whole || turns)) rotate16(fa, fb, cs, sn, il);
+      if (KIND == 0 || is_q) {
+        xa.set(fa);
+        xb.set(fb);
+        xa.store(out + (h * D + oa));
+        xb.store(out + (h * D + ob));
+      } else {
+        const int g = is_v ? h - a.nq - a.nkv : h - a.nq;
+        const int64_t off = slot_off + g * a.stride_head;
+        if (KIND == 1) {
+          __nv_bfloat16* c = static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + off;
+          Raw8<__nv_bfloat16> t;
+          t.set(fa);
+          t.store(c + oa);
+          t.set(fb);
+          t.store(c + ob);
+        } else {
+          uint8_t* c = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + off;
+          const float* isc = is_v ? a.v_inv_scale : a.k_inv_scale;
+          if (isc) {
+            const float sc = isc[g];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              fa[i] = __fdiv_rn(fa[i], sc);
+              fb[i] = __fdiv_rn(fb[i], sc);
+            }
+          }
+          *reinterpret_cast<uint2*>(c + oa) = e4m3x8(fa);
+          *reinterpret_cast<uint2*>(c + ob) = e4m3x8(fb);
+        }
       }
     }
+    st.it += items.stride;
+    more = items.enter(st);
   }
   cp_wait<0>();
 }
@@ -418,7 +445,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a,
                                                                        const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
-  constexpr int S = Ahead<T>::BWD, STEP = 4 * Ahead<T>::CHUNK * 32;
+  constexpr int S = Ahead<T>::bwd(D), STEP = 4 * Ahead<T>::CHUNK * 32;
   extern __shared__ __align__(16) uint4 s_queue[];
   __shared__ __align__(16) float2 s_cs[WARPS][D / 2];
   __shared__ float s_dw[WARPS][D];
@@ -427,113 +454,133 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
   const bool active = u < HL::UNITS;
   const bool il = fr.interleaved != 0;
   const int rot = fr.rot;
-  const bool turns = u < rot / 16;  // the others pass, whatever lies beside them
+  // lanes behind the rotated part pass their values, whatever lies beside them;
+  // `whole` spares the warp the question where there are none (6% of the forward)
+  const bool turns = u < rot / 16, whole = HL::UNITS == HL::LANES && rot == D;
   int oa, ob;
   unit_offsets(active ? u : 0, rot, il, oa, ob);
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
-  uint4* queue = s_queue + warp * S * STEP + lane;
+  uint4* const queue = s_queue + warp * S * STEP + lane;
+  __shared__ __align__(16) float s_w[2][D];
+  if (a.q_norm_w || a.k_norm_w) stage_weights<T, D>(s_w, a.q_norm_w, a.k_norm_w);
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
     const T* w = static_cast<const T*>(part ? a.k_norm_w : a.q_norm_w);
     float acc[16], cs[8], sn[8];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    Steps ld;  // the step to load next
+    Items items;
+    items.count = a.rows * a.splits;
+    items.stride = (int64_t)gridDim.x * WARPS;
+    items.splits = a.splits;
+    items.begin = part ? a.nq : 0;
+    items.end = part ? a.nq + a.nkv : a.nq;
+    items.groups = HL::GROUPS;
+    items.group = group;
+    items.step = a.splits * HL::GROUPS;
+    const int end = active ? items.end : 0;  // lanes without a unit never have work
+    Walk ld, st;
     ld.it = (int64_t)blockIdx.x * WARPS + warp;
-    ld.items = a.rows * a.splits;
-    ld.stride = (int64_t)gridDim.x * WARPS;
-    ld.splits = a.splits;
-    ld.begin = part ? a.nq : 0;
-    ld.end = part ? a.nq + a.nkv : a.nq;
-    ld.groups = HL::GROUPS;
-    ld.step = a.splits * HL::GROUPS;
-    ld.enter();
-    Steps st = ld;  // the step to work on
-    auto load = [&](int slot) {
-      if (ld.more()) {
-        const int h = ld.h + group;
-        if (active && h < ld.end) {
-          const T* g = static_cast<const T*>(a.dout) + ld.row * a.ld_dout + (int64_t)h * D;
-          uint4* q = queue + slot * STEP;
-          queue_load<T>(q, 0, g + oa);
-          queue_load<T>(q, 1, g + ob);
+    bool more = items.enter(ld);
+    st = ld;
+    const T *src = nullptr, *srx = nullptr;
+    auto aim = [&] {
+      src = static_cast<const T*>(a.dout) + ld.row * a.ld_dout;
+      srx = static_cast<const T*>(a.x) + ld.row * a.ld_x;
+    };
+    auto load = [&](uint4* slot) {
+      if (ld.left > 0) {
+        if (ld.h < end) {
+          const int ha = ld.h * D + oa, hb = ld.h * D + ob;
+          queue_load<T>(slot, 0, src + ha);
+          queue_load<T>(slot, 1, src + hb);
           if (w) {
-            const T* x = static_cast<const T*>(a.x) + ld.row * a.ld_x + (int64_t)h * D;
-            queue_load<T>(q, 2, x + oa);
-            queue_load<T>(q, 3, x + ob);
+            queue_load<T>(slot, 2, srx + ha);
+            queue_load<T>(slot, 3, srx + hb);
           }
         }
-        ld.next();
+        ld.h += items.step;
+        if (--ld.left == 0) {
+          ld.it += items.stride;
+          if (items.enter(ld)) aim();
+        }
       }
       cp_commit();
     };
+    if (more) {
+      aim();
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) load(i);
-    int slot = 0;
-    int64_t cur_it = -1;
-    for (; st.more(); st.next(), slot = slot + 1 == S ? 0 : slot + 1) {
-      load(slot == 0 ? S - 1 : slot - 1);
-      if (st.it != cur_it) {  // a new row
-        cur_it = st.it;
-        const int pos = a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
-        if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
-        if (turns) unit_angles(s_cs[warp], u, -1.0f, cs, sn);
-      }
-      cp_wait<S - 1>();
-      const int h = st.h + group;
-      const bool work = active && h < st.end;
-      const uint4* q = queue + slot * STEP;
-      const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      Raw8<T> ra, rb;
-      float fa[8], fb[8];
-      ra.set(z);
-      rb.set(z);
-      if (work) {
-        queue_get(q, 0, ra);
-        queue_get(q, 1, rb);
-      }
-      ra.get(fa);
-      rb.get(fb);
-      if (turns) rotate16(fa, fb, cs, sn, il);
-      if (w) {
-        float va[8], vb[8], wa[8], wb[8];
-        ra.set(z);
-        rb.set(z);
+      for (int i = 0; i < S - 1; ++i) load(queue + i * STEP);
+    }
+    uint4 *slot = queue, *fill = queue + (S - 1) * STEP;
+    while (more) {
+      // ---- a row
+      const int pos = a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
+      if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
+      if (turns) unit_angles(s_cs[warp], u, -1.0f, cs, sn);
+      T* const dx = static_cast<T*>(a.dx) + st.row * a.ld_dx;
+      for (; st.left > 0; --st.left, st.h += items.step) {
+        load(fill);
+        cp_wait<S - 1>();
+        const uint4* q = slot;
+        fill = slot;
+        slot = slot == queue + (S - 1) * STEP ? queue : slot + STEP;
+        const int h = st.h;
+        const bool work = h < end;
+        Raw8<T> ra, rb;
+        float fa[8], fb[8];
+        ra.zero();
+        rb.zero();
         if (work) {
-          queue_get(q, 2, ra);
-          queue_get(q, 3, rb);
+          queue_get(q, 0, ra);
+          queue_get(q, 1, rb);
         }
-        ra.get(va);
-        rb.get(vb);
-        ra.load(w + oa);
-        ra.get(wa);
-        rb.load(w + ob);
-        rb.get(wb);
-        // both sums at once: sum x^2 and sum w g x = mean(w g xh) d / r
-        float ss = 0.0f, dot = 0.0f;
+        ra.get(fa);
+        rb.get(fb);
+        if (whole || turns) rotate16(fa, fb, cs, sn, il);
+        if (w) {
+          float va[8], vb[8], wa[8], wb[8];
+          ra.zero();
+          rb.zero();
+          if (work) {
+            queue_get(q, 2, ra);
+            queue_get(q, 3, rb);
+          }
+          ra.get(va);
+          rb.get(vb);
+          load8(&s_w[part][oa], wa);
+          load8(&s_w[part][ob], wb);
+          // both sums at once: sum x^2 and sum w g x = mean(w g xh) d / r
+          float ss = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
-          dot = fmaf(wa[i] * fa[i], va[i], fmaf(wb[i] * fb[i], vb[i], dot));
-        }
-        HL::sum2(ss, dot);
-        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-        const float c = dot * (1.0f / D) * r * r * r;
+          for (int i = 0; i < 8; ++i) {
+            wa[i] *= fa[i];  // w g
+            wb[i] *= fb[i];
+            ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
+            dot = fmaf(wa[i], va[i], fmaf(wb[i], vb[i], dot));
+          }
+          HL::sum2(ss, dot);
+          const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+          const float c = -dot * (1.0f / D) * r * r;  // dx = r w g + c xh
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc[i] = fmaf(fa[i], va[i] * r, acc[i]);
-          acc[8 + i] = fmaf(fb[i], vb[i] * r, acc[8 + i]);
-          fa[i] = fmaf(r * wa[i], fa[i], -c * va[i]);
-          fb[i] = fmaf(r * wb[i], fb[i], -c * vb[i]);
+          for (int i = 0; i < 8; ++i) {
+            va[i] *= r;  // xh
+            vb[i] *= r;
+            acc[i] = fmaf(fa[i], va[i], acc[i]);
+            acc[8 + i] = fmaf(fb[i], vb[i], acc[8 + i]);
+            fa[i] = fmaf(r, wa[i], c * va[i]);
+            fb[i] = fmaf(r, wb[i], c * vb[i]);
+          }
         }
+        if (!work) continue;
+        ra.set(fa);
+        rb.set(fb);
+        ra.store(dx + (h * D + oa));
+        rb.store(dx + (h * D + ob));
       }
-      if (!work) continue;
-      T* dx = static_cast<T*>(a.dx) + st.row * a.ld_dx + (int64_t)h * D;
-      ra.set(fa);
-      rb.set(fb);
-      ra.store(dx + oa);
-      rb.store(dx + ob);
+      st.it += items.stride;
+      more = items.enter(st);
     }
     cp_wait<0>();
     if (!a.part) continue;
@@ -585,8 +632,8 @@ int head_splits(int64_t rows, int heads, int groups, int num_sms) {
 
 template <typename T>
 constexpr int ROWS_QUEUE = WARPS * Ahead<T>::ROWS * 2 * Ahead<T>::CHUNK * 32 * 16;
-template <typename T>
-constexpr int BWD_QUEUE = WARPS * Ahead<T>::BWD * 4 * Ahead<T>::CHUNK * 32 * 16;
+template <typename T, int D>
+constexpr int BWD_QUEUE = WARPS * Ahead<T>::bwd(D) * 4 * Ahead<T>::CHUNK * 32 * 16;
 
 template <auto K, typename A>
 cudaError_t launch_kernel(int64_t blocks, int queue, cudaStream_t st, const A& a, const RopeFreqs& fr) {
@@ -623,10 +670,10 @@ cudaError_t launch_bwd(RopeBwdArgs a, const RopeFreqs& fr, int d, int num_sms, c
   if (blocks > ROPE_MAX_PARTS) blocks = ROPE_MAX_PARTS;
   *blocks_out = (int)blocks;
   switch (d) {
-    case 64: return launch_kernel<rope_bwd_kernel<T, 64>>(blocks, BWD_QUEUE<T>, st, a, fr);
-    case 128: return launch_kernel<rope_bwd_kernel<T, 128>>(blocks, BWD_QUEUE<T>, st, a, fr);
-    case 192: return launch_kernel<rope_bwd_kernel<T, 192>>(blocks, BWD_QUEUE<T>, st, a, fr);
-    case 256: return launch_kernel<rope_bwd_kernel<T, 256>>(blocks, BWD_QUEUE<T>, st, a, fr);
+    case 64: return launch_kernel<rope_bwd_kernel<T, 64>>(blocks, BWD_QUEUE<T, 64>, st, a, fr);
+    case 128: return launch_kernel<rope_bwd_kernel<T, 128>>(blocks, BWD_QUEUE<T, 128>, st, a, fr);
+    case 192: return launch_kernel<rope_bwd_kernel<T, 192>>(blocks, BWD_QUEUE<T, 192>, st, a, fr);
+    case 256: return launch_kernel<rope_bwd_kernel<T, 256>>(blocks, BWD_QUEUE<T, 256>, st, a, fr);
     default: return cudaErrorInvalidValue;
   }
 }
