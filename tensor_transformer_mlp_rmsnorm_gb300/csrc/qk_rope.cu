@@ -46,7 +46,9 @@ struct Ahead {
   // backward: 4 chunks a step; heads of 256 values leave room for one step less
   static constexpr __host__ __device__ int bwd(int d) { return (sizeof(T) == 2 ? 6 : 3) - (d == 256 ? 1 : 0); }
 };
-constexpr int ROWS_BLOCKS = 3, BWD_BLOCKS = 2;
+// (rows to rows: two blocks of 128 registers a thread are 8% faster than three
+// of 80, the append 2% slower: it has more latency to hide behind other warps)
+constexpr int ROWS_BLOCKS[3] = {2, 3, 3}, BWD_BLOCKS = 2;
 
 __device__ __forceinline__ void cp_async16(void* smem, const void* g) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(g)
@@ -174,16 +176,17 @@ struct HeadLanes {
   }
 };
 
-// The two chunks of unit u: partners 8u + i and rot/2 + 8u + i for pairs
-// (j, j + rot/2), or 16 neighbouring values; either way the unit's pairs have
-// the frequencies 8u .. 8u + 7.
-__device__ __forceinline__ void unit_offsets(int u, int rot, bool interleaved, int& a, int& b) {
-  const bool half = !interleaved && u < rot / 16;
-  a = half ? 8 * u : 16 * u;
-  b = half ? rot / 2 + 8 * u : 16 * u + 8;
+// The two chunks of unit u of a head of d values: the halves of the rotated
+// part, or of what lies behind it, 8 values a unit, so that a warp's accesses
+// are contiguous.  With pairs (j, j + rot/2) they are each other's partners,
+// with neighbouring pairs each chunk holds four pairs.
+__device__ __forceinline__ void unit_offsets(int u, int d, int rot, int& a, int& b) {
+  const int v = u - rot / 16;
+  a = v < 0 ? 8 * u : rot + 8 * v;
+  b = v < 0 ? rot / 2 + 8 * u : (rot + d) / 2 + 8 * v;
 }
 
-// Rotates a lane's 16 values by the unit's eight angles (sn = -sin for the inverse).
+// Rotates a lane's 16 values by its eight angles (sn = -sin for the inverse).
 __device__ __forceinline__ void rotate16(float* a, float* b, const float* cs, const float* sn, bool interleaved) {
   if (interleaved) {
 #pragma unroll
@@ -231,12 +234,14 @@ __device__ __forceinline__ void load_turns(const RopeFreqs& fr, uint64_t* turn) 
   }
 }
 
-// The eight angles of unit u, which lies in the rotated part; sign -1 for the
-// inverse rotation.
-__device__ __forceinline__ void unit_angles(const float2* cs_warp, int u, float sign, float* cs, float* sn) {
+// The eight angles of unit u, which turns: of its partners, or four of the
+// neighbours of each chunk; sign -1 for the inverse rotation.
+__device__ __forceinline__ void unit_angles(const float2* cs_warp, int u, int rot, bool il, float sign, float* cs,
+                                            float* sn) {
+  const float2* at[2] = {cs_warp + (il ? 4 * u : 8 * u), cs_warp + (il ? rot / 4 + 4 * u : 8 * u + 4)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 t = reinterpret_cast<const float4*>(cs_warp)[4 * u + i];
+    const float4 t = *reinterpret_cast<const float4*>(at[i / 2] + 2 * (i % 2));
     cs[2 * i] = t.x;
     sn[2 * i] = sign * t.y;
     cs[2 * i + 1] = t.z;
@@ -291,7 +296,7 @@ __device__ __forceinline__ int append_place(const RopeArgs& a, int64_t row, int6
 
 // KIND 0: rows to rows (RopeArgs); 1, 2: append to a bf16 or E4M3 cache.
 template <typename T, int D, int KIND>
-__global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const __grid_constant__ RopeArgs a,
+__global__ void __launch_bounds__(THREADS, ROWS_BLOCKS[KIND]) rope_rows_kernel(const __grid_constant__ RopeArgs a,
                                                                          const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
   constexpr int S = Ahead<T>::ROWS, STEP = 2 * Ahead<T>::CHUNK * 32;  // a step's uint4 of a warp
@@ -302,11 +307,12 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
   const bool active = u < HL::UNITS;
   const bool il = fr.interleaved != 0, norm = a.q_norm_w != nullptr || a.k_norm_w != nullptr;
   const int rot = fr.rot;
-  // lanes behind the rotated part pass their values, whatever lies beside them;
-  // `whole` spares the warp the question where there are none (6% of the forward)
-  const bool turns = u < rot / 16, whole = HL::UNITS == HL::LANES && rot == D;
   int oa, ob;
-  unit_offsets(active ? u : 0, rot, il, oa, ob);
+  unit_offsets(active ? u : 0, D, rot, oa, ob);
+  // Values behind the rotated part pass, whatever lies beside them; `whole`
+  // spares the warp the question where there are none (6% of the forward).
+  const bool whole = HL::UNITS == HL::LANES && rot == D;
+  const bool turns = u < rot / 16;
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
   uint4* const queue = s_queue + warp * S * STEP + lane;
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS) rope_rows_kernel(const _
         KIND ? append_place(a, st.row, slot_off) : a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
     if (slot_off >= 0) {
       if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
-      if (turns) unit_angles(s_cs[warp], u, 1.0f, cs, sn);
+      if (turns) unit_angles(s_cs[warp], u, rot, il, 1.0f, cs, sn);
     }
     T* const out = static_cast<T*>(a.out) + st.row * a.ld_out;
     for (; st.left > 0; --st.left, st.h += items.step) {
@@ -454,11 +460,12 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
   const bool active = u < HL::UNITS;
   const bool il = fr.interleaved != 0;
   const int rot = fr.rot;
-  // lanes behind the rotated part pass their values, whatever lies beside them;
-  // `whole` spares the warp the question where there are none (6% of the forward)
-  const bool turns = u < rot / 16, whole = HL::UNITS == HL::LANES && rot == D;
   int oa, ob;
-  unit_offsets(active ? u : 0, rot, il, oa, ob);
+  unit_offsets(active ? u : 0, D, rot, oa, ob);
+  // Values behind the rotated part pass, whatever lies beside them; `whole`
+  // spares the warp the question where there are none (6% of the forward).
+  const bool whole = HL::UNITS == HL::LANES && rot == D;
+  const bool turns = u < rot / 16;
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
   uint4* const queue = s_queue + warp * S * STEP + lane;
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
       // ---- a row
       const int pos = a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
       if (rot) row_angles<D>(turn, rot / 2, pos, s_cs[warp]);
-      if (turns) unit_angles(s_cs[warp], u, -1.0f, cs, sn);
+      if (turns) unit_angles(s_cs[warp], u, rot, il, -1.0f, cs, sn);
       T* const dx = static_cast<T*>(a.dx) + st.row * a.ld_dx;
       for (; st.left > 0; --st.left, st.h += items.step) {
         load(fill);
@@ -650,7 +657,7 @@ cudaError_t launch_rows(RopeArgs a, const RopeFreqs& fr, int d, int num_sms, cud
   a.splits = head_splits(a.rows, heads, groups, num_sms);
   const int64_t items = a.rows * a.splits;
   int64_t blocks = (items + WARPS - 1) / WARPS;
-  if (blocks > (int64_t)ROWS_BLOCKS * num_sms) blocks = (int64_t)ROWS_BLOCKS * num_sms;  // one wave
+  if (blocks > (int64_t)ROWS_BLOCKS[KIND] * num_sms) blocks = (int64_t)ROWS_BLOCKS[KIND] * num_sms;  // one wave
   switch (d) {
     case 64: return launch_kernel<rope_rows_kernel<T, 64, KIND>>(blocks, ROWS_QUEUE<T>, st, a, fr);
     case 128: return launch_kernel<rope_rows_kernel<T, 128, KIND>>(blocks, ROWS_QUEUE<T>, st, a, fr);
