@@ -278,7 +278,7 @@ tpmlp_status tpkv_create(const tpkv_config* cfg, void* stream, tpkv_ctx** out) {
   c->stream = static_cast<cudaStream_t>(stream);
   c->device = dev;
   c->num_sms = sms;
-  c->box_tokens = kv_decode_tile(cfg->head_dim, cfg->cache_dtype == TPKV_E4M3);
+  c->box_tokens = kv_decode_tile(cfg->head_dim);
   while (cfg->page_size % c->box_tokens) c->box_tokens /= 2;  // ends at 8 at the latest
   c->workers = kv_decode_workers(sms);
   if (c->workers > KV_MAX_WORKERS) c->workers = KV_MAX_WORKERS;

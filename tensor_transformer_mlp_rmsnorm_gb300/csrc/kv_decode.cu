@@ -63,7 +63,7 @@ struct Cfg {
   static constexpr int RING_BYTES = 96 * 1024;             // two CTAs an SM
   static constexpr int ROW = D * (F8 ? 1 : 2);             // bytes of a token's key or value
   static constexpr int BLOCK = ROW % 128 == 0 ? 128 : 64;  // bytes of a row that lie together (the swizzle's width)
-  static constexpr int TK = ROW <= 128 ? 128 : 64;         // tokens of a tile
+  static constexpr int TK = D <= 128 ? 128 : 64;           // tokens of a tile
   static constexpr int SLOT = TK * ROW;                    // one operand of a tile
   // Every computing warp works on every tile, so each waits for every use of a
   // slot: a barrier's one-bit phase is never asked about two rounds ahead.
@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(NTHR, 2)
   }
   const int nhc = a.nkv * a.chunks;
   const int64_t T = total * nhc;
-  // two tiles a worker where there are few: fewer partial results to join
-  const int64_t want = (T + 1) / 2;
+  // four tiles a worker where there are few: fewer partial results to join (one
+  // sequence of 500 tokens and 8 key heads: 9.0 us, 10.3 with two, 15.4 with one)
+  const int64_t want = (T + 3) / 4;
   const int64_t G = want < a.workers ? want : a.workers;
   if ((int64_t)blockIdx.x >= G) return;
   Cursor<TK> c;
@@ -859,7 +860,7 @@ cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& km, const CUtensorM
 
 }  // namespace
 
-int kv_decode_tile(int d, bool e4m3) { return d * (e4m3 ? 1 : 2) <= 128 ? 128 : 64; }  // Cfg::TK
+int kv_decode_tile(int d) { return d <= 128 ? 128 : 64; }  // Cfg::TK
 
 int kv_decode_workers(int num_sms) { return 2 * num_sms; }
 

@@ -38,7 +38,7 @@ struct DecodeArgs {
 // Query heads worked on together: the smallest tile that holds a key head's, at most 32.
 inline int kv_decode_head_tile(int hpg) { return hpg <= 8 ? 8 : hpg <= 16 ? 16 : 32; }
 // Tokens of a tile.
-int kv_decode_tile(int d, bool e4m3);
+int kv_decode_tile(int d);
 // CTAs the kernel runs with.
 int kv_decode_workers(int num_sms);
 inline size_t kv_decode_part_floats(int d, int hpg) {

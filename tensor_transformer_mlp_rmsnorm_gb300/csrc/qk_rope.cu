@@ -610,12 +610,16 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
   }
 }
 
-// dw[c] = sum over blocks of part[block][c]: 32 columns a block, 32 rows of threads.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ part, int nparts, int d,
+// dw[c] = sum over blocks of part[block][c]: 32 columns a block, 32 rows of
+// threads.  Launched while the backward kernel still runs (its launch latency
+// is then hidden) and waiting here for the kernel's end.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int nparts, int d,
                                                        float* __restrict__ dq_w, float* __restrict__ dk_w) {
   __shared__ float red[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;  // d is a multiple of 32
   float v = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll 8
   for (int p = threadIdx.y; p < nparts; p += 32) v += part[(int64_t)p * 2 * d + c];
   red[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
@@ -712,8 +716,16 @@ cudaError_t launch_qk_rope_bwd(int dtype, int d, const RopeBwdArgs& a, const Rop
   cudaError_t e = dtype == 0 ? launch_bwd<float>(a, fr, d, num_sms, st, &nparts)
                              : launch_bwd<__nv_bfloat16>(a, fr, d, num_sms, st, &nparts);
   if (e != cudaSuccess || !dw) return e;
-  rope_dw_kernel<<<2 * d / 32, dim3(32, 32), 0, st>>>(a.part, nparts, d, dq_w, dk_w);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * d / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_dw_kernel, static_cast<const float*>(a.part), nparts, d, dq_w, dk_w);
 }
 
 }  // namespace tpmlp
