@@ -575,9 +575,11 @@ TPMLP_API tpmlp_status tpkv_set_rotary(tpkv_ctx* ctx, const tpattn_rotary* rot, 
  * The i-th row of sequence b has position past_lens[b] + i (past_lens: device
  * [batch]; negative: an inactive sequence) and goes to page
  * block_table[b, position / page_size], slot position % page_size.
- * block_table: device int32 [batch, max_pages], row stride ld_table.
+ * block_table: device int32 [batch, max_pages], row stride ld_table, at most
+ * 2^30 tokens a sequence.
  * q_out: bf16 [rows, n_heads d], row stride ld_q: the normed and rotated
- * queries, or NULL.  transform 0 stores keys (and copies queries) as they are,
+ * queries, or NULL; it may be qkv itself with the same stride, and must not
+ * overlap it otherwise.  transform 0 stores keys (and copies queries) as they are,
  * for rows that are normed and rotated already.  Rows of padding, of nobody or
  * of inactive sequences leave cache and q_out as they were.  E4M3:
  * code = round-to-nearest-even(value / inv_scale), saturated to +-448. */

@@ -376,6 +376,7 @@ tpmlp_status tpkv_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q
   if (rows == 0 || batch == 0) return TPMLP_OK;
   if (!qkv) return c->fail(TPMLP_ERR_ARG, "qkv is NULL");
   if (!a16(qkv) || !a16(q_out)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
+  if (q_out == qkv && ld_q != ld_qkv) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
   QkTransform tr;
   if (transform) tr = {&c->freqs, c->q_norm_w, c->k_norm_w, c->eps};
   return kv_run_append(c, rows, batch, qkv, ld_qkv, cu_rows, new_lens, past_lens, table, ld_table, max_pages, tr,
@@ -434,8 +435,8 @@ tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, cons
   if (!c->status) return c->fail(TPMLP_ERR_ORDER, "no workspace bound");
   if (!c->k) return c->fail(TPMLP_ERR_ORDER, "no cache bound");
   if (batch < 0 || batch > c->cfg.max_batch) return c->fail(TPMLP_ERR_SHAPE, "batch exceeds max_batch");
-  if (max_pages < 0 || ld_table < max_pages || (int64_t)max_pages * c->cfg.page_size > 0x7fffffff)
-    return c->fail(TPMLP_ERR_SHAPE, "block table out of range");
+  if (max_pages < 0 || ld_table < max_pages || (int64_t)max_pages * c->cfg.page_size > (1 << 30))
+    return c->fail(TPMLP_ERR_SHAPE, "block table out of range (at most 2^30 tokens a sequence)");
   if (batch > 0 && (!lens || (!table && max_pages > 0))) return c->fail(TPMLP_ERR_ARG, "NULL lengths or block table");
   if ((reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(table)) & 3u)
     return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");

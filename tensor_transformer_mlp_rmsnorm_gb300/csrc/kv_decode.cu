@@ -5,33 +5,46 @@
 //   lse = log sum exp s.  No visible token: out 0, lse -inf.
 //
 // What bounds it: reading the cache once.  A key head's query heads are worked
-// on together, so a cache byte meets at most 16 of them: about 16 flops a byte
+// on together, so a cache byte meets at most 32 of them: some 32 flops a byte
 // in bf16, far below what even the mma.sync tensor path gives, which is why
 // the products use m16n8k16 with the keys (and for P V the head dimension) as
 // M and 8 query heads as N; a 128-row tcgen05 tile would be all padding.
 //
-// The split.  The cache is cut into tiles of 64 tokens; the tiles of every
-// (sequence, key head) laid end to end are divided evenly over a fixed number
-// of CTAs (two an SM), whatever the lengths are.  They are read on the device:
-// each CTA scans them once.  A CTA walks its range; where a (sequence, key
-// head) ends inside it, its result is written, and where one is shared with
-// other CTAs, each leaves an unnormalised partial (sum, maximum, weighted
-// values) in the workspace and the last to arrive joins them: in groups of 16,
+// The split.  The cache is cut into tiles of 64 or 128 tokens; the tiles of
+// every (sequence, key head) laid end to end are divided evenly over two CTAs
+// an SM, whatever the lengths are.  They are read on the device: each CTA scans
+// them once.  A CTA walks its range; where a (sequence, key head) lies inside
+// it, its result is written, and where one is shared with other CTAs, each
+// leaves an unnormalised partial (weighted values, maximum, sum) in the
+// workspace and the last to arrive joins them: in groups of about sqrt(parts),
 // then the groups, so one CTA never reads hundreds of partials.  Nobody waits
 // for another CTA, and partials are added in the order of the tokens, so the
 // result does not depend on which came last.
 //
-// The pipe.  One warp fetches tiles by TMA (one box per page and operand, the
-// swizzle making ldmatrix conflict-free) into a ring of 96 KB a CTA, which
-// keeps 192 KB in flight on an SM; four warps compute, each on 16 tokens of a
-// tile with its own running maximum and sum, joined at the end of a segment.
+// The pipe.  One warp fetches tiles by TMA (one box a page and operand, the
+// swizzle making ldmatrix conflict-free) into a ring of 96 KB a CTA, 192 KB in
+// flight on an SM; it reads block-table entries a batch of boxes ahead.  Four
+// warps compute, each on its share of a tile's tokens for 8 query heads.  Two
+// warpgroups of 128 registers a thread are launched and the fetching one gives
+// 72 of them up: with 168 for all, heads of 256 values spilled and took 1.5
+// times as long.  Tokens that a window or the length hides are cleared in
+// shared memory, only in the tiles that have some: masking the fragments put
+// branches between the products (8% at d = 128 with E4M3).
+//
+// Measured on a GB300 (copy rate 6.68 TB/s): 64 sequences of up to 8192 tokens,
+// 8 key heads of 128, 32 query heads, bf16: 155 us, 6.6 TB/s; 128 such with
+// E4M3: 177 us, 5.9 TB/s, where the conversions of codes to f16 (two and a
+// shuffle for four codes) compete for issue slots; one of 131072 tokens: 86 us,
+// 6.2 TB/s, of which the two-level join is about 5 us.  Tiles of 64 tokens took
+// 168 us on the first: a tile costs a warp two waits and a chain of dependent
+// steps whatever its size.  Heads of 192 and 256 values keep 64, where a ring
+// of 128 would hold three operands or fewer.
 //
 // Rounding.  Scores, maxima, sums and outputs are f32.  With a bf16 cache P is
 // the sum of two bf16 values (16 bits), because a single one would add as much
-// error as the final rounding of the output; the second product costs nothing
-// that is not hidden behind the reads.  With an E4M3 cache, codes are converted
-// to f16 exactly, q is brought to f16 after a power-of-two scale per head, and
-// P is f16.
+// error as the final rounding of the output; the second product costs about
+// 1%.  With an E4M3 cache, codes are converted to f16 exactly, q is brought to
+// f16 after a power-of-two scale per head, and P is f16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

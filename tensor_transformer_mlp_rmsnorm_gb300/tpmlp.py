@@ -754,7 +754,7 @@ def _rows(t, width: int, dtype, name: str, index: int, rows: int = -1):
         n = shape[0]
         ld, inner = t.stride()
         if (rows < 0 or n == rows) and (inner == 1 or shape[1] == 1):
-            return t.data_ptr(), n, ld if n > 1 and ld != 0 else max(ld, shape[1])
+            return t.data_ptr(), n, ld if n > 1 else width
     raise _bad(t, name, f"{'' if rows < 0 else f'{rows} '}{dtype} rows of at least {width} contiguous values on "
                         f"cuda:{index}")
 

@@ -288,3 +288,59 @@ def test_prompt_then_tokens(kind, d, nq, nkv, il):
         _check_decode(out, lse, qo, table, [n + i + 1 for n in lens], k, v, ks, vs, nq, d, page, kind, 0, 0)
     kv.sync()
     assert past.tolist() == [n + steps for n in lens]
+
+
+def test_append_writes_queries_in_place():
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    g = _gen(3)
+    nq, nkv, d, n = 6, 2, 128, 77
+    table, pages = _table(g, [n], 16)
+    (k, v), (k2, v2) = _caches(g, pages, nkv, 16, d, "bf16"), _caches(g, pages, nkv, 16, d, "bf16")
+    x = torch.randn((n, (nq + 2 * nkv) * d), generator=g).to(torch.bfloat16).cuda()
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    cu, past = torch.tensor([0, n], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = []
+    for kc, vc, inplace in ((k, v, False), (k2, v2, True)):
+        kv = T.TPKV(kc, vc, nq, max_batch=1)
+        kv.set_rotary(T.Rotary(d), w, w, EPS)
+        rows = x.clone()
+        got.append(kv.append(rows, past, table.cuda(), cu_rows=cu, q_out=rows if inplace else None))
+        kv.sync()
+    assert torch.equal(got[0], got[1][:, : nq * d])
+    t = torch.arange(n)
+    at = table[0][t // 16].long(), slice(None), t % 16
+    assert torch.equal(k[at], k2[at]) and torch.equal(v[at], v2[at])
+
+
+def test_refusals_of_a_context():
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    k = torch.zeros(1, 1, 65536, 64, dtype=torch.bfloat16, device="cuda")
+    kv = T.TPKV(k, k.clone(), 2, max_batch=2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 128, dtype=torch.bfloat16, device="cuda")
+    one, table = torch.ones(1, **i32), torch.zeros(1, 2, **i32)
+
+    def refused(status, f):
+        with pytest.raises(T.TPMLPError) as e:
+            f()
+        assert e.value.status == status
+
+    refused(T.ERR_SHAPE, lambda: kv.decode(q, one, torch.zeros(1, 16385, **i32)))     # above 2^30 tokens a sequence
+    refused(T.ERR_SHAPE, lambda: kv.decode(q.expand(3, 128).contiguous(), torch.ones(3, **i32), torch.zeros(3, 2, **i32)))
+    refused(T.ERR_ARG, lambda: kv.decode(q, one, table, window=-1))
+    refused(T.ERR_ARG, lambda: kv.decode(q, one, table, scale=float("nan")))
+    refused(T.ERR_ARG, lambda: kv.decode(q.float(), one, table))
+    refused(T.ERR_ARG, lambda: kv.decode(q, one.long(), table))
+    refused(T.ERR_ARG, lambda: kv.decode(q, one, table.cpu()))
+    refused(T.ERR_ARG, lambda: kv.decode(q[:, :64], one, table))
+    x = torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda")
+    refused(T.ERR_SHAPE, lambda: kv.append(x, torch.zeros(2, **i32), torch.zeros(2, 2, **i32)))  # 3 rows for 2 sequences
+    cu = torch.zeros(2, **i32)
+    refused(T.ERR_ARG, lambda: kv.append(x, one, table, cu_rows=cu, new_lens=one))
+    refused(T.ERR_ARG, lambda: T.TPKV(k, k[:, :, ::2], 2))
+    refused(T.ERR_SHAPE, lambda: T.TPKV(k[:, :, :100], k[:, :, :100], 2))                # 100 tokens a page
+    refused(T.ERR_SHAPE, lambda: T.TPKV(k[..., :32], k[..., :32], 2))                    # heads of 32
+    refused(T.ERR_UNSUPPORTED, lambda: T.TPKV(k.float(), k.float(), 2))
+    refused(T.ERR_ARG, lambda: T.TPKV(k, k, 2, k_inv_scale=torch.ones(1, device="cuda")))  # scales without E4M3
+    kv.decode(q, one, table)
+    kv.sync()

@@ -181,3 +181,23 @@ def test_graph_replay_and_side_stream():
     # every output is odd in x but the weight gradients, which are even
     assert torch.equal(out, -ref[0]) and torch.equal(dx, -ref[1])
     assert torch.equal(dq, ref[2]) and torch.equal(dk, ref[3])
+
+
+@pytest.mark.parametrize("il", [False, True])
+def test_infinity_behind_the_rotated_part_stays_there(il):
+    """Values that pass take nothing from, and give nothing to, what lies beside them."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    x = torch.randn(5, 192).cuda()
+    x[2, 64 + 40] = float("inf")
+    x[3, 64 + 63] = float("nan")
+    r = T.Rotary(32, interleaved=il)
+    out = T.qk_norm_rope(x, 2, 1, 64, r)
+    bad = ~out.isfinite()
+    want = torch.zeros_like(bad)
+    want[2, 64 + 40] = want[3, 64 + 63] = True
+    assert torch.equal(bad, want)
+    clean = torch.where(want, 1.0, x)
+    ref = T.qk_norm_rope(clean, 2, 1, 64, r)
+    assert torch.equal(out[~want], ref[~want])
+    dx, _, _ = T.qk_norm_rope_backward(x, None, 2, 1, 64, r)
+    assert torch.equal(~dx.isfinite(), want)
