@@ -646,7 +646,7 @@ class TPAttn:
         p.rot = ctypes.pointer(rotary.spec) if rotary is not None else None
         p.q_norm_w, p.k_norm_w = _vec(q_norm_w, d, _BF, "q_norm_w", i), _vec(k_norm_w, d, _BF, "k_norm_w", i)
         norm = q_norm_w is not None
-        grads = {k: torch.zeros(d, dtype=_F32T, device=self.device) for k in ("q_norm_w", "k_norm_w")} if norm else {}
+        grads = {k: torch.empty(d, dtype=_F32T, device=self.device) for k in ("q_norm_w", "k_norm_w")} if norm else {}
         if norm:
             p.dq_norm_w, p.dk_norm_w = grads["q_norm_w"].data_ptr(), grads["k_norm_w"].data_ptr()
         for names, given in ((("master_q", "master_k"), masters), (("m_q", "m_k", "v_q", "v_k"), moments)):
@@ -735,9 +735,7 @@ _BF, _F32T, _I32T = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_of(device, index: int, stream):
-    if stream is not None:
-        return stream.cuda_stream
+def _stream_of(device, index: int):
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
@@ -769,19 +767,15 @@ def _vec(t, n: int, dtype, name: str, index: int):
     return t.data_ptr()
 
 
-class _on:
-    """The device `index` made current while a call without a context runs, where it is not."""
-
-    def __init__(self, index: int):
-        self.dev = None if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.dev is not None:
-            self.dev.__enter__()
-
-    def __exit__(self, *exc):
-        if self.dev is not None:
-            self.dev.__exit__(*exc)
+def _on_device(index: int, fn, *args):
+    """A call without a context, on device `index`."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args)
+    if status:
+        _check(status)
 
 
 def _qk_desc(n, dtype, index, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps) -> QkDesc:
@@ -805,15 +799,17 @@ def qk_norm_rope(x, n_heads: int, n_kv_heads: int, head_dim: int, rotary: Rotary
     """RMS norm (where a weight is given) and position rotation of the query and key heads at the start of each
     row of x (tpattn_qk_rope_forward); out may be x.  Positions: int32 per row, or row % seq (seq 0: the row).
     Runs on `stream`, torch's current stream where it is None."""
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(x, n_heads, n_kv_heads, head_dim, rotary, positions, seq, q_norm_w, k_norm_w, eps, out)
     width, dtype, index = (n_heads + n_kv_heads) * head_dim, x.dtype, _cuda_index(x, "x")
     xp, n, ldx = _rows(x, width, dtype, "x", index)
     if out is None:
         out = x.new_empty((n, width))
     op, _, ldo = _rows(out, width, dtype, "out", index, n)
     d = _qk_desc(n, dtype, index, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
-    with _on(index):
-        _check(lib().tpattn_qk_rope_forward(d, rotary.spec if rotary is not None else None, xp, ldx, op, ldo,
-                                            _stream_of(x.device, index, stream)))
+    _on_device(index, lib().tpattn_qk_rope_forward, d, rotary.spec if rotary is not None else None, xp, ldx, op, ldo,
+               _stream_of(x.device, index))
     return out
 
 
@@ -822,6 +818,10 @@ def qk_norm_rope_backward(dout, x, n_heads: int, n_kv_heads: int, head_dim: int,
                           dq_norm_w=None, dk_norm_w=None, workspace=None, stream=None):
     """Backward of qk_norm_rope: (dx, dq_norm_w, dk_norm_w), the weights' gradients in float32 (None without the
     weight).  x: the forward's input (only read with norm weights, else it may be None); dx may be dout."""
+    if stream is not None:  # what is allocated here belongs to that stream too
+        with torch.cuda.stream(stream):
+            return qk_norm_rope_backward(dout, x, n_heads, n_kv_heads, head_dim, rotary, positions, seq, q_norm_w,
+                                         k_norm_w, eps, dx, dq_norm_w, dk_norm_w, workspace)
     width, dtype, index = (n_heads + n_kv_heads) * head_dim, dout.dtype, _cuda_index(dout, "dout")
     norm = q_norm_w is not None or k_norm_w is not None
     gp, n, ldg = _rows(dout, width, dtype, "dout", index)
@@ -836,20 +836,17 @@ def qk_norm_rope_backward(dout, x, n_heads: int, n_kv_heads: int, head_dim: int,
             if workspace.get_device() != index or not workspace.is_contiguous():
                 raise _bad(workspace, "workspace", f"a contiguous tensor on cuda:{index}")
             wp, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        no_dq, no_dk = q_norm_w is not None and dq_norm_w is None, k_norm_w is not None and dk_norm_w is None
-        if workspace is None or no_dq or no_dk:
-            # one allocation for what was not given: every torch call here costs more than the launch
-            parts = torch.empty(2 * head_dim + (0 if wp else need // 4), dtype=_F32T,
-                                device=dout.device).split_with_sizes((head_dim, head_dim, 0 if wp else need // 4))
-            dq_norm_w, dk_norm_w = parts[0] if no_dq else dq_norm_w, parts[1] if no_dk else dk_norm_w
-            if wp is None:
-                wp, wbytes = parts[2].data_ptr(), need
+        else:  # separate tensors: views of one cost more than allocating each
+            workspace = torch.empty(need // 4, dtype=_F32T, device=dout.device)
+            wp, wbytes = workspace.data_ptr(), need
+        if q_norm_w is not None and dq_norm_w is None:
+            dq_norm_w = torch.empty(head_dim, dtype=_F32T, device=dout.device)
+        if k_norm_w is not None and dk_norm_w is None:
+            dk_norm_w = torch.empty(head_dim, dtype=_F32T, device=dout.device)
     d = _qk_desc(n, dtype, index, n_heads, n_kv_heads, head_dim, positions, seq, q_norm_w, k_norm_w, eps)
-    with _on(index):
-        _check(lib().tpattn_qk_rope_backward(
-            d, rotary.spec if rotary is not None else None, xp, ldx, gp, ldg, dp, ldd,
-            _vec(dq_norm_w, head_dim, _F32T, "dq_norm_w", index), _vec(dk_norm_w, head_dim, _F32T, "dk_norm_w", index),
-            wp, wbytes, _stream_of(dout.device, index, stream)))
+    _on_device(index, lib().tpattn_qk_rope_backward, d, rotary.spec if rotary is not None else None, xp, ldx, gp, ldg, dp,
+               ldd, _vec(dq_norm_w, head_dim, _F32T, "dq_norm_w", index),
+               _vec(dk_norm_w, head_dim, _F32T, "dk_norm_w", index), wp, wbytes, _stream_of(dout.device, index))
     return dx, dq_norm_w, dk_norm_w
 
 
@@ -881,7 +878,15 @@ class TPKV:
         self._norm = (None, None)
         self.index = k_cache.get_device()
         self._fixed = stream
-        self._stream = _stream_of(dev, self.index, stream)
+        if stream is not None:  # the scratch belongs to the stream that its first use runs on
+            with torch.cuda.stream(stream):
+                self._create(pages, page, d)
+        else:
+            self._create(pages, page, d)
+
+    def _create(self, pages: int, page: int, d: int):
+        dev, (k_cache, v_cache) = self.device, (self.k_cache, self.v_cache)
+        self._stream = _stream_of(dev, self.index)
         ctx = ctypes.c_void_p()
         with torch.cuda.device(dev):
             self._ck(lib().tpkv_create(ctypes.byref(self.cfg), self._stream, ctypes.byref(ctx)))
@@ -891,8 +896,8 @@ class TPKV:
         self._ck(lib().tpkv_bind_workspace(ctx, self.workspace.data_ptr(), nbytes))
         f32 = torch.float32
         self._ck(lib().tpkv_bind_cache(ctx, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
-                                       _vec(k_inv_scale, nkv, f32, "k_inv_scale", self.index),
-                                       _vec(v_inv_scale, nkv, f32, "v_inv_scale", self.index)))
+                                       _vec(self._scales[0], self.nkv, f32, "k_inv_scale", self.index),
+                                       _vec(self._scales[1], self.nkv, f32, "v_inv_scale", self.index)))
 
     def _ck(self, status: int):
         if status != OK:
@@ -915,8 +920,12 @@ class TPKV:
         """Run later calls on `stream` (None: torch's current stream at each call)."""
         self._fixed = stream
 
+    def _elsewhere(self) -> bool:
+        """Whether torch's current stream is not the fixed one."""
+        return self._fixed is not None and _stream_of(self.device, self.index) != self._fixed.cuda_stream
+
     def _enter(self):
-        s = _stream_of(self.device, self.index, self._fixed)
+        s = _stream_of(self.device, self.index)
         if s != self._stream:
             self._ck(lib().tpkv_set_stream(self.ctx, s))
             self._stream = s
@@ -940,6 +949,9 @@ class TPKV:
         """Store the keys and values of packed rows [Q | K | V] behind each sequence's ``past_lens`` tokens and
         return the normed and rotated queries [rows, n_heads * d] (None without ``with_queries``); see tpkv_append.
         Rows that are no sequence's leave ``q_out`` as it was (undefined where it is made here)."""
+        if self._elsewhere():  # what is allocated here belongs to that stream too
+            with torch.cuda.stream(self._fixed):
+                return self.append(qkv, past_lens, block_table, cu_rows, new_lens, q_out, transform, with_queries)
         index, batch, width = self.index, past_lens.shape[0], self.nq * self.d
         xp, n, ldx = _rows(qkv, width + 2 * self.nkv * self.d, _BF, "qkv", index)
         if q_out is None and with_queries:
@@ -960,6 +972,9 @@ class TPKV:
         """Attention of one token per sequence over its first ``lens + len_add`` cached tokens; with a window, over
         its last ``window`` tokens and first ``sinks``.  scale: 1 / sqrt(head_dim) unless given.  Returns out
         [batch, n_heads * d], with ``return_lse`` or ``lse`` (out, lse float32 [batch, n_heads]); see tpkv_decode."""
+        if self._elsewhere():
+            with torch.cuda.stream(self._fixed):
+                return self.decode(q, lens, block_table, scale, window, sinks, out, lse, return_lse, len_add)
         index, width = self.index, self.nq * self.d
         qp, batch, ldq = _rows(q, width, _BF, "q", index)
         if out is None:
@@ -981,8 +996,7 @@ class TPKV:
         return out if lse is None else (out, lse)
 
     def sync(self):
-        """Wait for the stream; raises where a page or length lay outside the cache."""
-        self._enter()
+        """Wait for the stream of the last call; raises where a page or length lay outside the cache."""
         self._ck(lib().tpkv_sync(self.ctx))
 
     def launch_count(self) -> int:

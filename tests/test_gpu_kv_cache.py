@@ -344,3 +344,23 @@ def test_refusals_of_a_context():
     refused(T.ERR_ARG, lambda: T.TPKV(k, k, 2, k_inv_scale=torch.ones(1, device="cuda")))  # scales without E4M3
     kv.decode(q, one, table)
     kv.sync()
+
+
+def test_fixed_stream():
+    """A context on a stream of its own, called while another one is current: the same bits."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    lens = [700, 64, 1, 3000]
+    kv, q, table, k, v, *_ = _decode_case(lens, 8, 2, 128, "bf16", 16, "hnd", 0, 0)
+    args = (q.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda())
+    ref = kv.decode(*args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    own = T.TPKV(k, v, 8, max_batch=4, stream=side)
+    outs = [own.decode(*args) for _ in range(5)]
+    x = torch.randn(9, 3 * 128, device="cuda")
+    torch.cuda.synchronize()
+    a = T.qk_norm_rope(x, 2, 1, 128, T.Rotary(128), stream=side)
+    own.sync()
+    side.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+    assert torch.equal(a, T.qk_norm_rope(x, 2, 1, 128, T.Rotary(128)))
