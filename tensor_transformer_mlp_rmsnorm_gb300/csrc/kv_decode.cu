@@ -63,7 +63,6 @@ constexpr int NTHR = 256;        // a warpgroup that computes and one whose firs
 // Registers a thread: 128 at launch (two CTAs an SM); the computing warpgroup
 // takes what the other gives up, 200 + 56 = 2 x 128.
 constexpr int COMPUTE_REGS = 200, FETCH_REGS = 56;
-constexpr int JOIN_MAX = 24;     // partials one CTA joins at a time: the square root of the most CTAs
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 100000000ull;
 
 // Shape of the kernel for heads of D values, F8: E4M3 cache, HG: groups of 8
@@ -205,16 +204,14 @@ struct JoinArgs {
   float vscale;
 };
 template <int D, int HT>
-__device__ __forceinline__ void join_parts(const JoinArgs a, float* s_o, float* s_mx, float* s_inv, volatile int* s_last) {
+__device__ __forceinline__ void join_parts(const JoinArgs& a, volatile int* s_last) {
   const int tid = threadIdx.x;
   const size_t part_sz = (size_t)HT * (D + 2);
-  // ---- the last CTA to arrive joins: groups of about sqrt(parts), then the groups' leaders
+  // groups of about sqrt(parts), then the groups' leaders
   int group = a.nparts;
   if (a.nparts > 8)
     for (group = 3; group * group < a.nparts;) ++group;
   const int ngroups = (a.nparts + group - 1) / group;
-  float* s_w = s_o;                  // [JOIN_MAX][HT] maxima, then weights
-  float* s_s = s_o + JOIN_MAX * HT;  // sums
   for (int level = 0; level < 2; ++level) {
     const int p0 = level == 0 ? a.p_me / group * group : 0;
     const int pstep = level == 0 ? 1 : group;
@@ -223,8 +220,8 @@ __device__ __forceinline__ void join_parts(const JoinArgs a, float* s_o, float* 
     if (cnt > 1) {
       bar_compute();
       if (tid == 0) {
-        // the fences order the whole CTA's partial before the count and
-        // the others' partials behind it (the barriers carry them)
+        // the fences order the whole CTA's partial before the count and the
+        // others' partials behind it (the barriers carry them)
         __threadfence();
         const uint32_t old = atomicAdd(ctr, 1u);
         __threadfence();
@@ -232,82 +229,89 @@ __device__ __forceinline__ void join_parts(const JoinArgs a, float* s_o, float* 
         if (old == (uint32_t)cnt - 1) *ctr = 0;  // ready for the next launch
       }
       bar_compute();
-      if (!*s_last) break;
+      if (!*s_last) return;
     }
+    const bool final_level = ngroups == 1 || level == 1;
+    if (!final_level && cnt == 1) continue;  // a group of one stands for itself
     auto part_of = [&](int i) -> float* {
       const int p = p0 + i * pstep;
       return a.part + (size_t)(2 * (a.w_first + p) + (p == 0)) * part_sz;
     };
-    const bool final_level = ngroups == 1 || level == 1;
-    if (!final_level && cnt == 1) continue;  // a group of one stands for itself
-    for (int x = tid; x < cnt * HT; x += NCW * 32) {
-      const float* pp = part_of(x / HT) + (size_t)HT * D + x % HT;
-      s_w[x] = __ldcg(pp);
-      s_s[x] = __ldcg(pp + HT);
-    }
-    bar_compute();
-    if (tid < HT) {
-      float mx = -INFINITY;
-      for (int i = 0; i < cnt; ++i) mx = fmaxf(mx, s_w[i * HT + tid]);
-      float s = 0.0f;
-      for (int i = 0; i < cnt; ++i) {
-        const float w = mx == -INFINITY ? 0.0f : ex2_fast(s_w[i * HT + tid] - mx);
-        s_w[i * HT + tid] = w;
-        s += w * s_s[i * HT + tid];
-      }
-      s_mx[tid] = mx;
-      s_inv[tid] = final_level ? (s > 0.0f ? a.vscale / s : (s == s ? 0.0f : s)) : s;
-      if (final_level && a.lse && tid < a.heads) a.lse[tid] = s == 0.0f ? -INFINITY : (mx + log2f(s)) * 0.69314718055994531f;
-    }
-    bar_compute();
-    float* lead = part_of(0);
-    // all of a thread's loads of eight parts in flight at once
-    constexpr int V = HT * D / 4 / (NCW * 32) >= 2 ? 2 : 1;  // float4 of a part that a thread adds up at a time
+    // Each thread joins float4 columns by itself: maxima, sums and values of
+    // eight parts in flight at once, added in the parts' order.
+    // A pass covers whole heads, so that none is read again once it is written.
+    constexpr int PER = HT * D / 4 / (NCW * 32), V = D == 192 ? 3 : PER >= 2 ? 2 : 1;
+    static_assert(PER % V == 0 && V * NCW * 128 % D == 0, "passes of whole heads");
     for (int x0 = tid; x0 < HT * D / 4; x0 += V * NCW * 32) {
       float4 v[V];
+      float mx[V], sum[V];
 #pragma unroll
-      for (int q = 0; q < V; ++q) v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int q = 0; q < V; ++q) {
+        v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        mx[q] = -INFINITY;
+        sum[q] = 0.0f;
+      }
       for (int i0 = 0; i0 < cnt; i0 += 8) {
         float4 y[8][V];
+        float m[8][V], l[8][V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < cnt) {
-            const float4* pp = reinterpret_cast<const float4*>(part_of(i0 + i)) + x0;
+        for (int i = 0; i < 8; ++i) {
+          const float* pp = part_of(i0 + i < cnt ? i0 + i : i0);
 #pragma unroll
-            for (int q = 0; q < V; ++q) y[i][q] = __ldcg(pp + q * NCW * 32);
+          for (int q = 0; q < V; ++q) {
+            const int x = x0 + q * NCW * 32, h = 4 * x / D;
+            m[i][q] = __ldcg(pp + (size_t)HT * D + h);
+            l[i][q] = __ldcg(pp + (size_t)HT * D + HT + h);
+            y[i][q] = __ldcg(reinterpret_cast<const float4*>(pp) + x);
           }
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < cnt) {
+        for (int q = 0; q < V; ++q) {
+          float top = mx[q];
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-              const float w = s_w[(i0 + i) * HT + 4 * (x0 + q * NCW * 32) / D];
+          for (int i = 0; i < 8; ++i)
+            if (i0 + i < cnt) top = fmaxf(top, m[i][q]);
+          const float base = top == -INFINITY ? 0.0f : top;  // nothing visible: all weights 0
+          const float f = ex2_fast(mx[q] - base);
+          mx[q] = top;
+          sum[q] *= f;
+          v[q] = make_float4(v[q].x * f, v[q].y * f, v[q].z * f, v[q].w * f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i0 + i < cnt) {
+              const float w = ex2_fast(m[i][q] - base);
+              sum[q] = fmaf(w, l[i][q], sum[q]);
               v[q].x = fmaf(w, y[i][q].x, v[q].x);
               v[q].y = fmaf(w, y[i][q].y, v[q].y);
               v[q].z = fmaf(w, y[i][q].z, v[q].z);
               v[q].w = fmaf(w, y[i][q].w, v[q].w);
             }
-          }
+        }
       }
+      float* lead = part_of(0);
+      if (!final_level) bar_compute();  // every thread has read the leader's partial
 #pragma unroll
       for (int q = 0; q < V; ++q) {
         const int x = x0 + q * NCW * 32, h = 4 * x / D, col = 4 * x % D;
+        const float s = sum[q];
         if (final_level) {
-          const float r = s_inv[h];
-          if (h < a.heads)
+          const float r = s > 0.0f ? a.vscale / s : (s == s ? 0.0f : s);
+          if (h < a.heads) {
             *reinterpret_cast<uint2*>(a.out + (int64_t)h * D + col) =
                 make_uint2(pack_bf16(v[q].x * r, v[q].y * r), pack_bf16(v[q].z * r, v[q].w * r));
+            if (a.lse && col == 0)
+              a.lse[h] = s == 0.0f ? -INFINITY : (mx[q] + log2f(s)) * 0.69314718055994531f;
+          }
         } else {
           __stcg(reinterpret_cast<float4*>(lead) + x, v[q]);
+          if (col == 0) {
+            __stcg(lead + (size_t)HT * D + h, mx[q]);
+            __stcg(lead + (size_t)HT * D + HT + h, s);
+          }
         }
       }
     }
-    if (!final_level && tid < HT) {
-      __stcg(lead + (size_t)HT * D + tid, s_mx[tid]);
-      __stcg(lead + (size_t)HT * D + HT + tid, s_inv[tid]);
-    }
-    bar_compute();
-    if (final_level) break;
+    if (final_level) return;
   }
 }
 
@@ -364,10 +368,8 @@ __global__ void __launch_bounds__(NTHR, 2)
   __shared__ Walk<TK> s_walk;
   __shared__ int64_t s_scan[NTHR / 32], s_base;
   __shared__ float s_m[KG][HT], s_l[KG][HT];
-  __shared__ float s_mx[HT], s_inv[HT];
-  // the warps' outputs of OD columns, [KG][HT][OD + 4]; the join's weights [JOIN_MAX][HT] and sums behind them
-  constexpr int S_O = KG * HT * (OD + 4), S_W = 2 * JOIN_MAX * HT;
-  __shared__ __align__(16) float s_o[S_O > S_W ? S_O : S_W];
+  __shared__ float s_inv[HT];
+  __shared__ __align__(16) float s_o[KG * HT * (OD + 4)];  // the warps' outputs of OD columns
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(NTHR, 2)
       ja.p_me = (int)(blockIdx.x - w_first);
       ja.heads = heads;
       ja.vscale = vscale;
-      join_parts<D, HT>(ja, s_o, s_mx, s_inv, &s_last);
+      join_parts<D, HT>(ja, &s_last);
     }
     if (tid == 0) s_walk.next(a, nhc);
     bar_compute();

@@ -154,6 +154,11 @@ DECODES = [  # lens, nq, nkv, d, kind, page, layout, window, sinks
     ([0, 1, 15, 16, 17, 63, 64, 65, 0, 127, 1000], 8, 2, 128, "e4m3", 24, "hnd", 0, 0),
     ([5000], 1, 1, 256, "bf16", 64, "hnd", 0, 0),          # one head over every CTA: groups of joins
     ([40000], 2, 1, 64, "e4m3", 128, "nhd", 0, 0),
+    ([9000], 1, 1, 192, "bf16", 64, "hnd", 0, 0),          # more parts than one CTA joins, in each head tile
+    ([9000, 5], 32, 1, 192, "e4m3", 64, "nhd", 0, 0),
+    ([0, 9000], 12, 1, 128, "bf16", 16, "hnd", 0, 0),
+    ([20000], 30, 1, 64, "bf16", 64, "hnd", 0, 0),
+    ([9000], 16, 1, 256, "bf16", 64, "nhd", 0, 0),
     ([777, 64, 3], 48, 2, 64, "bf16", 8, "hnd", 0, 0),     # 24 heads a key head: two tiles of 16
     ([777, 64, 3], 36, 3, 192, "bf16", 48, "nhd", 0, 0),   # 12 heads a key head
     ([300, 2500], 33, 3, 256, "e4m3", 32, "hnd", 0, 0),    # 11 heads a key head
