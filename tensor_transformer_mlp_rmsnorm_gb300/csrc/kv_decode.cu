@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(NTHR, 2)
   extern __shared__ __align__(1024) uint8_t ring_raw[];
   __shared__ __align__(8) uint64_t full[R::N], empty[R::N];
   __shared__ int s_abort, s_b, s_last;
-  __shared__ Walk<TK> s_walk;
+  __shared__ Walk<TK> s_walks[2];  // the segment at hand and the next one
   __shared__ int64_t s_scan[NTHR / 32], s_base;
   __shared__ float s_m[KG][HT], s_l[KG][HT];
   __shared__ float s_inv[HT];
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(NTHR, 2)
     w.hc = (int)(rel / c.s.tiles);
     w.j = (int)(rel - (int64_t)w.hc * c.s.tiles);
     w.set();
-    s_walk = w;
+    s_walks[0] = w;
   }
   __syncthreads();
 
@@ -549,52 +549,76 @@ __global__ void __launch_bounds__(NTHR, 2)
   uint32_t nu = 0;  // ring uses so far
   bool ok = true;
 
-  for (;;) {
+  // A segment's queries as they are in memory, fetched before the join of the
+  // segment in front of it (heads of up to 128 values: more would not fit the
+  // registers).
+  constexpr bool EARLY = D <= 128;
+  uint32_t qr[KS][2];
+  float kinv = 1.0f, vscale = 1.0f;  // E4M3: what the head's codes stand for
+  auto fetch_q = [&](const Walk<TK>& w) {
+    const int g = w.hc / a.chunks, h0 = (w.hc - g * a.chunks) * HT, heads = min(HT, a.hpg - h0);
+    const int h = hgrp * 8 + g8;
+    const __nv_bfloat16* q =
+        static_cast<const __nv_bfloat16*>(a.q) + (int64_t)w.c.b * a.ld_q + (int64_t)(g * a.hpg + h0 + h) * D;
+    if (F8 && a.k_inv_scale) kinv = a.k_inv_scale[g];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      qr[k][0] = qr[k][1] = 0;
+      if (h < heads) {
+        if (F8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(q + 16 * k + 4 * c4);
+          qr[k][0] = v.x;
+          qr[k][1] = v.y;
+        } else {
+          qr[k][0] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4);
+          qr[k][1] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * c4);
+        }
+      }
+    }
+  };
+  int cur = 0;
+  if (EARLY) fetch_q(s_walks[0]);
+
+  for (;; cur ^= 1) {
     // ---- one segment: the worker's tiles of (sequence b, key head g, chunk)
+    const Walk<TK>& s_walk = s_walks[cur];
     const int ntiles = s_walk.ntiles, j = s_walk.j;
     if (ntiles == 0) break;
     const Seq<TK> seq = s_walk.c.s;
+    if (!EARLY) fetch_q(s_walk);
+    if (F8 && a.v_inv_scale) vscale = a.v_inv_scale[s_walk.hc / a.chunks];
+    if (tid == 0) {
+      s_walks[cur ^ 1] = s_walk;
+      s_walks[cur ^ 1].next(a, nhc);
+    }
     uint32_t qf[KS][2];
     float qs[2];  // log2-domain scale of this lane's two score columns
-    {
-      const int hc = s_walk.hc, g = hc / a.chunks, h0 = (hc - g * a.chunks) * HT, heads = min(HT, a.hpg - h0);
-      const float kscale = a.scale_log2 * (F8 && a.k_inv_scale ? a.k_inv_scale[g] : 1.0f);
-      const int h = hgrp * 8 + g8;
-      const __nv_bfloat16* q =
-          static_cast<const __nv_bfloat16*>(a.q) + (int64_t)s_walk.c.b * a.ld_q + (int64_t)(g * a.hpg + h0 + h) * D;
-      if (F8) {
-        float mx = 0.0f;
+    if (F8) {
+      float mx = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint2 v = make_uint2(0, 0);
-          if (h < heads) v = *reinterpret_cast<const uint2*>(q + 16 * k + 4 * c4);
-          qf[k][0] = v.x;
-          qf[k][1] = v.y;
-          mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf_lo(v.x)), fabsf(bf_hi(v.x))), fmaxf(fabsf(bf_lo(v.y)), fabsf(bf_hi(v.y)))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // q / 2^e with 2^e <= max|q| < 2^(e+1): exact in f16 down to 2^-14 of the largest
-        int e = (int)(__float_as_uint(mx) >> 23) - 127;
-        e = mx > 0.0f && mx < INFINITY ? max(-120, min(120, e)) : 0;
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int i = 0; i < 2; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(qr[k][i])), fabsf(bf_hi(qr[k][i]))));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // q / 2^e with 2^e <= max|q| < 2^(e+1): exact in f16 down to 2^-14 of the largest
+      int e = (int)(__float_as_uint(mx) >> 23) - 127;
+      e = mx > 0.0f && mx < INFINITY ? max(-120, min(120, e)) : 0;
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+      const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) qf[k][i] = pack_f16(bf_lo(qf[k][i]) * inv, bf_hi(qf[k][i]) * inv);
-        qs[0] = kscale * __shfl_sync(0xffffffffu, mul, 8 * c4);
-        qs[1] = kscale * __shfl_sync(0xffffffffu, mul, 8 * c4 + 4);
-      } else {
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int i = 0; i < 2; ++i) qf[k][i] = pack_f16(bf_lo(qr[k][i]) * inv, bf_hi(qr[k][i]) * inv);
+      qs[0] = a.scale_log2 * kinv * __shfl_sync(0xffffffffu, mul, 8 * c4);
+      qs[1] = a.scale_log2 * kinv * __shfl_sync(0xffffffffu, mul, 8 * c4 + 4);
+    } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            qf[k][i] = 0;
-            if (h < heads) qf[k][i] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * c4);
-          }
-        qs[0] = qs[1] = kscale;
+      for (int k = 0; k < KS; ++k) {
+        qf[k][0] = qr[k][0];
+        qf[k][1] = qr[k][1];
       }
+      qs[0] = qs[1] = a.scale_log2;
     }
     float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -762,12 +786,12 @@ __global__ void __launch_bounds__(NTHR, 2)
       }
     }
     if (bar_compute_any(!ok)) return;  // a wait gave up: all four warps leave together
+    if (EARLY && s_walks[cur ^ 1].ntiles) fetch_q(s_walks[cur ^ 1]);
     const size_t part_sz = (size_t)HT * (D + 2);
     const bool direct = s_walk.direct;
     const int hc = s_walk.hc, g = hc / a.chunks, h0 = (hc - g * a.chunks) * HT, heads = min(HT, a.hpg - h0), b = s_walk.c.b;
     const int64_t w_first = direct ? blockIdx.x : ((s_walk.item0 + 1) * s_walk.G + s_walk.T - 1) / s_walk.T - 1;
     float* my_part = a.part + (size_t)(2 * blockIdx.x + (blockIdx.x == w_first)) * part_sz;
-    const float vscale = F8 && a.v_inv_scale ? a.v_inv_scale[g] : 1.0f;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (int64_t)b * a.ld_out + (int64_t)(g * a.hpg + h0) * D;
     float* lse = a.lse ? a.lse + (int64_t)b * a.nq + g * a.hpg + h0 : nullptr;
     float al[2];
@@ -845,8 +869,7 @@ __global__ void __launch_bounds__(NTHR, 2)
       ja.vscale = vscale;
       join_parts<D, HT>(ja, &s_last);
     }
-    if (tid == 0) s_walk.next(a, nhc);
-    bar_compute();
+    bar_compute();  // everyone is done with this segment's walk
   }
 }
 

@@ -15,14 +15,22 @@
 // slow pipe here) and no table to read.  The top 32 bits go through
 // sincospif; that is 2^-25 of a half turn, the rounding of the f32 result.
 //
-// What bounds it: memory (about 8 flops a byte are far below the f32 rate).
+// What bounds it: memory, with the instruction rate close behind (512 values of
+// 16 bits leave an SM about 90 cycles of its share of the copy rate forward).
 // A head belongs to d / 16 lanes; a lane holds two 16-byte (bf16) chunks whose
 // values are each other's rotation partners, so the rotation needs no shuffle
 // and the norm three or four.  A warp walks rows, four heads at a time at
-// d = 128, and takes a row's sines and cosines once.  Loads run several steps
-// ahead, across rows, through a queue in shared memory (cp.async): each lane
-// reads back only what it copied itself, so nothing but its own copies is
-// waited for, and no registers are held by loads in flight.
+// d = 128, and takes a row's sines, cosines and addresses once.  Loads run
+// several steps ahead, across rows, through a queue in shared memory
+// (cp.async): each lane reads back only what it copied itself, so nothing but
+// its own copies is waited for, and no registers are held by loads in flight.
+//
+// Measured on a GB300 (copy rate 6.68 TB/s), bf16, 32 + 8 heads of 128, norms:
+// forward of 32768 rows 107 us, 6.3 TB/s; append of 16000 rows with 8 value
+// heads 69 us, 5.7 TB/s; backward of 8192 rows 55 us, 4.6 TB/s, bound by issue
+// slots (some 450 instructions a step for three operands, two sums and the
+// weight gradient; 256 values a head: 5.5 TB/s).  With the loads in registers
+// instead of the queue: 115, 78 and 58 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
