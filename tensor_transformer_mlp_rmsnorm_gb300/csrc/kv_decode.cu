@@ -407,9 +407,12 @@ __global__ void __launch_bounds__(NTHR, 2)
   }
   const int nhc = a.nkv * a.chunks;
   const int64_t T = total * nhc;
-  // four tiles a worker where there are few: fewer partial results to join (one
-  // sequence of 500 tokens and 8 key heads: 9.0 us, 10.3 with two, 15.4 with one)
-  const int64_t want = (T + 3) / 4;
+  // Four tiles a worker where there are few, as fewer partial results are then
+  // joined (one sequence of 500 tokens and 8 key heads in tiles of 64: 9.0 us,
+  // 10.3 with two, 15.4 in tiles of 32 with one), but as many workers as there
+  // are key heads of sequences (69 sequences of 16 tokens, 2 key heads: 13 us
+  // without this).
+  const int64_t want = max((T + 3) / 4, (int64_t)a.batch * nhc);
   const int64_t G = want < a.workers ? want : a.workers;
   if ((int64_t)blockIdx.x >= G) return;
   Cursor<TK> c;

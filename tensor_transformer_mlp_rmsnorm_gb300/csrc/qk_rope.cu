@@ -58,9 +58,16 @@ struct Ahead {
 // of 80, the append 2% slower: it has more latency to hide behind other warps)
 constexpr int ROWS_BLOCKS[3] = {2, 3, 3}, BWD_BLOCKS = 2;
 
-__device__ __forceinline__ void cp_async16(void* smem, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(g)
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t smem) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem)
                : "memory");
+  return v;
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -102,18 +109,20 @@ struct Raw8<float> {
   }
 };
 
-// A lane's queue slot: chunk c of a step lies 32 lanes x 16 bytes apart, so a
-// warp's accesses are contiguous.
+// A lane's queue slot (a shared-memory address): chunk c of a step lies 32
+// lanes x 16 bytes behind the one before it, so a warp's accesses are
+// contiguous.
 template <typename T>
-__device__ __forceinline__ void queue_load(uint4* slot, int c, const T* g) {
+__device__ __forceinline__ void queue_load(uint32_t slot, int c, const T* g) {
 #pragma unroll
   for (int i = 0; i < Ahead<T>::CHUNK; ++i)
-    cp_async16(slot + (c * Ahead<T>::CHUNK + i) * 32, reinterpret_cast<const uint4*>(g) + i);
+    cp_async16(slot + (c * Ahead<T>::CHUNK + i) * 512, reinterpret_cast<const uint4*>(g) + i);
 }
-__device__ __forceinline__ void queue_get(const uint4* slot, int c, Raw8<__nv_bfloat16>& r) { r.v = slot[c * 32]; }
-__device__ __forceinline__ void queue_get(const uint4* slot, int c, Raw8<float>& r) {
-  r.a = *reinterpret_cast<const float4*>(slot + 2 * c * 32);
-  r.b = *reinterpret_cast<const float4*>(slot + (2 * c + 1) * 32);
+__device__ __forceinline__ void queue_get(uint32_t slot, int c, Raw8<__nv_bfloat16>& r) { r.v = lds16(slot + c * 512); }
+__device__ __forceinline__ void queue_get(uint32_t slot, int c, Raw8<float>& r) {
+  const uint4 x = lds16(slot + 2 * c * 512), y = lds16(slot + (2 * c + 1) * 512);
+  r.a = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
+  r.b = make_float4(__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w));
 }
 
 // A warp's items are (row, share of its heads).  `left` steps remain of the
@@ -307,7 +316,7 @@ template <typename T, int D, int KIND>
 __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS[KIND]) rope_rows_kernel(const __grid_constant__ RopeArgs a,
                                                                          const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
-  constexpr int S = Ahead<T>::ROWS, STEP = 2 * Ahead<T>::CHUNK * 32;  // a step's uint4 of a warp
+  constexpr int S = Ahead<T>::ROWS, STEP = 2 * Ahead<T>::CHUNK * 512;  // bytes of a warp's step
   extern __shared__ __align__(16) uint4 s_queue[];
   __shared__ __align__(16) float2 s_cs[WARPS][D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS[KIND]) rope_rows_kernel(c
   const bool turns = u < rot / 16;
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
-  uint4* const queue = s_queue + warp * S * STEP + lane;
+  const uint32_t queue = (uint32_t)__cvta_generic_to_shared(s_queue) + warp * S * STEP + lane * 16;
   __shared__ __align__(16) float s_w[2][D];
 
   Items items;
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS[KIND]) rope_rows_kernel(c
   bool more = items.enter(ld);
   st = ld;
   const T* src = static_cast<const T*>(a.in) + ld.row * a.ld_in;
-  auto load = [&](uint4* slot) {
+  auto load = [&](uint32_t slot) {
     if (ld.left > 0) {
       if (ld.h < end) {
         queue_load<T>(slot, 0, src + (ld.h * D + oa));
@@ -360,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS[KIND]) rope_rows_kernel(c
     for (int i = 0; i < S - 1; ++i) load(queue + i * STEP);
   }
   if (norm) stage_weights<T, D>(s_w, a.q_norm_w, a.k_norm_w);  // behind the first loads
-  uint4 *slot = queue, *fill = queue + (S - 1) * STEP;
+  uint32_t slot = queue, fill = queue + (S - 1) * STEP;
   float cs[8], sn[8];
   while (more) {
     // ---- a row
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS[KIND]) rope_rows_kernel(c
     for (; st.left > 0; --st.left, st.h += items.step) {
       load(fill);
       cp_wait<S - 1>();
-      const uint4* now = slot;
+      const uint32_t now = slot;
       fill = slot;
       slot = slot == queue + (S - 1) * STEP ? queue : slot + STEP;
       if (KIND && slot_off < 0) continue;  // a row that is nobody's
@@ -459,7 +468,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a,
                                                                        const __grid_constant__ RopeFreqs fr) {
   using HL = HeadLanes<D>;
-  constexpr int S = Ahead<T>::bwd(D), STEP = 4 * Ahead<T>::CHUNK * 32;
+  constexpr int S = Ahead<T>::bwd(D), STEP = 4 * Ahead<T>::CHUNK * 512;
   extern __shared__ __align__(16) uint4 s_queue[];
   __shared__ __align__(16) float2 s_cs[WARPS][D / 2];
   __shared__ float s_dw[WARPS][D];
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
   const bool turns = u < rot / 16;
   uint64_t turn[D / 64];
   load_turns<D>(fr, turn);
-  uint4* const queue = s_queue + warp * S * STEP + lane;
+  const uint32_t queue = (uint32_t)__cvta_generic_to_shared(s_queue) + warp * S * STEP + lane * 16;
   __shared__ __align__(16) float s_w[2][D];
   if (a.q_norm_w || a.k_norm_w) stage_weights<T, D>(s_w, a.q_norm_w, a.k_norm_w);
 #pragma unroll 1
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
       src = static_cast<const T*>(a.dout) + ld.row * a.ld_dout;
       srx = static_cast<const T*>(a.x) + ld.row * a.ld_x;
     };
-    auto load = [&](uint4* slot) {
+    auto load = [&](uint32_t slot) {
       if (ld.left > 0) {
         if (ld.h < end) {
           const int ha = ld.h * D + oa, hb = ld.h * D + ob;
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
 #pragma unroll
       for (int i = 0; i < S - 1; ++i) load(queue + i * STEP);
     }
-    uint4 *slot = queue, *fill = queue + (S - 1) * STEP;
+    uint32_t slot = queue, fill = queue + (S - 1) * STEP;
     while (more) {
       // ---- a row
       const int pos = a.pos ? a.pos[st.row] : (int)(a.seq > 0 ? st.row % a.seq : st.row);
@@ -538,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
       for (; st.left > 0; --st.left, st.h += items.step) {
         load(fill);
         cp_wait<S - 1>();
-        const uint4* q = slot;
+        const uint32_t q = slot;
         fill = slot;
         slot = slot == queue + (S - 1) * STEP ? queue : slot + STEP;
         const int h = st.h;
