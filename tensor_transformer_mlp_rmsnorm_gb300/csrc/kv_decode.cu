@@ -26,19 +26,19 @@
 // flight on an SM; it reads block-table entries a batch of boxes ahead.  Four
 // warps compute, each on its share of a tile's tokens for 8 query heads.  Two
 // warpgroups of 128 registers a thread are launched and the fetching one gives
-// 72 of them up: with 168 for all, heads of 256 values spilled and took 1.5
-// times as long.  Tokens that a window or the length hides are cleared in
+// 72 of them up: with 168 for all, heads of 256 values spilled and took 1.2 to
+// 1.9 times as long.  Tokens that a window or the length hides are cleared in
 // shared memory, only in the tiles that have some: masking the fragments put
-// branches between the products (8% at d = 128 with E4M3).
+// branches between the products (7% at d = 128 with E4M3).
 //
 // Measured on a GB300 (copy rate 6.68 TB/s): 64 sequences of up to 8192 tokens,
-// 8 key heads of 128, 32 query heads, bf16: 155 us, 6.6 TB/s; 128 such with
-// E4M3: 177 us, 5.9 TB/s, where the conversions of codes to f16 (two and a
-// shuffle for four codes) compete for issue slots; one of 131072 tokens: 86 us,
-// 6.2 TB/s, of which the two-level join is about 5 us.  Tiles of 64 tokens took
-// 168 us on the first: a tile costs a warp two waits and a chain of dependent
-// steps whatever its size.  Heads of 192 and 256 values keep 64, where a ring
-// of 128 would hold three operands or fewer.
+// 8 key heads of 128, 32 query heads, bf16: 154 us, 6.5 TB/s; 128 such with
+// E4M3: 168 us, 6.1 TB/s, where the conversions of codes to f16 (two and a
+// shuffle for four codes) keep the ALU half busy; one of 131072 tokens: 87 us,
+// 6.2 TB/s, of which the start and the two-level join are about 8 us.  Tiles of
+// 64 tokens took 168 us on the first: a tile costs a warp two waits and a chain
+// of dependent steps whatever its size.  Heads of 192 and 256 values keep 64,
+// where a ring of 128 would hold three operands or fewer (5 to 10% slower).
 //
 // Rounding.  Scores, maxima, sums and outputs are f32.  With a bf16 cache P is
 // the sum of two bf16 values (16 bits), because a single one would add as much

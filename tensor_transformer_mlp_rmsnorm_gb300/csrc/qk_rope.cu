@@ -26,10 +26,10 @@
 // its own copies is waited for, and no registers are held by loads in flight.
 //
 // Measured on a GB300 (copy rate 6.68 TB/s), bf16, 32 + 8 heads of 128, norms:
-// forward of 32768 rows 107 us, 6.3 TB/s; append of 16000 rows with 8 value
-// heads 69 us, 5.7 TB/s; backward of 8192 rows 55 us, 4.6 TB/s, bound by issue
-// slots (some 450 instructions a step for three operands, two sums and the
-// weight gradient; 256 values a head: 5.5 TB/s).  With the loads in registers
+// forward of 32768 rows 105 us, 6.4 TB/s; append of 16000 rows with 8 value
+// heads 68 us, 5.8 TB/s; backward of 8192 rows 52 us, 4.8 TB/s, bound by issue
+// slots (some 400 instructions a step for three operands, two sums and the
+// weight gradient; 256 values a head: 5.7 TB/s).  With the loads in registers
 // instead of the queue: 115, 78 and 58 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
