@@ -629,7 +629,8 @@ TPMLP_API tpmlp_status tpattn_set_qk(tpattn_ctx* ctx, const tpattn_qk_params* pa
 /* Store the keys and values of the last forward's prompts in a cache: sequence
  * b's first new_lens[b] tokens (device [batch]; NULL: all seq) at positions
  * 0, 1, ...  The cache's heads must be the sublayer's (TPMLP_ERR_SHAPE).  Runs
- * on the attention context's stream; cache errors are reported by tpkv_sync. */
+ * on the attention context's stream (as tpattn_decode does); cache errors are
+ * reported by tpkv_sync, behind a tpattn_sync where the streams differ. */
 TPMLP_API tpmlp_status tpattn_append_kv(tpattn_ctx* ctx, tpkv_ctx* kv, const int32_t* new_lens,
                                         const int32_t* block_table, int64_t ld_table, int32_t max_pages);
 

@@ -122,10 +122,11 @@ __device__ __forceinline__ uint32_t movm(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t lo16) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(lo16));
-  return r;
+// Four E4M3 codes as two pairs of f16: bytes 0 and 1, bytes 2 and 3.
+__device__ __forceinline__ void f16_of_e4m3(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
@@ -650,8 +651,9 @@ __global__ void __launch_bounds__(NTHR, 2)
           if (F8) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {  // chunk 2k + x
-              const uint32_t af[4] = {f16x2_of_e4m3x2(r[2 * x]), f16x2_of_e4m3x2(r[2 * x + 1]),
-                                      f16x2_of_e4m3x2(r[2 * x] >> 16), f16x2_of_e4m3x2(r[2 * x + 1] >> 16)};
+              uint32_t af[4];
+              f16_of_e4m3(r[2 * x], af[0], af[2]);
+              f16_of_e4m3(r[2 * x + 1], af[1], af[3]);
               mma16816<true>(sc[y], af, qf[(2 * k + x) % KS][0], qf[(2 * k + x) % KS][1]);
             }
           } else {
@@ -757,9 +759,7 @@ __global__ void __launch_bounds__(NTHR, 2)
             uint32_t ev[4], od[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const uint32_t s = __byte_perm(r[x], 0, 0x3120);
-              ev[x] = f16x2_of_e4m3x2(s);
-              od[x] = f16x2_of_e4m3x2(s >> 16);
+              f16_of_e4m3(__byte_perm(r[x], 0, 0x3120), ev[x], od[x]);
             }
             const uint32_t ea[4] = {ev[0], ev[2], ev[1], ev[3]}, oa[4] = {od[0], od[2], od[1], od[3]};
             mma16816<true>(o[(2 * i) % MT], ea, pf[y][0], pf[y][1]);
