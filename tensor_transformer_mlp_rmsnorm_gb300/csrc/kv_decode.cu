@@ -32,10 +32,10 @@
 // branches between the products (7% at d = 128 with E4M3).
 //
 // Measured on a GB300 (copy rate 6.68 TB/s): 64 sequences of up to 8192 tokens,
-// 8 key heads of 128, 32 query heads, bf16: 154 us, 6.5 TB/s; 128 such with
-// E4M3: 168 us, 6.1 TB/s, where the conversions of codes to f16 (two and a
-// shuffle for four codes) keep the ALU half busy; one of 131072 tokens: 87 us,
-// 6.2 TB/s, of which the start and the two-level join are about 8 us.  Tiles of
+// 8 key heads of 128, 32 query heads, bf16: 153 us, 6.5 TB/s; 128 such with
+// E4M3: 167 us, 6.1 TB/s, where the conversions of codes to f16 (two for four
+// codes) keep the ALU half busy; one of 131072 tokens: 86 us, 6.2 TB/s, of
+// which the start and the two-level join are about 8 us.  Tiles of
 // 64 tokens took 168 us on the first: a tile costs a warp two waits and a chain
 // of dependent steps whatever its size.  Heads of 192 and 256 values keep 64,
 // where a ring of 128 would hold three operands or fewer (5 to 10% slower).
@@ -80,6 +80,9 @@ struct Cfg {
   // Every computing warp works on every tile, so each waits for every use of a
   // slot: a barrier's one-bit phase is never asked about two rounds ahead.
   static constexpr int N = RING_BYTES / SLOT;
+  // Two head groups on one warp, so that a fragment is read and converted once
+  // for both, took 3 to 14% longer at 16 query heads: the chain of a tile
+  // (products, softmax, products) is then twice as long on each warp.
   static constexpr int KG = NCW / HG;                      // warps that share a tile's tokens
   static constexpr int KW = TK / KG;                       // tokens of a tile that a warp works on
   static constexpr int OD = 64;                            // columns of O joined at a time
