@@ -8,7 +8,9 @@
 // on together, so a cache byte meets at most 32 of them: some 32 flops a byte
 // in bf16, far below what even the mma.sync tensor path gives, which is why
 // the products use m16n8k16 with the keys (and for P V the head dimension) as
-// M and 8 query heads as N; a 128-row tcgen05 tile would be all padding.
+// M and 8 query heads as N.  tcgen05 with 128 keys as M would hand scores and P
+// through TMEM and shared memory for 8 columns of work: nothing to gain at up to
+// 8 query heads a key head, where the kernel runs at 89 to 98% of the copy rate (d = 128).
 //
 // The split.  The cache is cut into tiles of 64 or 128 tokens; the tiles of
 // every (sequence, key head) laid end to end are divided evenly over two CTAs
