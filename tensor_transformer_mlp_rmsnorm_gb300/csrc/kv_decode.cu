@@ -811,13 +811,15 @@ __global__ void __launch_bounds__(NTHR, 2)
       for (int w = 1; w < KG; ++w) mx = fmaxf(mx, s_m[w][h]);
       al[e] = mx == -INFINITY ? 0.0f : ex2_fast(m[e] - mx);
     }
+    // (max drops NaN: where every score of a warp is one its maximum stays -inf,
+    // and its sum carries the NaN, so no sum is replaced by 0)
     if (tid < HT) {
       float mx = s_m[0][tid];
 #pragma unroll
       for (int w = 1; w < KG; ++w) mx = fmaxf(mx, s_m[w][tid]);
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < KG; ++w) s += mx == -INFINITY ? 0.0f : s_l[w][tid] * ex2_fast(s_m[w][tid] - mx);
+      for (int w = 0; w < KG; ++w) s += s_l[w][tid] * ex2_fast(s_m[w][tid] - (mx == -INFINITY ? 0.0f : mx));
       if (direct) {
         s_inv[tid] = s > 0.0f ? vscale / s : (s == s ? 0.0f : s);
         if (lse && tid < heads) lse[tid] = s == 0.0f ? -INFINITY : (mx + log2f(s)) * 0.69314718055994531f;

@@ -1,0 +1,58 @@
+"""The cache calls where the formulas meet NaN, infinities and extreme weights, and their smallest calls."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _attn_ops as R
+from tests._util import to_np
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+def _cache(n, nkv, d, kind, page=16, seed=1):
+    """Key and value pages of one sequence of n tokens in order, and its table."""
+    pages = max(1, (n + page - 1) // page)
+    g = torch.Generator().manual_seed(seed)
+    kv = [torch.randn((pages, nkv, page, d), generator=g).to(torch.bfloat16 if kind == "bf16" else E4M3).cuda()
+          for _ in "kv"]
+    return kv[0], kv[1], torch.arange(pages, **I32)[None, :]
+
+
+def _set_keys(k, first, last, value):
+    """Every component of the keys of tokens [first, last) of the only sequence."""
+    raw = k.view(torch.uint8) if k.dtype == E4M3 else k
+    t = torch.arange(first, last, device="cuda")
+    raw[t // k.shape[2], :, t % k.shape[2]] = value
+
+
+# n tokens: one part; several joined at once; groups of parts and then their leaders
+@pytest.mark.parametrize("n", [100, 2000, 9000])
+@pytest.mark.parametrize("kind,d,nq", [("bf16", 64, 2), ("e4m3", 128, 12), ("bf16", 192, 3), ("e4m3", 256, 20)])
+def test_nan_scores_reach_the_lse(n, kind, d, nq):
+    """A head whose scores hold a NaN has NaN for its log-sum-exp, as for its output; the others are as without it."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    k, v, table = _cache(n, 1, d, kind)
+    kv = T.TPKV(k, v, nq, max_batch=1)
+    q = torch.randn(1, nq * d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    lens = torch.tensor([n], **I32)
+    ref, ref_lse = kv.decode(q, lens, table, return_lse=True)
+    assert ref_lse.isfinite().all()
+    # a NaN in one query: every one of its scores
+    bad = q.clone()
+    bad[0, d + 5] = float("nan")
+    out, lse = kv.decode(bad, lens, table, return_lse=True)
+    kv.sync()
+    keep = torch.arange(nq, device="cuda") != 1
+    assert out.view(nq, d)[1].isnan().all() and lse[0, 1].isnan()
+    assert torch.equal(out.view(nq, d)[keep], ref.view(nq, d)[keep]) and torch.equal(lse[0, keep], ref_lse[0, keep])
+    # NaN keys in the first part of the sequence, wherever it is split: every head
+    nan = 0x7F if kind == "e4m3" else float("nan")
+    _set_keys(k, 0, min(n, 600), nan)
+    out, lse = kv.decode(q, lens, table, return_lse=True)
+    kv.sync()
+    assert out.isnan().all() and lse.isnan().all()
