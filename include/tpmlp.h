@@ -594,7 +594,8 @@ TPMLP_API tpmlp_status tpkv_append(tpkv_ctx* ctx, int64_t rows, int32_t batch, c
  *  q bf16 [batch, n_heads d] (row stride ld_q) -> out bf16 [batch, n_heads d]
  *  (row stride ld_out; may be q), lse float [batch, n_heads] or NULL: the
  *  natural log of the sum of exp(scale q.k); a sequence without visible tokens
- *  gets out 0 and lse -inf.  len_add 1 attends to a token just appended with
+ *  gets out 0 and lse -inf; a head whose scores are all -inf gets out NaN and
+ *  lse -inf, one with a NaN score NaN for both.  len_add 1 attends to a token just appended with
  *  past_lens = lens.  Nothing behind a sequence's last visible token, in
  *  pages or table, influences the result.  Repeated calls give the same bits. */
 TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, int64_t ld_q, const int32_t* lens,

@@ -2,7 +2,8 @@
 //
 //   s_t = scale q . k_t over the visible tokens t < len (with a window: the
 //   last `window` tokens and the first `sinks`),  out = softmax(s) V,
-//   lse = log sum exp s.  No visible token: out 0, lse -inf.
+//   lse = log sum exp s.  No visible token: out 0, lse -inf.  Scores that are
+//   all -inf: out NaN, as 0 / 0 has it, lse -inf.
 //
 // What bounds it: reading the cache once.  A key head's query heads are worked
 // on together, so a cache byte meets at most 32 of them: some 32 flops a byte
@@ -301,7 +302,8 @@ __device__ __forceinline__ void join_parts(const JoinArgs& a, volatile int* s_la
         const int x = x0 + q * NCW * 32, h = 4 * x / D, col = 4 * x % D;
         const float s = sum[q];
         if (final_level) {
-          const float r = s > 0.0f ? a.vscale / s : (s == s ? 0.0f : s);
+          // (a sequence without tokens is one tile and never comes here)
+          const float r = s > 0.0f ? a.vscale / s : NAN;
           if (h < a.heads) {
             *reinterpret_cast<uint2*>(a.out + (int64_t)h * D + col) =
                 make_uint2(pack_bf16(v[q].x * r, v[q].y * r), pack_bf16(v[q].z * r, v[q].w * r));
@@ -821,7 +823,7 @@ __global__ void __launch_bounds__(NTHR, 2)
 #pragma unroll
       for (int w = 0; w < KG; ++w) s += s_l[w][tid] * ex2_fast(s_m[w][tid] - (mx == -INFINITY ? 0.0f : mx));
       if (direct) {
-        s_inv[tid] = s > 0.0f ? vscale / s : (s == s ? 0.0f : s);
+        s_inv[tid] = s > 0.0f ? vscale / s : seq.len > 0 ? NAN : 0.0f;
         if (lse && tid < heads) lse[tid] = s == 0.0f ? -INFINITY : (mx + log2f(s)) * 0.69314718055994531f;
       } else {
         __stcg(my_part + (size_t)HT * D + tid, mx);

@@ -56,3 +56,28 @@ def test_nan_scores_reach_the_lse(n, kind, d, nq):
     out, lse = kv.decode(q, lens, table, return_lse=True)
     kv.sync()
     assert out.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("n", [100, 2000, 9000])
+@pytest.mark.parametrize("d,nq", [(64, 2), (128, 20), (256, 9)])
+def test_scores_of_minus_infinity(n, d, nq):
+    """softmax of scores that are all -inf is NaN, as the formula has it; one finite score takes all the weight; a
+    sequence without tokens keeps its 0."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    k, v, table = _cache(n, 1, d, "bf16")
+    k.zero_()
+    k[..., 3] = float("-inf")
+    kv = T.TPKV(k, v, nq, max_batch=1)
+    q = torch.ones(1, nq * d, dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([n], **I32)
+    out, lse = kv.decode(q, lens, table, return_lse=True)
+    kv.sync()
+    assert out.isnan().all() and torch.equal(lse, torch.full_like(lse, float("-inf")))
+    at = n - 7
+    k[at // 16, 0, at % 16, 3] = 0.0
+    out, lse = kv.decode(q, lens, table, return_lse=True)
+    kv.sync()
+    assert torch.equal(out.view(nq, d), v[at // 16, 0, at % 16].expand(nq, d)) and not lse.any()
+    out, lse = kv.decode(q, torch.zeros(1, **I32), table, return_lse=True)
+    kv.sync()
+    assert not out.any() and torch.equal(lse, torch.full_like(lse, float("-inf")))
