@@ -940,9 +940,9 @@ class TPKV:
     def _table(self, t, batch: int):
         shape = t.shape
         if (len(shape) != 2 or t.dtype is not _I32T or shape[0] != batch or t.get_device() != self.index
-                or (shape[1] > 1 and t.stride(1) != 1)):
-            raise _bad(t, "block_table", f"int32 [{batch}, pages] on cuda:{self.index}")
-        return t.data_ptr(), max(t.stride(0), shape[1]), shape[1]
+                or (shape[1] > 1 and t.stride(1) != 1) or (batch > 1 and t.stride(0) < shape[1])):
+            raise _bad(t, "block_table", f"int32 [{batch}, pages] on cuda:{self.index}, a row of its own for each sequence")
+        return t.data_ptr(), t.stride(0) if batch > 1 else shape[1], shape[1]
 
     def append(self, qkv, past_lens, block_table, cu_rows=None, new_lens=None, q_out=None, transform: bool = True,
                with_queries: bool = True):
