@@ -497,7 +497,8 @@ typedef struct {
 
 /* out = rotated (normed) rows of x.  ld_x, ld_out: row strides in elements,
  * multiples of 8.  `rot` NULL: no rotation.  out may be x itself with the same
- * stride (in place); otherwise the two must not overlap.  Columns behind the
+ * stride (in place; a single row has no use for its stride); otherwise the two
+ * must not overlap.  Columns behind the
  * (n_heads + n_kv_heads) * head_dim first are neither read nor written. */
 TPMLP_API tpmlp_status tpattn_qk_rope_forward(const tpattn_qk_desc* desc, const tpattn_rotary* rot, const void* x,
                                               int64_t ld_x, void* out, int64_t ld_out, void* cuda_stream);

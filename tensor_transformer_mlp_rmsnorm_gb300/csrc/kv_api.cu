@@ -182,7 +182,7 @@ tpmlp_status tpattn_qk_rope_forward(const tpattn_qk_desc* q, const tpattn_rotary
   const bool empty = q->rows == 0 || width == 0;
   KV_TRY(check_rows("x is NULL", x, ld_x, width, empty));
   KV_TRY(check_rows("out is NULL", out, ld_out, width, empty));
-  if (x == out && ld_x != ld_out) return bad(TPMLP_ERR_ARG, "in place needs equal strides");
+  if (x == out && ld_x != ld_out && q->rows > 1) return bad(TPMLP_ERR_ARG, "in place needs equal strides");
   if (empty) return TPMLP_OK;
   int sms = 0;
   KV_TRY(current_sms(&sms));
@@ -217,7 +217,7 @@ tpmlp_status tpattn_qk_rope_backward(const tpattn_qk_desc* q, const tpattn_rotar
   if (norm) KV_TRY(check_rows("x is NULL", x, ld_x, width, empty));
   KV_TRY(check_rows("dout is NULL", dout, ld_dout, width, empty));
   KV_TRY(check_rows("dx is NULL", dx, ld_dx, width, empty));
-  if (dout == dx && ld_dout != ld_dx) return bad(TPMLP_ERR_ARG, "in place needs equal strides");
+  if (dout == dx && ld_dout != ld_dx && q->rows > 1) return bad(TPMLP_ERR_ARG, "in place needs equal strides");
   if (!q->q_norm_w != !dq_norm_w || !q->k_norm_w != !dk_norm_w)
     return bad(TPMLP_ERR_ARG, "weight gradients are given exactly for the norm weights");
   if (!a16(dq_norm_w) || !a16(dk_norm_w)) return bad(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
@@ -376,7 +376,7 @@ tpmlp_status tpkv_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q
   if (rows == 0 || batch == 0) return TPMLP_OK;
   if (!qkv) return c->fail(TPMLP_ERR_ARG, "qkv is NULL");
   if (!a16(qkv) || !a16(q_out)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
-  if (q_out == qkv && ld_q != ld_qkv) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
+  if (q_out == qkv && ld_q != ld_qkv && rows > 1) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
   QkTransform tr;
   if (transform) tr = {&c->freqs, c->q_norm_w, c->k_norm_w, c->eps};
   return kv_run_append(c, rows, batch, qkv, ld_qkv, cu_rows, new_lens, past_lens, table, ld_table, max_pages, tr,
@@ -397,7 +397,7 @@ tpmlp_status tpkv_decode(tpkv_ctx* c, int32_t batch, const void* q, int64_t ld_q
   if (!q || !out) return c->fail(TPMLP_ERR_ARG, "NULL tensor");
   if (!a16(q) || !a16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
-  if (q == out && ld_q != ld_out) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
+  if (q == out && ld_q != ld_out && batch > 1) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
   return kv_run_decode(c, batch, q, ld_q, lens, len_add, table, ld_table, max_pages, scale, window, sinks, out, ld_out,
                        lse, c->stream);
 }

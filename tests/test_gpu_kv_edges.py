@@ -81,3 +81,56 @@ def test_scores_of_minus_infinity(n, d, nq):
     out, lse = kv.decode(q, torch.zeros(1, **I32), table, return_lse=True)
     kv.sync()
     assert not out.any() and torch.equal(lse, torch.full_like(lse, float("-inf")))
+
+
+@pytest.mark.parametrize("inplace", ["rows", "columns"])
+@pytest.mark.parametrize("n", [1, 2])
+@pytest.mark.parametrize("transform", [True, False])
+def test_append_in_place_of_one_row(n, inplace, transform):
+    """Queries written over their own columns, for a single row too."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    nq, nkv, d = 6, 2, 128
+    x = torch.randn((n, (nq + 2 * nkv) * d), generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda()
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    past, table = torch.full((n,), 5, **I32), torch.arange(n, **I32)[:, None]
+    got = []
+    for where in ("apart", inplace):
+        k, v = (torch.zeros(n, nkv, 16, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        kv = T.TPKV(k, v, nq, max_batch=n)
+        kv.set_rotary(T.Rotary(d), w, w, 1e-6)
+        rows = x.clone()
+        q_out = {"apart": None, "rows": rows, "columns": rows[:, : nq * d]}[where]
+        q = kv.append(rows, past, table, q_out=q_out, transform=transform)
+        kv.sync()
+        got.append((q[:, : nq * d].clone(), k, v))
+        if where != "apart":
+            assert torch.equal(rows[:, nq * d:], x[:, nq * d:])
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][1].any()
+
+
+def test_strides_of_a_single_row_do_not_matter():
+    """The C calls in place with one row: its strides are of no use, so they may differ."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    d, nq = 64, 2
+    L, s = T.lib(), torch.cuda.current_stream().cuda_stream
+    x = torch.randn(1, 512, device="cuda").to(torch.bfloat16)
+    r = T.Rotary(d)
+    want = T.qk_norm_rope(x, nq, 1, d, r, torch.tensor([9], **I32))
+    pos = torch.tensor([9], **I32)
+    desc = T.tpmlp.QkDesc(1, nq, 1, d, T.BF16, pos.data_ptr(), 0, None, None, 1e-6, 0)
+    y = x.clone()
+    assert L.tpattn_qk_rope_forward(desc, r.spec, y.data_ptr(), 256, y.data_ptr(), 192, s) == 0
+    assert torch.equal(y[:, :192], want) and torch.equal(y[:, 192:], x[:, 192:])
+    wdx = T.qk_norm_rope_backward(want, None, nq, 1, d, r, pos)[0]
+    z = want.clone()
+    assert L.tpattn_qk_rope_backward(desc, r.spec, None, 0, z.data_ptr(), 192, z.data_ptr(), 256, None, None, None, 0,
+                                     s) == 0
+    assert torch.equal(z, wdx)
+    k, v, table = _cache(50, 1, d, "bf16")
+    kv = T.TPKV(k, v, nq, max_batch=1)
+    q, lens = x[:, : nq * d].contiguous(), torch.tensor([50], **I32)
+    out = kv.decode(q, lens, table)
+    assert L.tpkv_decode(kv.ctx, 1, q.data_ptr(), 128, lens.data_ptr(), 0, table.data_ptr(), table.shape[1],
+                         table.shape[1], d ** -0.5, 0, 0, q.data_ptr(), 256, None) == 0
+    kv.sync()
+    assert torch.equal(q, out)
