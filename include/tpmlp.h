@@ -553,7 +553,9 @@ typedef struct {
 
 TPMLP_API size_t tpkv_workspace_bytes(const tpkv_config* cfg);
 TPMLP_API tpmlp_status tpkv_create(const tpkv_config* cfg, void* cuda_stream, tpkv_ctx** out);
-/* As tpmlp_bind_workspace (tpkv_workspace_bytes, 256-byte aligned). */
+/* As tpmlp_bind_workspace (tpkv_workspace_bytes, 256-byte aligned).  It is
+ * cleared on the context's stream; launches on another stream (tpkv_set_stream,
+ * the sublayer's calls) wait for that, captured ones by holding the host. */
 TPMLP_API tpmlp_status tpkv_bind_workspace(tpkv_ctx* ctx, void* dev, size_t bytes);
 TPMLP_API tpmlp_status tpkv_set_stream(tpkv_ctx* ctx, void* cuda_stream);
 /* The cache, strides in elements, each a multiple of 16 bytes and positive;

@@ -145,6 +145,41 @@ struct OnDevice {
   }
 };
 
+// Clears `bytes` of the workspace on the context's stream; launches on other
+// streams wait for it (wait_for_clear).
+cudaError_t clear_workspace(tpkv_ctx* c, void* p, size_t bytes) {
+  cudaError_t e = cudaMemsetAsync(p, 0, bytes, c->stream);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (e == cudaSuccess) e = cudaStreamIsCapturing(c->stream, &cap);
+  if (e != cudaSuccess) return e;
+  c->clear_pending = cap == cudaStreamCaptureStatusNone;  // in a graph it is ordered by the graph
+  if (!c->clear_pending) return cudaSuccess;
+  c->clear_stream = c->clear_seen = c->stream;
+  return cudaEventRecord(c->cleared, c->stream);
+}
+
+// Orders what is launched on `st` next behind the last clear.  A captured
+// launch cannot wait for an event from outside its graph, so the host does.
+cudaError_t wait_for_clear(tpkv_ctx* c, cudaStream_t st) {
+  if (!c->clear_pending) return cudaSuccess;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(st, &cap);
+  if (e != cudaSuccess) return e;
+  if (cap != cudaStreamCaptureStatusNone) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    e = cudaEventSynchronize(c->cleared);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) c->clear_pending = false;
+    return e != cudaSuccess ? e : back;
+  }
+  if (st == c->clear_stream || st == c->clear_seen) return cudaSuccess;
+  e = cudaStreamWaitEvent(st, c->cleared, 0);
+  if (e == cudaSuccess) c->clear_seen = st;
+  return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -274,6 +309,12 @@ tpmlp_status tpkv_create(const tpkv_config* cfg, void* stream, tpkv_ctx** out) {
     g_kv_err = "out of host memory";
     return TPMLP_ERR_CUDA;
   }
+  const cudaError_t e = cudaEventCreateWithFlags(&c->cleared, cudaEventDisableTiming);
+  if (e != cudaSuccess) {
+    g_kv_err = cudaGetErrorString(e);
+    delete c;
+    return TPMLP_ERR_CUDA;
+  }
   c->cfg = *cfg;
   c->stream = static_cast<cudaStream_t>(stream);
   c->device = dev;
@@ -294,7 +335,7 @@ tpmlp_status tpkv_bind_workspace(tpkv_ctx* c, void* dev, size_t bytes) {
   if (bytes < L.total) return c->fail(TPMLP_ERR_ARG, "workspace too small");
   OnDevice on(c->device);
   // the status word and the arrival counters; partial results need no initial contents
-  const cudaError_t e = cudaMemsetAsync(dev, 0, L.part, c->stream);
+  const cudaError_t e = clear_workspace(c, dev, L.part);
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
   uint8_t* w = static_cast<uint8_t*>(dev);
   c->status = reinterpret_cast<uint32_t*>(w + L.status);
@@ -408,23 +449,28 @@ tpmlp_status tpkv_sync(tpkv_ctx* c) {
   cudaError_t e = cudaStreamSynchronize(c->stream);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
+  if (c->clear_stream == c->stream) c->clear_pending = false;  // it is done
   if (!c->status) return TPMLP_OK;
   uint32_t st = 0;
   e = cudaMemcpy(&st, c->status, sizeof st, cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
   if (!st) return TPMLP_OK;
-  cudaMemsetAsync(c->status, 0, sizeof st, c->stream);
-  if (st & STATUS_TIMEOUT) {
-    // a CTA that gave up has not counted its arrival: the counters start anew
-    cudaMemsetAsync(c->counters, 0, 3 * (size_t)KV_MAX_WORKERS * sizeof(uint32_t), c->stream);
-    return c->fail(TPMLP_ERR_TIMEOUT, "a bounded device wait gave up");
-  }
+  // a CTA that gave up has not counted its arrival: the counters, which lie
+  // behind the status word, then start anew too
+  const KvLayout L = kv_layout(c->cfg);
+  e = clear_workspace(c, c->status, st & STATUS_TIMEOUT ? L.part - L.status : sizeof st);
+  if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
+  if (st & STATUS_TIMEOUT) return c->fail(TPMLP_ERR_TIMEOUT, "a bounded device wait gave up");
   return c->fail(TPMLP_ERR_ARG, "a page or a length was outside the cache");
 }
 
 uint64_t tpkv_launch_count(const tpkv_ctx* c) { return c ? c->launches : 0; }
 const char* tpkv_last_error(const tpkv_ctx* c) { return c ? c->err : g_kv_err; }
-void tpkv_destroy(tpkv_ctx* c) { delete c; }
+void tpkv_destroy(tpkv_ctx* c) {
+  if (!c) return;
+  cudaEventDestroy(c->cleared);
+  delete c;
+}
 
 }  // extern "C"
 
@@ -478,8 +524,10 @@ tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void*
   a.v_inv_scale = c->v_inv_scale;
   a.status = c->status;
   OnDevice on(c->device);
-  const cudaError_t e = launch_kv_append(cf.cache_dtype == TPKV_E4M3, cf.head_dim, a,
-                                         tr.freqs ? *tr.freqs : RopeFreqs{}, c->num_sms, st);
+  cudaError_t e = wait_for_clear(c, st);
+  if (e == cudaSuccess)
+    e = launch_kv_append(cf.cache_dtype == TPKV_E4M3, cf.head_dim, a, tr.freqs ? *tr.freqs : RopeFreqs{}, c->num_sms,
+                         st);
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
   ++c->launches;
   return TPMLP_OK;
@@ -519,7 +567,8 @@ tpmlp_status kv_run_decode(tpkv_ctx* c, int32_t batch, const void* q, int64_t ld
   a.counters = c->counters;
   a.status = c->status;
   OnDevice on(c->device);
-  const cudaError_t e = launch_kv_decode(a, c->kmap, c->vmap, cf.head_dim, cf.cache_dtype == TPKV_E4M3, st);
+  cudaError_t e = wait_for_clear(c, st);
+  if (e == cudaSuccess) e = launch_kv_decode(a, c->kmap, c->vmap, cf.head_dim, cf.cache_dtype == TPKV_E4M3, st);
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
   ++c->launches;
   return TPMLP_OK;

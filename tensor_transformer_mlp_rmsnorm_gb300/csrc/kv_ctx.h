@@ -19,6 +19,11 @@ struct tpkv_ctx {
   int device = 0, num_sms = 0, box_tokens = 64, workers = 0;
   uint32_t *status = nullptr, *counters = nullptr;
   float* part = nullptr;
+  // The clears of status and counters: an event behind them until the host has
+  // seen it, their stream, and the last other stream that waits for it.
+  cudaEvent_t cleared = nullptr;
+  bool clear_pending = false;
+  cudaStream_t clear_stream = nullptr, clear_seen = nullptr;
   void *k = nullptr, *v = nullptr;
   int64_t stride_page = 0, stride_head = 0, stride_slot = 0;
   const float *k_inv_scale = nullptr, *v_inv_scale = nullptr;
