@@ -1052,8 +1052,14 @@ cudaError_t launch_inst(const Maps& mp, const TcParams& p, int num_sms, cudaStre
       q.split_first = q.num_tiles - r;
       q.num_units = q.split_first + r * S;
       // Arrival flags are not reset: a flag counts only when it holds this
-      // launch's epoch, which no earlier launch wrote.
+      // launch's epoch, which no earlier launch wrote.  A captured launch has
+      // one epoch for all its replays, so there each replay clears the flags.
       q.epoch = next_split_epoch();
+      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+      cudaError_t e = cudaStreamIsCapturing(st, &cap);
+      if (e == cudaSuccess && cap != cudaStreamCaptureStatusNone)
+        e = cudaMemsetAsync(q.counters, 0, (size_t)r * 8 * (S - 1) * sizeof(uint32_t), st);
+      if (e != cudaSuccess) return e;
     }
   }
   const int workers = q.num_units < W ? q.num_units : W;

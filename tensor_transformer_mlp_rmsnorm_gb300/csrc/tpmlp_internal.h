@@ -79,10 +79,11 @@ struct GemmDesc {
   // accumulators in `split_scratch` and count their arrival in
   // `split_counters` by writing the launch's epoch there, and the first
   // part adds the partials in part order.  NULL disables the split.  The
-  // flags are zeroed when the workspace is bound and epochs are unique in
-  // the process (so workspaces shared between contexts stay safe); a 32-bit
-  // epoch repeats after 2^32 - 1 split launches, and a stale flag could then
-  // match only if its slot had gone unwritten for all of them.
+  // flags are zeroed when the workspace is bound and by each replay of a
+  // captured launch (whose epoch stays the same), and epochs are unique in the
+  // process (so workspaces shared between contexts stay safe); a 32-bit epoch
+  // repeats after 2^32 - 1 split launches, and a stale flag could then match
+  // only if its slot had gone unwritten for all of them.
   float* split_scratch = nullptr;
   size_t split_scratch_bytes = 0;
   uint32_t* split_counters = nullptr;
