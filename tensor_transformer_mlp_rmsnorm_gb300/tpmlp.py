@@ -501,7 +501,11 @@ def _acheck(status: int, ctx=None):
 
 class TPAttn:
     """The tensor-parallel attention sublayer through the C ABI (tpattn_*):
-    bf16 tensors on one CUDA device; the workspace is a torch uint8 tensor."""
+    bf16 tensors on one CUDA device; the workspace is a torch uint8 tensor.
+
+    Calls run on ``stream`` (torch's current stream at construction unless given).  Where another one is current at a
+    call, ordering the two is the caller's; the memory of what the call uses is not handed out again before the
+    stream is past it."""
 
     def __init__(self, max_tokens: int, hidden: int, n_heads: int, n_kv_heads: int, head_dim: int,
                  max_seq: int, max_t: int = 8, device=None, stream=None, fused_only: bool = False):
@@ -515,7 +519,7 @@ class TPAttn:
         self.W = (n_heads + 2 * n_kv_heads) * head_dim
         self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
         ctx = ctypes.c_void_p()
-        with torch.cuda.device(dev):
+        with torch.cuda.device(dev), torch.cuda.stream(self.stream):  # the workspace belongs to that stream
             _acheck(lib().tpattn_create(ctypes.byref(self.cfg), self.stream.cuda_stream, ctypes.byref(ctx)))
             self.ctx = ctx
             nbytes = int(lib().tpattn_workspace_bytes(ctypes.byref(self.cfg)))
@@ -535,6 +539,12 @@ class TPAttn:
         except Exception:
             pass
 
+    def _uses(self, *tensors):
+        """Keeps the memory of a call's tensors from reuse until the stream is past the call, where they may belong to
+        another stream."""
+        if _stream_of(self.device, self.device.index) != self.stream.cuda_stream:
+            _record(self.stream, *tensors)
+
     def _t(self, t, shape, dtype=torch.bfloat16, name="tensor"):
         if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
             raise TPMLPError(ERR_ARG, f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}")
@@ -549,6 +559,7 @@ class TPAttn:
                                      self._t(w_o, (self.H, self.nq * self.d), name="w_o"),
                                      self._t(b_o, (self.H,), name="b_o"), float(eps), int(t),
                                      self._t(y, (n, self.H), name="y")), self.ctx)
+        self._uses(x, norm_w, w_qkv, w_o, b_o, y)
         # the library keeps these pointers (backward reads x; the updates write the parameters):
         # hold the tensors until the next forward so that a temporary argument is not freed
         self._fwd_tensors = (x, norm_w, w_qkv, w_o, b_o)
@@ -573,6 +584,7 @@ class TPAttn:
                                       self._t(g["w_qkv"], (self.W, self.H), f32, "dw_qkv"),
                                       self._t(g["w_o"], (self.H, self.nq * self.d), f32, "dw_o"),
                                       self._t(g["b_o"], (self.H,), f32, "db_o")), self.ctx)
+        self._uses(dy, dx, *g.values())
         # the updates read these gradients later: hold them until the next backward
         self._grads = g
         return dx, g
@@ -588,6 +600,7 @@ class TPAttn:
                                          self._t(m["w_o"], (self.H, self.nq * self.d), f32, "w_o"),
                                          self._t(m["b_o"], (self.H,), f32, "b_o")), self.ctx)
         self._masters = m
+        self._uses(*m.values())
 
     def sgd_step(self, lr: float):
         _acheck(lib().tpattn_sgd_step(self.ctx, float(lr)), self.ctx)
@@ -622,18 +635,21 @@ class TPAttn:
         ms, vs = self._param_set(m, "m"), self._param_set(v, "v")
         _acheck(lib().tpattn_bind_adam_state(self.ctx, ctypes.byref(ms), ctypes.byref(vs)), self.ctx)
         self._adam = (m, v)  # keep the tensors alive while bound
+        self._uses(*m.values(), *v.values())
 
     def adamw_step(self, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                    weight_decay: float = 0.1, max_grad_norm: float = 1.0, grad_norm=None):
         """One clipped AdamW update; returns the device float holding the global gradient norm."""
         if grad_norm is None:
             if getattr(self, "_gn", None) is None:
-                self._gn = torch.zeros(1, dtype=torch.float32, device=self.device)
+                with torch.cuda.stream(self.stream):
+                    self._gn = torch.zeros(1, dtype=torch.float32, device=self.device)
             grad_norm = self._gn
         hp = AdamWParams(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
                          float(max_grad_norm), int(step))
         _acheck(lib().tpattn_adamw_step(self.ctx, ctypes.byref(hp),
                                         self._t(grad_norm, (1,), torch.float32, "grad_norm")), self.ctx)
+        self._uses(grad_norm)
         return grad_norm
 
     def set_qk(self, rotary: Rotary | None = None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6, masters=None,
@@ -654,8 +670,10 @@ class TPAttn:
                 setattr(p, name, _vec(t, d, _F32T, name, i))
         p.eps = float(eps)
         nbytes = int(lib().tpattn_qk_workspace_bytes(ctypes.byref(self.cfg))) if norm else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if norm else None
+        with torch.cuda.stream(self.stream):  # the rows and sums belong to the stream that its kernels run on
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if norm else None
         _acheck(lib().tpattn_set_qk(self.ctx, ctypes.byref(p), _ptr(ws), nbytes), self.ctx)
+        self._uses(q_norm_w, k_norm_w, *(masters or ()), *(moments or ()), *grads.values())
         self._qk = (rotary, q_norm_w, k_norm_w, masters, moments, grads, ws)  # the context keeps their pointers
         return grads
 
@@ -672,6 +690,8 @@ class TPAttn:
         tp, ldt, pages = kv._table(block_table, batch)
         _acheck(lib().tpattn_append_kv(self.ctx, kv.ctx, _vec(new_lens, batch, _I32T, "new_lens", self.device.index),
                                        tp, ldt, pages), self.ctx)
+        self._uses(block_table, new_lens)
+        kv._used_by(self.stream)
 
     def decode(self, kv: TPKV, x, norm_w, w_qkv, w_o, b_o, eps: float, t: int, past_lens, block_table, window: int = 0,
                sinks: int = 0, y=None):
@@ -687,6 +707,8 @@ class TPAttn:
                                     self._t(b_o, (self.H,), name="b_o"), float(eps), int(t),
                                     _vec(past_lens, n, _I32T, "past_lens", self.device.index), tp, ldt, pages, window,
                                     sinks, self._t(y, (n, self.H), name="y")), self.ctx)
+        self._uses(x, norm_w, w_qkv, w_o, b_o, past_lens, block_table, y)
+        kv._used_by(self.stream)
         return y
 
     def sync(self):
@@ -737,6 +759,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream_of(device, index: int):
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _record(stream, *tensors):
+    """Their memory is handed out again only when `stream` is past what it holds now (nothing to do for its own)."""
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
 
 
 def _bad(t, name: str, want: str):
@@ -800,6 +829,7 @@ def qk_norm_rope(x, n_heads: int, n_kv_heads: int, head_dim: int, rotary: Rotary
     row of x (tpattn_qk_rope_forward); out may be x.  Positions: int32 per row, or row % seq (seq 0: the row).
     Runs on `stream`, torch's current stream where it is None."""
     if stream is not None:  # what is allocated here belongs to that stream too
+        _record(stream, x, positions, q_norm_w, k_norm_w, out)
         with torch.cuda.stream(stream):
             return qk_norm_rope(x, n_heads, n_kv_heads, head_dim, rotary, positions, seq, q_norm_w, k_norm_w, eps, out)
     width, dtype, index = (n_heads + n_kv_heads) * head_dim, x.dtype, _cuda_index(x, "x")
@@ -819,6 +849,7 @@ def qk_norm_rope_backward(dout, x, n_heads: int, n_kv_heads: int, head_dim: int,
     """Backward of qk_norm_rope: (dx, dq_norm_w, dk_norm_w), the weights' gradients in float32 (None without the
     weight).  x: the forward's input (only read with norm weights, else it may be None); dx may be dout."""
     if stream is not None:  # what is allocated here belongs to that stream too
+        _record(stream, dout, x, positions, q_norm_w, k_norm_w, dx, dq_norm_w, dk_norm_w, workspace)
         with torch.cuda.stream(stream):
             return qk_norm_rope_backward(dout, x, n_heads, n_kv_heads, head_dim, rotary, positions, seq, q_norm_w,
                                          k_norm_w, eps, dx, dq_norm_w, dk_norm_w, workspace)
@@ -894,6 +925,8 @@ class TPKV:
             nbytes = int(lib().tpkv_workspace_bytes(ctypes.byref(self.cfg)))
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self._ck(lib().tpkv_bind_workspace(ctx, self.workspace.data_ptr(), nbytes))
+        if self._fixed is not None:
+            _record(self._fixed, *self._held())
         f32 = torch.float32
         self._ck(lib().tpkv_bind_cache(ctx, k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
                                        _vec(self._scales[0], self.nkv, f32, "k_inv_scale", self.index),
@@ -924,11 +957,21 @@ class TPKV:
         """Whether torch's current stream is not the fixed one."""
         return self._fixed is not None and _stream_of(self.device, self.index) != self._fixed.cuda_stream
 
+    def _held(self):
+        """What the context keeps by pointer."""
+        return self.workspace, self.k_cache, self.v_cache, *self._scales, *self._norm
+
+    def _used_by(self, stream):
+        """A call of this context ran on `stream`, which need not be the context's own."""
+        if stream.cuda_stream != self._stream:
+            _record(stream, *self._held())
+
     def _enter(self):
         s = _stream_of(self.device, self.index)
         if s != self._stream:
             self._ck(lib().tpkv_set_stream(self.ctx, s))
             self._stream = s
+            _record(torch.cuda.current_stream(self.device), *self._held())
 
     def set_rotary(self, rotary: Rotary | None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6):
         """What append does to queries and keys: norm where a bf16 weight is given, then the rotation."""
@@ -936,6 +979,7 @@ class TPKV:
                                        _vec(q_norm_w, self.d, _BF, "q_norm_w", self.index),
                                        _vec(k_norm_w, self.d, _BF, "k_norm_w", self.index), float(eps)))
         self._norm = (q_norm_w, k_norm_w)  # the context keeps their pointers
+        self._stream = None  # whatever stream is next enters anew, with them
 
     def _table(self, t, batch: int):
         shape = t.shape
@@ -950,6 +994,7 @@ class TPKV:
         return the normed and rotated queries [rows, n_heads * d] (None without ``with_queries``); see tpkv_append.
         Rows that are no sequence's leave ``q_out`` as it was (undefined where it is made here)."""
         if self._elsewhere():  # what is allocated here belongs to that stream too
+            _record(self._fixed, qkv, past_lens, block_table, cu_rows, new_lens, q_out)
             with torch.cuda.stream(self._fixed):
                 return self.append(qkv, past_lens, block_table, cu_rows, new_lens, q_out, transform, with_queries)
         index, batch, width = self.index, past_lens.shape[0], self.nq * self.d
@@ -973,6 +1018,7 @@ class TPKV:
         its last ``window`` tokens and first ``sinks``.  scale: 1 / sqrt(head_dim) unless given.  Returns out
         [batch, n_heads * d], with ``return_lse`` or ``lse`` (out, lse float32 [batch, n_heads]); see tpkv_decode."""
         if self._elsewhere():
+            _record(self._fixed, q, lens, block_table, out, lse)
             with torch.cuda.stream(self._fixed):
                 return self.decode(q, lens, block_table, scale, window, sinks, out, lse, return_lse, len_add)
         index, width = self.index, self.nq * self.d
