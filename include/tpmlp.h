@@ -612,7 +612,8 @@ TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, 
  * [head_dim]) are parameters: backward writes their gradients (float
  * [head_dim]) and tpattn_sgd_step, tpattn_adamw_step and the update in
  * backward update them with the others, without decay, through the masters
- * where given. */
+ * where given; the update in backward needs them, as it does the others'
+ * (TPMLP_ERR_ORDER from tpattn_backward). */
 typedef struct {
   const tpattn_rotary* rot; /* copied; NULL: no rotation */
   void *q_norm_w, *k_norm_w; /* both or neither */

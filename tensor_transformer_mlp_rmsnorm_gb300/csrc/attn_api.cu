@@ -634,6 +634,8 @@ tpmlp_status tpattn_backward(tpattn_ctx* c, const void* dy, void* dx, float* dno
   const bool upd = c->upd_in_bwd;
   if (upd && (!c->m_norm_w || !c->m_w_qkv || !c->m_w_o || !c->m_b_o))
     return c->fail(TPMLP_ERR_ORDER, "the update in backward needs bound fp32 masters");
+  if (upd && c->qk_on && c->qk.q_norm_w && !c->qk.master_q)
+    return c->fail(TPMLP_ERR_ORDER, "the update in backward needs fp32 masters of the query and key norm weights");
   // W_qkv and W_o are updated in their weight-gradient epilogues from 8192
   // tokens (as in the MLP), otherwise by the update kernel after backward
   const bool fuse = upd && N >= ATTN_UPDATE_IN_EPILOGUE_MIN_TOKENS;
