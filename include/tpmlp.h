@@ -645,7 +645,8 @@ TPMLP_API tpmlp_status tpattn_append_kv(tpattn_ctx* ctx, tpkv_ctx* kv, const int
  * past_lens[b] + 1 tokens (window and sinks as in tpkv_decode), output
  * projection, bias and residual.  A sequence with past_lens[b] < 0 is inactive:
  * nothing is stored and its attention output is 0.  Overwrites the workspace
- * of the last forward, whose backward is then TPMLP_ERR_ORDER. */
+ * of the last forward, whose backward is then TPMLP_ERR_ORDER; an update with
+ * gradients written before still runs. */
 TPMLP_API tpmlp_status tpattn_decode(tpattn_ctx* ctx, tpkv_ctx* kv, int32_t batch, const void* x, const void* norm_w,
                                      const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
                                      const int32_t* past_lens, const int32_t* block_table, int64_t ld_table,

@@ -990,7 +990,9 @@ tpmlp_status tpattn_decode(tpattn_ctx* c, tpkv_ctx* kv, int32_t batch, const voi
   if (s != TPMLP_OK) return c->fail(s, kv->err);
   const int N = batch, H = (int)cf.hidden, d = cf.head_dim, nq = cf.n_heads, nkv = cf.n_kv_heads;
   const int W = (nq + 2 * nkv) * d, Zc = nq * d;
-  c->fwd_done = c->bwd_done = false;  // the workspace of the last forward is overwritten
+  // The last forward's workspace is overwritten; gradients that a backward has
+  // written already are the caller's and may still be applied.
+  c->fwd_done = false;
   void* nrm = c->wsp<void>(c->L.nrm);
   void* qkv = c->wsp<void>(c->L.qkv);
   void* z = c->wsp<void>(c->L.z);

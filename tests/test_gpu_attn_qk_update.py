@@ -89,3 +89,31 @@ def test_update_in_backward_needs_every_master():
     m.sgd_step(LR)  # in bf16, as asked for
     m.sync()
     assert not torch.equal(dev["q_norm_w"].cpu(), p["q_norm_w"])
+
+
+def test_update_after_a_decode():
+    """A decode between backward and the update takes the forward's workspace, not the gradients."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    B, S, H, nq, nkv, d = 1, 64, 128, 2, 1, 64
+    x, dy, p = _inputs(B * S, H, nq, nkv, d)
+    got = []
+    for decode in (False, True):
+        dev = {k: v.cuda() for k, v in p.items()}
+        m = T.TPAttn(B * S, H, nq, nkv, d, S, max_t=1)
+        m.set_qk(T.Rotary(d), dev["q_norm_w"], dev["k_norm_w"], EPS)
+        w = [dev[k] for k in MAIN]
+        m.forward(x.cuda(), *w, EPS, 1, B, S)
+        m.backward(dy.cuda())
+        if decode:
+            k = torch.zeros(1, nkv, 16, d, dtype=torch.bfloat16, device="cuda")
+            kv = T.TPKV(k, k.clone(), nq, max_batch=1)
+            z = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+            m.decode(kv, x[:1].cuda(), *w, EPS, 1, z[0], z)
+            with pytest.raises(T.TPMLPError) as e:
+                m.backward(dy.cuda())
+            assert e.value.status == T.ERR_ORDER
+        m.sgd_step(LR)
+        m.sync()
+        got.append({k: to_np(v) for k, v in dev.items()})
+    for k in p:
+        np.testing.assert_array_equal(got[0][k], got[1][k], err_msg=k)
