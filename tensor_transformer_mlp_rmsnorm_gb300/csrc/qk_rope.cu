@@ -585,7 +585,8 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
             dot = fmaf(wa[i], va[i], fmaf(wb[i], vb[i], dot));
           }
           HL::sum2(ss, dot);
-          const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+          // (idle lanes hold zeros, whose rsqrt is infinite where eps is 0)
+          const float r = work ? rsqrtf(ss * (1.0f / D) + a.eps) : 0.0f;
           const float c = -dot * (1.0f / D) * r * r;  // dx = r w g + c xh
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
