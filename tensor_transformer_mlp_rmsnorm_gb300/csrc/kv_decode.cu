@@ -47,7 +47,13 @@
 // the sum of two bf16 values (16 bits), because a single one would add as much
 // error as the final rounding of the output; the second product costs about
 // 1%.  With an E4M3 cache, codes are converted to f16 exactly, q is brought to
-// f16 after a power-of-two scale per head, and P is f16.
+// f16 after a power-of-two scale per head, and P is f16: its 2^-11 a weight,
+// random in sign and averaged over the tokens, stays below the output's 2^-8,
+// and a second f16 product would double the tensor work of a kernel that the
+// conversions already hold up.  Weights are taken relative to 2^-15 of the
+// maximum, so that all of f16's range is theirs: 2^-29 of the largest keeps 11
+// bits and 2^-39 is not 0 (relative to the maximum itself, weights below 2^-25
+// were lost from the product but not from the sum; the time is the same).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -697,7 +703,8 @@ __global__ void __launch_bounds__(NTHR, 2)
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(m[e], mx[e]);
+        // (behind 2^20 a float's step is too wide to subtract 15 from)
+        const float mn = fmaxf(m[e], F8 && fabsf(mx[e]) < 0x1p20f ? mx[e] - 15.0f : mx[e]);
         const float mu = mn == -INFINITY ? 0.0f : mn;  // nothing visible yet
         alpha[e] = ex2_fast(m[e] - mu);                // m = -inf: 0
         m[e] = mn;

@@ -134,3 +134,50 @@ def test_strides_of_a_single_row_do_not_matter():
                          table.shape[1], d ** -0.5, 0, 0, q.data_ptr(), 256, None) == 0
     kv.sync()
     assert torch.equal(q, out)
+
+
+@pytest.mark.parametrize("n", [300, 20000])
+@pytest.mark.parametrize("d,nq", [(64, 1), (128, 9), (256, 17)])
+def test_many_small_weights_of_an_e4m3_cache(n, d, nq):
+    """A page's first token has value 0 and weight 1, its others value 1 and weight e^-18, below 2^-25: together they
+    are the output.
+
+    Tolerance, relative: the output's rounding 2^-8, a weight's in f16 2^-11, the exponential and the sums 2^-14."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    k, v, table = _cache(n, 1, d, "e4m3")
+    k.view(torch.uint8).zero_()
+    v.copy_(torch.ones_like(v, dtype=torch.float32).to(E4M3))
+    k[:, 0, 0, 0] = torch.tensor(18.0, device="cuda").to(E4M3)
+    v.view(torch.uint8)[:, 0, 0] = 0
+    kv = T.TPKV(k, v, nq, max_batch=1)
+    q = torch.zeros(1, nq * d, dtype=torch.bfloat16, device="cuda")
+    q.view(nq, d)[:, 0] = 1.0
+    out, lse = kv.decode(q, torch.tensor([n], **I32), table, scale=1.0, return_lse=True)
+    kv.sync()
+    first = (n + 15) // 16
+    rest = (n - first) * math.exp(-18.0)
+    assert np.abs(to_np(out) / (rest / (first + rest)) - 1.0).max() <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14
+    # the scores are exact; the sum, its logarithm and 18 round a few times each
+    assert np.abs(to_np(lse) - (18.0 + math.log(first + rest))).max() <= 28 * 2.0 ** -22 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("log_q", [10, 14, 20, 40, 100])
+@pytest.mark.parametrize("d,nq", [(64, 1), (128, 9)])
+def test_scores_of_any_size(log_q, d, nq):
+    """Scores up to 448 x 2^100: the greatest takes all the weight (the next is 32 x 2^10 below it), exactly."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    n = 3000
+    k, v, table = _cache(n, 1, d, "e4m3")
+    g = torch.Generator().manual_seed(log_q)
+    codes = torch.tensor([-448.0, -20.0, 0.0, 1.0, 2.0, 256.0, 416.0])[torch.randint(0, 7, (k.shape[0], 16), generator=g)]
+    k.view(torch.uint8).zero_()
+    k[:, 0, :, 0] = codes.cuda().to(E4M3)
+    at = 1777
+    k[at // 16, 0, at % 16, 0] = torch.tensor(448.0, device="cuda").to(E4M3)
+    kv = T.TPKV(k, v, nq, max_batch=1)
+    q = torch.zeros(1, nq * d, dtype=torch.bfloat16, device="cuda")
+    q.view(nq, d)[:, 0] = 2.0 ** log_q
+    out, lse = kv.decode(q, torch.tensor([n], **I32), table, scale=1.0, return_lse=True)
+    kv.sync()
+    assert torch.equal(out.view(nq, d), v[at // 16, 0, at % 16].to(torch.bfloat16).expand(nq, d))
+    assert np.abs(to_np(lse) / (448.0 * 2.0 ** log_q) - 1.0).max() <= 2.0 ** -21
