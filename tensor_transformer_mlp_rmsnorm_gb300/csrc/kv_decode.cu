@@ -11,7 +11,12 @@
 // the products use m16n8k16 with the keys (and for P V the head dimension) as
 // M and 8 query heads as N.  tcgen05 with 128 keys as M would hand scores and P
 // through TMEM and shared memory for 8 columns of work: nothing to gain at up to
-// 8 query heads a key head, where the kernel runs at 89 to 98% of the copy rate (d = 128).
+// 8 query heads a key head, where the kernel runs at 89 to 98% of the copy rate
+// (d = 128, long caches; heads of 192 and 256 values 81 and 86%, E4M3 of 256
+// 63%).  It would pay beyond: with 16 query heads a key head this kernel is at
+// 71% (E4M3 57%), with 32 at 41% (33%), as each group of 8 reads and converts
+// the tile on warps of its own and its chain of products, softmax and products
+// is longer.
 //
 // The split.  The cache is cut into tiles of 64 or 128 tokens; the tiles of
 // every (sequence, key head) laid end to end are divided evenly over two CTAs
@@ -36,7 +41,7 @@
 //
 // Measured on a GB300 (copy rate 6.68 TB/s): 64 sequences of up to 8192 tokens,
 // 8 key heads of 128, 32 query heads, bf16: 153 us, 6.5 TB/s; 128 such with
-// E4M3: 167 us, 6.1 TB/s, where the conversions of codes to f16 (two for four
+// E4M3: 166 us, 6.2 TB/s, where the conversions of codes to f16 (two for four
 // codes) keep the ALU half busy; one of 131072 tokens: 86 us, 6.2 TB/s, of
 // which the start and the two-level join are about 8 us.  Tiles of
 // 64 tokens took 168 us on the first: a tile costs a warp two waits and a chain
@@ -422,10 +427,12 @@ __global__ void __launch_bounds__(NTHR, 2)
   const int nhc = a.nkv * a.chunks;
   const int64_t T = total * nhc;
   // Four tiles a worker where there are few, as fewer partial results are then
-  // joined (one sequence of 500 tokens and 8 key heads in tiles of 64: 9.0 us,
-  // 10.3 with two, 15.4 in tiles of 32 with one), but as many workers as there
-  // are key heads of sequences (69 sequences of 16 tokens, 2 key heads: 13 us
-  // without this).
+  // joined.  Measured in today's tiles with 1, 2, 4 and 8 tiles a worker: one
+  // sequence of 500 tokens and 8 key heads of 128: 8.5, 9.3, 8.4, 8.5 us; of
+  // 2000 tokens: 12.0, 9.4, 10.8, 14.6; 500 tokens, heads of 256: 10.3, 11.2,
+  // 12.8, 12.2; batches that fill the machine do not care.  But as many workers
+  // as there are key heads of sequences: 69 sequences of 16 tokens, 2 key heads:
+  // 6.6 us, 13 without this.
   const int64_t want = max((T + 3) / 4, (int64_t)a.batch * nhc);
   const int64_t G = want < a.workers ? want : a.workers;
   if ((int64_t)blockIdx.x >= G) return;
@@ -927,7 +934,7 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, bool e4m3, int d, int page_
   if (!enc) return false;
   const uint64_t e = e4m3 ? 1 : 2;
   // {block of columns, slot, block, key head, page}: a box of all blocks lands
-  // as [box_tokens][block] one behind the other (Ring::BLOCK bytes a block's row)
+  // as [box_tokens][block] one behind the other (Cfg::BLOCK bytes a block's row)
   const uint64_t row = d * e, blk = row % 128 == 0 ? 128 : 64;
   cuuint64_t dims[5] = {blk / e, (cuuint64_t)page_size, row / blk, (cuuint64_t)nkv, (cuuint64_t)num_pages};
   cuuint64_t strides[4] = {(cuuint64_t)stride_slot * e, blk, (cuuint64_t)stride_head * e, (cuuint64_t)stride_page * e};

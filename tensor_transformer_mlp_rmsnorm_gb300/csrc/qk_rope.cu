@@ -15,8 +15,15 @@
 // slow pipe here) and no table to read.  The top 32 bits go through
 // sincospif; that is 2^-25 of a half turn, the rounding of the f32 result.
 //
-// What bounds it: memory, with the instruction rate close behind (512 values of
-// 16 bits leave an SM about 90 cycles of its share of the copy rate forward).
+// What bounds it: forward and append of many 16-bit rows, memory, with the
+// instruction rate close behind (512 values leave an SM about 90 cycles of its
+// share of the copy rate).  The backward, neither bytes nor issue slots (60% of
+// them active, 65% forward): each step is one chain of two sums of 16 values,
+// shuffles, rsqrt and products, with four warps a scheduler to hide it.  f32
+// rows lose more: a lane's 8 values are two 16-byte pieces, so a warp's
+// accesses have gaps of 16 bytes (by reading; not profiled).  A warp never
+// works on two rows at once, so rows of fewer heads than it takes in a step
+// leave lanes idle and pay the row's angles and addresses all the same.
 // A head belongs to d / 16 lanes; a lane holds two 16-byte (bf16) chunks whose
 // values are each other's rotation partners, so the rotation needs no shuffle
 // and the norm three or four.  A warp walks rows, four heads at a time at
@@ -26,11 +33,20 @@
 // its own copies is waited for, and no registers are held by loads in flight.
 //
 // Measured on a GB300 (copy rate 6.68 TB/s), bf16, 32 + 8 heads of 128, norms:
-// forward of 32768 rows 105 us, 6.4 TB/s; append of 16000 rows with 8 value
-// heads 68 us, 5.8 TB/s; backward of 8192 rows 52 us, 4.8 TB/s, bound by issue
-// slots (some 400 instructions a step for three operands, two sums and the
-// weight gradient; 256 values a head: 5.7 TB/s).  With the loads in registers
-// instead of the queue: 115, 78 and 58 us.
+// forward of 32768 rows 106 us, 6.4 TB/s; append of 16000 rows with 8 value
+// heads 68 us, 5.8 TB/s (E4M3 cache: 79 us, 4.6 TB/s, with 16 divisions a lane
+// and step); backward of 8192 rows 52 us, 4.8 TB/s (heads of 256, half
+// rotated: 5.6 TB/s; 16 + 4 of them, all rotated: 4.9 TB/s).  f32, 4096 rows of
+// 32 + 8 heads of 128: 41 us, 4.1 TB/s; backward 72 us, 3.5 TB/s.  8 + 1 heads
+// of 128, bf16: 3.2 TB/s forward, 3.0 backward; 1 + 1 of 64: 0.8 and 0.5.  With
+// the loads in registers instead of the queue the first three took 115, 78 and
+// 58 us.
+//
+// Rounding.  Everything between a load and a store is f32.  The weight
+// gradients are f32 sums: a lane's rows one after the other, then lanes, warps
+// and blocks as trees or in order; an f64 addition a value would go through a
+// slow pipe.  333 f32 rows: dx and the weight gradients together 1.3e-7 off the
+// definition in 64 bits, 8e-8 for f32 arithmetic with the sums in 64 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -54,8 +70,9 @@ struct Ahead {
   // backward: 4 chunks a step; heads of 256 values leave room for one step less
   static constexpr __host__ __device__ int bwd(int d) { return (sizeof(T) == 2 ? 6 : 3) - (d == 256 ? 1 : 0); }
 };
-// (rows to rows: two blocks of 128 registers a thread are 8% faster than three
-// of 80, the append 2% slower: it has more latency to hide behind other warps)
+// (rows to rows: two blocks, which may take 128 registers a thread and take 93
+// to 102, are 8% faster than three of 80; the append is 2% slower with two: it
+// has more latency to hide behind other warps)
 constexpr int ROWS_BLOCKS[3] = {2, 3, 3}, BWD_BLOCKS = 2;
 
 __device__ __forceinline__ void cp_async16(uint32_t smem, const void* g) {
@@ -462,8 +479,10 @@ __global__ void __launch_bounds__(THREADS, ROWS_BLOCKS[KIND]) rope_rows_kernel(c
 }
 
 // Backward.  All rows' query heads are taken first, then their key heads, so
-// that a lane holds its 16 columns of one weight gradient at a time in registers; blocks leave their sums as partials, added in a fixed order by
-// rope_dw_kernel, so the gradients are the same every run.
+// that a lane holds its 16 columns of one weight gradient at a time in
+// registers (a row's angles are computed in both passes); blocks leave their
+// sums as partials, added in a fixed order by rope_dw_kernel, so the gradients
+// are the same every run.
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a,
                                                                        const __grid_constant__ RopeFreqs fr) {
@@ -479,8 +498,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
   const int rot = fr.rot;
   int oa, ob;
   unit_offsets(active ? u : 0, D, rot, oa, ob);
-  // Values behind the rotated part pass, whatever lies beside them; `whole`
-  // spares the warp the question where there are none (6% of the forward).
+  // (as in the forward)
   const bool whole = HL::UNITS == HL::LANES && rot == D;
   const bool turns = u < rot / 16;
   uint64_t turn[D / 64];
@@ -629,8 +647,9 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) rope_bwd_kernel(const __g
 }
 
 // dw[c] = sum over blocks of part[block][c]: 32 columns a block, 32 rows of
-// threads.  Launched while the backward kernel still runs (its launch latency
-// is then hidden) and waiting here for the kernel's end.
+// threads.  A programmatic launch: it may start once the backward kernel's
+// blocks have exited, before their writes are visible, and waits here for
+// those (the backward triggers nothing earlier).
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int nparts, int d,
                                                        float* __restrict__ dq_w, float* __restrict__ dk_w) {
   __shared__ float red[32][33];
