@@ -510,7 +510,8 @@ TPMLP_API size_t tpattn_qk_rope_workspace_bytes(int32_t head_dim);
  * there are norm weights; x is not read otherwise and may be NULL), given dout
  * of the forward's output.  dx may be dout itself with the same stride.
  * dq_norm_w, dk_norm_w: float [head_dim], overwritten, exactly where the
- * forward had that weight (else NULL); they are summed in a fixed order.
+ * forward had that weight (else NULL), two tensors; they are summed in a fixed
+ * order.
  * workspace: tpattn_qk_rope_workspace_bytes, 16-byte aligned, needed with norm
  * weights; it needs no initial contents and is free again after the call's
  * kernels. */
@@ -560,7 +561,8 @@ TPMLP_API tpmlp_status tpkv_bind_workspace(tpkv_ctx* ctx, void* dev, size_t byte
 TPMLP_API tpmlp_status tpkv_set_stream(tpkv_ctx* ctx, void* cuda_stream);
 /* The cache, strides in elements, each a multiple of 16 bytes and positive;
  * k and v 16-byte aligned.  k_inv_scale, v_inv_scale: device float
- * [n_kv_heads], positive, or NULL (1); NULL for a bf16 cache. */
+ * [n_kv_heads], positive, or NULL (1); NULL for a bf16 cache.  v may be k for
+ * reading; appends then return TPMLP_ERR_ARG. */
 TPMLP_API tpmlp_status tpkv_bind_cache(tpkv_ctx* ctx, void* k, void* v, int64_t stride_page, int64_t stride_head,
                                        int64_t stride_slot, const float* k_inv_scale, const float* v_inv_scale);
 /* What tpkv_append does to queries and keys: rotation (copied; NULL: none) and
@@ -585,7 +587,9 @@ TPMLP_API tpmlp_status tpkv_set_rotary(tpkv_ctx* ctx, const tpattn_rotary* rot, 
  * overlap it otherwise.  transform 0 stores keys (and copies queries) as they are,
  * for rows that are normed and rotated already.  Rows of padding, of nobody or
  * of inactive sequences leave cache and q_out as they were.  E4M3:
- * code = round-to-nearest-even(value / inv_scale), saturated to +-448. */
+ * code = round-to-nearest-even(value / inv_scale), saturated to +-448.  Rows of
+ * one call that name the same slot, through a page that two sequences share
+ * behind both their pasts, leave it undefined. */
 TPMLP_API tpmlp_status tpkv_append(tpkv_ctx* ctx, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,
                                    const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
                                    const int32_t* block_table, int64_t ld_table, int32_t max_pages, int32_t transform,
@@ -613,7 +617,9 @@ TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, 
  * [head_dim]) and tpattn_sgd_step, tpattn_adamw_step and the update in
  * backward update them with the others, without decay, through the masters
  * where given; the update in backward needs them, as it does the others'
- * (TPMLP_ERR_ORDER from tpattn_backward). */
+ * (TPMLP_ERR_ORDER from tpattn_backward).  Gradients, masters and moments are
+ * different tensors (TPMLP_ERR_ARG); one weight for both queries and keys has
+ * no update (TPMLP_ERR_ARG from the three above). */
 typedef struct {
   const tpattn_rotary* rot; /* copied; NULL: no rotation */
   void *q_norm_w, *k_norm_w; /* both or neither */

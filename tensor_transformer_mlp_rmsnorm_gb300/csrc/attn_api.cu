@@ -599,6 +599,10 @@ tpmlp_status tpattn_forward(tpattn_ctx* c, int64_t batch, int64_t seq, const voi
 
 constexpr int64_t ATTN_UPDATE_IN_EPILOGUE_MIN_TOKENS = 8192;
 
+// Queries and keys with one norm weight: an update would write it twice at once.
+static bool qk_shared(const tpattn_ctx* c) { return c->qk_on && c->qk.q_norm_w && c->qk.q_norm_w == c->qk.k_norm_w; }
+static const char* const kSharedNorm = "the norm weights of queries and keys are the same tensor, which has no update";
+
 // SGD w <- w - lr g over the parameters of the last forward with the gradients
 // of the last backward; the two projection matrices only when `matrices`.
 static tpmlp_status attn_run_sgd(tpattn_ctx* c, float lr, bool matrices) {
@@ -636,6 +640,7 @@ tpmlp_status tpattn_backward(tpattn_ctx* c, const void* dy, void* dx, float* dno
     return c->fail(TPMLP_ERR_ORDER, "the update in backward needs bound fp32 masters");
   if (upd && c->qk_on && c->qk.q_norm_w && !c->qk.master_q)
     return c->fail(TPMLP_ERR_ORDER, "the update in backward needs fp32 masters of the query and key norm weights");
+  if (upd && qk_shared(c)) return c->fail(TPMLP_ERR_ARG, kSharedNorm);
   // W_qkv and W_o are updated in their weight-gradient epilogues from 8192
   // tokens (as in the MLP), otherwise by the update kernel after backward
   const bool fuse = upd && N >= ATTN_UPDATE_IN_EPILOGUE_MIN_TOKENS;
@@ -810,6 +815,7 @@ tpmlp_status tpattn_sgd_step(tpattn_ctx* c, float lr) {
   if (!c->bwd_done) return c->fail(TPMLP_ERR_ORDER, "sgd_step before backward");
   if (c->upd_done) return c->fail(TPMLP_ERR_ORDER, "the last backward already applied the update");
   if (!std::isfinite(lr)) return c->fail(TPMLP_ERR_ARG, "lr must be finite");
+  if (qk_shared(c)) return c->fail(TPMLP_ERR_ARG, kSharedNorm);
   return attn_run_sgd(c, lr, true);
 }
 
@@ -854,6 +860,7 @@ tpmlp_status tpattn_adamw_step(tpattn_ctx* c, const tpmlp_adamw_params* hp, floa
   if (!c->adam_bound) return c->fail(TPMLP_ERR_ARG, "AdamW moments are not bound");
   if (c->qk_on && c->qk.q_norm_w && !c->qk.m_q)
     return c->fail(TPMLP_ERR_ARG, "AdamW moments of the query and key norm weights are not set");
+  if (qk_shared(c)) return c->fail(TPMLP_ERR_ARG, kSharedNorm);
   if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay) || !std::isfinite(hp->max_grad_norm) ||
       !(hp->beta1 >= 0.f && hp->beta1 < 1.f) || !(hp->beta2 >= 0.f && hp->beta2 < 1.f) ||
       !(hp->eps >= 0.f && std::isfinite(hp->eps)) || hp->step < 1)
@@ -921,6 +928,11 @@ tpmlp_status tpattn_set_qk(tpattn_ctx* c, const tpattn_qk_params* p, void* ws, s
   if (!p->master_q != !p->master_k) return c->fail(TPMLP_ERR_ARG, "set both masters or neither");
   if (!p->m_q != !p->m_k || !p->m_q != !p->v_q || !p->m_q != !p->v_k)
     return c->fail(TPMLP_ERR_ARG, "set all four moments or none");
+  const float* const written[] = {p->dq_norm_w, p->dk_norm_w, p->master_q, p->master_k, p->m_q, p->m_k, p->v_q, p->v_k};
+  for (size_t i = 0; i < sizeof written / sizeof *written; ++i)
+    for (size_t j = 0; j < i; ++j)
+      if (written[i] && written[i] == written[j])
+        return c->fail(TPMLP_ERR_ARG, "the same tensor among gradients, masters and moments");
   for (const void* q : {(const void*)p->q_norm_w, (const void*)p->k_norm_w, (const void*)p->dq_norm_w,
                         (const void*)p->dk_norm_w, (const void*)p->master_q, (const void*)p->master_k,
                         (const void*)p->m_q, (const void*)p->m_k, (const void*)p->v_q, (const void*)p->v_k})
@@ -961,6 +973,7 @@ tpmlp_status tpattn_append_kv(tpattn_ctx* c, tpkv_ctx* kv, const int32_t* new_le
   const int64_t rows = c->batch * c->seq, W = (int64_t)(cf.n_heads + 2 * cf.n_kv_heads) * cf.head_dim;
   if (reinterpret_cast<uintptr_t>(new_lens) & 3u) return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
   tpmlp_status s = kv_check_call(kv, c->batch, table, table, ld_table, max_pages);
+  if (s == TPMLP_OK) s = kv_check_append(kv);
   if (s != TPMLP_OK) return c->fail(s, kv->err);
   s = TPMLP_OK;
   const tpmlp_status r = c->run(A_KV_APPEND, [&] {
@@ -987,6 +1000,7 @@ tpmlp_status tpattn_decode(tpattn_ctx* c, tpkv_ctx* kv, int32_t batch, const voi
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return c->fail(TPMLP_ERR_ARG, "eps must be finite and >= 0");
   if (window < 0 || sinks < 0) return c->fail(TPMLP_ERR_ARG, "window and sinks must be >= 0");
   tpmlp_status s = kv_check_call(kv, batch, past_lens, table, ld_table, max_pages);
+  if (s == TPMLP_OK) s = kv_check_append(kv);
   if (s != TPMLP_OK) return c->fail(s, kv->err);
   const int N = batch, H = (int)cf.hidden, d = cf.head_dim, nq = cf.n_heads, nkv = cf.n_kv_heads;
   const int W = (nq + 2 * nkv) * d, Zc = nq * d;

@@ -255,6 +255,7 @@ tpmlp_status tpattn_qk_rope_backward(const tpattn_qk_desc* q, const tpattn_rotar
   if (dout == dx && ld_dout != ld_dx && q->rows > 1) return bad(TPMLP_ERR_ARG, "in place needs equal strides");
   if (!q->q_norm_w != !dq_norm_w || !q->k_norm_w != !dk_norm_w)
     return bad(TPMLP_ERR_ARG, "weight gradients are given exactly for the norm weights");
+  if (dq_norm_w && dq_norm_w == dk_norm_w) return bad(TPMLP_ERR_ARG, "the same tensor for both weight gradients");
   if (!a16(dq_norm_w) || !a16(dk_norm_w)) return bad(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
   if (norm && !empty) {
     if (!workspace || !a16(workspace)) return bad(TPMLP_ERR_ARG, "workspace must be 16-byte aligned");
@@ -403,6 +404,7 @@ tpmlp_status tpkv_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q
                          int64_t ld_q) {
   if (!c) return TPMLP_ERR_ARG;
   KV_TRY(kv_check_call(c, batch, past_lens, table, ld_table, max_pages));
+  KV_TRY(kv_check_append(c));
   const tpkv_config& cf = c->cfg;
   const int64_t W = (int64_t)(cf.n_heads + 2 * cf.n_kv_heads) * cf.head_dim, Z = (int64_t)cf.n_heads * cf.head_dim;
   if (rows < 0 || rows > 0x7fffffff) return c->fail(TPMLP_ERR_SHAPE, "rows out of range");
@@ -487,6 +489,11 @@ tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, cons
   if ((reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(table)) & 3u)
     return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
   return TPMLP_OK;
+}
+
+tpmlp_status kv_check_append(tpkv_ctx* c) {
+  return c->k == c->v ? c->fail(TPMLP_ERR_ARG, "keys and values are the same tensor, which cannot be appended to")
+                      : TPMLP_OK;
 }
 
 tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,

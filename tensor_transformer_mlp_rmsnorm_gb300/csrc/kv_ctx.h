@@ -54,6 +54,7 @@ RopeFreqs freqs_of(const tpattn_rotary* r);
 // before the two launches below.  past_lens null: all 0.
 tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, const int32_t* table, int64_t ld_table,
                            int32_t max_pages);
+tpmlp_status kv_check_append(tpkv_ctx* c);
 tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,
                            const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
                            const int32_t* table, int64_t ld_table, int32_t max_pages, const QkTransform& tr,
