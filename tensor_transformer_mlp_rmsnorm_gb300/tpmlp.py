@@ -503,9 +503,9 @@ class TPAttn:
     """The tensor-parallel attention sublayer through the C ABI (tpattn_*):
     bf16 tensors on one CUDA device; the workspace is a torch uint8 tensor.
 
-    Calls run on ``stream`` (torch's current stream at construction unless given).  Where another one is current at a
-    call, ordering the two is the caller's; the memory of what the call uses is not handed out again before the
-    stream is past it."""
+    Calls run on ``stream`` (torch's current stream at construction unless given; the one that is captured, for calls
+    to be replayed from a graph).  Where another one is current at a call, ordering the two is the caller's; the memory
+    of what the call uses is not handed out again before the stream is past it."""
 
     def __init__(self, max_tokens: int, hidden: int, n_heads: int, n_kv_heads: int, head_dim: int,
                  max_seq: int, max_t: int = 8, device=None, stream=None, fused_only: bool = False):
