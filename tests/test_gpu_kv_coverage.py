@@ -119,3 +119,35 @@ def test_lse_of_exact_scores(n, kind, d, nq):
     err = np.abs(to_np(lse)[0] - want)
     assert (err <= tol).all(), (err / tol).max()
     assert math.isfinite(float(out.float().sum()))
+
+
+@pytest.mark.parametrize("B", [1, 129, 257])
+def test_sublayer_decode_of_any_batch(B):
+    """One, and more sequences than rows of a GEMM tile, against float64 attention over the cache's own contents."""
+    import tensor_transformer_mlp_rmsnorm_gb300 as T
+    from tests._util import compare
+    H, nq, nkv, d, page, n = 256, 4, 2, 64, 16, 40
+    g = _gen(B)
+    r = lambda *s, std=0.05: (torch.randn(*s, generator=g) * std).to(torch.bfloat16).cuda()  # noqa: E731
+    w = (1 + r(H), r((nq + 2 * nkv) * d, H), r(H, nq * d), r(H))
+    k, v = r(B * 3, nkv, page, d, std=1.0), r(B * 3, nkv, page, d, std=1.0)
+    table = torch.randperm(B * 3, generator=g).to(torch.int32).reshape(B, 3)
+    lens = torch.randint(-1, n, (B,), generator=g).to(torch.int32)
+    x = r(B, H, std=1.0)
+    m = T.TPAttn(B, H, nq, nkv, d, 64, max_t=1)
+    kv = T.TPKV(k, v, nq, max_batch=B)
+    y = m.decode(kv, x, *w, 1e-6, 1, lens.cuda(), table.cuda())
+    m.sync()
+    kv.sync()
+    W, K, V, X = [to_np(t) for t in w], to_np(k), to_np(v), to_np(x)
+    nrm = X / np.sqrt((X * X).mean(1, keepdims=True) + 1e-6) * W[0]
+    q = (nrm @ W[1].T)[:, : nq * d].reshape(B, nq, d)
+    z = np.zeros((B, nq, d))
+    for b in range(B):
+        t = np.arange(int(lens[b]) + 1)  # the token's own key and value are in the cache by now
+        if t.size:
+            kk, vv = (c[table.numpy()[b][t // page], :, t % page].repeat(nq // nkv, 1) for c in (K, V))
+            s = np.einsum("hd,thd->ht", q[b], kk) / d ** 0.5
+            pr = np.exp(s - s.max(1, keepdims=True))
+            z[b] = np.einsum("ht,thd->hd", pr / pr.sum(1, keepdims=True), vv)
+    compare("y", to_np(y), X + z.reshape(B, nq * d) @ W[2].T + W[3], "bf16")
