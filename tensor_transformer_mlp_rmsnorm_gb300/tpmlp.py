@@ -698,6 +698,7 @@ class TPAttn:
         """The sublayer for one new token per sequence, appended to the cache at position past_lens[b]
         (tpattn_decode); returns y [batch, H]."""
         n = x.shape[0]
+        _int32(t=t, window=window, sinks=sinks)
         y = torch.empty_like(x) if y is None else y
         tp, ldt, pages = kv._table(block_table, n)
         _acheck(lib().tpattn_decode(self.ctx, kv.ctx, n, self._t(x, (n, self.H), name="x"),
@@ -771,6 +772,16 @@ def _record(stream, *tensors):
 def _bad(t, name: str, want: str):
     return TPMLPError(ERR_ARG, f"{name}: need {want}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
                                f"{t.device}")
+
+
+_I31 = 1 << 31
+
+
+def _int32(**values):
+    """Refuses whole numbers that ctypes would mask to 32 bits."""
+    for name, v in values.items():
+        if not -_I31 <= v < _I31:
+            raise TPMLPError(ERR_ARG, f"{name} {v} does not fit 32 bits")
 
 
 def _rows(t, width: int, dtype, name: str, index: int, rows: int = -1):
@@ -902,6 +913,7 @@ class TPKV:
             raise TPMLPError(ERR_ARG, "k_cache and v_cache must agree in type, shape, device and strides, the last 1")
         self.device = dev = k_cache.device
         pages, nkv, page, d = k_cache.shape
+        _int32(n_heads=n_heads, max_batch=max_batch)
         self.cfg = KvConfig(pages, page, max_batch, n_heads, nkv, d, kinds[k_cache.dtype], 0)
         self.nq, self.nkv, self.d, self.page_size = n_heads, nkv, d, page
         self.k_cache, self.v_cache = k_cache, v_cache
@@ -1022,6 +1034,8 @@ class TPKV:
             with torch.cuda.stream(self._fixed):
                 return self.decode(q, lens, block_table, scale, window, sinks, out, lse, return_lse, len_add)
         index, width = self.index, self.nq * self.d
+        if not (-_I31 <= window < _I31 and -_I31 <= sinks < _I31 and -_I31 <= len_add < _I31):
+            _int32(window=window, sinks=sinks, len_add=len_add)
         qp, batch, ldq = _rows(q, width, _BF, "q", index)
         if out is None:
             out = q.new_empty((batch, width))
