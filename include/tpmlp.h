@@ -383,6 +383,16 @@ TPMLP_API tpmlp_status tpattn_bind_workspace(tpattn_ctx* ctx, void* dev, size_t 
 TPMLP_API tpmlp_status tpattn_forward(tpattn_ctx* ctx, int64_t batch, int64_t seq, const void* x, const void* norm_w,
                                       const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
                                       void* y);
+/* The same over `batch` packed sequences of any lengths (tpattn_packed_forward):
+ * x, y [tokens, H], tokens <= max_tokens, cu_rows device [batch + 1], ascending,
+ * kept by pointer until the backward or tpattn_append_kv.  Positions count from
+ * each sequence's first row; max_seq does not matter.  Rows outside every
+ * sequence have attention output 0.  tpattn_backward, the updates and
+ * tpattn_append_kv follow as after tpattn_forward.  A bad cu_rows is reported by
+ * tpattn_sync (TPMLP_ERR_ARG). */
+TPMLP_API tpmlp_status tpattn_forward_packed(tpattn_ctx* ctx, int64_t tokens, int32_t batch, const int32_t* cu_rows,
+                                             const void* x, const void* norm_w, const void* w_qkv, const void* w_o,
+                                             const void* b_o, float eps, int32_t t, void* y);
 /* dx (bf16) and float gradients dnorm_w [H], dw_qkv, dw_o, db_o. */
 TPMLP_API tpmlp_status tpattn_backward(tpattn_ctx* ctx, const void* dy, void* dx, float* dnorm_w, float* dw_qkv,
                                        float* dw_o, float* db_o);
@@ -520,6 +530,55 @@ TPMLP_API tpmlp_status tpattn_qk_rope_backward(const tpattn_qk_desc* desc, const
                                                int64_t ld_dx, float* dq_norm_w, float* dk_norm_w, void* workspace,
                                                size_t workspace_bytes, void* cuda_stream);
 
+/* ---------------------------------------------------------------- packed sequences
+ * Causal attention over whole sequences of different lengths, packed one behind
+ * the other, and its gradient.  For the token at position p of its sequence
+ * (its row less the sequence's first), over the tokens t <= p of the sequence
+ * and, with window > 0, t > p - window or t < sinks:
+ *     out = sum_t exp(s_t - lse) v_t,  s_t = scale q . k_t,  lse = log sum_t exp(s_t)
+ * Query head h reads key head h / (n_heads / n_kv_heads).  bf16 rows, f32 sums.
+ * A row depends on rows of its own sequence only, whatever the others hold.
+ * Calls without a context run on the current device; their errors are in
+ * tpmlp_last_error(NULL). */
+typedef struct {
+  int64_t rows;        /* of every tensor, at most 2^28 */
+  int32_t batch;       /* sequences, at most 2^20 */
+  int32_t n_heads, n_kv_heads;
+  int32_t head_dim;    /* 64, 128, 192 or 256 */
+  const int32_t* cu_rows; /* device [batch + 1], ascending: sequence b has the rows [cu_rows[b], cu_rows[b+1]) */
+  float scale;         /* finite */
+  int32_t window, sinks; /* window 0: no limit */
+  int32_t reserved;    /* 0 */
+} tpattn_packed_desc;
+
+/* q [rows, n_heads d], k and v [rows, n_kv_heads d] bf16, each with a row
+ * stride in elements (a multiple of 8), so that all three may be columns of
+ * packed projection rows -> out [rows, n_heads d] bf16 (it may be q with the
+ * same stride; otherwise it overlaps no input) and lse float [rows, n_heads]
+ * or NULL.  Rows outside every sequence are left as they were.  status: a
+ * device word that the caller zeroes; cu_rows that descend or leave [0, rows]
+ * set bit 2 (such sequences are cut to the rows that exist, their outputs
+ * unspecified), a bounded wait that gives up bit 1. */
+TPMLP_API tpmlp_status tpattn_packed_forward(const tpattn_packed_desc* desc, const void* q, int64_t ld_q,
+                                             const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* out,
+                                             int64_t ld_out, float* lse, uint32_t* status, void* cuda_stream);
+
+/* Device scratch of the backward (two floats a row and query head); 0 if a
+ * count is out of range. */
+TPMLP_API size_t tpattn_packed_workspace_bytes(int64_t rows, int32_t n_heads);
+
+/* Gradients dq, dk, dv (bf16, strides of their own, overwritten; they overlap
+ * no input and not each other) of the forward's inputs, given its out and lse
+ * and the gradient dout of out.  dk and dv are summed over a key head's query
+ * heads.  Repeated calls give the same bits.  workspace: 16-byte aligned, no
+ * initial contents, free again after the call's kernels. */
+TPMLP_API tpmlp_status tpattn_packed_backward(const tpattn_packed_desc* desc, const void* q, int64_t ld_q,
+                                              const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                              const void* out, int64_t ld_out, const float* lse, const void* dout,
+                                              int64_t ld_dout, void* dq, int64_t ld_dq, void* dk, int64_t ld_dk,
+                                              void* dv, int64_t ld_dv, void* workspace, size_t workspace_bytes,
+                                              uint32_t* status, void* cuda_stream);
+
 /* ---------------------------------------------------------------- paged key/value cache
  * Answering with a trained attention sublayer: keys and values of the tokens
  * so far live in pages of page_size tokens, and a block table names each
@@ -609,6 +668,22 @@ TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, 
                                    int32_t len_add, const int32_t* block_table, int64_t ld_table, int32_t max_pages,
                                    float scale, int32_t window, int32_t sinks, void* out, int64_t ld_out, float* lse);
 
+/* Attention of new tokens, any number a sequence, over a cache that holds them
+ * already: rows, cu_rows, new_lens, past_lens and the table as in tpkv_append,
+ * called after it.  The i-th row of sequence b is the token at position
+ * p = past_lens[b] + i and sees the tokens t <= p (with window > 0: t > p -
+ * window or t < sinks).
+ *  q bf16 [rows, n_heads d] (row stride ld_q) -> out bf16 [rows, n_heads d]
+ *  (row stride ld_out; may be q with the same stride), lse float [rows, n_heads]
+ *  or NULL, as in tpkv_decode.  Rows of an inactive sequence get out 0 and lse
+ *  -inf; rows of padding and of nobody are left as they were.  Nothing behind a
+ *  sequence's last token, in pages or table, and no page that all of its rows'
+ *  windows have left, influences the result.  Repeated calls give the same bits. */
+TPMLP_API tpmlp_status tpkv_extend(tpkv_ctx* ctx, int64_t rows, int32_t batch, const void* q, int64_t ld_q,
+                                   const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
+                                   const int32_t* block_table, int64_t ld_table, int32_t max_pages, float scale,
+                                   int32_t window, int32_t sinks, void* out, int64_t ld_out, float* lse);
+
 /* ---- the attention sublayer with rotation, norms and a cache */
 
 /* The attention sublayer's rotation and per-head norms: queries and keys of
@@ -638,8 +713,8 @@ TPMLP_API size_t tpattn_qk_workspace_bytes(const tpattn_config* cfg);
 TPMLP_API tpmlp_status tpattn_set_qk(tpattn_ctx* ctx, const tpattn_qk_params* params, void* workspace, size_t bytes);
 
 /* Store the keys and values of the last forward's prompts in a cache: sequence
- * b's first new_lens[b] tokens (device [batch]; NULL: all seq) at positions
- * 0, 1, ...  The cache's heads must be the sublayer's (TPMLP_ERR_SHAPE).  Runs
+ * b's first new_lens[b] tokens (device [batch]; NULL: all seq; NULL after a
+ * packed forward, whose sequences are stored whole) at positions 0, 1, ...  The cache's heads must be the sublayer's (TPMLP_ERR_SHAPE).  Runs
  * on the attention context's stream (as tpattn_decode does); cache errors are
  * reported by tpkv_sync, behind a tpattn_sync where the streams differ. */
 TPMLP_API tpmlp_status tpattn_append_kv(tpattn_ctx* ctx, tpkv_ctx* kv, const int32_t* new_lens,
@@ -655,6 +730,19 @@ TPMLP_API tpmlp_status tpattn_append_kv(tpattn_ctx* ctx, tpkv_ctx* kv, const int
  * gradients written before still runs. */
 TPMLP_API tpmlp_status tpattn_decode(tpattn_ctx* ctx, tpkv_ctx* kv, int32_t batch, const void* x, const void* norm_w,
                                      const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
+                                     const int32_t* past_lens, const int32_t* block_table, int64_t ld_table,
+                                     int32_t max_pages, int32_t window, int32_t sinks, void* y);
+
+/* The sublayer for new tokens, any number a sequence (x, y [rows, H]; rows <=
+ * max_tokens), rows, cu_rows, new_lens and past_lens as in tpkv_append:
+ * pre-norm, projection, rotation and norms, append, attention of each token
+ * over what its sequence holds up to itself (tpkv_extend), output projection,
+ * bias and residual.  Rows of padding, of nobody and of inactive sequences
+ * store nothing and have attention output 0.  The workspace of the last forward is
+ * overwritten, as by tpattn_decode. */
+TPMLP_API tpmlp_status tpattn_extend(tpattn_ctx* ctx, tpkv_ctx* kv, int64_t rows, int32_t batch, const void* x,
+                                     const void* norm_w, const void* w_qkv, const void* w_o, const void* b_o, float eps,
+                                     int32_t t, const int32_t* cu_rows, const int32_t* new_lens,
                                      const int32_t* past_lens, const int32_t* block_table, int64_t ld_table,
                                      int32_t max_pages, int32_t window, int32_t sinks, void* y);
 

@@ -19,4 +19,5 @@ from .tpmlp import (  # noqa: F401
     fp8_gemm, fp8_quantize, kernel_names, lib,
     make_config, tpmlp_create, tpmlp_workspace_bytes,
     Rotary, TPKV, qk_norm_rope, qk_norm_rope_backward,
+    packed_attention, packed_attention_backward, packed_attention_check,
 )

@@ -16,6 +16,10 @@
 //   adamw   : grad_sqnorm -> adamw_update
 //   with tpattn_set_qk: qk_rope behind gemm_qkv, qk_rope_bwd before gemm_dgrad_norm
 //   decode  : rmsnorm_fwd -> gemm_qkv -> kv_append -> kv_decode -> gemm_out_proj
+//   extend  : the same with kv_extend, any number of new tokens a sequence
+// Packed sequences (tpattn_forward_packed): packed_rows (positions, rows that
+// are nobody's cleared), and var_attn_fwd / var_attn_bwd in place of the
+// attention kernels.
 // Fused path (head_dim 128, seq % 128 == 0; the default): gemm_scores ->
 // softmax_fwd -> gemm_pv become flash_attn_fwd (Z and each row's log-sum-exp),
 // and gemm_dp .. group_sum become flash_bwd_prep (D = rowsum(dZ o Z), dQ
@@ -70,6 +74,10 @@ enum AttnKernel {
   A_QK_ROPE_BWD,
   A_KV_APPEND,
   A_KV_DECODE,
+  A_PACKED_ROWS,
+  A_VAR_FWD,
+  A_VAR_BWD,
+  A_KV_EXTEND,
   A_COUNT
 };
 const char* const kAttnNames[A_COUNT] = {
@@ -78,7 +86,8 @@ const char* const kAttnNames[A_COUNT] = {
     "group_sum",       "softmax_bwd",     "gemm_dq",         "gemm_dk",          "gemm_wgrad_qkv",
     "gemm_dgrad_norm", "rmsnorm_bwd_residual", "colsum_finalize", "sgd_update",
     "flash_attn_fwd",  "flash_bwd_prep",  "flash_attn_bwd",  "flash_dq_cast",   "grad_sqnorm",
-    "adamw_update",   "qk_rope",         "qk_rope_bwd",     "kv_append",       "kv_decode"};
+    "adamw_update",   "qk_rope",         "qk_rope_bwd",     "kv_append",       "kv_decode",
+    "packed_rows",    "var_attn_fwd",    "var_attn_bwd",    "kv_extend"};
 
 constexpr int MAX_PARTS = 1024;
 thread_local std::string g_attn_err;
@@ -88,7 +97,7 @@ bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct AttnLayout {
   size_t status, split_ctr, nrm, rstd, qkv, z, dz, dqkv, dnrm, scores, probs, dkv_head, lse2, dsum, part_dw, part_db,
-      norm_part, split_scratch, total;
+      norm_part, split_scratch, pos, total;
 };
 
 bool attn_config_error(const tpattn_config* c, std::string* why) {
@@ -147,6 +156,7 @@ AttnLayout attn_layout(const tpattn_config& c) {
   L.part_db = take((size_t)MAX_PARTS * H * 4);
   L.norm_part = take((size_t)MAX_NORM_PARTS * sizeof(double));  // AdamW: per-block partial sums of g^2
   L.split_scratch = take(SPLIT_SCRATCH_BYTES);  // tail-split partial accumulators of the GEMMs
+  L.pos = take(N * 4);  // positions of packed rows
   L.total = off;
   return L;
 }
@@ -164,7 +174,9 @@ struct tpattn_ctx {
   bool upd_in_bwd = false, upd_done = false, upd_epi = false;
   float upd_lr = 0.0f;
   bool fused = true, fwd_fused = false;
-  int64_t batch = 0, seq = 0;
+  int64_t batch = 0, seq = 0;  // the last forward's; seq 0: packed
+  int64_t tokens = 0;
+  const int32_t* cu_rows = nullptr;  // packed only
   const void *x = nullptr, *norm_w = nullptr, *w_qkv = nullptr, *w_o = nullptr, *b_o = nullptr;
   float *g_norm_w = nullptr, *g_w_qkv = nullptr, *g_w_o = nullptr, *g_b_o = nullptr;
   float *m_norm_w = nullptr, *m_w_qkv = nullptr, *m_w_o = nullptr, *m_b_o = nullptr;
@@ -247,6 +259,14 @@ BatchDesc head_batch(int B, int n_kv, int hpg) {
   bd.dims[1] = n_kv;
   bd.dims[2] = hpg;
   return bd;
+}
+
+SeqRows packed_seqs(const tpattn_ctx* c) {
+  SeqRows s{};
+  s.cu_rows = c->cu_rows;
+  s.batch = (int)c->batch;
+  s.rows = c->tokens;
+  return s;
 }
 
 // Unfused attention core: scores, causal softmax and P V as batched GEMMs
@@ -499,6 +519,23 @@ tpmlp_status tpattn_bind_workspace(tpattn_ctx* c, void* dev, size_t bytes) {
   return e == cudaSuccess ? TPMLP_OK : c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
 }
 
+// Tensors, eps and t of a forward.
+static tpmlp_status attn_check_forward(tpattn_ctx* c, const void* x, const void* norm_w, const void* w_qkv,
+                                       const void* w_o, const void* b_o, float eps, int32_t t, const void* y) {
+  const tpattn_config& cf = c->cfg;
+  if (t < 1 || t > cf.max_t || cf.n_kv_heads % t != 0) return c->fail(TPMLP_ERR_SHAPE, "t must divide n_kv_heads");
+  if (!x || !norm_w || !w_qkv || !w_o || !b_o || !y) return c->fail(TPMLP_ERR_ARG, "NULL tensor");
+  for (const void* p : {x, norm_w, w_qkv, w_o, b_o, y})
+    if (!a16(p)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return c->fail(TPMLP_ERR_ARG, "eps must be finite and >= 0");
+  return TPMLP_OK;
+}
+
+// B sequences of S tokens, or with cu_rows (S 0) B packed ones of N tokens.
+static tpmlp_status attn_run_forward(tpattn_ctx* c, int B, int S, int N, const int32_t* cu_rows, const void* x,
+                                     const void* norm_w, const void* w_qkv, const void* w_o, const void* b_o, float eps,
+                                     void* y);
+
 tpmlp_status tpattn_forward(tpattn_ctx* c, int64_t batch, int64_t seq, const void* x, const void* norm_w,
                             const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t, void* y) {
   if (!c) return TPMLP_ERR_ARG;
@@ -506,18 +543,36 @@ tpmlp_status tpattn_forward(tpattn_ctx* c, int64_t batch, int64_t seq, const voi
   const tpattn_config& cf = c->cfg;
   if (batch < 1 || seq < 64 || seq % 64 != 0 || seq > cf.max_seq || batch * seq > cf.max_tokens)
     return c->fail(TPMLP_ERR_SHAPE, "seq must be a multiple of 64 within max_seq, batch * seq within max_tokens");
-  if (t < 1 || t > cf.max_t || cf.n_kv_heads % t != 0) return c->fail(TPMLP_ERR_SHAPE, "t must divide n_kv_heads");
   if ((cf.flags & TPATTN_FUSED_ONLY) && seq % 128 != 0)
     return c->fail(TPMLP_ERR_SHAPE, "a fused-only context needs seq to be a multiple of 128");
-  if (!x || !norm_w || !w_qkv || !w_o || !b_o || !y) return c->fail(TPMLP_ERR_ARG, "NULL tensor");
-  for (const void* p : {x, norm_w, w_qkv, w_o, b_o, (const void*)y})
-    if (!a16(p)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
-  if (!(eps >= 0.0f) || !std::isfinite(eps)) return c->fail(TPMLP_ERR_ARG, "eps must be finite and >= 0");
-  const int B = (int)batch, S = (int)seq, N = B * S, H = (int)cf.hidden, d = cf.head_dim;
+  ATTN_TRY(attn_check_forward(c, x, norm_w, w_qkv, w_o, b_o, eps, t, y));
+  return attn_run_forward(c, (int)batch, (int)seq, (int)(batch * seq), nullptr, x, norm_w, w_qkv, w_o, b_o, eps, y);
+}
+
+tpmlp_status tpattn_forward_packed(tpattn_ctx* c, int64_t tokens, int32_t batch, const int32_t* cu_rows, const void* x,
+                                   const void* norm_w, const void* w_qkv, const void* w_o, const void* b_o, float eps,
+                                   int32_t t, void* y) {
+  if (!c) return TPMLP_ERR_ARG;
+  if (!c->ws) return c->fail(TPMLP_ERR_ORDER, "no workspace bound");
+  if (tokens < 1 || tokens > c->cfg.max_tokens) return c->fail(TPMLP_ERR_SHAPE, "tokens must be within max_tokens");
+  if (batch < 1 || batch > (1 << 20)) return c->fail(TPMLP_ERR_SHAPE, "batch out of range (1 to 2^20)");
+  if (!cu_rows) return c->fail(TPMLP_ERR_ARG, "cu_rows is NULL");
+  if (reinterpret_cast<uintptr_t>(cu_rows) & 3u) return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
+  ATTN_TRY(attn_check_forward(c, x, norm_w, w_qkv, w_o, b_o, eps, t, y));
+  return attn_run_forward(c, batch, 0, (int)tokens, cu_rows, x, norm_w, w_qkv, w_o, b_o, eps, y);
+}
+
+static tpmlp_status attn_run_forward(tpattn_ctx* c, int B, int S, int N, const int32_t* cu_rows, const void* x,
+                                     const void* norm_w, const void* w_qkv, const void* w_o, const void* b_o, float eps,
+                                     void* y) {
+  const tpattn_config& cf = c->cfg;
+  const int H = (int)cf.hidden, d = cf.head_dim;
   const int nq = cf.n_heads, nkv = cf.n_kv_heads, W = (nq + 2 * nkv) * d, Zc = nq * d;
   c->fwd_done = c->bwd_done = false;
-  c->batch = batch;
-  c->seq = seq;
+  c->batch = B;
+  c->seq = S;
+  c->tokens = N;
+  c->cu_rows = cu_rows;
   c->x = x;
   c->norm_w = norm_w;
   c->w_qkv = w_qkv;
@@ -528,7 +583,16 @@ tpmlp_status tpattn_forward(tpattn_ctx* c, int64_t batch, int64_t seq, const voi
   void* z = c->wsp<void>(c->L.z);
   float* sc = c->wsp<float>(c->L.scores);
   void* pr = c->wsp<void>(c->L.probs);
-  c->fwd_fused = c->fused && d == 128 && S % 128 == 0;
+  c->fwd_fused = !cu_rows && c->fused && d == 128 && S % 128 == 0;
+  const int32_t* pos = nullptr;
+  if (cu_rows) {
+    int32_t* out = c->wsp<int32_t>(c->L.pos);
+    ATTN_TRY(c->run(A_PACKED_ROWS, [&] {
+      return launch_packed_rows(packed_seqs(c), out, z, (int64_t)Zc * 2, c->wsp<void>(c->L.dqkv), (int64_t)W * 2,
+                                c->wsp<uint32_t>(c->L.status), c->num_sms, c->stream);
+    }));
+    pos = out;
+  }
   ATTN_TRY(c->run(A_RMSNORM_FWD, [&] {
     return launch_rmsnorm_fwd(1, x, norm_w, eps, nrm, c->wsp<float>(c->L.rstd), N, H, c->stream);
   }));
@@ -561,10 +625,27 @@ tpmlp_status tpattn_forward(tpattn_ctx* c, int64_t batch, int64_t seq, const voi
     r.q_norm_w = c->qk.q_norm_w;
     r.k_norm_w = c->qk.k_norm_w;
     r.eps = c->qk.eps;
+    r.pos = pos;
     r.seq = S;
     ATTN_TRY(c->run(A_QK_ROPE, [&] { return launch_qk_rope(1, d, r, c->qk_freqs, c->num_sms, c->stream); }));
   }
-  if (c->fwd_fused) {
+  if (cu_rows) {
+    VarFwdArgs v{};
+    v.seq = packed_seqs(c);
+    v.q = qkv;
+    v.k = static_cast<const uint16_t*>(qkv) + Zc;
+    v.v = static_cast<const uint16_t*>(qkv) + Zc + nkv * d;
+    v.ld_q = v.ld_k = v.ld_v = W;
+    v.out = z;
+    v.ld_out = Zc;
+    v.lse = c->wsp<float>(c->L.lse2);
+    v.nq = nq;
+    v.nkv = nkv;
+    v.d = d;
+    v.scale = 1.0f / std::sqrt((float)d);
+    v.status = c->wsp<uint32_t>(c->L.status);
+    ATTN_TRY(c->run(A_VAR_FWD, [&] { return launch_var_fwd(v, c->num_sms, c->stream); }));
+  } else if (c->fwd_fused) {
     ATTN_TRY(c->run(A_FLASH_FWD, [&] {
       return launch_flash_attn_fwd(qkv, B, S, nq, nkv, d, z, c->wsp<float>(c->L.lse2), c->wsp<uint32_t>(c->L.status),
                                    c->stream);
@@ -633,7 +714,7 @@ tpmlp_status tpattn_backward(tpattn_ctx* c, const void* dy, void* dx, float* dno
                         (const void*)db_o})
     if (!a16(p)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
   const tpattn_config& cf = c->cfg;
-  const int B = (int)c->batch, S = (int)c->seq, N = B * S, H = (int)cf.hidden, d = cf.head_dim;
+  const int B = (int)c->batch, S = (int)c->seq, N = (int)c->tokens, H = (int)cf.hidden, d = cf.head_dim;
   const int nq = cf.n_heads, nkv = cf.n_kv_heads, W = (nq + 2 * nkv) * d, Zc = nq * d;
   const bool upd = c->upd_in_bwd;
   if (upd && (!c->m_norm_w || !c->m_w_qkv || !c->m_w_o || !c->m_b_o))
@@ -697,7 +778,29 @@ tpmlp_status tpattn_backward(tpattn_ctx* c, const void* dy, void* dx, float* dno
     wo.ep.sgd_lr = c->upd_lr;
   }
   ATTN_TRY(c->gemm(A_GEMM_WGRAD_OUT, wo));
-  if (c->fwd_fused) {
+  if (c->cu_rows) {
+    VarBwdArgs v{};
+    v.seq = packed_seqs(c);
+    v.q = qkv;
+    v.k = static_cast<const uint16_t*>(qkv) + Zc;
+    v.v = static_cast<const uint16_t*>(qkv) + Zc + nkv * d;
+    v.ld_q = v.ld_k = v.ld_v = W;
+    v.out = z;
+    v.dout = dz;
+    v.ld_out = v.ld_dout = Zc;
+    v.lse = c->wsp<float>(c->L.lse2);
+    v.dq = dqkv;
+    v.dk = static_cast<uint16_t*>(dqkv) + Zc;
+    v.dv = static_cast<uint16_t*>(dqkv) + Zc + nkv * d;
+    v.ld_dq = v.ld_dk = v.ld_dv = W;
+    v.stats = c->wsp<float2>(c->L.dkv_head);
+    v.nq = nq;
+    v.nkv = nkv;
+    v.d = d;
+    v.scale = 1.0f / std::sqrt((float)d);
+    v.status = c->wsp<uint32_t>(c->L.status);
+    ATTN_TRY(c->run(A_VAR_BWD, [&] { return launch_var_bwd(v, c->num_sms, c->stream); }));
+  } else if (c->fwd_fused) {
     float* dq_acc = c->wsp<float>(c->L.dkv_head);
     float* dsum = c->wsp<float>(c->L.dsum);
     ATTN_TRY(c->run(A_FLASH_BWD_PREP,
@@ -726,6 +829,7 @@ tpmlp_status tpattn_backward(tpattn_ctx* c, const void* dy, void* dx, float* dno
     r.k_norm_w = c->qk.k_norm_w;
     r.eps = c->qk.eps;
     r.seq = S;
+    if (c->cu_rows) r.pos = c->wsp<int32_t>(c->L.pos);
     if (c->qk.q_norm_w) r.part = reinterpret_cast<float*>(c->qk_ws + c->qk_part_off);
     ATTN_TRY(c->run(A_QK_ROPE_BWD, [&] {
       return launch_qk_rope_bwd(1, d, r, c->qk_freqs, c->num_sms, c->stream, c->qk.dq_norm_w, c->qk.dk_norm_w);
@@ -970,40 +1074,48 @@ tpmlp_status tpattn_append_kv(tpattn_ctx* c, tpkv_ctx* kv, const int32_t* new_le
   ATTN_TRY(attn_check_kv(c, kv));
   if (!c->fwd_done) return c->fail(TPMLP_ERR_ORDER, "append_kv before forward");
   const tpattn_config& cf = c->cfg;
-  const int64_t rows = c->batch * c->seq, W = (int64_t)(cf.n_heads + 2 * cf.n_kv_heads) * cf.head_dim;
+  const int64_t rows = c->tokens, W = (int64_t)(cf.n_heads + 2 * cf.n_kv_heads) * cf.head_dim;
+  if (c->cu_rows && new_lens) return c->fail(TPMLP_ERR_ARG, "packed sequences are stored whole: new_lens must be NULL");
   if (reinterpret_cast<uintptr_t>(new_lens) & 3u) return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
   tpmlp_status s = kv_check_call(kv, c->batch, table, table, ld_table, max_pages);
   if (s == TPMLP_OK) s = kv_check_append(kv);
   if (s != TPMLP_OK) return c->fail(s, kv->err);
   s = TPMLP_OK;
   const tpmlp_status r = c->run(A_KV_APPEND, [&] {
-    s = kv_run_append(kv, rows, (int32_t)c->batch, c->wsp<void>(c->L.qkv), W, nullptr, new_lens, nullptr, table, ld_table,
+    s = kv_run_append(kv, rows, (int32_t)c->batch, c->wsp<void>(c->L.qkv), W, c->cu_rows, new_lens, nullptr, table, ld_table,
                       max_pages, QkTransform{}, nullptr, 0, c->stream);
     return cudaSuccess;
   });
   return s != TPMLP_OK ? c->fail(s, kv->err) : r;
 }
 
-tpmlp_status tpattn_decode(tpattn_ctx* c, tpkv_ctx* kv, int32_t batch, const void* x, const void* norm_w,
-                           const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
-                           const int32_t* past_lens, const int32_t* table, int64_t ld_table, int32_t max_pages,
-                           int32_t window, int32_t sinks, void* y) {
-  if (!c) return TPMLP_ERR_ARG;
+}  // extern "C"
+
+namespace {
+
+// What tpattn_decode and tpattn_extend check alike.
+tpmlp_status attn_check_answer(tpattn_ctx* c, tpkv_ctx* kv, int64_t rows, int32_t batch, const void* x,
+                                      const void* norm_w, const void* w_qkv, const void* w_o, const void* b_o, float eps,
+                                      int32_t t, const int32_t* past_lens, const int32_t* table, int64_t ld_table,
+                                      int32_t max_pages, int32_t window, int32_t sinks, const void* y) {
   if (!c->ws) return c->fail(TPMLP_ERR_ORDER, "no workspace bound");
   ATTN_TRY(attn_check_kv(c, kv));
-  const tpattn_config& cf = c->cfg;
-  if (batch < 1 || batch > cf.max_tokens) return c->fail(TPMLP_ERR_SHAPE, "batch must be within max_tokens");
-  if (t < 1 || t > cf.max_t || cf.n_kv_heads % t != 0) return c->fail(TPMLP_ERR_SHAPE, "t must divide n_kv_heads");
-  if (!x || !norm_w || !w_qkv || !w_o || !b_o || !y) return c->fail(TPMLP_ERR_ARG, "NULL tensor");
-  for (const void* p : {x, norm_w, w_qkv, w_o, b_o, (const void*)y})
-    if (!a16(p)) return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
-  if (!(eps >= 0.0f) || !std::isfinite(eps)) return c->fail(TPMLP_ERR_ARG, "eps must be finite and >= 0");
+  if (batch < 1 || rows < 1 || rows > c->cfg.max_tokens)
+    return c->fail(TPMLP_ERR_SHAPE, "batch and rows must be within max_tokens");
+  ATTN_TRY(attn_check_forward(c, x, norm_w, w_qkv, w_o, b_o, eps, t, y));
   if (window < 0 || sinks < 0) return c->fail(TPMLP_ERR_ARG, "window and sinks must be >= 0");
   tpmlp_status s = kv_check_call(kv, batch, past_lens, table, ld_table, max_pages);
   if (s == TPMLP_OK) s = kv_check_append(kv);
-  if (s != TPMLP_OK) return c->fail(s, kv->err);
-  const int N = batch, H = (int)cf.hidden, d = cf.head_dim, nq = cf.n_heads, nkv = cf.n_kv_heads;
-  const int W = (nq + 2 * nkv) * d, Zc = nq * d;
+  return s == TPMLP_OK ? s : c->fail(s, kv->err);
+}
+
+// The sublayer over new tokens; attend(qkv, z) enqueues append and attention
+// and returns a cache status.
+template <typename Attend>
+tpmlp_status attn_answer(tpattn_ctx* c, int N, const void* x, const void* norm_w, const void* w_qkv,
+                                const void* w_o, const void* b_o, float eps, void* y, Attend&& attend) {
+  const tpattn_config& cf = c->cfg;
+  const int H = (int)cf.hidden, d = cf.head_dim, W = (cf.n_heads + 2 * cf.n_kv_heads) * d, Zc = cf.n_heads * d;
   // The last forward's workspace is overwritten; gradients that a backward has
   // written already are the caller's and may still be applied.
   c->fwd_done = false;
@@ -1027,21 +1139,7 @@ tpmlp_status tpattn_decode(tpattn_ctx* c, tpkv_ctx* kv, int32_t batch, const voi
   g.ep.out0 = qkv;
   g.ep.ld_out0 = W;
   ATTN_TRY(c->gemm(A_GEMM_QKV, g));
-  QkTransform tr;
-  if (c->qk_on) tr = {&c->qk_freqs, c->qk.q_norm_w, c->qk.k_norm_w, c->qk.eps};
-  tpmlp_status r = c->run(A_KV_APPEND, [&] {  // the queries in place
-    s = kv_run_append(kv, N, N, qkv, W, nullptr, nullptr, past_lens, table, ld_table, max_pages, tr, qkv, W, c->stream);
-    return cudaSuccess;
-  });
-  if (s != TPMLP_OK) return c->fail(s, kv->err);
-  ATTN_TRY(r);
-  r = c->run(A_KV_DECODE, [&] {
-    s = kv_run_decode(kv, N, qkv, W, past_lens, 1, table, ld_table, max_pages, 1.0f / std::sqrt((float)d), window, sinks, z,
-                      Zc, nullptr, c->stream);
-    return cudaSuccess;
-  });
-  if (s != TPMLP_OK) return c->fail(s, kv->err);
-  ATTN_TRY(r);
+  ATTN_TRY(attend(qkv, z));
   GemmDesc o;
   o.M = N;
   o.N = H;
@@ -1061,6 +1159,74 @@ tpmlp_status tpattn_decode(tpattn_ctx* c, tpkv_ctx* kv, int32_t batch, const voi
   return c->gemm(A_GEMM_OUT, o);
 }
 
+// A launch through the cache context, whose status and message are its own.
+template <typename Fn>
+tpmlp_status attn_run_kv(tpattn_ctx* c, tpkv_ctx* kv, int id, Fn&& fn) {
+  tpmlp_status s = TPMLP_OK;
+  const tpmlp_status r = c->run(id, [&] {
+    s = fn();
+    return cudaSuccess;
+  });
+  return s != TPMLP_OK ? c->fail(s, kv->err) : r;
+}
+
+}  // namespace
+
+extern "C" {
+
+tpmlp_status tpattn_decode(tpattn_ctx* c, tpkv_ctx* kv, int32_t batch, const void* x, const void* norm_w,
+                           const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
+                           const int32_t* past_lens, const int32_t* table, int64_t ld_table, int32_t max_pages,
+                           int32_t window, int32_t sinks, void* y) {
+  if (!c) return TPMLP_ERR_ARG;
+  ATTN_TRY(attn_check_answer(c, kv, batch, batch, x, norm_w, w_qkv, w_o, b_o, eps, t, past_lens, table, ld_table,
+                             max_pages, window, sinks, y));
+  const tpattn_config& cf = c->cfg;
+  const int N = batch, d = cf.head_dim, W = (cf.n_heads + 2 * cf.n_kv_heads) * d, Zc = cf.n_heads * d;
+  QkTransform tr;
+  if (c->qk_on) tr = {&c->qk_freqs, c->qk.q_norm_w, c->qk.k_norm_w, c->qk.eps};
+  return attn_answer(c, N, x, norm_w, w_qkv, w_o, b_o, eps, y, [&](void* qkv, void* z) {
+    ATTN_TRY(attn_run_kv(c, kv, A_KV_APPEND, [&] {  // the queries in place
+      return kv_run_append(kv, N, N, qkv, W, nullptr, nullptr, past_lens, table, ld_table, max_pages, tr, qkv, W,
+                           c->stream);
+    }));
+    return attn_run_kv(c, kv, A_KV_DECODE, [&] {
+      return kv_run_decode(kv, N, qkv, W, past_lens, 1, table, ld_table, max_pages, 1.0f / std::sqrt((float)d), window,
+                           sinks, z, Zc, nullptr, c->stream);
+    });
+  });
+}
+
+tpmlp_status tpattn_extend(tpattn_ctx* c, tpkv_ctx* kv, int64_t rows, int32_t batch, const void* x, const void* norm_w,
+                           const void* w_qkv, const void* w_o, const void* b_o, float eps, int32_t t,
+                           const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
+                           const int32_t* table, int64_t ld_table, int32_t max_pages, int32_t window, int32_t sinks,
+                           void* y) {
+  if (!c) return TPMLP_ERR_ARG;
+  ATTN_TRY(attn_check_answer(c, kv, rows, batch, x, norm_w, w_qkv, w_o, b_o, eps, t, past_lens, table, ld_table,
+                             max_pages, window, sinks, y));
+  if (const tpmlp_status s = kv_check_rows(kv, rows, batch, cu_rows, new_lens)) return c->fail(s, kv->err);
+  const tpattn_config& cf = c->cfg;
+  const int N = (int)rows, d = cf.head_dim, W = (cf.n_heads + 2 * cf.n_kv_heads) * d, Zc = cf.n_heads * d;
+  const SeqRows seq{cu_rows, new_lens, past_lens, batch, N / batch, rows};
+  QkTransform tr;
+  if (c->qk_on) tr = {&c->qk_freqs, c->qk.q_norm_w, c->qk.k_norm_w, c->qk.eps};
+  return attn_answer(c, N, x, norm_w, w_qkv, w_o, b_o, eps, y, [&](void* qkv, void* z) {
+    ATTN_TRY(attn_run_kv(c, kv, A_KV_APPEND, [&] {  // the queries in place
+      return kv_run_append(kv, N, batch, qkv, W, cu_rows, new_lens, past_lens, table, ld_table, max_pages, tr, qkv, W,
+                           c->stream);
+    }));
+    if (cu_rows || new_lens)  // rows that are no token's
+      ATTN_TRY(c->run(A_PACKED_ROWS, [&] {
+        return launch_packed_rows(seq, nullptr, z, (int64_t)Zc * 2, nullptr, 0, kv->status, c->num_sms, c->stream);
+      }));
+    return attn_run_kv(c, kv, A_KV_EXTEND, [&] {
+      return kv_run_extend(kv, seq, qkv, W, table, ld_table, max_pages, 1.0f / std::sqrt((float)d), window, sinks, z, Zc,
+                           nullptr, c->stream);
+    });
+  });
+}
+
 tpmlp_status tpattn_sync(tpattn_ctx* c) {
   if (!c) return TPMLP_ERR_ARG;
   cudaError_t e = cudaStreamSynchronize(c->stream);
@@ -1072,6 +1238,7 @@ tpmlp_status tpattn_sync(tpattn_ctx* c) {
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
   if (st) {
     cudaMemsetAsync(c->wsp<uint32_t>(c->L.status), 0, sizeof st, c->stream);
+    if (st == STATUS_BAD_INDEX) return c->fail(TPMLP_ERR_ARG, "cu_rows descend or leave the rows");
     return c->fail(TPMLP_ERR_TIMEOUT, "a bounded device wait gave up");
   }
   return TPMLP_OK;

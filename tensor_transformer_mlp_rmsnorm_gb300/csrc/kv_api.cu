@@ -407,12 +407,7 @@ tpmlp_status tpkv_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q
   KV_TRY(kv_check_append(c));
   const tpkv_config& cf = c->cfg;
   const int64_t W = (int64_t)(cf.n_heads + 2 * cf.n_kv_heads) * cf.head_dim, Z = (int64_t)cf.n_heads * cf.head_dim;
-  if (rows < 0 || rows > 0x7fffffff) return c->fail(TPMLP_ERR_SHAPE, "rows out of range");
-  if (cu_rows && new_lens) return c->fail(TPMLP_ERR_ARG, "cu_rows or new_lens, not both");
-  if (!cu_rows && (batch == 0 ? rows != 0 : rows % batch != 0))
-    return c->fail(TPMLP_ERR_SHAPE, "without cu_rows, rows must be a multiple of batch");
-  if ((reinterpret_cast<uintptr_t>(cu_rows) | reinterpret_cast<uintptr_t>(new_lens)) & 3u)
-    return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
+  KV_TRY(kv_check_rows(c, rows, batch, cu_rows, new_lens));
   if (transform != 0 && transform != 1) return c->fail(TPMLP_ERR_ARG, "transform must be 0 or 1");
   if (ld_qkv % 8 != 0 || ld_qkv < W || (q_out && (ld_q % 8 != 0 || ld_q < Z)))
     return c->fail(TPMLP_ERR_SHAPE, "row strides must be multiples of 8 and hold a row");
@@ -443,6 +438,27 @@ tpmlp_status tpkv_decode(tpkv_ctx* c, int32_t batch, const void* q, int64_t ld_q
   if (q == out && ld_q != ld_out && batch > 1) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
   return kv_run_decode(c, batch, q, ld_q, lens, len_add, table, ld_table, max_pages, scale, window, sinks, out, ld_out,
                        lse, c->stream);
+}
+
+tpmlp_status tpkv_extend(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q, int64_t ld_q, const int32_t* cu_rows,
+                         const int32_t* new_lens, const int32_t* past_lens, const int32_t* table, int64_t ld_table,
+                         int32_t max_pages, float scale, int32_t window, int32_t sinks, void* out, int64_t ld_out,
+                         float* lse) {
+  if (!c) return TPMLP_ERR_ARG;
+  KV_TRY(kv_check_call(c, batch, past_lens, table, ld_table, max_pages));
+  KV_TRY(kv_check_rows(c, rows, batch, cu_rows, new_lens));
+  const int64_t Z = (int64_t)c->cfg.n_heads * c->cfg.head_dim;
+  if (ld_q % 8 != 0 || ld_q < Z || ld_out % 8 != 0 || ld_out < Z)
+    return c->fail(TPMLP_ERR_SHAPE, "row strides must be multiples of 8 and hold a row");
+  if (!std::isfinite(scale)) return c->fail(TPMLP_ERR_ARG, "scale must be finite");
+  if (window < 0 || sinks < 0) return c->fail(TPMLP_ERR_ARG, "window and sinks must be >= 0");
+  if (rows == 0 || batch == 0) return TPMLP_OK;
+  if (!q || !out) return c->fail(TPMLP_ERR_ARG, "NULL tensor");
+  if (!a16(q) || !a16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
+  if (q == out && ld_q != ld_out && rows > 1) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
+  const SeqRows seq{cu_rows, new_lens, past_lens, batch, (int)(rows / batch), rows};
+  return kv_run_extend(c, seq, q, ld_q, table, ld_table, max_pages, scale, window, sinks, out, ld_out, lse, c->stream);
 }
 
 tpmlp_status tpkv_sync(tpkv_ctx* c) {
@@ -487,6 +503,16 @@ tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, cons
     return c->fail(TPMLP_ERR_SHAPE, "block table out of range (at most 2^30 tokens a sequence)");
   if (batch > 0 && (!lens || (!table && max_pages > 0))) return c->fail(TPMLP_ERR_ARG, "NULL lengths or block table");
   if ((reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(table)) & 3u)
+    return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
+  return TPMLP_OK;
+}
+
+tpmlp_status kv_check_rows(tpkv_ctx* c, int64_t rows, int32_t batch, const int32_t* cu_rows, const int32_t* new_lens) {
+  if (rows < 0 || rows > 0x7fffffff) return c->fail(TPMLP_ERR_SHAPE, "rows out of range");
+  if (cu_rows && new_lens) return c->fail(TPMLP_ERR_ARG, "cu_rows or new_lens, not both");
+  if (!cu_rows && (batch == 0 ? rows != 0 : rows % batch != 0))
+    return c->fail(TPMLP_ERR_SHAPE, "without cu_rows, rows must be a multiple of batch");
+  if ((reinterpret_cast<uintptr_t>(cu_rows) | reinterpret_cast<uintptr_t>(new_lens)) & 3u)
     return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
   return TPMLP_OK;
 }
@@ -576,6 +602,46 @@ tpmlp_status kv_run_decode(tpkv_ctx* c, int32_t batch, const void* q, int64_t ld
   OnDevice on(c->device);
   cudaError_t e = wait_for_clear(c, st);
   if (e == cudaSuccess) e = launch_kv_decode(a, c->kmap, c->vmap, cf.head_dim, cf.cache_dtype == TPKV_E4M3, st);
+  if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
+  ++c->launches;
+  return TPMLP_OK;
+}
+
+tpmlp_status kv_run_extend(tpkv_ctx* c, const SeqRows& seq, const void* q, int64_t ld_q, const int32_t* table,
+                           int64_t ld_table, int32_t max_pages, float scale, int32_t window, int32_t sinks, void* out,
+                           int64_t ld_out, float* lse, cudaStream_t st) {
+  const tpkv_config& cf = c->cfg;
+  VarFwdArgs a{};
+  a.seq = seq;
+  a.q = q;
+  a.ld_q = ld_q;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.lse = lse;
+  a.nq = cf.n_heads;
+  a.nkv = cf.n_kv_heads;
+  a.d = cf.head_dim;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.status = c->status;
+  a.paged = true;
+  a.e4m3 = cf.cache_dtype == TPKV_E4M3;
+  a.table = table;
+  a.ld_table = ld_table;
+  a.max_pages = max_pages;
+  a.page_size = cf.page_size;
+  a.num_pages = cf.num_pages;
+  a.k_cache = c->k;
+  a.v_cache = c->v;
+  a.stride_page = c->stride_page;
+  a.stride_head = c->stride_head;
+  a.stride_slot = c->stride_slot;
+  a.k_inv_scale = c->k_inv_scale;
+  a.v_inv_scale = c->v_inv_scale;
+  OnDevice on(c->device);
+  cudaError_t e = wait_for_clear(c, st);
+  if (e == cudaSuccess) e = launch_var_fwd(a, c->num_sms, st);
   if (e != cudaSuccess) return c->fail(TPMLP_ERR_CUDA, cudaGetErrorString(e));
   ++c->launches;
   return TPMLP_OK;

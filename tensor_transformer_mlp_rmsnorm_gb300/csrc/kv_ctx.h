@@ -8,6 +8,7 @@
 #include "../../include/tpmlp.h"
 #include "kv_decode.h"
 #include "qk_rope.h"
+#include "varlen.h"
 
 namespace tpmlp {
 constexpr int KV_MAX_WORKERS = 512;  // CTAs of the decode kernel
@@ -55,6 +56,7 @@ RopeFreqs freqs_of(const tpattn_rotary* r);
 tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, const int32_t* table, int64_t ld_table,
                            int32_t max_pages);
 tpmlp_status kv_check_append(tpkv_ctx* c);
+tpmlp_status kv_check_rows(tpkv_ctx* c, int64_t rows, int32_t batch, const int32_t* cu_rows, const int32_t* new_lens);
 tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,
                            const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
                            const int32_t* table, int64_t ld_table, int32_t max_pages, const QkTransform& tr,
@@ -62,5 +64,8 @@ tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void*
 tpmlp_status kv_run_decode(tpkv_ctx* c, int32_t batch, const void* q, int64_t ld_q, const int32_t* lens,
                            int32_t len_add, const int32_t* table, int64_t ld_table, int32_t max_pages, float scale,
                            int32_t window, int32_t sinks, void* out, int64_t ld_out, float* lse, cudaStream_t st);
+tpmlp_status kv_run_extend(tpkv_ctx* c, const SeqRows& seq, const void* q, int64_t ld_q, const int32_t* table,
+                           int64_t ld_table, int32_t max_pages, float scale, int32_t window, int32_t sinks, void* out,
+                           int64_t ld_out, float* lse, cudaStream_t st);
 
 }  // namespace tpmlp

@@ -1,0 +1,70 @@
+// Attention of sequences of different lengths: kernel arguments, shared by the
+// calls over packed rows and over a paged cache.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tpmlp_internal.h"
+
+namespace tpmlp {
+
+// Which rows are whose.  Sequence b has `count` rows from `first` on, the i-th
+// of them at position past + i; past < 0: an inactive sequence.
+struct SeqRows {
+  const int32_t* cu_rows;    // [batch + 1], or null: rows_per_seq rows each
+  const int32_t* new_lens;   // [batch] tokens among them, or null: all
+  const int32_t* past_lens;  // [batch], or null: 0
+  int batch;
+  int rows_per_seq;
+  int64_t rows;
+};
+
+// Forward: q, out [rows, >= nq d] bf16, lse [rows, nq] natural log or null.
+// Keys and values: rows of their own (packed), or a paged cache.
+struct VarFwdArgs {
+  SeqRows seq;
+  const void *q, *k, *v;  // k, v: packed only
+  int64_t ld_q, ld_k, ld_v;
+  void* out;
+  int64_t ld_out;
+  float* lse;
+  int nq, nkv, d;
+  float scale;
+  int window, sinks;  // window 0: no limit
+  uint32_t* status;
+  // the cache
+  bool paged, e4m3;
+  const int32_t* table;
+  int64_t ld_table;
+  int max_pages, page_size;
+  int64_t num_pages;
+  const void *k_cache, *v_cache;
+  int64_t stride_page, stride_head, stride_slot;
+  const float *k_inv_scale, *v_inv_scale;  // E4M3: [nkv] or null
+};
+
+// Backward over packed rows.
+struct VarBwdArgs {
+  SeqRows seq;
+  const void *q, *k, *v, *out, *dout;
+  int64_t ld_q, ld_k, ld_v, ld_out, ld_dout;
+  const float* lse;
+  void *dq, *dk, *dv;
+  int64_t ld_dq, ld_dk, ld_dv;
+  float2* stats;  // scratch [rows, nq]
+  int nq, nkv, d;
+  float scale;
+  int window, sinks;
+  uint32_t* status;
+};
+
+// For each row its position (pos, or null), and zeros in rows of z and dz (row
+// bytes, multiples of 16; null: none) that are no sequence's.  past is not used.
+cudaError_t launch_packed_rows(const SeqRows& s, int32_t* pos, void* z, int64_t z_bytes, void* dz, int64_t dz_bytes,
+                               uint32_t* status, int num_sms, cudaStream_t st);
+cudaError_t launch_var_fwd(const VarFwdArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_var_bwd(const VarBwdArgs& a, int num_sms, cudaStream_t st);
+
+}  // namespace tpmlp

@@ -92,6 +92,14 @@ class QkParams(ctypes.Structure):
                                        "m_k", "v_q", "v_k")] + [("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class PackedDesc(ctypes.Structure):
+    """tpattn_packed_desc."""
+    _fields_ = [("rows", ctypes.c_int64), ("batch", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("cu_rows", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class KvConfig(ctypes.Structure):
     """tpkv_config."""
     _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("max_batch", ctypes.c_int32),
@@ -156,6 +164,14 @@ _SIGNATURES = {
     "tpattn_qk_rope_workspace_bytes": (ctypes.c_size_t, [_i32]),
     "tpattn_qk_rope_backward": (_i32, [ctypes.POINTER(QkDesc), ctypes.POINTER(RotarySpec), _vp, _i64, _vp, _i64, _vp,
                                        _i64, _fp, _fp, _vp, ctypes.c_size_t, _vp]),
+    "tpattn_packed_forward": (_i32, [ctypes.POINTER(PackedDesc), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _fp, _vp,
+                                     _vp]),
+    "tpattn_packed_workspace_bytes": (ctypes.c_size_t, [_i64, _i32]),
+    "tpattn_packed_backward": (_i32, [ctypes.POINTER(PackedDesc), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _fp, _vp,
+                                      _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_size_t, _vp, _vp]),
+    "tpattn_forward_packed": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _vp]),
+    "tpattn_extend": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _vp, _vp, _vp, _vp, _i64, _i32,
+                             _i32, _i32, _vp]),
     "tpattn_qk_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AttnConfig)]),
     "tpattn_set_qk": (_i32, [_vp, ctypes.POINTER(QkParams), _vp, ctypes.c_size_t]),
     "tpattn_append_kv": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32]),
@@ -168,6 +184,8 @@ _SIGNATURES = {
     "tpkv_set_rotary": (_i32, [_vp, ctypes.POINTER(RotarySpec), _vp, _vp, _f32]),
     "tpkv_append": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _i64]),
     "tpkv_decode": (_i32, [_vp, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _i32, _f32, _i32, _i32, _vp, _i64, _fp]),
+    "tpkv_extend": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _f32, _i32, _i32, _vp, _i64,
+                           _fp]),
     "tpkv_sync": (_i32, [_vp]),
     "tpkv_launch_count": (ctypes.c_uint64, [_vp]),
     "tpkv_last_error": (ctypes.c_char_p, [_vp]),
@@ -568,6 +586,27 @@ class TPAttn:
         self._batch = batch
         return y
 
+    def forward_packed(self, x, norm_w, w_qkv, w_o, b_o, eps: float, t: int, cu_rows, y=None):
+        """The sublayer over packed sequences of any lengths (tpattn_forward_packed): sequence b has the rows
+        [cu_rows[b], cu_rows[b + 1]) of x, cu_rows int32 on the device.  backward, the updates and append_kv follow as
+        after forward."""
+        n = x.shape[0]
+        y = torch.empty_like(x) if y is None else y
+        cp = _vec(cu_rows, cu_rows.shape[0], _I32T, "cu_rows", self.device.index)
+        _acheck(lib().tpattn_forward_packed(self.ctx, n, cu_rows.shape[0] - 1, cp, self._t(x, (n, self.H), name="x"),
+                                            self._t(norm_w, (self.H,), name="norm_w"),
+                                            self._t(w_qkv, (self.W, self.H), name="w_qkv"),
+                                            self._t(w_o, (self.H, self.nq * self.d), name="w_o"),
+                                            self._t(b_o, (self.H,), name="b_o"), float(eps), int(t),
+                                            self._t(y, (n, self.H), name="y")), self.ctx)
+        self._uses(x, norm_w, w_qkv, w_o, b_o, cu_rows, y)
+        # held as by forward; backward and append_kv read cu_rows
+        self._fwd_tensors = (x, norm_w, w_qkv, w_o, b_o, cu_rows)
+        self.params = (norm_w, w_qkv, w_o, b_o)
+        self.tokens = n
+        self._batch = cu_rows.shape[0] - 1
+        return y
+
     def new_grads(self):
         f = dict(dtype=torch.float32, device=self.device)
         return {"norm_w": torch.empty(self.H, **f), "w_qkv": torch.empty(self.W, self.H, **f),
@@ -685,7 +724,7 @@ class TPAttn:
     def append_kv(self, kv: TPKV, block_table, new_lens=None):
         """Store the last forward's keys and values in a cache, the first new_lens[b] of each sequence (or all)."""
         batch = block_table.shape[0]
-        if self.tokens is not None and (batch < 1 or self.tokens % batch or batch != self._batch):
+        if self.tokens is not None and (batch < 1 or batch != self._batch):
             raise TPMLPError(ERR_SHAPE, "block_table needs a row for each sequence of the last forward")
         tp, ldt, pages = kv._table(block_table, batch)
         _acheck(lib().tpattn_append_kv(self.ctx, kv.ctx, _vec(new_lens, batch, _I32T, "new_lens", self.device.index),
@@ -709,6 +748,28 @@ class TPAttn:
                                     _vec(past_lens, n, _I32T, "past_lens", self.device.index), tp, ldt, pages, window,
                                     sinks, self._t(y, (n, self.H), name="y")), self.ctx)
         self._uses(x, norm_w, w_qkv, w_o, b_o, past_lens, block_table, y)
+        kv._used_by(self.stream)
+        return y
+
+    def extend(self, kv: TPKV, x, norm_w, w_qkv, w_o, b_o, eps: float, t: int, past_lens, block_table, cu_rows=None,
+               new_lens=None, window: int = 0, sinks: int = 0, y=None):
+        """The sublayer for new tokens, any number a sequence, appended to the cache behind its ``past_lens`` tokens
+        (tpattn_extend); rows, cu_rows and new_lens as in TPKV.append.  Returns y [rows, H]."""
+        n, batch = x.shape[0], past_lens.shape[0]
+        _int32(t=t, window=window, sinks=sinks)
+        y = torch.empty_like(x) if y is None else y
+        tp, ldt, pages = kv._table(block_table, batch)
+        i = self.device.index
+        _acheck(lib().tpattn_extend(self.ctx, kv.ctx, n, batch, self._t(x, (n, self.H), name="x"),
+                                    self._t(norm_w, (self.H,), name="norm_w"),
+                                    self._t(w_qkv, (self.W, self.H), name="w_qkv"),
+                                    self._t(w_o, (self.H, self.nq * self.d), name="w_o"),
+                                    self._t(b_o, (self.H,), name="b_o"), float(eps), int(t),
+                                    _vec(cu_rows, batch + 1, _I32T, "cu_rows", i),
+                                    _vec(new_lens, batch, _I32T, "new_lens", i),
+                                    _vec(past_lens, batch, _I32T, "past_lens", i), tp, ldt, pages, window, sinks,
+                                    self._t(y, (n, self.H), name="y")), self.ctx)
+        self._uses(x, norm_w, w_qkv, w_o, b_o, past_lens, block_table, cu_rows, new_lens, y)
         kv._used_by(self.stream)
         return y
 
@@ -892,6 +953,127 @@ def qk_norm_rope_backward(dout, x, n_heads: int, n_kv_heads: int, head_dim: int,
     return dx, dq_norm_w, dk_norm_w
 
 
+def _lse(lse, wanted: bool, rows: int, heads: int, device, index: int):
+    """The given log-sum-exp tensor, checked, or a new one where it is wanted."""
+    if lse is None:
+        return torch.empty((rows, heads), dtype=_F32T, device=device) if wanted else None
+    if (lse.dtype is not _F32T or tuple(lse.shape) != (rows, heads) or lse.get_device() != index
+            or not lse.is_contiguous()):
+        raise _bad(lse, "lse", f"contiguous float32 {(rows, heads)} on cuda:{index}")
+    return lse
+
+
+_packed_words = {}  # device index -> the status word of the calls on it that were given none
+
+
+def _packed_status(status, device, index: int):
+    if status is not None:
+        if status.numel() < 1 or status.get_device() != index or status.dtype not in (torch.int32, torch.uint32):
+            raise _bad(status, "status", f"a 32-bit integer tensor on cuda:{index}")
+        return status.data_ptr()
+    word = _packed_words.get(index)
+    if word is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise TPMLPError(ERR_ORDER, "call once outside a capture first, or give a status tensor")
+        word = torch.zeros(1, dtype=_I32T, device=device)
+        torch.cuda.current_stream(device).synchronize()  # calls on any stream find it cleared
+        _packed_words[index] = word
+    return word.data_ptr()
+
+
+def packed_attention_check(device=None):
+    """Waits for the device's current stream and raises where a packed_attention call on the device (those without a
+    ``status`` of their own) met cu_rows that descend or leave the rows, or gave up a wait.  Clears the report."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    word = _packed_words.get(index)
+    if word is None:
+        return
+    with torch.cuda.device(index):
+        st = int(word.item())
+        if st:
+            word.zero_()
+    if st & 1:
+        raise TPMLPError(ERR_TIMEOUT, "a bounded device wait gave up")
+    if st:
+        raise TPMLPError(ERR_ARG, "cu_rows descend or leave the rows")
+
+
+def _packed_args(q, k, v, cu_rows, n_heads, n_kv_heads, scale, window, sinks):
+    _int32(n_heads=n_heads, n_kv_heads=n_kv_heads, window=window, sinks=sinks)
+    index = _cuda_index(q, "q")
+    shape = q.shape
+    if len(shape) != 2 or n_heads < 1 or n_kv_heads < 1 or shape[1] % n_heads:
+        raise _bad(q, "q", f"rows of {n_heads} heads")
+    d = shape[1] // n_heads
+    qp, n, ldq = _rows(q, n_heads * d, _BF, "q", index)
+    kp, _, ldk = _rows(k, n_kv_heads * d, _BF, "k", index, n)
+    vp, _, ldv = _rows(v, n_kv_heads * d, _BF, "v", index, n)
+    if len(cu_rows.shape) != 1 or cu_rows.shape[0] < 1:
+        raise _bad(cu_rows, "cu_rows", "int32 [batch + 1]")
+    desc = PackedDesc(n, cu_rows.shape[0] - 1, n_heads, n_kv_heads, d,
+                      _vec(cu_rows, cu_rows.shape[0], _I32T, "cu_rows", index), d ** -0.5 if scale is None else scale,
+                      window, sinks, 0)
+    return desc, index, n, d, (qp, ldq, kp, ldk, vp, ldv)
+
+
+def packed_attention(q, k, v, cu_rows, n_heads: int, n_kv_heads: int, scale: float | None = None, window: int = 0,
+                     sinks: int = 0, out=None, lse=None, return_lse: bool = False, status=None, stream=None):
+    """Causal attention over whole sequences of different lengths, packed one behind the other
+    (tpattn_packed_forward): sequence b has the rows [cu_rows[b], cu_rows[b + 1]) of q [rows, n_heads * d], k and v
+    [rows, n_kv_heads * d], bf16 with row strides of their own (columns of packed rows, say); cu_rows int32 on the
+    device.  With a window a token sees the last ``window`` tokens up to itself and the sequence's first ``sinks``.
+    Returns out, with ``return_lse`` or ``lse`` (out, lse float32 [rows, n_heads]).  Bad cu_rows show in ``status``
+    (a zeroed 32-bit device word), or in packed_attention_check where none is given."""
+    if stream is not None:  # what is allocated here belongs to that stream too
+        _record(stream, q, k, v, cu_rows, out, lse, status)
+        with torch.cuda.stream(stream):
+            return packed_attention(q, k, v, cu_rows, n_heads, n_kv_heads, scale, window, sinks, out, lse, return_lse,
+                                    status)
+    desc, index, n, d, ptrs = _packed_args(q, k, v, cu_rows, n_heads, n_kv_heads, scale, window, sinks)
+    if out is None:
+        out = q.new_empty((n, n_heads * d))
+    op, _, ldo = _rows(out, n_heads * d, _BF, "out", index, n)
+    lse = _lse(lse, return_lse, n, n_heads, q.device, index)
+    _on_device(index, lib().tpattn_packed_forward, desc, *ptrs, op, ldo, lse.data_ptr() if lse is not None else None,
+               _packed_status(status, q.device, index), _stream_of(q.device, index))
+    return out if lse is None else (out, lse)
+
+
+def packed_attention_backward(dout, q, k, v, out, lse, cu_rows, n_heads: int, n_kv_heads: int,
+                              scale: float | None = None, window: int = 0, sinks: int = 0, dq=None, dk=None, dv=None,
+                              workspace=None, status=None, stream=None):
+    """Backward of packed_attention: (dq, dk, dv) in bf16, given the forward's inputs, its out and lse, and the
+    gradient of out (tpattn_packed_backward).  dk and dv are sums over the query heads of a key head."""
+    if stream is not None:  # what is allocated here belongs to that stream too
+        _record(stream, dout, q, k, v, out, lse, cu_rows, dq, dk, dv, workspace, status)
+        with torch.cuda.stream(stream):
+            return packed_attention_backward(dout, q, k, v, out, lse, cu_rows, n_heads, n_kv_heads, scale, window,
+                                             sinks, dq, dk, dv, workspace, status)
+    desc, index, n, d, ptrs = _packed_args(q, k, v, cu_rows, n_heads, n_kv_heads, scale, window, sinks)
+    wq, wk = n_heads * d, n_kv_heads * d
+    op, _, ldo = _rows(out, wq, _BF, "out", index, n)
+    gp, _, ldg = _rows(dout, wq, _BF, "dout", index, n)
+    if lse is None:
+        raise TPMLPError(ERR_ARG, "lse is None")
+    lse = _lse(lse, True, n, n_heads, q.device, index)
+    dq = q.new_empty((n, wq)) if dq is None else dq
+    dk = q.new_empty((n, wk)) if dk is None else dk
+    dv = q.new_empty((n, wk)) if dv is None else dv
+    need = int(lib().tpattn_packed_workspace_bytes(n, n_heads))
+    if workspace is None:
+        workspace = torch.empty(need // 4, dtype=_F32T, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise _bad(workspace, "workspace", f"a contiguous tensor on cuda:{index}")
+    dqp, _, ldq = _rows(dq, wq, _BF, "dq", index, n)
+    dkp, _, ldk = _rows(dk, wk, _BF, "dk", index, n)
+    dvp, _, ldv = _rows(dv, wk, _BF, "dv", index, n)
+    _on_device(index, lib().tpattn_packed_backward, desc, *ptrs, op, ldo, lse.data_ptr(), gp, ldg, dqp, ldq, dkp, ldk,
+               dvp, ldv, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+               _packed_status(status, q.device, index), _stream_of(q.device, index))
+    return dq, dk, dv
+
+
 class TPKV:
     """A paged key/value cache (tpkv_*): append new tokens, attend with one token per sequence.
 
@@ -1040,16 +1222,42 @@ class TPKV:
         if out is None:
             out = q.new_empty((batch, width))
         op, _, ldo = _rows(out, width, _BF, "out", index, batch)
-        if lse is None:
-            if return_lse:
-                lse = torch.empty((batch, self.nq), dtype=_F32T, device=self.device)
-        elif (lse.dtype is not _F32T or tuple(lse.shape) != (batch, self.nq) or lse.get_device() != index
-                or not lse.is_contiguous()):
-            raise _bad(lse, "lse", f"contiguous float32 {(batch, self.nq)} on cuda:{index}")
+        lse = _lse(lse, return_lse, batch, self.nq, self.device, index)
         tp, ldt, pages = self._table(block_table, batch)
         self._enter()
         status = lib().tpkv_decode(self.ctx, batch, qp, ldq, _vec(lens, batch, _I32T, "lens", index), len_add, tp,
                                    ldt, pages, self.d ** -0.5 if scale is None else scale, window, sinks, op, ldo,
+                                   lse.data_ptr() if lse is not None else None)
+        if status:
+            self._ck(status)
+        return out if lse is None else (out, lse)
+
+    def extend(self, q, past_lens, block_table, cu_rows=None, new_lens=None, scale: float | None = None, window: int = 0,
+               sinks: int = 0, out=None, lse=None, return_lse: bool = False):
+        """Attention of new tokens, any number a sequence, over a cache that holds them already: rows, ``past_lens``,
+        ``cu_rows`` and ``new_lens`` as in the append before it, q its result.  The token at position p sees the cached
+        tokens up to itself; with a window, those at p - window + 1 and later and the first ``sinks``.  scale:
+        1 / sqrt(head_dim) unless given.  Returns out [rows, n_heads * d], with ``return_lse`` or ``lse`` (out, lse
+        float32 [rows, n_heads]); rows that are no token's stay as they were (undefined where made here); see
+        tpkv_extend."""
+        if self._elsewhere():
+            _record(self._fixed, q, past_lens, block_table, cu_rows, new_lens, out, lse)
+            with torch.cuda.stream(self._fixed):
+                return self.extend(q, past_lens, block_table, cu_rows, new_lens, scale, window, sinks, out, lse,
+                                   return_lse)
+        index, width, batch = self.index, self.nq * self.d, past_lens.shape[0]
+        _int32(window=window, sinks=sinks)
+        qp, n, ldq = _rows(q, width, _BF, "q", index)
+        if out is None:
+            out = q.new_empty((n, width))
+        op, _, ldo = _rows(out, width, _BF, "out", index, n)
+        lse = _lse(lse, return_lse, n, self.nq, self.device, index)
+        tp, ldt, pages = self._table(block_table, batch)
+        self._enter()
+        status = lib().tpkv_extend(self.ctx, n, batch, qp, ldq, _vec(cu_rows, batch + 1, _I32T, "cu_rows", index),
+                                   _vec(new_lens, batch, _I32T, "new_lens", index),
+                                   _vec(past_lens, batch, _I32T, "past_lens", index), tp, ldt, pages,
+                                   self.d ** -0.5 if scale is None else scale, window, sinks, op, ldo,
                                    lse.data_ptr() if lse is not None else None)
         if status:
             self._ck(status)
