@@ -18,4 +18,18 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// A kernel whose warps exchange registers waits forever if it was not launched
+// with as many as they take together: refused then.  Looked up once.
+template <auto Kernel>
+cudaError_t check_regs(int threads, int needed) {
+  static int regs = 0;  // only ever set to one value
+  if (!regs) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, Kernel);
+    if (e != cudaSuccess) return e;
+    regs = a.numRegs;
+  }
+  return regs * threads >= needed ? cudaSuccess : cudaErrorLaunchOutOfResources;
+}
+
 }  // namespace tpmlp

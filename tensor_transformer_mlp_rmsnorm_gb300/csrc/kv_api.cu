@@ -128,8 +128,11 @@ KvLayout kv_layout(const tpkv_config& c) {
   L.status = 0;
   L.counters = 256;
   L.part = al256(L.counters + 3 * (size_t)KV_MAX_WORKERS * sizeof(uint32_t));
-  L.total = al256(L.part + 2 * (size_t)KV_MAX_WORKERS *
-                               kv_decode_part_floats(c.head_dim, c.n_heads / c.n_kv_heads) * sizeof(float));
+  // the partial results of a decode, or of an extend: one call behind the other
+  size_t floats = 2 * (size_t)KV_MAX_WORKERS * kv_decode_part_floats(c.head_dim, c.n_heads / c.n_kv_heads);
+  const size_t extend = (size_t)VAR_MAX_PARTS * var_part_floats(c.head_dim);
+  if (extend > floats) floats = extend;
+  L.total = al256(L.part + floats * sizeof(float));
   return L;
 }
 
@@ -639,6 +642,7 @@ tpmlp_status kv_run_extend(tpkv_ctx* c, const SeqRows& seq, const void* q, int64
   a.stride_slot = c->stride_slot;
   a.k_inv_scale = c->k_inv_scale;
   a.v_inv_scale = c->v_inv_scale;
+  a.part = c->part;
   OnDevice on(c->device);
   cudaError_t e = wait_for_clear(c, st);
   if (e == cudaSuccess) e = launch_var_fwd(a, c->num_sms, st);

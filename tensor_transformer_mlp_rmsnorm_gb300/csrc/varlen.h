@@ -10,6 +10,10 @@
 
 namespace tpmlp {
 
+// Parts of blocks that are split over the length of a cache, and the floats of one.
+constexpr int VAR_MAX_PARTS = 160;
+inline size_t var_part_floats(int d) { return (size_t)(d <= 128 ? 256 : 128) * (d + 2); }
+
 // Which rows are whose.  Sequence b has `count` rows from `first` on, the i-th
 // of them at position past + i; past < 0: an inactive sequence.
 struct SeqRows {
@@ -43,6 +47,7 @@ struct VarFwdArgs {
   const void *k_cache, *v_cache;
   int64_t stride_page, stride_head, stride_slot;
   const float *k_inv_scale, *v_inv_scale;  // E4M3: [nkv] or null
+  float* part;  // scratch of VAR_MAX_PARTS parts, or null: blocks are not split
 };
 
 // Backward over packed rows.
