@@ -589,7 +589,7 @@ static tpmlp_status attn_run_forward(tpattn_ctx* c, int B, int S, int N, const i
     int32_t* out = c->wsp<int32_t>(c->L.pos);
     ATTN_TRY(c->run(A_PACKED_ROWS, [&] {
       return launch_packed_rows(packed_seqs(c), out, z, (int64_t)Zc * 2, c->wsp<void>(c->L.dqkv), (int64_t)W * 2,
-                                c->wsp<uint32_t>(c->L.status), c->num_sms, c->stream);
+                                c->num_sms, c->stream);
     }));
     pos = out;
   }
@@ -1218,7 +1218,7 @@ tpmlp_status tpattn_extend(tpattn_ctx* c, tpkv_ctx* kv, int64_t rows, int32_t ba
     }));
     if (cu_rows || new_lens)  // rows that are no token's
       ATTN_TRY(c->run(A_PACKED_ROWS, [&] {
-        return launch_packed_rows(seq, nullptr, z, (int64_t)Zc * 2, nullptr, 0, kv->status, c->num_sms, c->stream);
+        return launch_packed_rows(seq, nullptr, z, (int64_t)Zc * 2, nullptr, 0, c->num_sms, c->stream);
       }));
     return attn_run_kv(c, kv, A_KV_EXTEND, [&] {
       return kv_run_extend(kv, seq, qkv, W, table, ld_table, max_pages, 1.0f / std::sqrt((float)d), window, sinks, z, Zc,

@@ -21,7 +21,6 @@ constexpr int KB = 128;  // keys of a step
 constexpr uint32_t SUB = 128 * 128;  // bytes of a [128 x 64] bf16 tile with the 128-byte swizzle
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
 constexpr float MOVE_LOG2 = 8.0f;  // the running maximum is moved when it is off by more than 2^8
-constexpr int LPT_BATCH = 512;     // sequences that blocks are ordered by length for
 constexpr int MIN_PART = 4;        // steps of a part at least
 
 enum Source { PACKED = 0, PAGED = 1, PAGED_F8 = 2 };
@@ -109,64 +108,6 @@ __device__ __forceinline__ int part_steps(int n, int nsplit) {
   return nsplit == 1 ? n : max(MIN_PART, (n + nsplit - 1) / nsplit);
 }
 
-// The rank-th block, longest first (more steps before fewer), by the lanes of
-// one warp over the sequences' (past, count) in shared memory.  The number of
-// blocks of at least x steps of a sequence is a closed form, so the steps of
-// the rank-th block are found by bisection.
-__device__ __forceinline__ void find_by_length(const int2* sq, int batch, int rank, int block_tok, int cap, int lane,
-                                               int* b_out, int* i_out) {
-  auto blocks_from = [&](int2 s, int x) -> int {  // blocks with at least x steps
-    const int nblk = (s.y + block_tok - 1) / block_tok;
-    if (x <= 1) return nblk;
-    if (x > cap || s.x < 0) return 0;
-    const int64_t y = (int64_t)(x - 1) * KB + 1;  // tokens that x steps need
-    if ((int64_t)s.x + s.y < y) return 0;
-    const int64_t before = (y - s.x + block_tok - 1) / block_tok - 1;
-    return nblk - (int)max((int64_t)0, before);
-  };
-  auto count = [&](int x) -> int {
-    int c = 0;
-    for (int b = lane; b < batch; b += 32) c += blocks_from(sq[b], x);
-    return __reduce_add_sync(0xffffffffu, c);
-  };
-  int most = 1;
-  for (int b = lane; b < batch; b += 32) most = max(most, (int)min(((int64_t)max(sq[b].x, 0) + sq[b].y + KB - 1) / KB, (int64_t)cap));
-  most = __reduce_max_sync(0xffffffffu, most);
-  *b_out = -1;
-  if (count(1) <= rank) return;
-  int lo = 1, hi = most + 1;  // count(lo) > rank >= count(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (count(mid) > rank) lo = mid;
-    else hi = mid;
-  }
-  int left = rank - count(hi);
-  for (int b0 = 0; b0 < batch; b0 += 32) {
-    const int b = b0 + lane;
-    int mine = 0, longer = 0, nblk = 0;
-    if (b < batch) {
-      longer = blocks_from(sq[b], hi);
-      nblk = blocks_from(sq[b], 1);
-      mine = blocks_from(sq[b], lo) - longer;
-    }
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint32_t has = __ballot_sync(0xffffffffu, upto > left);
-    if (has) {
-      const int src = __ffs(has) - 1;
-      const int i = nblk - longer - mine + (left - (upto - mine));
-      *b_out = b0 + src;
-      *i_out = __shfl_sync(0xffffffffu, i, src);
-      return;
-    }
-    left -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-}
-
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
                                             int c3) {
   asm volatile(
@@ -174,18 +115,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
           "r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
-}
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
 }
 // Two E4M3 codes (the low or high half of v) as bf16: exact, NaN stays NaN.
 __device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t v, bool high) {
@@ -261,7 +190,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
     int b, i = 0;
     if (p.by_length) {
       const int most = p.window > 0 ? (p.window + block_tok) / KB + 2 + (p.sinks + KB - 1) / KB : 0x7fffffff;
-      find_by_length(sq, p.seq.batch, rank, block_tok, most, lane, &b, &i);
+      find_by_length<KB>(sq, p.seq.batch, rank, block_tok, most, lane, &b, &i);
     } else {
       const int slot = p.slots - 1 - rank;
       b = find_slot(p.seq, slot, block_tok, lane);
@@ -750,20 +679,7 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p) {
   if (id >= p.seq.rows * p.nq) return;
   const int row = (int)(id / p.nq), head = (int)(id % p.nq);
   const int block_tok = NT * p.tok;
-  // the row's sequence: the last whose first row is not behind it
-  int b;
-  if (p.seq.cu_rows) {
-    int lo = 0, hi = p.seq.batch;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, c = lo + lane * step;
-      const int n = __popc(__ballot_sync(0xffffffffu, c < hi && p.seq.cu_rows[c] <= row));
-      lo += max(n - 1, 0) * step;
-      hi = min(hi, lo + step);
-    }
-    b = lo;
-  } else {
-    b = row / p.seq.rows_per_seq;
-  }
+  const int b = find_row(p.seq, row, lane);
   bool bad = false;
   const SeqSpan s = seq_span(p.seq, b, (int64_t)p.max_pages * p.page_size, &bad);
   if (row < s.first || row - s.first >= s.count) return;
@@ -805,19 +721,6 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p) {
 #pragma unroll
   for (int v = 0; v < V; ++v) out[lane + 32 * v] = pack_bf16(acc[v].x * inv, acc[v].y * inv);
   if (p.lse && lane == 0) p.lse[id] = (top + log2f(sum)) * 0.69314718055994531f;
-}
-
-// {64 columns, mid, rows} boxes of a tensor {d, mid count, rows} with strides in elements.
-bool map3(CUtensorMap* m, const void* ptr, int d, int mid, int64_t rows, int64_t ld, int box_mid, int box_rows) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)mid, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_mid, (cuuint32_t)box_rows};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // {64 columns, box slots} of a cache {d, page_size, nkv, pages}; E4M3 codes lie unswizzled, 64 bytes a row.

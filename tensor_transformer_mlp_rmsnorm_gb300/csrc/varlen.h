@@ -68,7 +68,7 @@ struct VarBwdArgs {
 // For each row its position (pos, or null), and zeros in rows of z and dz (row
 // bytes, multiples of 16; null: none) that are no sequence's.  past is not used.
 cudaError_t launch_packed_rows(const SeqRows& s, int32_t* pos, void* z, int64_t z_bytes, void* dz, int64_t dz_bytes,
-                               uint32_t* status, int num_sms, cudaStream_t st);
+                               int num_sms, cudaStream_t st);
 cudaError_t launch_var_fwd(const VarFwdArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_var_bwd(const VarBwdArgs& a, int num_sms, cudaStream_t st);
 
