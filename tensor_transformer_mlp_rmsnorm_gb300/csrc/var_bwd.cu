@@ -14,6 +14,7 @@ namespace tpmlp {
 namespace {
 
 constexpr int KB = 64;  // rows of a step
+constexpr int TWICE = 4;  // DQ: blocks of 2 to TWICE steps run over their keys twice
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
 
 // What a CTA accumulates.  DQ: 128 rows of (token, head) stay, their keys and
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(384, 1)
   __shared__ BwdBlock blk;
   __shared__ __align__(16) float2 s_stat[NSTAT][Q_STAYS ? 2 : KB];
   __shared__ __align__(16) int s_pos[NSTAT][Q_STAYS ? 4 : KB];
-  __shared__ float s_D[Q_STAYS ? 128 : 1];
+  __shared__ float2 s_row[Q_STAYS ? 128 : 1];  // sums of the rows that stay
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring1 = smem + C::NRES * C::RB;
   uint8_t* ring2 = ring1 + N1 * C::EB;
@@ -198,9 +199,18 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
-  const int nk = blk.n;
+  // DQ: D = dO . O takes the output as it was rounded.  For tokens that see few
+  // others D is as large as what it is taken from, and that rounding would be a
+  // good part of a small gradient (dq off by 0.0026 of its norm where its own
+  // rounding is 0.0017).  Blocks of few steps run over their keys once more,
+  // before, for D = sum P dP: with 256 keys or more the rounding is averaged out.
+  const int pre = Q_STAYS && blk.n > 1 && blk.n <= TWICE ? blk.n : 0;
+  const int nk = blk.n + pre;
   constexpr uint32_t T_DP = 128, T_ACC = 256;  // score slots at 0 and 64, dP slots at 128 and 192
-  auto tile_of = [&](int j) -> int { return j < blk.sink_tiles ? j : j - blk.sink_tiles + blk.win_tile; };
+  auto tile_of = [&](int n) -> int {
+    const int j = n < pre ? n : n - pre;
+    return j < blk.sink_tiles ? j : j - blk.sink_tiles + blk.win_tile;
+  };
   auto wait_all = [&](uint64_t* bar, uint32_t par) -> int {
     return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS));
   };
@@ -281,7 +291,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int kk = 0; kk < KB / 16; ++kk)
           tc_mma_f16_ts(tmem_base + acc + e * EC, tmem_base + a_col + kk * 8, desc_advance(b, kk * 2048), IDESC_A,
-                        n > 0 || kk > 0 ? 1u : 0u);
+                        n > pre || kk > 0 ? 1u : 0u);
       }
     };
     auto release = [&](uint64_t* bars, int stages, int n) {
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = wait_all(&ds_full[slot], par))) break;
         tc_fence_after();
         if (elect_one()) {
-          accumulate(N1, x1m, n, T_DP + slot * KB, T_ACC);
+          if (n >= pre) accumulate(N1, x1m, n, T_DP + slot * KB, T_ACC);
           release(empty1, N1, n);
           if (n + 1 == nk) tc_commit(&acc_full);
         }
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(384, 1)
     if (Q_STAYS) {
       const int64_t at = (int64_t)(blk.first + tk) * p.nq + h0 + hh;
       if (stored) lse2 = p.lse[at] * 1.4426950408889634f;
-      if (!one) {
+      if (!one && !pre) {
         // D = dO . O of 16 rows a warp, D / 8 lanes a row
         constexpr int LPR = D / 8, RPP = D == 192 ? 1 : 32 / LPR;
         for (int i = 0; i < 16; i += RPP) {
@@ -408,15 +418,26 @@ __global__ void __launch_bounds__(384, 1)
           }
 #pragma unroll
           for (int o = (RPP > 1 ? LPR : 32) / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (c == 0) s_D[rr] = s;
+          if (c == 0) s_row[rr].x = s;
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        dsum = s_D[r];
+        dsum = s_row[r].x;
         if (stored && grp == 0) p.stats[at] = make_float2(lse2, dsum);
       }
     }
     int ok = 1;
+    float l = 0.0f;  // of the steps before: sum P
     for (int n = grp; n < nk; n += 2) {
+      if (Q_STAYS && pre && (n == pre || n == pre + 1)) {  // both groups' sums
+        if (grp == 1) s_row[r] = make_float2(l, dsum);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (grp == 0) s_row[r] = make_float2(l + s_row[r].x, dsum + s_row[r].y);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        l = s_row[r].x;
+        dsum = s_row[r].y / l;
+        lse2 += log2f(l);
+        if (stored && grp == 0) p.stats[(int64_t)(blk.first + tk) * p.nq + h0 + hh] = make_float2(lse2, dsum);
+      }
       const uint32_t par = (uint32_t)((n >> 1) & 1);
       const int st = n % NSTAT;
       if (!Q_STAYS && !(ok = wait_all(&stat_full[st], (uint32_t)((n / NSTAT) & 1)))) break;
@@ -527,7 +548,6 @@ __global__ void __launch_bounds__(384, 1)
         if (one) {
           // The softmax and D from the step itself: the gradient of a token that sees one or
           // two is close to 0, and the output's rounding in D would be all of it.
-          float l = 0.0f;
 #pragma unroll
           for (int c = 0; c < 64; ++c) l += __uint_as_float(v[c]);
 #pragma unroll
@@ -543,6 +563,24 @@ __global__ void __launch_bounds__(384, 1)
           }
           lse2 += log2f(l);
           if (stored) p.stats[(int64_t)(blk.first + tk) * p.nq + h0 + hh] = make_float2(lse2, dsum);
+        }
+        if (Q_STAYS && n < pre) {  // the sums alone
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t d[32];
+            tmem_ld_32x32b_x32(t_dp + 32 * hf, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c)  // hidden values may be anything
+              if (v[32 * hf + c] != 0u) {
+                l += __uint_as_float(v[32 * hf + c]);
+                dsum = fmaf(__uint_as_float(v[32 * hf + c]), __uint_as_float(d[c]), dsum);
+              }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ds_full[grp]);
+          continue;
         }
         uint32_t w[32];
 #pragma unroll
@@ -638,7 +676,7 @@ __global__ void __launch_bounds__(384, 1)
 template <int D, int ROLE>
 cudaError_t launch_role(BwdParams p, const VarBwdArgs& a, int num_sms, cudaStream_t st) {
   using C = Cfg<D, ROLE>;
-  static_assert(C::SMEM + C::NSTAT * (ROLE == DQ ? 32 : KB * 12) + (ROLE == DQ ? 512 : 0) + 500 <= 232448, "shared memory");
+  static_assert(C::SMEM + C::NSTAT * (ROLE == DQ ? 32 : KB * 12) + (ROLE == DQ ? 1024 : 0) + 500 <= 232448, "shared memory");
   const int block_tok = ROLE == DQ ? p.tok : 128;
   p.heads = ROLE == DQ ? a.nkv * p.chunks : a.nkv;
   const int64_t slots = a.seq.rows / block_tok + a.seq.batch, units = slots * p.heads;
