@@ -141,13 +141,9 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_desc(&map_x1);
     tma_prefetch_desc(&map_x2);
   }
-  int2* sq = reinterpret_cast<int2*>(smem);  // until the first copy
-  if (p.by_length || blockIdx.x == 0) {
+  if (blockIdx.x == 0) {
     bool bad = false;
-    for (int b = threadIdx.x; b < p.seq.batch; b += blockDim.x) {
-      const SeqSpan s = seq_span(p.seq, b, -1, &bad);
-      if (p.by_length) sq[b] = make_int2(0, s.count);
-    }
+    for (int b = threadIdx.x; b < p.seq.batch; b += blockDim.x) seq_span(p.seq, b, -1, &bad);
     if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
   }
   // Rows of a step that no copy fills: the products run over them, so they hold zeros.
@@ -160,12 +156,13 @@ __global__ void __launch_bounds__(384, 1)
       }
   }
   fence_proxy_async_smem();
-  if (p.by_length) __syncthreads();
   if (warp == 2) {
     int b, i = 0;
     if (p.by_length) {
       const int most = p.window > 0 ? (p.window + block_tok) / KB + 2 + (Q_STAYS ? (p.sinks + KB - 1) / KB : 0) : 0x7fffffff;
-      find_by_length<KB>(sq, p.seq.batch, rank, block_tok, most, lane, &b, &i);
+      ByLength<KB> order;
+      order.init(p.seq, -1, block_tok, most, lane);
+      order.find(rank, lane, &b, &i);
     } else {
       b = find_slot(p.seq, p.slots - 1 - rank, block_tok, lane);
       i = -1;  // below

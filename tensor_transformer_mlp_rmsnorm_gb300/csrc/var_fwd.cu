@@ -28,22 +28,21 @@ enum Source { PACKED = 0, PAGED = 1, PAGED_F8 = 2 };
 template <int D, int SRC>
 struct Cfg {
   static constexpr bool F8 = SRC == PAGED_F8;
-  static constexpr int NT = D <= 128 ? 2 : 1;              // query tiles of a CTA
-  static constexpr int EC = D % 128 == 0 ? 128 : 64;       // columns of a ring element
-  static constexpr int NE = D / EC;                        // elements of an operand
-  static constexpr uint32_t EB = EC / 64 * SUB;            // bytes of an element
-  static constexpr uint32_t RB = EC * 128;                 // bytes of an element in E4M3 codes
-  static constexpr uint32_t QT = D / 64 * SUB;             // bytes of a query tile
-  static constexpr int NR = F8 ? (EC == 128 ? 2 : 4) : 0;  // code stages
-  static constexpr int FIT = (int)((225 * 1024 - NT * QT - NR * RB) / EB);
-  static constexpr int NST = FIT < 12 ? FIT : 12;          // ring stages
-  static constexpr uint32_t SMEM = NT * QT + NST * EB + NR * RB + 1024;
-  static constexpr int WGS = 1 + NT + (F8 ? 1 : 0);        // issuing, softmax a tile, converting
+  static constexpr int NT = D <= 128 ? 2 : 1;         // query tiles of a CTA
+  static constexpr int EC = D % 128 == 0 ? 128 : 64;  // columns of a ring element
+  static constexpr int NE = D / EC;                   // elements of an operand
+  static constexpr uint32_t EB = EC / 64 * SUB;       // bytes of an element
+  static constexpr uint32_t QT = D / 64 * SUB;        // bytes of a query tile
+  static constexpr int FIT = (int)((225 * 1024 - NT * QT) / EB);
+  static constexpr int NST = FIT < 12 ? FIT : 12;     // ring stages
+  static constexpr uint32_t SMEM = NT * QT + NST * EB + 1024;
+  static constexpr int WGS = 1 + NT + (F8 ? 1 : 0);   // issuing, softmax a tile, converting
   static constexpr int THREADS = 128 * WGS;
+  static constexpr int READERS = 2 + 4 * NT + (F8 ? 4 : 0);  // warps that a piece of work is handed to
   // registers a thread after the exchange (0: none takes place)
-  static constexpr int SOFTMAX_REGS = WGS == 4 ? 192 : WGS == 3 ? (F8 ? 232 : 216) : 0;
-  static constexpr int ISSUE_REGS = WGS == 4 ? 48 : 72;
-  static constexpr int CONVERT_REGS = WGS == 4 ? 80 : 168;
+  static constexpr int SOFTMAX_REGS = WGS == 4 ? 184 : WGS == 3 ? (F8 ? 232 : 208) : 0;
+  static constexpr int ISSUE_REGS = WGS == 4 ? 80 : F8 ? 72 : 88;
+  static constexpr int CONVERT_REGS = WGS == 4 ? 64 : 168;
   static constexpr int REGS = 128 * (NT * SOFTMAX_REGS + ISSUE_REGS + (F8 ? CONVERT_REGS : 0));
 };
 
@@ -57,6 +56,7 @@ struct FwdParams {
   int ht, chunks;    // heads of a tile, tiles of heads a key head
   int tok;           // tokens of a tile
   int slots, heads;  // block slots, key heads times chunks
+  int units;         // slots times heads times parts
   int nsplit;
   bool by_length;
   float scale_log2;
@@ -125,91 +125,62 @@ __device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t v, bool high) {
   return pack_bf16(f.x, f.y);
 }
 
+// A piece of work: a block, or with nsplit > 1 a part of its steps.
+struct Work : Block {
+  int hd, split;
+  int j0, nk;      // steps [j0, j0 + nk) of the block
+  int na, nb;      // those of the first and the second tile
+  bool whole;      // all steps of the block
+  bool dual;       // one tile of rows: the two tiles take turns at its steps
+};
+constexpr int NONE = -2;  // Work::b behind the last piece
+
 template <int D, int SRC>
 __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
     var_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const FwdParams p) {
   using C = Cfg<D, SRC>;
-  constexpr int NT = C::NT, NE = C::NE, EC = C::EC, NST = C::NST, NR = C::NR;
+  constexpr int NT = C::NT, NE = C::NE, EC = C::EC, NST = C::NST;
   constexpr bool F8 = C::F8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_full, full[NST], empty[NST], raw_full[NR + 1], raw_empty[NR + 1], s_full[2],
-      p_full[2][2], o_full[2], pv_done, drain_bar;
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], full[NST], empty[NST], raw_full[F8 ? NST : 1], s_full[2],
+      p_full[2][2], o_full[2], pv_done, post, taken, work_full[2], work_empty[2], drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ Block blk;
+  __shared__ Work work_sh[2];
+  __shared__ float2 other[NT == 2 ? 128 : 1];  // second tile's maximum and sum
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + NT * C::QT;
-  uint8_t* raw = ring + NST * C::EB;
   volatile int* abort_flag = &abort_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = (int)(blockIdx.x % p.nsplit), unit = (int)(blockIdx.x / p.nsplit);
-  const int rank = unit / p.heads, hd = unit % p.heads;
-  const int g = hd / p.chunks, h0 = g * p.hpg + hd % p.chunks * p.ht;  // key head, first query head
-  const int nh = min(p.ht, (g + 1) * p.hpg - h0);                      // query heads of the tile
   const int64_t cap = SRC == PACKED ? -1 : (int64_t)p.max_pages * p.page_size;
   const int block_tok = NT * p.tok;
 
-  // ---- which block
   if (threadIdx.x == 0) {
-    mbar_init(&q_full, 1);
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], F8 ? 4 : 1);
       mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < NR; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      if (F8) mbar_init(&raw_full[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i][0], 4);
       mbar_init(&p_full[i][1], 4);
       mbar_init(&o_full[i], 1);
+      mbar_init(&work_full[i], 1);
+      mbar_init(&work_empty[i], C::READERS);
     }
     mbar_init(&pv_done, 1);
+    mbar_init(&post, 4);
+    mbar_init(&taken, 4);
     mbar_init(&drain_bar, 1);
     abort_sh = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
-  }
-  int2* sq = reinterpret_cast<int2*>(smem);  // until the first copy
-  if (p.by_length || blockIdx.x == 0) {  // one CTA looks at every sequence, for the report
-    bool bad = false;
-    for (int b = threadIdx.x; b < p.seq.batch; b += blockDim.x) {
-      const SeqSpan s = seq_span(p.seq, b, cap, &bad);
-      if (p.by_length) sq[b] = make_int2(s.past, s.count);
-    }
-    if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
-    fence_proxy_async_smem();
-  }
-  if (p.by_length) __syncthreads();
-  if (warp == 2) {
-    int b, i = 0;
-    if (p.by_length) {
-      const int most = p.window > 0 ? (p.window + block_tok) / KB + 2 + (p.sinks + KB - 1) / KB : 0x7fffffff;
-      find_by_length<KB>(sq, p.seq.batch, rank, block_tok, most, lane, &b, &i);
-    } else {
-      const int slot = p.slots - 1 - rank;
-      b = find_slot(p.seq, slot, block_tok, lane);
-      i = -1;  // below
-    }
-    if (lane == 0) {
-      Block k;
-      k.b = -1;
-      k.n = 0;
-      bool bad = false;
-      if (b >= 0) {
-        const SeqSpan s = seq_span(p.seq, b, cap, &bad);
-        if (i < 0) i = p.slots - 1 - rank - slot_base(s.first, b, block_tok);
-        if (i >= 0 && (int64_t)i * block_tok < s.count)
-          fill_block(&k, s, b, i, p.tok, block_tok, p.window, p.sinks);
-      }
-      if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
-      blk = k;
-    }
   }
   if (warp == 1) {
     tmem_alloc(&tmem_base_sh, 512);
@@ -219,444 +190,607 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
-  // this CTA's steps [j0, j0 + nk) of the block
-  const int per = part_steps(blk.n, p.nsplit);
-  const int j0 = split * per;
-  const bool whole = per >= blk.n;
-  const bool mine = blk.b >= 0 && (split == 0 || j0 < blk.n);
-  const bool has_b = NT == 2 && blk.count > p.tok;
-  const int nk_x[2] = {mine ? max(0, min(blk.n_a, j0 + per) - j0) : 0,
-                       mine && has_b ? max(0, min(blk.n, j0 + per) - j0) : 0};
-  const int nk = max(nk_x[0], nk_x[1]);
-  // where a step's operands lie in the ring, in the order that they are used
-  auto k_at = [&](int j) -> int { return (NT == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1) * NE; };
-  auto v_at = [&](int j) -> int { return (NT == 2 ? 2 * j + 1 : j < nk - 1 ? 2 * j + 2 : 2 * nk - 1) * NE; };
+  auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS));
+  };
+  // The t-th piece of this CTA's work, in shared memory until it is given back;
+  // null behind the last.
+  auto next = [&](int t) -> const Work* {
+    if (!wait_all(&work_full[t & 1], (uint32_t)((t >> 1) & 1))) return nullptr;
+    return work_sh[t & 1].b == NONE ? nullptr : &work_sh[t & 1];
+  };
+  auto give_back = [&](int t) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&work_empty[t & 1]);
+  };
+  // Where a step's operands lie in the ring, in the order that they are used,
+  // from `base` on: the elements of the pieces before.
+  auto k_at = [&](int base, const Work& w, int j) -> int {
+    return base + (NT == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1) * NE;
+  };
+  auto v_at = [&](int base, const Work& w, int j) -> int {
+    return base + (NT == 2 ? 2 * j + 1 : j < w.nk - 1 ? 2 * j + 2 : 2 * w.nk - 1) * NE;
+  };
 
   // Registers: what the issuing and converting warpgroups give up, the softmax
-  // takes.  Every warp passes the exchange, with or without steps: an increase
+  // takes.  Every warp passes the exchange, with or without work: an increase
   // waits until the others have given theirs up.
   if (warp < 4) {
-  if constexpr (C::SOFTMAX_REGS > 0) regs_dec<C::ISSUE_REGS>();
-  if (warp == 0 && nk > 0) {
-    // -------------------------------------------------------------- producer
-    constexpr int CB = EC / 64;  // 64-column boxes of an element's row
-    const int boxes = SRC == PACKED ? 1 : KB / p.box;
-    const int my_box = lane / CB, my_col = lane % CB;
-    const bool issues = my_box < boxes;
-    uint32_t armed = 0, par_armed = 0;  // by stage of the ring that copies land in
-    constexpr int LST = F8 ? NR : NST;
-    uint64_t *lfull = F8 ? raw_full : full, *lempty = F8 ? raw_empty : empty;
-    bool ok = true;
-    if (lane == 0) {
-      const int tiles = has_b ? 2 : 1;
-      mbar_arrive_expect_tx(&q_full, (uint32_t)(tiles * (D / 64) * p.ht * p.tok * 128));
-      for (int x = 0; x < tiles; ++x)
-        for (int t = 0; t < D / 64; ++t)
-          tma_load_3d(smem + x * C::QT + t * SUB, &map_q, &q_full, 64 * t, h0, blk.first + x * p.tok);
-    }
-    __syncwarp();
-    // page of this lane's box in a tile: num_pages (nothing is read, zeros land) where no row sees it
-    auto page_of = [&](int tile) -> int {
-      const int t = tile * KB + my_box * p.box;
-      const bool seen = (t < blk.end && t + p.box > blk.lo) || t < blk.sink_end;
-      if (!issues || !seen) return (int)p.num_pages;
-      const int pi = t / p.page_size;
-      int pg = -1;
-      if (pi < p.max_pages) pg = p.table[(int64_t)blk.b * p.ld_table + pi];
-      if (pg < 0 || pg >= p.num_pages) {
-        atomicOr(p.status, STATUS_BAD_INDEX);
-        pg = (int)p.num_pages;
-      }
-      return pg;
-    };
-    auto load = [&](int at, const CUtensorMap* map, int tile, int page) -> bool {
-      for (int e = 0; e < NE; ++e, ++at) {
-        const int s = at % LST;
-        const uint32_t par = (uint32_t)((at / LST) & 1);
-        if (!__all_sync(0xffffffffu, mbar_wait(&lempty[s], par ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS)))
-          return false;
-        if (lane == 0) mbar_arrive_expect_tx(&lfull[s], F8 ? C::RB : C::EB);
-        __syncwarp();
-        armed |= 1u << s;
-        par_armed = (par_armed & ~(1u << s)) | (par << s);
-        if (issues) {
-          const int col = e * EC + my_col * 64;
-          if constexpr (SRC == PACKED) {
-            tma_load_3d(ring + s * C::EB + my_col * SUB, map, &lfull[s], col, g, blk.first - blk.i * block_tok + tile * KB);
-          } else {
-            const int t = tile * KB + my_box * p.box;
-            uint8_t* dst = F8 ? raw + s * C::RB + my_col * (KB * 64) + my_box * p.box * 64
-                              : ring + s * C::EB + my_col * SUB + my_box * p.box * 128;
-            tma_load_4d(dst, map, &lfull[s], col, t % p.page_size, g, page);
+    if constexpr (C::SOFTMAX_REGS > 0) regs_dec<C::ISSUE_REGS>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      constexpr int CB = EC / 64;  // 64-column boxes of an element's row
+      const int boxes = SRC == PACKED ? 1 : KB / p.box;
+      const int my_box = lane / CB, my_col = lane % CB;
+      const bool issues = my_box < boxes;
+      // E4M3 codes land in the upper half of the space of the bf16 rows that the same warp makes of them
+      const int row0 = my_box * p.box;
+      const uint32_t my_dst = my_col * SUB + (SRC == PACKED ? 0 : F8 ? row0 / 32 * 4096 + 2048 + row0 % 32 * 64 : row0 * 128);
+      uint64_t* land = F8 ? raw_full : full;
+      uint32_t armed = 0, par_armed = 0;  // by stage
+      uint32_t q_a = 0, q_b = 0;          // pieces whose queries are in each tile
+      bool ok = true;
+      const Work* wp;
+      for (int t = 0, base = 0; ok && (wp = next(t)); give_back(t++)) {
+        const Work& w = *wp;
+        const int g = w.hd / p.chunks, h0 = g * p.hpg + w.hd % p.chunks * p.ht;
+        // page of this lane's box in a step: num_pages (nothing is read, zeros land) where no row sees it
+        auto look = [&](int j) -> int {
+          const int at = w.tile(w.j0 + j) * KB + row0, pi = at / p.page_size;
+          const bool seen = (at < w.end && at + p.box > w.lo) || at < w.sink_end;
+          if (!issues || !seen) return (int)p.num_pages;
+          return pi < p.max_pages ? __ldg(p.table + (int64_t)w.b * p.ld_table + pi) : -1;
+        };
+        auto valid = [&](int page) -> int {
+          if (page >= 0 && page <= p.num_pages) return page;
+          atomicOr(p.status, STATUS_BAD_INDEX);
+          return (int)p.num_pages;
+        };
+        auto load = [&](int at, const CUtensorMap* map, int j, int page) -> bool {
+          const int tile = w.tile(w.j0 + j);
+          for (int e = 0; e < NE; ++e, ++at) {
+            const int s = at % NST;
+            const uint32_t par = (uint32_t)((at / NST) & 1);
+            if (!wait_all(&empty[s], par ^ 1u)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&land[s], F8 ? C::EB / 2 : C::EB);
+            __syncwarp();
+            armed |= 1u << s;
+            par_armed = (par_armed & ~(1u << s)) | (par << s);
+            if (issues) {
+              const int col = e * EC + my_col * 64;
+              uint8_t* dst = ring + s * C::EB + my_dst;
+              if constexpr (SRC == PACKED) tma_load_3d(dst, map, &land[s], col, g, w.first - w.i * block_tok + tile * KB);
+              else tma_load_4d(dst, map, &land[s], col, (tile * KB + row0) % p.page_size, g, page);
+            }
+          }
+          return true;
+        };
+        int page = 0, page_n = 0, page_v = 0;
+        if (w.nk > 0) {
+          if constexpr (SRC != PACKED) {
+            page = valid(look(0));
+            if (w.nk > 1) page_n = look(1);
+          }
+          ok = load(k_at(base, w, 0), &map_k, 0, page);
+          auto queries = [&](int x, uint32_t n) -> bool {
+            if (!wait_all(&q_empty[x], (n & 1u) ^ 1u)) return false;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full[x], (uint32_t)(D / 64 * p.ht * p.tok * 128));
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(smem + x * C::QT + c * SUB, &map_q, &q_full[x], 64 * c, h0, w.first + x * p.tok);
+            }
+            __syncwarp();
+            return true;
+          };
+          if (ok && w.na > 0) ok = queries(0, q_a++);
+          if (NT == 2 && ok && w.nb > 0 && !w.dual) ok = queries(1, q_b++);
+        }
+        for (int j = 0; ok && j < w.nk; ++j) {
+          if (j > 0) {
+            if constexpr (SRC != PACKED) {
+              page = valid(page_n);
+              if (j + 1 < w.nk) page_n = look(j + 1);
+            }
+            ok = load(k_at(base, w, j), &map_k, j, page);
+          }
+          if constexpr (NT == 2) {
+            if (ok) ok = load(v_at(base, w, j), &map_v, j, page);
+          } else {  // the values one step behind
+            if (ok && j > 0) ok = load(v_at(base, w, j - 1), &map_v, j - 1, page_v);
+            page_v = page;
           }
         }
+        if constexpr (NT == 1)
+          if (ok && w.nk > 0) ok = load(v_at(base, w, w.nk - 1), &map_v, w.nk - 1, page_v);
+        base += 2 * w.nk * NE;
       }
-      return true;
-    };
-    int page_k = 0, page_v = 0, page_n = 0;
-    if constexpr (SRC != PACKED) page_n = page_of(blk.tile(j0));
-    for (int j = 0; ok && j < nk; ++j) {
-      const int tile = blk.tile(j0 + j);
-      page_k = page_n;
-      if constexpr (SRC != PACKED)
-        if (j + 1 < nk) page_n = page_of(blk.tile(j0 + j + 1));
-      ok = load(k_at(j), &map_k, tile, page_k);
-      if constexpr (NT == 2) {
-        if (ok) ok = load(v_at(j), &map_v, tile, page_k);
-      } else {  // the values one step behind
-        if (ok && j > 0) ok = load(v_at(j - 1), &map_v, blk.tile(j0 + j - 1), page_v);
-        page_v = page_k;
+      if (!ok || *abort_flag) {  // copies still in flight land on the barriers armed last
+        int no_abort = 0;
+        if (q_a) mbar_wait(&q_full[0], (q_a - 1) & 1u, &no_abort, p.status, 0u, DRAIN_NS);
+        if (q_b) mbar_wait(&q_full[1], (q_b - 1) & 1u, &no_abort, p.status, 0u, DRAIN_NS);
+        for (int s = 0; s < NST; ++s)
+          if (armed & (1u << s)) mbar_wait(&land[s], (par_armed >> s) & 1u, &no_abort, p.status, 0u, DRAIN_NS / 8);
       }
-    }
-    if constexpr (NT == 1)
-      if (ok) ok = load(v_at(nk - 1), &map_v, blk.tile(j0 + nk - 1), page_v);
-    if (!ok || *abort_flag) {  // copies still in flight land on the barriers armed last
-      int no_abort = 0;
-      mbar_wait(&q_full, 0, &no_abort, p.status, 0u, DRAIN_NS);
-      for (int s = 0; s < LST; ++s)
-        if (armed & (1u << s)) mbar_wait(&lfull[s], (par_armed >> s) & 1u, &no_abort, p.status, 0u, DRAIN_NS / 8);
-    }
-  } else if (warp == 1 && nk > 0) {
-    // ---------------------------------------------------------------- issuer
-    constexpr uint32_t IDESC_S = idesc_bf16_f32(128, KB, false, false);
-    constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, EC, false, true);
-    const uint64_t q_desc = sw128_desc(smem_u32(smem), 16, 1024);
-    const uint64_t k_desc = sw128_desc(smem_u32(ring), 16, 1024);
-    const uint64_t v_desc = sw128_desc(smem_u32(ring), SUB, 1024);
-    auto wait_all = [&](uint64_t* bar, uint32_t par) -> int {
-      return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS));
-    };
-    auto wait_elems = [&](int at) -> int {
-      int r = 1;
-      for (int e = 0; r && e < NE; ++e) r = wait_all(&full[(at + e) % NST], (uint32_t)(((at + e) / NST) & 1));
-      return r;
-    };
-    // S = Q_x K_j^T into score slot `slot`; frees the keys when asked to
-    auto mma_s = [&](int x, int slot, int at, bool last) {
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- issuer
+      // A wait takes some 150 cycles although what it waits for is there: the
+      // copies are waited for before the row groups, so that a tile's second
+      // half of P V and its next scores are issued together.
+      constexpr uint32_t IDESC_S = idesc_bf16_f32(128, KB, false, false);
+      constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, EC, false, true);
+      const uint64_t q_desc = sw128_desc(smem_u32(smem), 16, 1024);
+      const uint64_t k_desc = sw128_desc(smem_u32(ring), 16, 1024);
+      const uint64_t v_desc = sw128_desc(smem_u32(ring), SUB, 1024);
+      auto wait_elems = [&](int at) -> bool {
+        bool r = true;
 #pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        const int s = (at + e) % NST;
-        const uint64_t kb = desc_advance(k_desc, s * C::EB), qa = desc_advance(q_desc, x * C::QT + e * C::EB);
+        for (int e = 0; e < NE; ++e) r = r && wait_all(&full[(at + e) % NST], (uint32_t)(((at + e) / NST) & 1));
+        return r;
+      };
+      // S = Q K_j^T into score slot `slot`, with the queries of tile `qt`; the last user of a ring element frees it
+      auto mma_s = [&](int qt, int slot, int at, bool last) {
 #pragma unroll
-        for (int kk = 0; kk < EC / 16; ++kk)
-          tc_mma_f16(tmem_base + slot * KB, desc_advance(qa, (kk >> 2) * SUB + (kk & 3) * 32),
-                     desc_advance(kb, (kk >> 2) * SUB + (kk & 3) * 32), IDESC_S, e > 0 || kk > 0 ? 1u : 0u);
-        if (last) tc_commit(&empty[s]);
-      }
-      tc_commit(&s_full[slot]);
-    };
-    // half of O_x += P V_j: keys 64 half .. 64 half + 63
-    auto mma_pv = [&](int x, int slot, int at, int half, bool first, bool last) {
+        for (int e = 0; e < NE; ++e) {
+          const int s = (at + e) % NST;
+          const uint64_t kb = desc_advance(k_desc, s * C::EB), qa = desc_advance(q_desc, qt * C::QT + e * C::EB);
 #pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        const int s = (at + e) % NST;
-        const uint64_t vb = desc_advance(v_desc, s * C::EB);
+          for (int kk = 0; kk < EC / 16; ++kk)
+            tc_mma_f16(tmem_base + slot * KB, desc_advance(qa, (kk >> 2) * SUB + (kk & 3) * 32),
+                       desc_advance(kb, (kk >> 2) * SUB + (kk & 3) * 32), IDESC_S, e > 0 || kk > 0 ? 1u : 0u);
+          if (last) tc_commit(&empty[s]);
+        }
+        tc_commit(&s_full[slot]);
+      };
+      // half of O_x += P V_j: keys 64 half .. 64 half + 63
+      auto mma_pv = [&](int x, int slot, int at, int half, bool first, bool last) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f16_ts(tmem_base + 256 + x * D + e * EC, tmem_base + slot * KB + (half * 4 + kk) * 8,
-                        desc_advance(vb, (half * 4 + kk) * 2048), IDESC_PV, !first || half > 0 || kk > 0 ? 1u : 0u);
-        if (last && half == 1) tc_commit(&empty[s]);
-      }
-    };
-    int ok = wait_all(&q_full, 0) && wait_elems(k_at(0));
-    tc_fence_after();
-    if constexpr (NT == 2) {
-      if (ok && elect_one()) {
-        if (nk_x[0] > 0) mma_s(0, 0, k_at(0), nk_x[1] == 0);
-        if (nk_x[1] > 0) mma_s(1, 1, k_at(0), true);
-      }
-      __syncwarp();
-      for (int j = 0; ok && j < nk; ++j) {
-        if (!(ok = wait_elems(v_at(j)))) break;
+        for (int e = 0; e < NE; ++e) {
+          const int s = (at + e) % NST;
+          const uint64_t vb = desc_advance(v_desc, s * C::EB);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (ok && j < nk_x[x]) {
-            // the last tile that uses the step's operands frees them
-            const bool last = x == 1 || j >= nk_x[1], lastn = x == 1 || j + 1 >= nk_x[1];
-            for (int half = 0; ok && half < 2; ++half) {
-              if (!(ok = wait_all(&p_full[x][half], j & 1))) break;
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_ts(tmem_base + 256 + x * D + e * EC, tmem_base + slot * KB + (half * 4 + kk) * 8,
+                          desc_advance(vb, (half * 4 + kk) * 2048), IDESC_PV, !first || half > 0 || kk > 0 ? 1u : 0u);
+          if (half == 1 && last) tc_commit(&empty[s]);
+        }
+      };
+      uint32_t q_a = 0, q_b = 0, steps_a = 0, steps_b = 0;  // queries and steps of each tile so far
+      bool ok = true;
+      const Work* wp;
+      for (int t = 0, base = 0; ok && (wp = next(t)); give_back(t++)) {
+        const Work& w = *wp;
+        if constexpr (NT == 2) {
+          const int na = w.na, nb = w.nb, nk = w.nk, most = max(na, nb);
+          const bool dual = w.dual;
+          int seen = base;  // elements of the ring that are there
+          auto there = [&](int at) -> bool {
+            if (at < seen) return true;
+            if (!wait_elems(at)) return false;
+            seen = at + NE;
+            return true;
+          };
+          auto step = [&](int x, int i) -> int { return dual ? 2 * i + x : i; };
+          auto put_s = [&](int x, int i) {
+            const int mine = x ? nb : na, j = step(x, i);
+            mma_s(x && !dual ? 1 : 0, x, k_at(base, w, j), dual || x == 1 || i >= nb);
+            if (dual ? j == nk - 1 : i == mine - 1) tc_commit(&q_empty[x && !dual ? 1 : 0]);
+          };
+          auto first = [&](int x) -> bool {
+            if (!there(k_at(base, w, step(x, 0)))) return false;
+            tc_fence_after();
+            if (elect_one()) put_s(x, 0);
+            __syncwarp();
+            return true;
+          };
+          // tile x's i-th step: O += P V, and the next step's scores
+          auto turn = [&](int x, int i, uint32_t par) -> bool {
+            const int mine = x ? nb : na, at = v_at(base, w, step(x, i));
+            const bool more = i + 1 < mine, last = dual || x == 1 || i >= nb;
+            if (!there(at) || (more && !there(k_at(base, w, step(x, i + 1))))) return false;
+            if (!wait_all(&p_full[x][0], par)) return false;
+            tc_fence_after();
+            if (elect_one()) mma_pv(x, x, at, 0, i == 0, last);
+            __syncwarp();
+            if (!wait_all(&p_full[x][1], par)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_pv(x, x, at, 1, i == 0, last);
+              if (more) put_s(x, i + 1);
+              else tc_commit(&o_full[x]);
+            }
+            __syncwarp();
+            return true;
+          };
+          if (na > 0) ok = wait_all(&q_full[0], q_a++ & 1u) && first(0);
+          if (ok && nb > 0) ok = (dual || wait_all(&q_full[1], q_b++ & 1u)) && first(1);
+#pragma unroll 1
+          for (int i = 0; ok && i < most; ++i) {
+            if (i < na) ok = turn(0, i, (steps_a + i) & 1u);
+            if (ok && i < nb) ok = turn(1, i, (steps_b + i) & 1u);
+          }
+          steps_a += na;
+          steps_b += nb;
+        } else if (w.nk > 0) {
+          auto scores = [&](int j) -> bool {
+            const int at = k_at(base, w, j);
+            if (!wait_elems(at)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_s(0, (steps_a + j) & 1, at, true);
+              if (j == w.nk - 1) tc_commit(&q_empty[0]);
+            }
+            __syncwarp();
+            return true;
+          };
+          ok = wait_all(&q_full[0], q_a++ & 1u) && scores(0);
+          for (int j = 0; ok && j < w.nk; ++j) {
+            const uint32_t n = steps_a + j;
+            const int slot = n & 1, at = v_at(base, w, j);
+            if (j + 1 < w.nk && !(ok = scores(j + 1))) break;
+            if (!(ok = wait_elems(at))) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (!(ok = wait_all(&p_full[slot][half], (n >> 1) & 1u))) break;
               tc_fence_after();
               if (elect_one()) {
-                mma_pv(x, x, v_at(j), half, j == 0, last);
-                if (half == 1 && j + 1 == nk_x[x]) tc_commit(&o_full[x]);
+                mma_pv(0, slot, at, half, j == 0, true);
+                if (half == 1) {
+                  tc_commit(&pv_done);
+                  if (j + 1 == w.nk) tc_commit(&o_full[0]);
+                }
               }
               __syncwarp();
             }
-            if (ok && j + 1 < nk_x[x]) {
-              if (!(ok = wait_elems(k_at(j + 1)))) break;
-              tc_fence_after();
-              if (elect_one()) mma_s(x, x, k_at(j + 1), lastn);
-              __syncwarp();
-            }
           }
+          steps_a += w.nk;
         }
+        base += 2 * w.nk * NE;
       }
-    } else {
-      if (ok && elect_one()) mma_s(0, 0, k_at(0), true);
+      if (elect_one()) tc_commit(&drain_bar);
       __syncwarp();
-      for (int j = 0; ok && j < nk; ++j) {
-        const int slot = j & 1;
-        if (j + 1 < nk) {
-          if (!(ok = wait_elems(k_at(j + 1)))) break;
-          tc_fence_after();
-          if (elect_one()) mma_s(0, slot ^ 1, k_at(j + 1), true);
-          __syncwarp();
-        }
-        if (!(ok = wait_elems(v_at(j)))) break;
-        for (int half = 0; ok && half < 2; ++half) {
-          if (!(ok = wait_all(&p_full[slot][half], (j >> 1) & 1))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            mma_pv(0, slot, v_at(j), half, j == 0, true);
-            if (half == 1) tc_commit(j + 1 == nk ? &o_full[0] : &pv_done);
+      int no_abort = 0;
+      mbar_wait(&drain_bar, 0, &no_abort, p.status, STATUS_TIMEOUT, DRAIN_NS);
+    } else if (warp == 2) {
+      // ----------------------------------------------------------- scheduler
+      if (blockIdx.x == 0) {  // looks at every sequence, for the report
+        bool bad = false;
+        for (int b = lane; b < p.seq.batch; b += 32) seq_span(p.seq, b, cap, &bad);
+        if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
+      }
+      ByLength<KB> order;
+      if (p.by_length)
+        order.init(p.seq, cap, block_tok,
+                   p.window > 0 ? (p.window + block_tok) / KB + 2 + (p.sinks + KB - 1) / KB : 0x7fffffff, lane);
+      bool ok = true;
+      int t = 0;
+      for (int k = 0; ok; ++k) {
+        const int64_t u = snake(k, (int)blockIdx.x, (int)gridDim.x);
+        const bool end = (int64_t)k * gridDim.x >= p.units;
+        Work w;
+        w.b = NONE;
+        if (!end) {
+          if (u >= p.units) continue;
+          const int unit = (int)u;
+          w.split = unit % p.nsplit;
+          w.hd = unit / p.nsplit % p.heads;
+          const int rank = unit / p.nsplit / p.heads;
+          int b, i = 0;
+          if (p.by_length) {
+            order.find(rank, lane, &b, &i);
+          } else {
+            const int slot = p.slots - 1 - rank;
+            b = find_slot(p.seq, slot, block_tok, lane);
+            i = -1;  // below
           }
-          __syncwarp();
+          if (b < 0) continue;
+          bool bad = false;
+          const SeqSpan s = seq_span(p.seq, b, cap, &bad);
+          if (i < 0) i = p.slots - 1 - rank - slot_base(s.first, b, block_tok);
+          if (i < 0 || (int64_t)i * block_tok >= s.count) continue;
+          fill_block(&w, s, b, i, p.tok, block_tok, p.window, p.sinks);
+          const int per = part_steps(w.n, p.nsplit);
+          w.j0 = w.split * per;
+          if (w.split > 0 && w.j0 >= w.n) continue;
+          w.whole = per >= w.n;
+          w.nk = min(w.n, w.j0 + per) - w.j0;
+          w.dual = NT == 2 && w.count <= p.tok && w.nk > 1;
+          if (w.dual) {
+            w.na = (w.nk + 1) / 2;
+            w.nb = w.nk / 2;
+          } else {
+            w.na = max(0, min(w.n_a, w.j0 + per) - w.j0);
+            w.nb = NT == 2 && w.count > p.tok ? w.nk : 0;
+          }
         }
+        const int q = t & 1;
+        ok = wait_all(&work_empty[q], (uint32_t)((t >> 1) & 1) ^ 1u);
+        if (ok && lane == 0) {
+          work_sh[q] = w;
+          mbar_arrive(&work_full[q]);
+        }
+        __syncwarp();
+        ++t;
+        if (end) break;
       }
     }
-    if (elect_one()) tc_commit(&drain_bar);
-    __syncwarp();
-    int no_abort = 0;
-    mbar_wait(&drain_bar, 0, &no_abort, p.status, STATUS_TIMEOUT, DRAIN_NS);
-  }
   } else if (warp < 4 + 4 * NT) {
     // --------------------------------------------------------------- softmax
     if constexpr (C::SOFTMAX_REGS > 0) regs_inc<C::SOFTMAX_REGS>();
     const int x = (warp - 4) >> 2;
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;
-    const int nkx = nk_x[x];
-    const int tk = x * p.tok + r / p.ht, hh = r % p.ht;  // token in the block, head in the tile
-    const bool stored = r < p.tok * p.ht && hh < nh && tk < blk.count;
-    const int pos = blk.past + tk;
-    const int pos_first = blk.past + x * p.tok, pos_last = blk.past + min(blk.count, (x + 1) * p.tok) - 1;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t t_o = tmem_base + lane_off + 256 + x * D;
-    float scale_log2 = p.scale_log2, vscale = 1.0f;
-    if constexpr (F8) {
-      if (p.k_inv_scale) scale_log2 *= p.k_inv_scale[g];
-      if (p.v_inv_scale) vscale = p.v_inv_scale[g];
-    }
-    float m_run = -INFINITY, l = 0.0f;
-    int ok = nkx > 0;
-    for (int j = 0; ok && j < nkx; ++j) {
-      const int slot = NT == 2 ? x : j & 1;
-      const uint32_t spar = (uint32_t)(NT == 2 ? j & 1 : (j >> 1) & 1);
-      const uint32_t t_s = tmem_base + lane_off + slot * KB;
-      const int t0 = blk.tile(j0 + j) * KB;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[slot], spar, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS));
+    uint32_t steps = 0, outs = 0, duals = 0;  // of this tile so far
+    bool ok = true;
+    const Work* wp;
+    for (int t = 0, base = 0; ok && (wp = next(t)); give_back(t++)) {
+      const Work& w = *wp;
+      const int nkx = x ? w.nb : w.na;
+      const int g = w.hd / p.chunks, h0 = g * p.hpg + w.hd % p.chunks * p.ht;
+      const int nh = min(p.ht, (g + 1) * p.hpg - h0);       // query heads of the tile
+      const int xt = w.dual ? 0 : x;                        // tile of rows
+      const int tk = xt * p.tok + r / p.ht, hh = r % p.ht;  // token in the block, head in the tile
+      const bool stored = r < p.tok * p.ht && hh < nh && tk < w.count;
+      const int pos = w.past + tk;
+      const int pos_first = w.past + xt * p.tok, pos_last = w.past + min(w.count, (xt + 1) * p.tok) - 1;
+      float scale_log2 = p.scale_log2, vscale = 1.0f;
+      if constexpr (F8) {
+        if (p.k_inv_scale) scale_log2 *= p.k_inv_scale[g];
+        if (p.v_inv_scale) vscale = p.v_inv_scale[g];
+      }
+      float m_run = -INFINITY, l = 0.0f;
+      for (int i = 0; ok && i < nkx; ++i) {
+        const int j = w.dual ? 2 * i + x : i;
+        const uint32_t n = steps + i;
+        const int slot = NT == 2 ? x : n & 1;
+        const uint32_t t_s = tmem_base + lane_off + slot * KB;
+        const int t0 = w.tile(w.j0 + j) * KB;
+        if (!(ok = wait_all(&s_full[slot], NT == 2 ? n & 1 : (n >> 1) & 1))) break;
+        tc_fence_after();
+        // values that no row of the block sees: cleared, so that they count nothing whatever they are
+        if (t0 + KB > w.end || (t0 < w.lo && t0 + KB > w.sink_end)) {
+          // (A wait for a ring stage is good for the next phase only: what was in
+          // the stage before has landed, as the scores of this step and, with two
+          // score slots, the products of the one before are complete.)
+          if constexpr (NT == 1)
+            if (n > 0) ok = wait_all(&pv_done, (n - 1) & 1u);
+          const int at = v_at(base, w, j);
+          const int tt = t0 + r;
+          const bool clear = tt >= w.end || (tt < w.lo && tt >= w.sink_end);
+          for (int e = 0; ok && e < NE; ++e) {
+            const int s = (at + e) % NST;
+            ok = wait_all(&full[s], (uint32_t)(((at + e) / NST) & 1));
+            if (ok && clear) {
+#pragma unroll
+              for (int cb = 0; cb < EC / 64; ++cb)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4*>(ring + s * C::EB + cb * SUB + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();
+        }
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+        tmem_ld_wait();
+        if (p.negate) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) v[c] ^= 0x80000000u;
+        }
+        if (t0 + KB - 1 > pos_first || (p.window > 0 && pos_last - t0 >= p.window && t0 + KB > p.sinks)) {
+          // What the row sees as bits, 32 columns a word: two instructions a column.
+          // (Few instructions matter here: those that the steps without a mask do not
+          // run have to be fetched first.)
+          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+          const int hi = pos - t0 + 1;                                // keys c < hi
+          const int lo = p.window > 0 ? pos + 1 - p.window - t0 : 0;  // and c >= lo
+          const int sk = p.window > 0 ? p.sinks - t0 : 0;             // or c < sk
+#pragma unroll
+          for (int c0 = 0; c0 < KB; c0 += 32) {
+            const uint32_t bits = below(hi - c0) & (~below(lo - c0) | below(sk - c0));
+            if (__any_sync(0xffffffffu, bits != ~0u)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1u)) v[c0 + c] = 0xff800000u;  // -inf
+            }
+          }
+        }
+        float mx[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float m = __uint_as_float(v[k]);
+#pragma unroll
+          for (int c = 1; c < 15; c += 2) m = fmax3(m, __uint_as_float(v[k + 8 * c]), __uint_as_float(v[k + 8 * c + 8]));
+          mx[k] = fmaxf(m, __uint_as_float(v[k + 120]));
+        }
+        const float mb =
+            fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale_log2;
+        const bool move = __any_sync(0xffffffffu, mb > m_run + MOVE_LOG2);
+        if (move) {
+          const float m_new = fmaxf(m_run, mb);
+          const float alpha = m_new == -INFINITY ? 1.0f : ex2_fast(m_run - m_new);  // 0 on the first step
+          l *= alpha;
+          m_run = m_new;
+          if (i > 0) {
+            if constexpr (NT == 1) {  // the products of the step before may still be running
+              if (!(ok = wait_all(&pv_done, (n - 1) & 1u))) break;
+              tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(t_o + 16 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st_32x32b_x16(t_o + 16 * c, o);
+            }
+          }
+        }
+        // P = 2^(s scale - m), a row that has seen nothing yet in the frame 0
+        const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+        const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m_use, -m_use);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const int c = half * 64 + e;
+            float a0, a1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nm2), a0, a1);
+            const float p0 = ex2_fast(a0), p1 = ex2_fast(a1);
+            v[c] = __float_as_uint(p0);
+            v[c + 1] = __float_as_uint(p1);
+            pk[e >> 1] = pack_bf16(p0, p1);
+          }
+          tmem_st_32x32b_x32(t_s + 32 * half, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[slot][half]);
+        }
+        uint64_t ps[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ps[k] = f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+#pragma unroll
+        for (int c = 8; c < 128; c += 2)
+          ps[(c >> 1) & 3] = f2_add(ps[(c >> 1) & 3], f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+        float s0, s1;
+        f2_unpack(f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3])), s0, s1);
+        l += s0 + s1;
+      }
+      steps += nkx;
+      base += 2 * w.nk * NE;
       if (!ok) break;
-      tc_fence_after();
-      // values that no row of the block sees: cleared, so that they count nothing whatever they are
-      if (t0 + KB > blk.end || (t0 < blk.lo && t0 + KB > blk.sink_end)) {
-        // (A wait for a ring stage is good for the next phase only: what was in
-        // the stage before has landed, as the scores of this step and, with two
-        // score slots, the products of the one before are complete.)
-        if constexpr (NT == 1)
-          if (j > 0)
-            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done, (uint32_t)((j - 1) & 1), abort_flag, p.status,
-                                                   STATUS_TIMEOUT, WAIT_NS));
-        const int at = v_at(j);
-        const int t = t0 + r;
-        const bool clear = t >= blk.end || (t < blk.lo && t >= blk.sink_end);
-        for (int e = 0; ok && e < NE; ++e) {
-          const int s = (at + e) % NST;
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)(((at + e) / NST) & 1), abort_flag, p.status,
-                                                 STATUS_TIMEOUT, WAIT_NS));
-          if (ok && clear) {
-#pragma unroll
-            for (int cb = 0; cb < EC / 64; ++cb)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(ring + s * C::EB + cb * SUB + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-          }
+      if (nkx > 0) {
+        if (!(ok = wait_all(&o_full[x], outs++ & 1u))) break;
+        tc_fence_after();
+      }
+      // ---- the piece's result
+      float fa = 1.0f, fb = 0.0f;  // weights of the two tiles' values
+      if (NT == 2 && w.dual) {
+        const uint32_t par = duals++ & 1u;
+        if (x == 1) {  // the first tile's warps take the second's values too
+          other[r] = make_float2(m_run, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&post);
+          if (!(ok = wait_all(&taken, par))) break;
+          tc_fence_after();
+          continue;
         }
-        if (!ok) break;
-        fence_proxy_async_smem();
+        if (!(ok = wait_all(&post, par))) break;
+        tc_fence_after();
+        const float2 o = other[r];
+        const float top = fmaxf(m_run, o.x), ref = top == -INFINITY ? 0.0f : top;
+        fa = ex2_fast(m_run - ref);
+        fb = ex2_fast(o.x - ref);
+        l = fa * l + fb * o.y;
+        m_run = top;
+      } else if (x == 1 && w.count <= p.tok) {
+        continue;  // no second tile
       }
-      uint32_t v[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-      tmem_ld_wait();
-      if (p.negate) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c) v[c] ^= 0x80000000u;
-      }
-      const bool masked = t0 + KB - 1 > pos_first ||
-                          (p.window > 0 && pos_last - t0 >= p.window && t0 + KB > p.sinks);
-      if (masked) {
-        const int hi = pos - t0;                                    // keys c <= hi
-        const int lo = p.window > 0 ? pos - p.window - t0 : -1;     // and c > lo
-        const int sk = p.window > 0 ? p.sinks - t0 : 0;             // or c < sk
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > hi || (c <= lo && c >= sk)) v[c] = 0xff800000u;  // -inf
-      }
-      float mx[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float m = __uint_as_float(v[k]);
-#pragma unroll
-        for (int i = 1; i < 15; i += 2) m = fmax3(m, __uint_as_float(v[k + 8 * i]), __uint_as_float(v[k + 8 * i + 8]));
-        mx[k] = fmaxf(m, __uint_as_float(v[k + 120]));
-      }
-      const float mb =
-          fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale_log2;
-      const bool move = __any_sync(0xffffffffu, mb > m_run + MOVE_LOG2);
-      float alpha = 1.0f;
-      if (move) {
-        const float m_new = fmaxf(m_run, mb);
-        alpha = m_new == -INFINITY ? 1.0f : ex2_fast(m_run - m_new);  // 0 on the first step
-        l *= alpha;
-        m_run = m_new;
-        if (j > 0) {
-          if constexpr (NT == 1) {  // the products of the step before may still be running
-            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done, (uint32_t)((j - 1) & 1), abort_flag, p.status,
-                                                   STATUS_TIMEOUT, WAIT_NS));
-            if (!ok) break;
-            tc_fence_after();
-          }
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(t_o + 16 * c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st_32x32b_x16(t_o + 16 * c, o);
-          }
-        }
-      }
-      // P = 2^(s scale - m), a row that has seen nothing yet in the frame 0
-      const float m_use = m_run == -INFINITY ? 0.0f : m_run;
-      const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m_use, -m_use);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const int c = half * 64 + i;
-          float a0, a1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nm2), a0, a1);
-          const float p0 = ex2_fast(a0), p1 = ex2_fast(a1);
-          v[c] = __float_as_uint(p0);
-          v[c + 1] = __float_as_uint(p1);
-          w[i >> 1] = pack_bf16(p0, p1);
-        }
-        tmem_st_32x32b_x32(t_s + 32 * half, w);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[slot][half]);
-      }
-      uint64_t ps[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) ps[k] = f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-#pragma unroll
-      for (int c = 8; c < 128; c += 2)
-        ps[(c >> 1) & 3] = f2_add(ps[(c >> 1) & 3], f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-      float s0, s1;
-      f2_unpack(f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3])), s0, s1);
-      l += s0 + s1;
-    }
-    if (mine && (x == 0 || has_b)) {
-      const int64_t row = (int64_t)blk.first + tk;
-      const int head = h0 + hh;
-      if (nkx > 0 && ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], 0, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS));
       const bool none = nkx == 0;  // nothing seen: zeros
-      if ((none || ok) && whole) {
-        tc_fence_after();
-        const float inv = blk.past < 0 ? 0.0f : vscale / l;
+      const float inv = none ? 0.0f : vscale / l;
+      const int64_t row = (int64_t)w.first + tk;
+      const int rr = xt * 128 + r;
+      uint8_t* dst;
+      if (w.whole) {
+        const int head = h0 + hh;
         if (stored && p.lse) p.lse[row * p.nq + head] = none ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994531f;
-        const int64_t off = stored ? row * p.ld_out + (int64_t)head * D : -1;
-        // the warp's rows, turned in its part of the tile's queries, which are no longer needed
-        uint8_t* stg = smem + x * C::QT + q4 * (C::QT / 4);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (!none) {
-            tmem_ld_32x32b_x32(t_o + 32 * c, o);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (!none)
-              w = make_uint4(pack_bf16(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
-                             pack_bf16(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
-                             pack_bf16(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
-                             pack_bf16(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
-            *reinterpret_cast<uint4*>(stg + lane * (D * 2) + (((4 * c + k) ^ (lane & 7)) << 4)) = w;
-          }
-        }
-        __syncwarp();
-        constexpr int CH = D / 8;  // 16-byte pieces of a row
-        uint8_t* out = static_cast<uint8_t*>(p.out);
-#pragma unroll 4
-        for (int u = lane; u < 32 * CH; u += 32) {
-          const int rr = u / CH, c = u % CH;
-          const int64_t to = __shfl_sync(0xffffffffu, off, rr);
-          if (to >= 0)
-            *reinterpret_cast<uint4*>(out + 2 * to + 16 * c) =
-                *reinterpret_cast<const uint4*>(stg + rr * (D * 2) + ((c ^ (rr & 7)) << 4));
-        }
-      } else if (none || ok) {  // a part: weighted values, maximum and sum
-        tc_fence_after();
-        const int64_t slot_b = slot_base(blk.first - blk.i * block_tok, blk.b, block_tok) + blk.i;
-        float* part = p.part + ((slot_b * p.heads + hd) * p.nsplit + split) * (NT * 128) * (D + 2);
-        const int rr = x * 128 + r;
+        dst = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + (int64_t)head * D);
+        fa *= inv;
+        fb *= inv;
+      } else {  // a part: weighted values, maximum and sum
+        const int64_t slot_b = slot_base(w.first - w.i * block_tok, w.b, block_tok) + w.i;
+        float* part = p.part + ((slot_b * p.heads + w.hd) * p.nsplit + w.split) * (NT * 128) * (D + 2);
         if (stored) {
           part[(size_t)NT * 128 * D + rr] = m_run;
           part[(size_t)NT * 128 * (D + 1) + rr] = l;
         }
+        dst = reinterpret_cast<uint8_t*>(part + (size_t)rr * D);
+      }
+      // 32 columns at a time: a load from tensor memory takes some 300 cycles beside
+      // the other tile's products whatever its size
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (!none) {
-            tmem_ld_32x32b_x32(t_o + 32 * c, o);
-            tmem_ld_wait();
-          }
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (!none) {
+          tmem_ld_32x32b_x32(t_o + c, o);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(fa * __uint_as_float(o[e]));
+        if (NT == 2 && w.dual) {
+          uint32_t y[32];
+          tmem_ld_32x32b_x32(t_o + D + c, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(fb, __uint_as_float(y[e]), __uint_as_float(o[e])));
+        }
+        if (stored && w.whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            reinterpret_cast<uint4*>(dst + 2 * c)[k] =
+                make_uint4(pack_bf16(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                           pack_bf16(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                           pack_bf16(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                           pack_bf16(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+        } else if (stored) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (stored)
-              *reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * c + 4 * k) =
-                  none ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            reinterpret_cast<uint4*>(dst + 4 * c)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
+        __syncwarp();
+      }
+      if (NT == 2 && w.dual) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken);
       }
     }
   } else {
     // ------------------------------------------------- E4M3 codes to bf16
-    if constexpr (F8) regs_dec<C::CONVERT_REGS>();
-    constexpr int NRX = F8 ? NR : 1;
-    const int tid = threadIdx.x - 128 * (1 + NT);
-    bool ok = true;
-    for (int at = 0; F8 && ok && at < 2 * nk * NE; ++at) {
-      const int rs = at % NRX, s = at % NST;
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait(&raw_full[rs], (uint32_t)((at / NRX) & 1), abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS) &&
-                          mbar_wait(&empty[s], (uint32_t)((at / NST) & 1) ^ 1u, abort_flag, p.status, STATUS_TIMEOUT,
-                                    WAIT_NS));
-      if (!ok) break;
+    if constexpr (F8) {
+      regs_dec<C::CONVERT_REGS>();
+      const int cw = warp - 4 - 4 * NT;
+      bool ok = true;
+      const Work* wp;
+      for (int t = 0, at = 0; ok && (wp = next(t)); give_back(t++)) {
+        const int end = at + 2 * wp->nk * NE;
+        for (; ok && at < end; ++at) {
+          const int s = at % NST;
+          if (!(ok = wait_all(&raw_full[s], (uint32_t)((at / NST) & 1)))) break;
+          // 32 rows of the tile, their codes in the upper half of their space
+          uint8_t* mine = ring + s * C::EB + cw * 4096;
+          uint4 c[EC / 64][4];
 #pragma unroll
-      for (int cb = 0; cb < EC / 64; ++cb)
+          for (int cb = 0; cb < EC / 64; ++cb)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int u = tid + 128 * k, piece = u & 3, row = u >> 2;
-          const uint4 c = *reinterpret_cast<const uint4*>(raw + rs * C::RB + cb * (KB * 64) + row * 64 + piece * 16);
-          uint8_t* dst = ring + s * C::EB + cb * SUB + row * 128;
-          *reinterpret_cast<uint4*>(dst + (((2 * piece) ^ (row & 7)) << 4)) =
-              make_uint4(bf16_of_e4m3(c.x, false), bf16_of_e4m3(c.x, true), bf16_of_e4m3(c.y, false),
-                         bf16_of_e4m3(c.y, true));
-          *reinterpret_cast<uint4*>(dst + (((2 * piece + 1) ^ (row & 7)) << 4)) =
-              make_uint4(bf16_of_e4m3(c.z, false), bf16_of_e4m3(c.z, true), bf16_of_e4m3(c.w, false),
-                         bf16_of_e4m3(c.w, true));
+            for (int k = 0; k < 4; ++k)
+              c[cb][k] = *reinterpret_cast<const uint4*>(mine + cb * SUB + 2048 + (lane + 32 * k) * 16);
+          __syncwarp();
+#pragma unroll
+          for (int cb = 0; cb < EC / 64; ++cb)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int piece = lane & 3, row = (lane >> 2) + 8 * k;
+              uint8_t* dst = mine + cb * SUB + row * 128;
+              const uint4 y = c[cb][k];
+              *reinterpret_cast<uint4*>(dst + (((2 * piece) ^ (row & 7)) << 4)) =
+                  make_uint4(bf16_of_e4m3(y.x, false), bf16_of_e4m3(y.x, true), bf16_of_e4m3(y.y, false),
+                             bf16_of_e4m3(y.y, true));
+              *reinterpret_cast<uint4*>(dst + (((2 * piece + 1) ^ (row & 7)) << 4)) =
+                  make_uint4(bf16_of_e4m3(y.z, false), bf16_of_e4m3(y.z, true), bf16_of_e4m3(y.w, false),
+                             bf16_of_e4m3(y.w, true));
+            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
         }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&raw_empty[rs]);
-        mbar_arrive(&full[s]);
       }
     }
   }
@@ -741,7 +875,7 @@ bool map_cache(CUtensorMap* m, const void* ptr, const VarFwdArgs& a, int box_tok
 template <int D, int SRC>
 cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStream_t st) {
   using C = Cfg<D, SRC>;
-  static_assert(C::SMEM + 1400 <= 232448, "shared memory");
+  static_assert(C::SMEM + 900 + (C::NT == 2 ? 1024 : 0) <= 232448, "shared memory");
   const int block_tok = C::NT * p.tok;
   const int64_t slots = a.seq.rows / block_tok + a.seq.batch;
   const int64_t units = slots * p.heads;
@@ -756,19 +890,20 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
     if (p.nsplit < 1) p.nsplit = 1;
   }
   p.by_length = units > num_sms && a.seq.batch <= LPT_BATCH;
+  p.units = (int)(units * p.nsplit);
   CUtensorMap mq, mk, mv;
   bool ok = map3(&mq, a.q, D, a.nq, a.seq.rows, a.ld_q, p.ht, p.tok);
   if (SRC == PACKED) {
     ok = ok && map3(&mk, a.k, D, a.nkv, a.seq.rows, a.ld_k, 1, KB) && map3(&mv, a.v, D, a.nkv, a.seq.rows, a.ld_v, 1, KB);
   } else {
-    for (p.box = KB; a.page_size % p.box;) p.box /= 2;  // ends at 8 at the latest
+    for (p.box = C::F8 ? 32 : KB; a.page_size % p.box;) p.box /= 2;  // ends at 8 at the latest
     ok = ok && map_cache(&mk, a.k_cache, a, p.box) && map_cache(&mv, a.v_cache, a, p.box);
   }
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = allow_smem<var_fwd_kernel<D, SRC>>(C::SMEM);
   if (e == cudaSuccess) e = check_regs<var_fwd_kernel<D, SRC>>(C::THREADS, C::SOFTMAX_REGS > 0 ? C::REGS : 0);
   if (e != cudaSuccess) return e;
-  var_fwd_kernel<D, SRC><<<(unsigned)(units * p.nsplit), C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
+  var_fwd_kernel<D, SRC><<<p.units < num_sms ? p.units : num_sms, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
   var_join_kernel<D><<<(unsigned)((a.seq.rows * a.nq + 7) / 8), 256, 0, st>>>(p);

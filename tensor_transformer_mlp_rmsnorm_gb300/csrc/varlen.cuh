@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 
+#include "ptx_sm103.cuh"
 #include "tma_maps.cuh"
 #include "varlen.h"
 
@@ -74,68 +75,98 @@ __device__ __forceinline__ int find_row(const SeqRows& s, int row, int lane) {
   return lo;
 }
 
-// Blocks are ordered by length up to this many sequences.  Looking at all of
-// them costs a CTA about a microsecond at 512; with more there are many blocks,
-// and the last ones count for little.
-constexpr int LPT_BATCH = 512;
+// Blocks are ordered by length up to this many sequences, two a lane; with
+// more there are many blocks, and the last ones count for little.
+constexpr int LPT_BATCH = 64;
 
-// The rank-th block, longest first (more steps before fewer), by the lanes of
-// one warp over the sequences' (past, count) in shared memory.  The number of
-// blocks of at least x steps of a sequence is a closed form, so the steps of
-// the rank-th block are found by bisection.  A step is KB tokens.
+// Finds the blocks of units of work, longest first (more steps of KB tokens
+// before fewer), by the lanes of one warp.  The number of blocks of at least x
+// steps of a sequence is a closed form, so the steps of the rank-th block are
+// found by bisection.
 template <int KB>
-__device__ __forceinline__ void find_by_length(const int2* sq, int batch, int rank, int block_tok, int cap, int lane,
-                                               int* b_out, int* i_out) {
-  auto blocks_from = [&](int2 s, int x) -> int {  // blocks with at least x steps
-    const int nblk = (s.y + block_tok - 1) / block_tok;
-    if (x <= 1) return nblk;
-    if (x > cap || s.x < 0) return 0;
-    const int64_t y = (int64_t)(x - 1) * KB + 1;  // tokens that x steps need
-    if ((int64_t)s.x + s.y < y) return 0;
-    const int64_t before = (y - s.x + block_tok - 1) / block_tok - 1;
-    return nblk - (int)max((int64_t)0, before);
-  };
-  auto count = [&](int x) -> int {
+struct ByLength {
+  int past[2], count[2], blocks[2];  // of the sequences lane + 32 k
+  int most;                          // steps of the longest block that is not found yet
+  int block_tok, cap;                // tokens of a block; steps that a window leaves at most
+  uint64_t inverse;                  // 2^64 / block_tok, rounded up: exact quotients of 32-bit numbers
+
+  __device__ __forceinline__ int div_up(int n) const {
+    return block_tok == 1 ? n : (int)__umul64hi((uint64_t)(n + block_tok - 1), inverse);
+  }
+  // blocks of sequence k with at least x steps
+  __device__ __forceinline__ int from(int k, int x) const {
+    if (x <= 1) return blocks[k];
+    if (x > cap || past[k] < 0) return 0;
+    const int y = (x - 1) * KB + 1;  // tokens that x steps need
+    if (past[k] + count[k] < y) return 0;
+    return y <= past[k] ? blocks[k] : blocks[k] - div_up(y - past[k]) + 1;
+  }
+  __device__ __forceinline__ int total(int x) const {
     int c = 0;
-    for (int b = lane; b < batch; b += 32) c += blocks_from(sq[b], x);
-    return __reduce_add_sync(0xffffffffu, c);
-  };
-  int most = 1;
-  for (int b = lane; b < batch; b += 32) most = max(most, (int)min(((int64_t)max(sq[b].x, 0) + sq[b].y + KB - 1) / KB, (int64_t)cap));
-  most = __reduce_max_sync(0xffffffffu, most);
-  *b_out = -1;
-  if (count(1) <= rank) return;
-  int lo = 1, hi = most + 1;  // count(lo) > rank >= count(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (count(mid) > rank) lo = mid;
-    else hi = mid;
-  }
-  int left = rank - count(hi);
-  for (int b0 = 0; b0 < batch; b0 += 32) {
-    const int b = b0 + lane;
-    int mine = 0, longer = 0, nblk = 0;
-    if (b < batch) {
-      longer = blocks_from(sq[b], hi);
-      nblk = blocks_from(sq[b], 1);
-      mine = blocks_from(sq[b], lo) - longer;
-    }
-    int upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint32_t has = __ballot_sync(0xffffffffu, upto > left);
-    if (has) {
-      const int src = __ffs(has) - 1;
-      const int i = nblk - longer - mine + (left - (upto - mine));
-      *b_out = b0 + src;
-      *i_out = __shfl_sync(0xffffffffu, i, src);
-      return;
-    }
-    left -= __shfl_sync(0xffffffffu, upto, 31);
+    for (int k = 0; k < 2; ++k)
+      c += from(k, x);
+    return __reduce_add_sync(0xffffffffu, c);
   }
+  // limit: tokens of the cache, or -1; packed: past counts as 0
+  __device__ __forceinline__ void init(const SeqRows& s, int64_t limit, int block_tok_, int cap_, int lane) {
+    block_tok = block_tok_;
+    cap = cap_;
+    inverse = ~0ull / (uint32_t)block_tok + 1;
+    int m = 1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      past[k] = count[k] = blocks[k] = 0;
+      if (lane + 32 * k < s.batch) {
+        bool bad = false;  // reported elsewhere
+        const SeqSpan sp = seq_span(s, lane + 32 * k, limit, &bad);
+        past[k] = sp.past;
+        count[k] = sp.count;
+        blocks[k] = div_up(sp.count);
+        m = max(m, min((max(sp.past, 0) + sp.count + KB - 1) / KB, cap));
+      }
+    }
+    most = __reduce_max_sync(0xffffffffu, m);
+  }
+  // The rank-th block: block i of sequence b, or b = -1.  Ranks are asked for in
+  // ascending order, so the steps only descend.
+  __device__ __forceinline__ void find(int rank, int lane, int* b, int* i) {
+    *b = -1;
+    *i = 0;
+    if (total(1) <= rank) return;
+    int lo = 1, hi = most + 1;  // total(lo) > rank >= total(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (total(mid) > rank) lo = mid;
+      else hi = mid;
+    }
+    most = lo;
+    int left = rank - total(hi);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int longer = from(k, hi), mine = from(k, lo) - longer;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const uint32_t has = __ballot_sync(0xffffffffu, upto > left);
+      if (has) {
+        const int src = __ffs(has) - 1;
+        *b = 32 * k + src;
+        *i = __shfl_sync(0xffffffffu, blocks[k] - longer - mine + (left - (upto - mine)), src);
+        return;
+      }
+      left -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+};
+
+// The unit of work of CTA c in its k-th turn among n CTAs: every other turn in
+// reverse, so that with units longest first nobody has the longer one each time.
+__device__ __forceinline__ int64_t snake(int k, int c, int n) {
+  return (int64_t)k * n + ((k & 1) ? n - 1 - c : c);
 }
 
 template <int N>
