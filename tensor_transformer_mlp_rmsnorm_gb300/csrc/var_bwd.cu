@@ -61,7 +61,8 @@ struct BwdParams {
   int nq, nkv, hpg;
   int ht, chunks, tok;     // DQ: heads and tokens of a tile of 128 rows
   int sht, schunks, stok;  // the others: of a step
-  int slots, heads;
+  Slots slots;
+  int heads;
   bool by_length;
   float scale, scale_log2;
   int window, sinks;
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(384, 1)
       order.init(p.seq, -1, block_tok, most, lane);
       order.find(rank, lane, &b, &i);
     } else {
-      b = find_slot(p.seq, p.slots - 1 - rank, block_tok, lane);
+      b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
       i = -1;  // below
     }
     if (lane == 0) {
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(384, 1)
       if (b >= 0) {
         bool bad = false;
         const SeqSpan s = seq_span(p.seq, b, -1, &bad);
-        if (i < 0) i = p.slots - 1 - rank - slot_base(s.first, b, block_tok);
+        if (i < 0) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
         if (i >= 0 && (int64_t)i * block_tok < s.count) {
           // key blocks from the first on are the long ones
           if (!Q_STAYS) i = (s.count - 1) / block_tok - i;
@@ -762,9 +763,9 @@ cudaError_t launch_role(BwdParams p, const VarBwdArgs& a, int num_sms, cudaStrea
   p.schunks = (p.hpg + C::KB - 1) / C::KB;
   p.sht = (p.hpg + p.schunks - 1) / p.schunks;
   p.stok = C::KB / p.sht;
-  const int64_t slots = a.seq.rows / block_tok + a.seq.batch, units = slots * p.heads;
+  p.slots = make_slots(a.seq, block_tok);
+  const int64_t units = p.slots.count * p.heads;
   if (units > 0x7fffffff / 2) return cudaErrorInvalidConfiguration;
-  p.slots = (int)slots;
   p.by_length = units > num_sms && a.seq.batch <= LPT_BATCH;
   CUtensorMap r1, r2, x1, x2;
   const int64_t rows = a.seq.rows;

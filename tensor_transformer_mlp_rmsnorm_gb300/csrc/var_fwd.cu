@@ -25,17 +25,33 @@ constexpr int MIN_PART = 4;        // steps of a part at least
 
 enum Source { PACKED = 0, PAGED = 1, PAGED_F8 = 2 };
 
-template <int D, int SRC>
+// FEW: blocks of one tile of rows, for sequences of few rows over long caches:
+// both tiles take turns at the steps, and the room of the second tile's queries
+// goes to copies in flight.
+template <int D, int SRC, bool FEW>
 struct Cfg {
   static constexpr bool F8 = SRC == PAGED_F8;
-  static constexpr int NT = D <= 128 ? 2 : 1;         // query tiles of a CTA
+  static constexpr int NT = D <= 128 ? 2 : 1;         // tiles in tensor memory
+  static constexpr int QTILES = FEW ? 1 : NT;         // query tiles of a block
   static constexpr int EC = D % 128 == 0 ? 128 : 64;  // columns of a ring element
   static constexpr int NE = D / EC;                   // elements of an operand
   static constexpr uint32_t EB = EC / 64 * SUB;       // bytes of an element
   static constexpr uint32_t QT = D / 64 * SUB;        // bytes of a query tile
-  static constexpr int FIT = (int)((225 * 1024 - NT * QT) / EB);
+  // E4M3 codes land in the space of the bf16 rows that are made of them, or, where the
+  // copies are what counts, in a ring of their own that is free again once they are read.
+  static constexpr bool RAW_RING = F8 && FEW;
+  static constexpr int NRAW = RAW_RING ? 3 * 128 / EC : 0;
+  static constexpr uint32_t RAW = NRAW * EB / 2;
+  // Results are turned in shared memory, 128 bytes of a row at a time, where there is
+  // room: a store of 16 bytes in each of 32 rows takes some 250 cycles.
+  static constexpr bool STAGED = D != 256;
+  static constexpr uint32_t STAGE = STAGED ? QTILES * 4 * 4096 : 0;
+  static constexpr int FIT = (int)((225 * 1024 - QTILES * QT - STAGE - RAW) / EB);
   static constexpr int NST = FIT < 12 ? FIT : 12;     // ring stages
-  static constexpr uint32_t SMEM = NT * QT + NST * EB + 1024;
+  // A turn at a step waits for its values and the tile's next keys, up to four operands on.
+  static_assert(NST >= (NT == 2 ? 4 : 2) * NE, "ring");
+  static constexpr int LAND = RAW_RING ? NRAW : NST;  // stages that copies land in
+  static constexpr uint32_t SMEM = QTILES * QT + NST * EB + RAW + STAGE + 1024;
   static constexpr int WGS = 1 + NT + (F8 ? 1 : 0);   // issuing, softmax a tile, converting
   static constexpr int THREADS = 128 * WGS;
   static constexpr int READERS = 2 + 4 * NT + (F8 ? 4 : 0);  // warps that a piece of work is handed to
@@ -55,7 +71,8 @@ struct FwdParams {
   int nq, nkv, hpg;
   int ht, chunks;    // heads of a tile, tiles of heads a key head
   int tok;           // tokens of a tile
-  int slots, heads;  // block slots, key heads times chunks
+  Slots slots;
+  int heads;  // block slots, key heads times chunks
   int units;         // slots times heads times parts
   int nsplit;
   bool by_length;
@@ -128,6 +145,7 @@ __device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t v, bool high) {
 // A piece of work: a block, or with nsplit > 1 a part of its steps.
 struct Work : Block {
   int hd, split;
+  int g, h0, nh;   // key head, first query head, query heads
   int j0, nk;      // steps [j0, j0 + nk) of the block
   int na, nb;      // those of the first and the second tile
   bool whole;      // all steps of the block
@@ -135,32 +153,36 @@ struct Work : Block {
 };
 constexpr int NONE = -2;  // Work::b behind the last piece
 
-template <int D, int SRC>
-__global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
+template <int D, int SRC, bool FEW>
+__global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
     var_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const FwdParams p) {
-  using C = Cfg<D, SRC>;
+  using C = Cfg<D, SRC, FEW>;
   constexpr int NT = C::NT, NE = C::NE, EC = C::EC, NST = C::NST;
-  constexpr bool F8 = C::F8;
+  constexpr bool F8 = C::F8, RAW_RING = C::RAW_RING;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], full[NST], empty[NST], raw_full[F8 ? NST : 1], s_full[2],
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], full[NST], empty[NST], raw_full[F8 ? C::LAND : 1], raw_empty[RAW_RING ? C::LAND : 1], s_full[2],
       p_full[2][2], o_full[2], pv_done, post, taken, work_full[2], work_empty[2], drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   __shared__ Work work_sh[2];
   __shared__ float2 other[NT == 2 ? 128 : 1];  // second tile's maximum and sum
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ring = smem + NT * C::QT;
+  uint8_t* ring = smem + C::QTILES * C::QT;
+  uint8_t* raw = ring + NST * C::EB;
   volatile int* abort_flag = &abort_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t cap = SRC == PACKED ? -1 : (int64_t)p.max_pages * p.page_size;
-  const int block_tok = NT * p.tok;
+  const int block_tok = C::QTILES * p.tok;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], F8 ? 4 : 1);
       mbar_init(&empty[i], 1);
-      if (F8) mbar_init(&raw_full[i], 1);
+    }
+    for (int i = 0; F8 && i < C::LAND; ++i) {
+      mbar_init(&raw_full[i], 1);
+      if (RAW_RING) mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
@@ -225,15 +247,18 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
       const bool issues = my_box < boxes;
       // E4M3 codes land in the upper half of the space of the bf16 rows that the same warp makes of them
       const int row0 = my_box * p.box;
-      const uint32_t my_dst = my_col * SUB + (SRC == PACKED ? 0 : F8 ? row0 / 32 * 4096 + 2048 + row0 % 32 * 64 : row0 * 128);
-      uint64_t* land = F8 ? raw_full : full;
+      const uint32_t my_dst = RAW_RING ? my_col * (KB * 64) + row0 * 64
+                              : my_col * SUB + (SRC == PACKED ? 0 : F8 ? row0 / 32 * 4096 + 2048 + row0 % 32 * 64 : row0 * 128);
+      uint64_t *land = F8 ? raw_full : full, *room = RAW_RING ? raw_empty : empty;
+      uint8_t* land_at = RAW_RING ? raw : ring;
+      constexpr uint32_t LAND_BYTES = RAW_RING ? C::EB / 2 : C::EB;
       uint32_t armed = 0, par_armed = 0;  // by stage
       uint32_t q_a = 0, q_b = 0;          // pieces whose queries are in each tile
       bool ok = true;
       const Work* wp;
       for (int t = 0, base = 0; ok && (wp = next(t)); give_back(t++)) {
         const Work& w = *wp;
-        const int g = w.hd / p.chunks, h0 = g * p.hpg + w.hd % p.chunks * p.ht;
+        const int g = w.g, h0 = w.h0;
         // page of this lane's box in a step: num_pages (nothing is read, zeros land) where no row sees it
         auto look = [&](int j) -> int {
           const int at = w.tile(w.j0 + j) * KB + row0, pi = at / p.page_size;
@@ -249,16 +274,16 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
         auto load = [&](int at, const CUtensorMap* map, int j, int page) -> bool {
           const int tile = w.tile(w.j0 + j);
           for (int e = 0; e < NE; ++e, ++at) {
-            const int s = at % NST;
-            const uint32_t par = (uint32_t)((at / NST) & 1);
-            if (!wait_all(&empty[s], par ^ 1u)) return false;
+            const int s = at % C::LAND;
+            const uint32_t par = (uint32_t)((at / C::LAND) & 1);
+            if (!wait_all(&room[s], par ^ 1u)) return false;
             if (lane == 0) mbar_arrive_expect_tx(&land[s], F8 ? C::EB / 2 : C::EB);
             __syncwarp();
             armed |= 1u << s;
             par_armed = (par_armed & ~(1u << s)) | (par << s);
             if (issues) {
               const int col = e * EC + my_col * 64;
-              uint8_t* dst = ring + s * C::EB + my_dst;
+              uint8_t* dst = land_at + s * LAND_BYTES + my_dst;
               if constexpr (SRC == PACKED) tma_load_3d(dst, map, &land[s], col, g, w.first - w.i * block_tok + tile * KB);
               else tma_load_4d(dst, map, &land[s], col, (tile * KB + row0) % p.page_size, g, page);
             }
@@ -308,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
         int no_abort = 0;
         if (q_a) mbar_wait(&q_full[0], (q_a - 1) & 1u, &no_abort, p.status, 0u, DRAIN_NS);
         if (q_b) mbar_wait(&q_full[1], (q_b - 1) & 1u, &no_abort, p.status, 0u, DRAIN_NS);
-        for (int s = 0; s < NST; ++s)
+        for (int s = 0; s < C::LAND; ++s)
           if (armed & (1u << s)) mbar_wait(&land[s], (par_armed >> s) & 1u, &no_abort, p.status, 0u, DRAIN_NS / 8);
       }
     } else if (warp == 1) {
@@ -473,19 +498,22 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
           const int unit = (int)u;
           w.split = unit % p.nsplit;
           w.hd = unit / p.nsplit % p.heads;
+          w.g = w.hd / p.chunks;
+          w.h0 = w.g * p.hpg + w.hd % p.chunks * p.ht;
+          w.nh = min(p.ht, (w.g + 1) * p.hpg - w.h0);
           const int rank = unit / p.nsplit / p.heads;
           int b, i = 0;
           if (p.by_length) {
             order.find(rank, lane, &b, &i);
           } else {
-            const int slot = p.slots - 1 - rank;
-            b = find_slot(p.seq, slot, block_tok, lane);
+            const int slot = (int)p.slots.count - 1 - rank;
+            b = find_slot(p.seq, p.slots, slot, lane);
             i = -1;  // below
           }
           if (b < 0) continue;
           bool bad = false;
           const SeqSpan s = seq_span(p.seq, b, cap, &bad);
-          if (i < 0) i = p.slots - 1 - rank - slot_base(s.first, b, block_tok);
+          if (i < 0) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
           if (i < 0 || (int64_t)i * block_tok >= s.count) continue;
           fill_block(&w, s, b, i, p.tok, block_tok, p.window, p.sinks);
           const int per = part_steps(w.n, p.nsplit);
@@ -493,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
           if (w.split > 0 && w.j0 >= w.n) continue;
           w.whole = per >= w.n;
           w.nk = min(w.n, w.j0 + per) - w.j0;
-          w.dual = NT == 2 && w.count <= p.tok && w.nk > 1;
+          w.dual = NT == 2 && (FEW || w.count <= p.tok) && w.nk > 1;
           if (w.dual) {
             w.na = (w.nk + 1) / 2;
             w.nb = w.nk / 2;
@@ -521,23 +549,23 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t t_o = tmem_base + lane_off + 256 + x * D;
+    const int tok_r = r / p.ht, hh = r - tok_r * p.ht;  // token in the tile, head
+    uint8_t* stg = raw + C::RAW + (FEW ? warp & 3 : warp - 4) * 4096;
     uint32_t steps = 0, outs = 0, duals = 0;  // of this tile so far
     bool ok = true;
     const Work* wp;
     for (int t = 0, base = 0; ok && (wp = next(t)); give_back(t++)) {
       const Work& w = *wp;
       const int nkx = x ? w.nb : w.na;
-      const int g = w.hd / p.chunks, h0 = g * p.hpg + w.hd % p.chunks * p.ht;
-      const int nh = min(p.ht, (g + 1) * p.hpg - h0);       // query heads of the tile
-      const int xt = w.dual ? 0 : x;                        // tile of rows
-      const int tk = xt * p.tok + r / p.ht, hh = r % p.ht;  // token in the block, head in the tile
-      const bool stored = r < p.tok * p.ht && hh < nh && tk < w.count;
+      const int xt = w.dual ? 0 : x;         // tile of rows
+      const int tk = xt * p.tok + tok_r;     // token in the block
+      const bool stored = r < p.tok * p.ht && hh < w.nh && tk < w.count;
       const int pos = w.past + tk;
       const int pos_first = w.past + xt * p.tok, pos_last = w.past + min(w.count, (xt + 1) * p.tok) - 1;
       float scale_log2 = p.scale_log2, vscale = 1.0f;
       if constexpr (F8) {
-        if (p.k_inv_scale) scale_log2 *= p.k_inv_scale[g];
-        if (p.v_inv_scale) vscale = p.v_inv_scale[g];
+        if (p.k_inv_scale) scale_log2 *= p.k_inv_scale[w.g];
+        if (p.v_inv_scale) vscale = p.v_inv_scale[w.g];
       }
       float m_run = -INFINITY, l = 0.0f;
       for (int i = 0; ok && i < nkx; ++i) {
@@ -572,6 +600,30 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
           if (!ok) break;
           fence_proxy_async_smem();
         }
+        if (t0 + KB - 1 > pos_first || (p.window > 0 && pos_last - t0 >= p.window && t0 + KB > p.sinks)) {
+          // Hidden scores are overwritten in place, 32 columns at a time and only where a
+          // row of the warp has any.  A short loop, because instructions that most steps
+          // do not run have to be fetched first: with all 128 columns unrolled the masked
+          // step took 2500 cycles longer than the others' 460 up to the maximum.
+          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+          const int hi = pos - t0 + 1;                                // keys c < hi
+          const int lo = p.window > 0 ? pos + 1 - p.window - t0 : 0;  // and c >= lo
+          const int sk = p.window > 0 ? p.sinks - t0 : 0;             // or c < sk
+          const uint32_t hidden = p.negate ? 0x7f800000u : 0xff800000u;
+#pragma unroll 1
+          for (int c0 = 0; c0 < KB; c0 += 32) {
+            const uint32_t bits = below(hi - c0) & (~below(lo - c0) | below(sk - c0));
+            if (!__any_sync(0xffffffffu, bits != ~0u)) continue;
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_s + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(bits >> c & 1u)) o[c] = hidden;
+            tmem_st_32x32b_x32(t_s + c0, o);
+          }
+          tmem_st_wait();
+        }
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
@@ -579,24 +631,6 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
         if (p.negate) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) v[c] ^= 0x80000000u;
-        }
-        if (t0 + KB - 1 > pos_first || (p.window > 0 && pos_last - t0 >= p.window && t0 + KB > p.sinks)) {
-          // What the row sees as bits, 32 columns a word: two instructions a column.
-          // (Few instructions matter here: those that the steps without a mask do not
-          // run have to be fetched first.)
-          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-          const int hi = pos - t0 + 1;                                // keys c < hi
-          const int lo = p.window > 0 ? pos + 1 - p.window - t0 : 0;  // and c >= lo
-          const int sk = p.window > 0 ? p.sinks - t0 : 0;             // or c < sk
-#pragma unroll
-          for (int c0 = 0; c0 < KB; c0 += 32) {
-            const uint32_t bits = below(hi - c0) & (~below(lo - c0) | below(sk - c0));
-            if (__any_sync(0xffffffffu, bits != ~0u)) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(bits >> c & 1u)) v[c0 + c] = 0xff800000u;  // -inf
-            }
-          }
         }
         float mx[8];
 #pragma unroll
@@ -697,31 +731,31 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
       const float inv = none ? 0.0f : vscale / l;
       const int64_t row = (int64_t)w.first + tk;
       const int rr = xt * 128 + r;
-      uint8_t* dst;
+      uint8_t* dst = nullptr;
       if (w.whole) {
-        const int head = h0 + hh;
-        if (stored && p.lse) p.lse[row * p.nq + head] = none ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994531f;
-        dst = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + (int64_t)head * D);
+        const int head = w.h0 + hh;
+        if (stored) {
+          if (p.lse) p.lse[row * p.nq + head] = none ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994531f;
+          dst = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + (int64_t)head * D);
+        }
         fa *= inv;
         fb *= inv;
       } else {  // a part: weighted values, maximum and sum
-        const int64_t slot_b = slot_base(w.first - w.i * block_tok, w.b, block_tok) + w.i;
-        float* part = p.part + ((slot_b * p.heads + w.hd) * p.nsplit + w.split) * (NT * 128) * (D + 2);
+        const int64_t slot_b = slot_base(p.slots, w.first - w.i * block_tok, w.b) + w.i;
+        float* part = p.part + ((slot_b * p.heads + w.hd) * p.nsplit + w.split) * (C::QTILES * 128) * (D + 2);
         if (stored) {
-          part[(size_t)NT * 128 * D + rr] = m_run;
-          part[(size_t)NT * 128 * (D + 1) + rr] = l;
+          part[(size_t)C::QTILES * 128 * D + rr] = m_run;
+          part[(size_t)C::QTILES * 128 * (D + 1) + rr] = l;
+          dst = reinterpret_cast<uint8_t*>(part + (size_t)rr * D);
         }
-        dst = reinterpret_cast<uint8_t*>(part + (size_t)rr * D);
       }
       // 32 columns at a time: a load from tensor memory takes some 300 cycles beside
       // the other tile's products whatever its size
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
-        if (!none) {
-          tmem_ld_32x32b_x32(t_o + c, o);
-          tmem_ld_wait();
-        }
+        tmem_ld_32x32b_x32(t_o + c, o);
+        tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(fa * __uint_as_float(o[e]));
         if (NT == 2 && w.dual) {
@@ -731,18 +765,36 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(fb, __uint_as_float(y[e]), __uint_as_float(o[e])));
         }
-        if (stored && w.whole) {
+        int pieces = 8;  // 16-byte pieces of o
+        if (w.whole) {
+          pieces = 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            reinterpret_cast<uint4*>(dst + 2 * c)[k] =
-                make_uint4(pack_bf16(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
-                           pack_bf16(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
-                           pack_bf16(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
-                           pack_bf16(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
-        } else if (stored) {
+          for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+        }
+        if constexpr (C::STAGED) {
+          const int k0 = w.whole ? (c & 32) >> 3 : 0;  // piece of the 128 bytes
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            reinterpret_cast<uint4*>(dst + 4 * c)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            if (k < pieces)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + (((k0 + k) ^ (lane & 7)) << 4)) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (w.whole && !(c & 32)) continue;  // not yet full
+          __syncwarp();
+          const int64_t to = reinterpret_cast<int64_t>(dst) + (w.whole ? 2 * (c - 32) : 4 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int y = 4 * k + lane / 8, piece = lane & 7;
+            const int64_t at = __shfl_sync(0xffffffffu, dst ? to : 0, y);
+            const uint4 u = *reinterpret_cast<const uint4*>(stg + y * 128 + ((piece ^ (y & 7)) << 4));
+            if (at) *reinterpret_cast<uint4*>(at + 16 * piece) = u;
+          }
+          __syncwarp();
+        } else if (dst) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < pieces)
+              reinterpret_cast<uint4*>(dst + (w.whole ? 2 : 4) * c)[k] =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
         __syncwarp();
       }
@@ -762,16 +814,22 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
       for (int t = 0, at = 0; ok && (wp = next(t)); give_back(t++)) {
         const int end = at + 2 * wp->nk * NE;
         for (; ok && at < end; ++at) {
-          const int s = at % NST;
-          if (!(ok = wait_all(&raw_full[s], (uint32_t)((at / NST) & 1)))) break;
-          // 32 rows of the tile, their codes in the upper half of their space
+          const int s = at % NST, rs = at % C::LAND;
+          if (!(ok = wait_all(&raw_full[rs], (uint32_t)((at / C::LAND) & 1)))) break;
+          // 32 rows of the tile; their codes in a ring of their own, or in the upper half of their space
           uint8_t* mine = ring + s * C::EB + cw * 4096;
+          const uint8_t* codes = RAW_RING ? raw + rs * (C::EB / 2) + cw * 2048 : mine + 2048;
           uint4 c[EC / 64][4];
 #pragma unroll
           for (int cb = 0; cb < EC / 64; ++cb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              c[cb][k] = *reinterpret_cast<const uint4*>(mine + cb * SUB + 2048 + (lane + 32 * k) * 16);
+              c[cb][k] = *reinterpret_cast<const uint4*>(codes + cb * (RAW_RING ? KB * 64 : SUB) + (lane + 32 * k) * 16);
+          if (RAW_RING) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[rs]);
+            if (!(ok = wait_all(&empty[s], (uint32_t)((at / NST) & 1) ^ 1u))) break;
+          }
           __syncwarp();
 #pragma unroll
           for (int cb = 0; cb < EC / 64; ++cb)
@@ -806,13 +864,13 @@ __global__ void __launch_bounds__(Cfg<D, SRC>::THREADS, 1)
 
 // Joins the parts of split blocks, a warp a row and head, in the parts' order.
 template <int D>
-__global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p) {
-  constexpr int NT = D <= 128 ? 2 : 1, V = D / 64;
+__global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p, int tiles) {
+  constexpr int V = D / 64;
   const int lane = threadIdx.x & 31;
   const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (id >= p.seq.rows * p.nq) return;
   const int row = (int)(id / p.nq), head = (int)(id % p.nq);
-  const int block_tok = NT * p.tok;
+  const int block_tok = tiles * p.tok;
   const int b = find_row(p.seq, row, lane);
   bool bad = false;
   const SeqSpan s = seq_span(p.seq, b, (int64_t)p.max_pages * p.page_size, &bad);
@@ -826,11 +884,11 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p) {
   const int g = head / p.hpg, hc = (head - g * p.hpg) / p.ht, hh = head - g * p.hpg - hc * p.ht;
   const int rr = tk / p.tok * 128 + tk % p.tok * p.ht + hh;
   const int hd = g * p.chunks + hc;
-  const size_t size = (size_t)NT * 128 * (D + 2);
-  const float* base = p.part + ((int64_t)(slot_base(s.first, b, block_tok) + i) * p.heads + hd) * p.nsplit * size;
+  const size_t size = (size_t)tiles * 128 * (D + 2);
+  const float* base = p.part + ((int64_t)(slot_base(p.slots, s.first, b) + i) * p.heads + hd) * p.nsplit * size;
   // all lanes look at the parts' maxima, 32 at a time
   float top = -INFINITY;
-  for (int q = lane; q < parts; q += 32) top = fmaxf(top, __ldcg(base + q * size + (size_t)NT * 128 * D + rr));
+  for (int q = lane; q < parts; q += 32) top = fmaxf(top, __ldcg(base + q * size + (size_t)tiles * 128 * D + rr));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top == -INFINITY ? 0.0f : top;
@@ -841,8 +899,8 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p) {
 #pragma unroll 4
   for (int q = 0; q < parts; ++q) {
     const float* src = base + q * size;
-    const float w = ex2_fast(__ldcg(src + (size_t)NT * 128 * D + rr) - ref);
-    sum = fmaf(w, __ldcg(src + (size_t)NT * 128 * (D + 1) + rr), sum);
+    const float w = ex2_fast(__ldcg(src + (size_t)tiles * 128 * D + rr) - ref);
+    sum = fmaf(w, __ldcg(src + (size_t)tiles * 128 * (D + 1) + rr), sum);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float2 y = __ldcg(reinterpret_cast<const float2*>(src + (size_t)rr * D) + lane + 32 * v);
@@ -872,15 +930,13 @@ bool map_cache(CUtensorMap* m, const void* ptr, const VarFwdArgs& a, int box_tok
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int SRC>
+template <int D, int SRC, bool FEW>
 cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStream_t st) {
-  using C = Cfg<D, SRC>;
+  using C = Cfg<D, SRC, FEW>;
   static_assert(C::SMEM + 900 + (C::NT == 2 ? 1024 : 0) <= 232448, "shared memory");
-  const int block_tok = C::NT * p.tok;
-  const int64_t slots = a.seq.rows / block_tok + a.seq.batch;
-  const int64_t units = slots * p.heads;
+  p.slots = make_slots(a.seq, C::QTILES * p.tok);
+  const int64_t units = p.slots.count * p.heads;
   if (units > 0x7fffffff / 2) return cudaErrorInvalidConfiguration;
-  p.slots = (int)slots;
   p.nsplit = 1;
   if (SRC != PACKED && a.part && units * 2 <= num_sms) {
     const int most = num_sms < VAR_MAX_PARTS ? num_sms : VAR_MAX_PARTS;
@@ -900,20 +956,24 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
     ok = ok && map_cache(&mk, a.k_cache, a, p.box) && map_cache(&mv, a.v_cache, a, p.box);
   }
   if (!ok) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<var_fwd_kernel<D, SRC>>(C::SMEM);
-  if (e == cudaSuccess) e = check_regs<var_fwd_kernel<D, SRC>>(C::THREADS, C::SOFTMAX_REGS > 0 ? C::REGS : 0);
+  cudaError_t e = allow_smem<var_fwd_kernel<D, SRC, FEW>>(C::SMEM);
+  if (e == cudaSuccess) e = check_regs<var_fwd_kernel<D, SRC, FEW>>(C::THREADS, C::SOFTMAX_REGS > 0 ? C::REGS : 0);
   if (e != cudaSuccess) return e;
-  var_fwd_kernel<D, SRC><<<p.units < num_sms ? p.units : num_sms, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
+  var_fwd_kernel<D, SRC, FEW><<<p.units < num_sms ? p.units : num_sms, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
-  var_join_kernel<D><<<(unsigned)((a.seq.rows * a.nq + 7) / 8), 256, 0, st>>>(p);
+  var_join_kernel<D><<<(unsigned)((a.seq.rows * a.nq + 7) / 8), 256, 0, st>>>(p, C::QTILES);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStream_t st) {
-  if (!a.paged) return launch_one<D, PACKED>(p, a, num_sms, st);
-  return a.e4m3 ? launch_one<D, PAGED_F8>(p, a, num_sms, st) : launch_one<D, PAGED>(p, a, num_sms, st);
+  if (!a.paged) return launch_one<D, PACKED, false>(p, a, num_sms, st);
+  // sequences of at most one tile of rows on average
+  constexpr bool CAN = D <= 128;
+  if (CAN && a.seq.rows <= (int64_t)a.seq.batch * p.tok)
+    return a.e4m3 ? launch_one<D, PAGED_F8, CAN>(p, a, num_sms, st) : launch_one<D, PAGED, CAN>(p, a, num_sms, st);
+  return a.e4m3 ? launch_one<D, PAGED_F8, false>(p, a, num_sms, st) : launch_one<D, PAGED, false>(p, a, num_sms, st);
 }
 
 }  // namespace

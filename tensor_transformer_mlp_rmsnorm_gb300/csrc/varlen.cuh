@@ -38,22 +38,35 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqRows& s, int b, int64_t cap
   return r;
 }
 
-// First of the block slots of sequence b: its blocks of `tokens` rows have the
-// slots base + i.  Slots of different sequences are different, because
-// first[b+1] >= first[b] + count[b]; there are rows / tokens + batch of them.
-__device__ __forceinline__ int slot_base(int first, int b, int tokens) { return first / tokens + b; }
+// Block slots: every block of `tokens` rows of every sequence has one of its own,
+// slot(b) + i, found from either side without looking at the other sequences.
+// Sequences of the same number of rows, and a single one: per_seq slots each.
+// Else slot(b) = first[b] / tokens + b: those of different sequences are
+// different, because first[b+1] >= first[b] + count[b].
+struct Slots {
+  int tokens, per_seq;  // per_seq 0: by rows
+  int64_t count;
+};
+inline Slots make_slots(const SeqRows& s, int tokens) {
+  Slots r;
+  r.tokens = tokens;
+  const int64_t rows = s.batch == 1 ? s.rows : s.cu_rows ? 0 : s.rows_per_seq;
+  r.per_seq = (int)((rows + tokens - 1) / tokens);
+  r.count = r.per_seq > 0 ? (int64_t)r.per_seq * s.batch : s.rows / tokens + s.batch;
+  return r;
+}
+__device__ __forceinline__ int slot_base(const Slots& t, int first, int b) {
+  return t.per_seq > 0 ? b * t.per_seq : first / t.tokens + b;
+}
 
 // The sequence whose slots hold `slot`, by the lanes of one warp: a search with
 // 32 probes a step.  Returns the last b whose base does not exceed the slot.
-__device__ __forceinline__ int find_slot(const SeqRows& s, int slot, int tokens, int lane) {
+__device__ __forceinline__ int find_slot(const SeqRows& s, const Slots& t, int slot, int lane) {
+  if (t.per_seq > 0) return slot / t.per_seq;
   int lo = 0, hi = s.batch;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, b = lo + lane * step;
-    bool le = false;
-    if (b < hi) {
-      const int first = s.cu_rows ? min(max(s.cu_rows[b], 0), (int)s.rows) : b * s.rows_per_seq;
-      le = slot_base(first, b, tokens) <= slot;
-    }
+    const bool le = b < hi && slot_base(t, min(max(s.cu_rows[b], 0), (int)s.rows), b) <= slot;
     const int n = __popc(__ballot_sync(0xffffffffu, le));
     lo += max(n - 1, 0) * step;
     hi = min(hi, lo + step);
