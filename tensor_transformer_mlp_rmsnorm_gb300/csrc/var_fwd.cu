@@ -600,30 +600,6 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
           if (!ok) break;
           fence_proxy_async_smem();
         }
-        if (t0 + KB - 1 > pos_first || (p.window > 0 && pos_last - t0 >= p.window && t0 + KB > p.sinks)) {
-          // Hidden scores are overwritten in place, 32 columns at a time and only where a
-          // row of the warp has any.  A short loop, because instructions that most steps
-          // do not run have to be fetched first: with all 128 columns unrolled the masked
-          // step took 2500 cycles longer than the others' 460 up to the maximum.
-          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-          const int hi = pos - t0 + 1;                                // keys c < hi
-          const int lo = p.window > 0 ? pos + 1 - p.window - t0 : 0;  // and c >= lo
-          const int sk = p.window > 0 ? p.sinks - t0 : 0;             // or c < sk
-          const uint32_t hidden = p.negate ? 0x7f800000u : 0xff800000u;
-#pragma unroll 1
-          for (int c0 = 0; c0 < KB; c0 += 32) {
-            const uint32_t bits = below(hi - c0) & (~below(lo - c0) | below(sk - c0));
-            if (!__any_sync(0xffffffffu, bits != ~0u)) continue;
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(t_s + c0, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(bits >> c & 1u)) o[c] = hidden;
-            tmem_st_32x32b_x32(t_s + c0, o);
-          }
-          tmem_st_wait();
-        }
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
@@ -631,6 +607,23 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         if (p.negate) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) v[c] ^= 0x80000000u;
+        }
+        if (t0 + KB - 1 > pos_first || (p.window > 0 && pos_last - t0 >= p.window && t0 + KB > p.sinks)) {
+          // What the row sees as bits, 32 columns a word: two instructions a column, and
+          // none for the words that every row of the warp sees whole.
+          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+          const int hi = pos - t0 + 1;                                // keys c < hi
+          const int lo = p.window > 0 ? pos + 1 - p.window - t0 : 0;  // and c >= lo
+          const int sk = p.window > 0 ? p.sinks - t0 : 0;             // or c < sk
+#pragma unroll
+          for (int c0 = 0; c0 < KB; c0 += 32) {
+            const uint32_t bits = below(hi - c0) & (~below(lo - c0) | below(sk - c0));
+            if (__any_sync(0xffffffffu, bits != ~0u)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(bits & (1u << c))) v[c0 + c] = 0xff800000u;  // -inf
+            }
+          }
         }
         float mx[8];
 #pragma unroll
