@@ -9,6 +9,7 @@
 #include "f32x2.cuh"
 #include "ptx_sm103.cuh"
 #include "varlen.cuh"
+#include "vec.cuh"
 
 namespace tpmlp {
 namespace {
@@ -40,21 +41,21 @@ struct Cfg {
   // the row work all the same), heads of 256 no room for a third step's rows.
   static constexpr int NS = ROLE == DKV || (D == 256 && HAS_DP) ? 1 : 2;
   // ring stages of the streamed operands, in steps
-  static constexpr int S1 = D == 64 ? 4 : NS == 1 && D == 256 ? 2 : 3;
+  static constexpr int S1 = D == 64 ? 4 : D == 128 ? 3 : 2;
   static constexpr int S2 = D == 64 ? 4 : NS == 1 && D == 256 ? 1 : 2;
   static constexpr int N1 = S1 * NE, N2 = S2 * NE;
-  // tensor memory: scores, dP, accumulators
   static constexpr uint32_t T_DP = KB == 128 && ROLE != DKV ? 256 : 128;
   static constexpr uint32_t T_ACC = KB == 128 && ROLE != DKV ? 384 : 256;
   static constexpr int TWICE = 256 / KB;
-  static constexpr uint32_t TILES = NRES * RB + (N1 + N2) * EB;
+  // Results are turned in shared memory, 64 bytes of a row at a time, where there is room.
+  static constexpr bool STAGED = !(D == 256 && HAS_DP) && D != 128;
+  static constexpr uint32_t STAGE = STAGED ? 8 * 2048 : 0;
+  static constexpr uint32_t TILES = NRES * RB + (N1 + N2) * EB + STAGE;
+  static constexpr int READERS = ROLE == DQ ? 10 : 11;  // warps that a block is handed to
 };
 
 struct BwdParams {
   SeqRows seq;
-  const __nv_bfloat16 *out, *dout;
-  int64_t ld_out, ld_dout;
-  const float* lse;
   float2* stats;  // base-2 log-sum-exp and D of each row and head
   __nv_bfloat16 *dq, *dk, *dv;
   int64_t ld_dq, ld_dk, ld_dv;
@@ -62,7 +63,7 @@ struct BwdParams {
   int ht, chunks, tok;     // DQ: heads and tokens of a tile of 128 rows
   int sht, schunks, stok;  // the others: of a step
   Slots slots;
-  int heads;
+  int heads, units;
   bool by_length;
   float scale, scale_log2;
   int window, sinks;
@@ -70,24 +71,27 @@ struct BwdParams {
 };
 
 struct BwdBlock {
-  int b;                 // < 0: none
+  int b;                 // NONE: no more
+  int g, h0, nh;         // key head, first query head, query heads
   int first, count;      // rows of the sequence
-  int at, n;             // first token of the block, steps
+  int at, n, pre;        // first token of the block, steps, of which before the gradient's (DQ)
   int sink_tiles, win_tile, lo, end, sink_end;  // DQ: as in the forward, in tiles of KB keys
 };
+constexpr int NONE = -2;
 
 // Shared memory behind the tiles.
 template <int D, int ROLE>
 struct Aux {
   using C = Cfg<D, ROLE>;
-  uint64_t r_full, full1[C::N1], empty1[C::N1], full2[C::N2], empty2[C::N2], s_full[2], p_full[2], dp_full, ds_full,
-      stat_full[2], stat_empty[2], acc_full, drain;
-  BwdBlock blk;
+  uint64_t r_full, r_empty, full1[C::N1], empty1[C::N1], full2[C::N2], empty2[C::N2], s_full[2], p_full[2], dp_full,
+      ds_full, stat_full[2], stat_empty[2], acc_full, sums[2], work_full[2], work_empty[2], drain;
+  BwdBlock work[2];
   uint32_t tmem;
   int abort;
-  alignas(16) float nlse2[2][ROLE == DQ ? 4 : C::KB];  // the streamed rows' statistics, negated
+  alignas(16) float nlse2[2][ROLE == DQ ? 4 : C::KB];    // the streamed rows' statistics, negated
   alignas(16) float nd[2][ROLE == DQ ? 4 : C::KB];
-  alignas(16) float4 row[ROLE == DQ ? 128 : 1];       // DQ: sums of the rows that stay
+  float2 row[ROLE == DQ ? 128 : 1];                      // DQ: sums of the rows that stay, and dref
+  float row_ref[ROLE == DQ ? 128 : 1];
 };
 
 template <int D, int ROLE>
@@ -109,14 +113,11 @@ __global__ void __launch_bounds__(384, 1)
   }
   volatile int* abort_flag = &x.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)(blockIdx.x / p.heads), hd = (int)(blockIdx.x % p.heads);
-  const int g = Q_STAYS ? hd / p.chunks : hd;                             // key head
-  const int h0 = Q_STAYS ? g * p.hpg + hd % p.chunks * p.ht : g * p.hpg;  // first query head
-  const int nh = Q_STAYS ? min(p.ht, (g + 1) * p.hpg - h0) : p.hpg;
   const int block_tok = Q_STAYS ? p.tok : 128;
 
   if (threadIdx.x == 0) {
     mbar_init(&x.r_full, 1);
+    mbar_init(&x.r_empty, 1);
     for (int i = 0; i < N1; ++i) {
       mbar_init(&x.full1[i], 1);
       mbar_init(&x.empty1[i], 1);
@@ -130,6 +131,9 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&x.p_full[i], 8);
       mbar_init(&x.stat_full[i], 1);
       mbar_init(&x.stat_empty[i], 8);
+      mbar_init(&x.sums[i], 8);
+      mbar_init(&x.work_full[i], 1);
+      mbar_init(&x.work_empty[i], C::READERS);
     }
     mbar_init(&x.dp_full, 1);
     mbar_init(&x.ds_full, 8);
@@ -142,11 +146,6 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_desc(&map_x1);
     tma_prefetch_desc(&map_x2);
   }
-  if (blockIdx.x == 0) {
-    bool bad = false;
-    for (int b = threadIdx.x; b < p.seq.batch; b += blockDim.x) seq_span(p.seq, b, -1, &bad);
-    if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
-  }
   // Rows of a step that no copy fills: the products run over them, so they hold zeros.
   if (!Q_STAYS) {
     const int used = p.sht * p.stok;
@@ -157,51 +156,6 @@ __global__ void __launch_bounds__(384, 1)
       }
   }
   fence_proxy_async_smem();
-  if (warp == 2) {
-    int b, i = 0;
-    if (p.by_length) {
-      const int most = p.window > 0 ? (p.window + block_tok) / KB + 2 + (Q_STAYS ? (p.sinks + KB - 1) / KB : 0) : 0x7fffffff;
-      ByLength<KB> order;
-      order.init(p.seq, -1, block_tok, most, lane);
-      order.find(rank, lane, &b, &i);
-    } else {
-      b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
-      i = -1;  // below
-    }
-    if (lane == 0) {
-      BwdBlock k;
-      k.b = -1;
-      k.n = 0;
-      if (b >= 0) {
-        bool bad = false;
-        const SeqSpan s = seq_span(p.seq, b, -1, &bad);
-        if (i < 0) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
-        if (i >= 0 && (int64_t)i * block_tok < s.count) {
-          // key blocks from the first on are the long ones
-          if (!Q_STAYS) i = (s.count - 1) / block_tok - i;
-          k.b = b;
-          k.first = s.first;
-          k.count = s.count;
-          k.at = i * block_tok;
-          if (Q_STAYS) {
-            k.end = min(k.at + block_tok, s.count);
-            k.lo = p.window > 0 ? max(0, k.at + 1 - p.window) : 0;
-            k.sink_end = min(p.sinks, k.lo);
-            k.win_tile = k.lo / KB;
-            k.sink_tiles = min((k.sink_end + KB - 1) / KB, k.win_tile);
-            k.n = k.sink_tiles + (k.end + KB - 1) / KB - k.win_tile;
-          } else {
-            // the tokens [at, end) see keys of the block
-            const int last = min(k.at + block_tok, s.count) - 1;
-            k.end = p.window > 0 && k.at >= p.sinks ? (int)min((int64_t)s.count, (int64_t)last + p.window) : s.count;
-            k.lo = k.sink_end = k.win_tile = k.sink_tiles = 0;
-            k.n = (k.end - k.at + p.stok - 1) / p.stok * p.schunks;
-          }
-        }
-      }
-      x.blk = k;
-    }
-  }
   if (warp == 1) {
     tmem_alloc(&x.tmem, 512);
     tmem_relinquish();
@@ -210,20 +164,22 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = x.tmem;
-  const BwdBlock blk = x.blk;
-  // DQ: D = dO . O takes the output as it was rounded.  For tokens that see few
-  // others D is as large as what it is taken from, and that rounding would be a
-  // good part of a small gradient (dq off by 0.0026 of its norm where its own
-  // rounding is 0.0017).  Blocks of few steps run over their keys once more,
-  // before, for D = sum P dP: with 256 keys or more the rounding is averaged out.
-  const int pre = Q_STAYS && blk.n <= C::TWICE ? blk.n : 0;
-  const int nk = blk.n + pre;
-  auto tile_of = [&](int n) -> int {
-    const int j = n < pre ? n : n - pre;
-    return j < blk.sink_tiles ? j : j - blk.sink_tiles + blk.win_tile;
+  // Step n of a block, n < pre: of the run before the gradient's
+  auto tile_of = [](const BwdBlock& k, int n) -> int {
+    const int j = n < k.pre ? n : n - k.pre;
+    return j < k.sink_tiles ? j : j - k.sink_tiles + k.win_tile;
   };
   auto wait_all = [&](uint64_t* bar, uint32_t par) -> int {
     return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS));
+  };
+  // The t-th block of this CTA, in shared memory until it is given back; null behind the last.
+  auto next = [&](int t) -> const BwdBlock* {
+    if (!wait_all(&x.work_full[t & 1], (uint32_t)((t >> 1) & 1))) return nullptr;
+    return x.work[t & 1].b == NONE ? nullptr : &x.work[t & 1];
+  };
+  auto give_back = [&](int t) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&x.work_empty[t & 1]);
   };
   // where dS goes: over the scores, with two score buffers; else over dP
   constexpr bool DS_OVER_S = NS == 2;
@@ -232,50 +188,59 @@ __global__ void __launch_bounds__(384, 1)
 
   if (warp < 4) {
   regs_dec<ISSUE_REGS>();
-  if (warp == 0 && nk > 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      uint32_t armed[2] = {0, 0}, par_armed[2] = {0, 0};
-      bool ok = true;
-      const uint32_t rows = Q_STAYS ? p.ht * p.tok : 128;
-      mbar_arrive_expect_tx(&x.r_full, C::NRES * (D / 64) * rows * 128);
-      for (int o = 0; o < C::NRES; ++o)
-        for (int t = 0; t < D / 64; ++t)
-          tma_load_3d(smem + o * C::RB + t * C::RSUB, o ? &map_r2 : &map_r1, &x.r_full, 64 * t, Q_STAYS ? h0 : g,
-                      blk.first + blk.at);
-      const uint32_t bytes = (uint32_t)(Q_STAYS ? KB : p.sht * p.stok) * EC * 2;
-      for (int n = 0; ok && n < nk; ++n) {
-        const int c1 = Q_STAYS ? g : h0 + n % p.schunks * p.sht;
-        const int c2 = blk.first + (Q_STAYS ? tile_of(n) * KB : blk.at + n / p.schunks * p.stok);
-        for (int o = 0; ok && o < 2; ++o) {
-          const int stages = o ? N2 : N1;
-          uint64_t *fb = o ? x.full2 : x.full1, *eb = o ? x.empty2 : x.empty1;
-          uint8_t* ring = o ? ring2 : ring1;
-          for (int e = 0; e < NE; ++e) {
-            const int at = n * NE + e, s = at % stages;
-            const uint32_t par = (uint32_t)((at / stages) & 1);
-            if (!mbar_wait(&eb[s], par ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS)) {
-              ok = false;
-              break;
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    uint32_t armed1 = 0, par1 = 0, armed2 = 0, par2 = 0;
+    bool ok = true;
+    const BwdBlock* kp;
+    int t = 0;
+    for (int c = 0; ok && (kp = next(t)); give_back(t++)) {
+      const BwdBlock& k = *kp;
+      if (lane == 0) {
+        const uint32_t rows = Q_STAYS ? p.ht * p.tok : 128;
+        const uint32_t bytes = (uint32_t)(Q_STAYS ? KB : p.sht * p.stok) * EC * 2;
+        for (int n = 0; ok && n < k.n; ++n) {
+          const int c1 = Q_STAYS ? k.g : k.h0 + n % p.schunks * p.sht;
+          const int c2 = k.first + (Q_STAYS ? tile_of(k, n) * KB : k.at + n / p.schunks * p.stok);
+          auto load = [&](uint64_t* fb, uint64_t* eb, uint8_t* ring, int stages, const CUtensorMap* map, uint32_t& armed,
+                          uint32_t& pars) -> bool {
+            for (int e = 0; e < NE; ++e) {
+              const int at = (c + n) * NE + e, st = at % stages;
+              const uint32_t par = (uint32_t)((at / stages) & 1);
+              if (!mbar_wait(&eb[st], par ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS)) return false;
+              mbar_arrive_expect_tx(&fb[st], bytes);
+              armed |= 1u << st;
+              pars = (pars & ~(1u << st)) | (par << st);
+              for (int u = 0; u < EC / 64; ++u)
+                tma_load_3d(ring + st * C::EB + u * C::SUB, map, &fb[st], e * EC + 64 * u, c1, c2);
             }
-            mbar_arrive_expect_tx(&fb[s], bytes);
-            armed[o] |= 1u << s;
-            par_armed[o] = (par_armed[o] & ~(1u << s)) | (par << s);
-            for (int t = 0; t < EC / 64; ++t)
-              tma_load_3d(ring + s * C::EB + t * C::SUB, o ? &map_x2 : &map_x1, &fb[s], e * EC + 64 * t, c1, c2);
+            return true;
+          };
+          ok = load(x.full1, x.empty1, ring1, N1, &map_x1, armed1, par1);
+          if (ok && n == 0) {
+            ok = mbar_wait(&x.r_empty, (uint32_t)(t & 1) ^ 1u, abort_flag, p.status, STATUS_TIMEOUT, WAIT_NS);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&x.r_full, C::NRES * (D / 64) * rows * 128);
+            for (int o = 0; o < C::NRES; ++o)
+              for (int u = 0; u < D / 64; ++u)
+                tma_load_3d(smem + o * C::RB + u * C::RSUB, o ? &map_r2 : &map_r1, &x.r_full, 64 * u,
+                            Q_STAYS ? k.h0 : k.g, k.first + k.at);
           }
+          ok = ok && load(x.full2, x.empty2, ring2, N2, &map_x2, armed2, par2);
         }
       }
-      if (!ok || *abort_flag) {  // copies still in flight land on the barriers armed last
-        int no_abort = 0;
-        mbar_wait(&x.r_full, 0, &no_abort, p.status, 0u, DRAIN_NS);
-        for (int o = 0; o < 2; ++o)
-          for (int s = 0; s < (o ? N2 : N1); ++s)
-            if (armed[o] & (1u << s))
-              mbar_wait(o ? &x.full2[s] : &x.full1[s], (par_armed[o] >> s) & 1u, &no_abort, p.status, 0u, DRAIN_NS / 16);
-      }
+      ok = __all_sync(0xffffffffu, ok);
+      c += k.n;
     }
-  } else if (warp == 1 && nk > 0) {
+    if (lane == 0 && (!ok || *abort_flag)) {  // copies still in flight land on the barriers armed last
+      int no_abort = 0;
+      if (t > 0 || armed1) mbar_wait(&x.r_full, (uint32_t)((t > 0 ? t - 1 : 0) & 1), &no_abort, p.status, 0u, DRAIN_NS);
+      for (int st = 0; st < N1; ++st)
+        if (armed1 & (1u << st)) mbar_wait(&x.full1[st], (par1 >> st) & 1u, &no_abort, p.status, 0u, DRAIN_NS / 16);
+      for (int st = 0; st < N2; ++st)
+        if (armed2 & (1u << st)) mbar_wait(&x.full2[st], (par2 >> st) & 1u, &no_abort, p.status, 0u, DRAIN_NS / 16);
+    }
+  } else if (warp == 1) {
     // ---------------------------------------------------------------- issuer
     // A wait costs the tensor core a gap of some 150 cycles where nothing is
     // queued: there is one on the row groups a step and gradient, and the
@@ -306,147 +271,244 @@ __global__ void __launch_bounds__(384, 1)
     };
     // accumulator at `acc` += (bf16 rows, each row group's half at the start of
     // its half of the columns from `a_col` on) times the streamed operand
-    auto accumulate = [&](int stages, uint64_t xm, int n, uint32_t a_col, uint32_t acc) {
+    auto accumulate = [&](int stages, uint64_t xm, int n, uint32_t a_col, uint32_t acc, bool first) {
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
         const uint64_t b = desc_advance(xm, ((n * NE + e) % stages) * C::EB);
 #pragma unroll
         for (int kk = 0; kk < KB / 16; ++kk)
           tc_mma_f16_ts(tmem_base + acc + e * EC, tmem_base + a_col + kk / (HC / 16) * HC + kk % (HC / 16) * 8,
-                        desc_advance(b, kk * 2048), IDESC_A, n > pre || kk > 0 ? 1u : 0u);
+                        desc_advance(b, kk * 2048), IDESC_A, !first || kk > 0 ? 1u : 0u);
       }
     };
     auto release = [&](uint64_t* bars, int stages, int n) {
 #pragma unroll
       for (int e = 0; e < NE; ++e) tc_commit(&bars[(n * NE + e) % stages]);
     };
-    auto put_s = [&](int n) {
-      product(0, N1, x1k, n, s_col(n));
-      tc_commit(&x.s_full[NS == 2 ? n & 1 : 0]);
-      if (!C::HAS_DP) release(x.empty1, N1, n);
-    };
-    auto put_dp = [&](int n) {
-      product(1, N2, x2k, n, C::T_DP);
-      tc_commit(&x.dp_full);
-      if (!C::HAS_PV) release(x.empty2, N2, n);
-    };
-    auto put_acc = [&](int n) {  // dS X1
-      if (n >= pre) accumulate(N1, x1m, n, ds_col(n), C::T_ACC);
-      release(x.empty1, N1, n);
-      if (n + 1 == nk) tc_commit(&x.acc_full);
-    };
-    auto put_pv = [&](int n) {  // P X2
-      accumulate(N2, x2m, n, s_col(n), C::T_ACC + (ROLE == DKV ? D : 0));
-      release(x.empty2, N2, n);
-      if (!C::HAS_DP && n + 1 == nk) tc_commit(&x.acc_full);
-    };
-    int ok = wait_all(&x.r_full, 0) && wait_elems(x.full1, N1, 0);
-    if (ok && C::HAS_DP) ok = wait_elems(x.full2, N2, 0);
-    tc_fence_after();
-    if (ok && elect_one()) {
-      put_s(0);
-      if (C::HAS_DP) put_dp(0);
-    }
-    __syncwarp();
-    if (ok && NS == 2 && nk > 1 && (ok = wait_elems(x.full1, N1, 1))) {
+    bool ok = true;
+    const BwdBlock* kp;
+    for (int t = 0, c = 0; ok && (kp = next(t)); give_back(t++)) {
+      const int nk = kp->n, pre = kp->pre;
+      // steps of this block; in the rings and barriers they count on from the blocks before
+      auto put_s = [&](int n) {
+        product(0, N1, x1k, c + n, s_col(c + n));
+        tc_commit(&x.s_full[NS == 2 ? (c + n) & 1 : 0]);
+        if (!C::HAS_DP) {
+          release(x.empty1, N1, c + n);
+          if (n + 1 == nk) tc_commit(&x.r_empty);
+        }
+      };
+      auto put_dp = [&](int n) {  // the last product of the operands that stay
+        product(1, N2, x2k, c + n, C::T_DP);
+        tc_commit(&x.dp_full);
+        if (!C::HAS_PV) release(x.empty2, N2, c + n);
+        if (n + 1 == nk) tc_commit(&x.r_empty);
+      };
+      auto put_acc = [&](int n) {  // dS X1
+        if (n >= pre) accumulate(N1, x1m, c + n, ds_col(c + n), C::T_ACC, n == pre);
+        release(x.empty1, N1, c + n);
+        if (n + 1 == nk) tc_commit(&x.acc_full);
+      };
+      auto put_pv = [&](int n) {  // P X2
+        accumulate(N2, x2m, c + n, s_col(c + n), C::T_ACC + (ROLE == DKV ? D : 0), n == 0);
+        release(x.empty2, N2, c + n);
+        if (!C::HAS_DP && n + 1 == nk) tc_commit(&x.acc_full);
+      };
+      auto have1 = [&](int n) -> bool { return wait_elems(x.full1, N1, c + n); };
+      auto have2 = [&](int n) -> bool { return wait_elems(x.full2, N2, c + n); };
+      ok = have1(0) && wait_all(&x.r_full, (uint32_t)(t & 1));
+      if (ok && C::HAS_DP) ok = have2(0);
       tc_fence_after();
-      if (elect_one()) put_s(1);
+      if (ok && elect_one()) {
+        put_s(0);
+        if (C::HAS_DP) put_dp(0);
+      }
       __syncwarp();
-    }
-    for (int n = 0; ok && n < nk; ++n) {
-      const uint32_t par = (uint32_t)(n & 1);
-      const bool n1 = n + 1 < nk, n2 = n + 2 < nk;
-      if constexpr (C::HAS_DP && !C::HAS_PV && NS == 2) {
-        // dP_{n+1}, then dS_n X1 and S_{n+2} while the row groups turn dP_{n+1} into dS
-        if (n1 && !(ok = wait_elems(x.full2, N2, n + 1))) break;
-        if (!(ok = wait_all(&x.ds_full, par))) break;
+      if (ok && NS == 2 && nk > 1 && (ok = have1(1))) {
         tc_fence_after();
-        if (elect_one()) {
-          if (n1) put_dp(n + 1);
-          put_acc(n);
-        }
-        __syncwarp();
-        if (n2) {  // its rows come into the place of step n - 1's
-          if (!(ok = wait_elems(x.full1, N1, n + 2))) break;
-          tc_fence_after();
-          if (elect_one()) put_s(n + 2);
-          __syncwarp();
-        }
-      } else if constexpr (C::HAS_DP && !C::HAS_PV) {
-        if (n1) {
-          if (!(ok = wait_elems(x.full1, N1, n + 1) && wait_all(&x.p_full[0], par))) break;  // the scores are read
-          tc_fence_after();
-          if (elect_one()) put_s(n + 1);
-          __syncwarp();
-        }
-        if (!(ok = wait_all(&x.ds_full, par))) break;
-        tc_fence_after();
-        if (elect_one()) put_acc(n);
-        __syncwarp();
-        if (n1) {
-          if (!(ok = wait_elems(x.full2, N2, n + 1))) break;
-          tc_fence_after();
-          if (elect_one()) put_dp(n + 1);
-          __syncwarp();
-        }
-      } else if constexpr (C::HAS_DP) {
-        // dV_n and S_{n+1} under the row groups' dS_n, dK_n and dP_{n+1} under their P_{n+1}
-        if (n1 && !(ok = wait_elems(x.full1, N1, n + 1))) break;
-        if (!(ok = wait_all(&x.p_full[0], par))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          put_pv(n);
-          if (n1) put_s(n + 1);
-        }
-        __syncwarp();
-        if (n1 && !(ok = wait_elems(x.full2, N2, n + 1))) break;
-        if (!(ok = wait_all(&x.ds_full, par))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          put_acc(n);
-          if (n1) put_dp(n + 1);
-        }
-        __syncwarp();
-      } else {
-        if (n2 && !(ok = wait_elems(x.full1, N1, n + 2))) break;
-        if (!(ok = wait_elems(x.full2, N2, n) && wait_all(&x.p_full[n & 1], (uint32_t)((n >> 1) & 1)))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          put_pv(n);
-          if (n2) put_s(n + 2);
-        }
+        if (elect_one()) put_s(1);
         __syncwarp();
       }
+#pragma unroll 1
+      for (int n = 0; ok && n < nk; ++n) {
+        const uint32_t par = (uint32_t)((c + n) & 1);
+        const bool n1 = n + 1 < nk, n2 = n + 2 < nk;
+        if constexpr (C::HAS_DP && !C::HAS_PV && NS == 2) {
+          // dP_{n+1}, then dS_n X1 and S_{n+2} while the row groups turn dP_{n+1} into dS
+          if (n1 && !(ok = have2(n + 1))) break;
+          if (!(ok = wait_all(&x.ds_full, par))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (n1) put_dp(n + 1);
+            put_acc(n);
+          }
+          __syncwarp();
+          if (n2) {  // its rows come into the place of step n's
+            if (!(ok = have1(n + 2))) break;
+            tc_fence_after();
+            if (elect_one()) put_s(n + 2);
+            __syncwarp();
+          }
+        } else if constexpr (C::HAS_DP && !C::HAS_PV) {
+          if (n1) {
+            if (!(ok = have1(n + 1) && wait_all(&x.p_full[0], par))) break;  // the scores are read
+            tc_fence_after();
+            if (elect_one()) put_s(n + 1);
+            __syncwarp();
+          } else if (!(ok = wait_all(&x.p_full[0], par))) {  // every phase is seen
+            break;
+          }
+          if (!(ok = wait_all(&x.ds_full, par))) break;
+          tc_fence_after();
+          if (elect_one()) put_acc(n);
+          __syncwarp();
+          if (n1) {
+            if (!(ok = have2(n + 1))) break;
+            tc_fence_after();
+            if (elect_one()) put_dp(n + 1);
+            __syncwarp();
+          }
+        } else if constexpr (C::HAS_DP) {
+          // dV_n and S_{n+1} under the row groups' dS_n, dK_n and dP_{n+1} under their P_{n+1}
+          if (n1 && !(ok = have1(n + 1))) break;
+          if (!(ok = wait_all(&x.p_full[0], par))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            put_pv(n);
+            if (n1) put_s(n + 1);
+          }
+          __syncwarp();
+          if (n1 && !(ok = have2(n + 1))) break;
+          if (!(ok = wait_all(&x.ds_full, par))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            put_acc(n);
+            if (n1) put_dp(n + 1);
+          }
+          __syncwarp();
+        } else {
+          if (n2 && !(ok = have1(n + 2))) break;
+          if (!(ok = have2(n) && wait_all(&x.p_full[(c + n) & 1], (uint32_t)(((c + n) >> 1) & 1)))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            put_pv(n);
+            if (n2) put_s(n + 2);
+          }
+          __syncwarp();
+        }
+      }
+      c += nk;
     }
     if (elect_one()) tc_commit(&x.drain);
     __syncwarp();
     int no_abort = 0;
     mbar_wait(&x.drain, 0, &no_abort, p.status, STATUS_TIMEOUT, DRAIN_NS);
-  } else if (warp == 2 && !Q_STAYS && nk > 0) {
+  } else if (warp == 2) {
     // ---------------------------------------- statistics of the streamed rows
-    int ok = 1;
-    for (int n = 0; ok && n < nk; ++n) {
-      const int st = n & 1;
-      const int tok0 = blk.at + n / p.schunks * p.stok, hc = n % p.schunks * p.sht;
-      float2 v[KB / 32];
+    bool ok = true;
+    const BwdBlock* kp;
+    for (int t = 0, c = 0; !Q_STAYS && ok && (kp = next(t)); give_back(t++)) {
+      const BwdBlock& k = *kp;
+      {
+        for (int n = 0; ok && n < k.n; ++n) {
+          const int st = (c + n) & 1;
+          const int tok0 = k.at + n / p.schunks * p.stok, hc = n % p.schunks * p.sht;
+          float2 v[KB / 32];
 #pragma unroll
-      for (int k = 0; k < KB / 32; ++k) {
-        const int r = lane + 32 * k, tk = tok0 + r / p.sht, hh = hc + r % p.sht;
-        const bool valid = r < p.sht * p.stok && tk < blk.end && hh < p.hpg;
-        v[k] = valid ? __ldg(p.stats + (int64_t)(blk.first + tk) * p.nq + h0 + hh) : make_float2(INFINITY, 0.0f);
+          for (int q = 0; q < KB / 32; ++q) {
+            const int r = lane + 32 * q, tk = tok0 + r / p.sht, hh = hc + r % p.sht;
+            const bool valid = r < p.sht * p.stok && tk < k.end && hh < p.hpg;
+            v[q] = valid ? __ldg(p.stats + (int64_t)(k.first + tk) * p.nq + k.h0 + hh) : make_float2(INFINITY, 0.0f);
+          }
+          if (!(ok = wait_all(&x.stat_empty[st], (uint32_t)(((c + n) >> 1) & 1) ^ 1u))) break;
+#pragma unroll
+          for (int q = 0; q < KB / 32; ++q) {
+            x.nlse2[st][lane + 32 * q] = -v[q].x;
+            x.nd[st][lane + 32 * q] = -v[q].y;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&x.stat_full[st]);
+        }
+        c += k.n;
       }
-      ok = wait_all(&x.stat_empty[st], (uint32_t)((n >> 1) & 1) ^ 1u);
-      if (!ok) break;
-#pragma unroll
-      for (int k = 0; k < KB / 32; ++k) {
-        x.nlse2[st][lane + 32 * k] = -v[k].x;
-        x.nd[st][lane + 32 * k] = -v[k].y;
+    }
+  } else {
+    // ------------------------------------------------------------- scheduler
+    if (blockIdx.x == 0) {  // looks at every sequence, for the report
+      bool bad = false;
+      for (int b = lane; b < p.seq.batch; b += 32) seq_span(p.seq, b, -1, &bad);
+      if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
+    }
+    ByLength<KB> order;
+    if (p.by_length)
+      order.init(p.seq, -1, block_tok,
+                 p.window > 0 ? (p.window + block_tok) / KB + 2 + (Q_STAYS ? (p.sinks + KB - 1) / KB : 0) : 0x7fffffff, lane);
+    bool ok = true;
+    int t = 0;
+    for (int turn = 0; ok; ++turn) {
+      const int64_t u = snake(turn, (int)blockIdx.x, (int)gridDim.x);
+      const bool last = (int64_t)turn * gridDim.x >= p.units;
+      BwdBlock k;
+      k.b = NONE;
+      if (!last) {
+        if (u >= p.units) continue;
+        const int rank = (int)u / p.heads, hd = (int)u % p.heads;
+        k.g = Q_STAYS ? hd / p.chunks : hd;
+        k.h0 = k.g * p.hpg + (Q_STAYS ? hd % p.chunks * p.ht : 0);
+        k.nh = Q_STAYS ? min(p.ht, (k.g + 1) * p.hpg - k.h0) : p.hpg;
+        int b, i = 0;
+        if (p.by_length) {
+          order.find(rank, lane, &b, &i);
+        } else {
+          b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
+          i = -1;  // below
+        }
+        if (b < 0) continue;
+        bool bad = false;
+        const SeqSpan s = seq_span(p.seq, b, -1, &bad);
+        if (i < 0) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
+        if (i < 0 || (int64_t)i * block_tok >= s.count) continue;
+        // key blocks from the first on are the long ones
+        if (!Q_STAYS) i = (s.count - 1) / block_tok - i;
+        k.b = b;
+        k.first = s.first;
+        k.count = s.count;
+        k.at = i * block_tok;
+        k.pre = 0;
+        if (Q_STAYS) {
+          k.end = min(k.at + block_tok, s.count);
+          k.lo = p.window > 0 ? max(0, k.at + 1 - p.window) : 0;
+          k.sink_end = min(p.sinks, k.lo);
+          k.win_tile = k.lo / KB;
+          k.sink_tiles = min((k.sink_end + KB - 1) / KB, k.win_tile);
+          k.n = k.sink_tiles + (k.end + KB - 1) / KB - k.win_tile;
+          // D = dO . O takes the output as it was rounded.  For tokens that see few
+          // others D is as large as what it is taken from, and that rounding would be a
+          // good part of a small gradient (dq off by 0.0026 of its norm where its own
+          // rounding is 0.0017).  Blocks of few steps run over their keys once more,
+          // before, for D = sum P dP: with 256 keys or more the rounding is averaged out.
+          if (k.n <= C::TWICE) k.pre = k.n;
+          k.n += k.pre;
+        } else {
+          // the tokens [at, end) see keys of the block
+          const int end = min(k.at + block_tok, s.count) - 1;
+          k.end = p.window > 0 && k.at >= p.sinks ? (int)min((int64_t)s.count, (int64_t)end + p.window) : s.count;
+          k.lo = k.sink_end = k.win_tile = k.sink_tiles = 0;
+          k.n = (k.end - k.at + p.stok - 1) / p.stok * p.schunks;
+        }
+      }
+      ok = wait_all(&x.work_empty[t & 1], (uint32_t)((t >> 1) & 1) ^ 1u);
+      if (ok && lane == 0) {
+        x.work[t & 1] = k;
+        mbar_arrive(&x.work_full[t & 1]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&x.stat_full[st]);
+      ++t;
+      if (last) break;
     }
   }
-  } else if (regs_inc<ROW_REGS>(), nk > 0) {
+  } else {
+    regs_inc<ROW_REGS>();
     // ------------------------------------------------------------ row groups
     // Both work on every step, each on half of its columns: that halves the
     // time from scores to P and from dP to dS, which the products of the other
@@ -456,69 +518,61 @@ __global__ void __launch_bounds__(384, 1)
     const int r = q4 * 32 + lane;  // row of the accumulators
     const int tid = grp * 128 + r;
     const uint32_t tl = tmem_base + ((uint32_t)(q4 * 32) << 16) + grp * HC;
-    // DQ: this row's token and head; else its key
-    const int tk = Q_STAYS ? blk.at + r / p.ht : blk.at + r;
-    const int hh = Q_STAYS ? r % p.ht : 0;
-    const bool stored = tk < blk.count && (!Q_STAYS || (r < p.ht * p.tok && hh < nh));
-    const int64_t stat_at = (int64_t)(blk.first + tk) * p.nq + h0 + hh;
+    const int tok_r = Q_STAYS ? r / p.ht : r, hh = Q_STAYS ? r - tok_r * p.ht : 0;  // token or key of the row, head
     const uint32_t magic = 65536u / (uint32_t)p.sht + 1u;  // c / sht = c magic >> 16 for c < 128
+    uint8_t* stg = ring2 + N2 * C::EB + (warp - 4) * 2048;
+    uint32_t pres = 0;
+    int ok = 1;
+    const BwdBlock* kp;
+    for (int t = 0, done = 0; ok && (kp = next(t)); give_back(t++)) {
+    const BwdBlock& blk = *kp;
+    const int nk = blk.n, pre = blk.pre, h0 = blk.h0, g = blk.g;
+    const int tk = blk.at + tok_r;
+    const bool stored = tk < blk.count && (!Q_STAYS || (r < p.ht * p.tok && hh < blk.nh));
+    const int64_t stat_at = (int64_t)(blk.first + tk) * p.nq + h0 + hh;
     float lse2 = 0.0f, dsum = 0.0f;
     if (Q_STAYS) {
-      if (stored) lse2 = p.lse[stat_at] * 1.4426950408889634f;
-      if (!pre) {
-        // D = dO . O of 16 rows a warp, D / 8 lanes a row
-        constexpr int LPR = D / 8, RPP = D == 192 ? 1 : 32 / LPR;
-        for (int i = 0; i < 16; i += RPP) {
-          const int rr = (warp - 4) * 16 + i + (RPP > 1 ? lane / LPR : 0);
-          const int c = RPP > 1 ? lane % LPR : lane;
-          const int t = blk.at + rr / p.ht, h = rr % p.ht;
-          float s = 0.0f;
-          if (t < blk.count && rr < p.ht * p.tok && h < nh && c < LPR) {
-            const int64_t row = blk.first + t, col = (int64_t)(h0 + h) * D + 8 * c;
-            const uint4 a = *reinterpret_cast<const uint4*>(p.dout + row * p.ld_dout + col);
-            const uint4 o = *reinterpret_cast<const uint4*>(p.out + row * p.ld_out + col);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, ow[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              s = fmaf(__uint_as_float(aw[k] << 16), __uint_as_float(ow[k] << 16), s);
-              s = fmaf(__uint_as_float(aw[k] & 0xffff0000u), __uint_as_float(ow[k] & 0xffff0000u), s);
-            }
-          }
-#pragma unroll
-          for (int o = (RPP > 1 ? LPR : 32) / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (c == 0) x.row[rr].x = s;
-        }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        dsum = x.row[r].x;
-        if (stored && grp == 0) p.stats[stat_at] = make_float2(lse2, dsum);
+      if (stored) {
+        const float2 z = p.stats[stat_at];
+        lse2 = z.x;
+        if (!pre) dsum = z.y;
       }
     }
-    int ok = 1;
     // The first run over few keys: sum P, and sum P (dP - dref) with dref the
     // dP of the first key that the row sees: exact where it sees no other.
     float l = 0.0f, dref = 0.0f;
     for (int n = 0; n < nk; ++n) {
-      const uint32_t par = (uint32_t)(n & 1), par2 = (uint32_t)((n >> 1) & 1);
-      const int st = n & 1;
+      const int N = done + n;  // as rings and barriers count
+      const uint32_t par = (uint32_t)(N & 1), par2 = (uint32_t)((N >> 1) & 1);
+      const int st = N & 1;
       if (Q_STAYS && pre && n == pre) {  // both groups' sums
-        if (grp == 1) x.row[r] = make_float4(l, dsum, dref, 0.0f);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (grp == 0) {
-          const float4 o = x.row[r];
-          const float all = l + o.x;
-          const float d = l != 0.0f ? dref + (dsum + o.y + (o.x != 0.0f ? o.x * (o.z - dref) : 0.0f)) / all
-                                    : o.z + (o.y + dsum) / all;
-          x.row[r] = make_float4(all, d, 0.0f, 0.0f);
+        auto meet = [&](int i) -> bool {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&x.sums[i]);
+          return wait_all(&x.sums[i], pres & 1u);
+        };
+        if (grp == 1) {
+          x.row[r] = make_float2(l, dsum);
+          x.row_ref[r] = dref;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (!(ok = meet(0))) break;
+        if (grp == 0) {
+          const float2 o = x.row[r];
+          const float ref = x.row_ref[r], all = l + o.x;
+          const float d = l != 0.0f ? dref + (dsum + o.y + (o.x != 0.0f ? o.x * (ref - dref) : 0.0f)) / all
+                                    : ref + (o.y + dsum) / all;
+          x.row[r] = make_float2(all, d);
+        }
+        if (!(ok = meet(1))) break;
+        ++pres;
         lse2 += log2f(x.row[r].x);
         dsum = x.row[r].y;
         if (stored && grp == 0) p.stats[stat_at] = make_float2(lse2, dsum);
       }
       if (!Q_STAYS && !(ok = wait_all(&x.stat_full[st], par2))) break;
-      if (!(ok = wait_all(&x.s_full[NS == 2 ? n & 1 : 0], NS == 2 ? par2 : par))) break;
+      if (!(ok = wait_all(&x.s_full[NS == 2 ? N & 1 : 0], NS == 2 ? par2 : par))) break;
       tc_fence_after();
-      const uint32_t t_s = tl + s_col(n);
+      const uint32_t t_s = tl + s_col(N);
       uint32_t v[HC];
       tmem_ld_32x32b_x32(t_s, *reinterpret_cast<uint32_t(*)[32]>(v));
       tmem_ld_wait();
@@ -537,7 +591,7 @@ __global__ void __launch_bounds__(384, 1)
       bool masked;
       int t0 = 0, tok0 = 0, hc = 0;
       if (Q_STAYS) {
-        const int tile0 = tile_of(n) * KB;
+        const int tile0 = tile_of(blk, n) * KB;
         t0 = tile0 + grp * HC;
         const int last = blk.at + min(p.tok, blk.count - blk.at) - 1;
         masked = t0 + HC - 1 > blk.at || (p.window > 0 && last - t0 >= p.window && t0 + HC > p.sinks);
@@ -549,7 +603,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int cb = 0; cb < EC / 64; ++cb)
 #pragma unroll
                 for (int c = 0; c < CPT; ++c)
-                  *reinterpret_cast<uint4*>(ring1 + ((n * NE + e) % N1) * C::EB + cb * C::SUB + crow * 128 +
+                  *reinterpret_cast<uint4*>(ring1 + ((N * NE + e) % N1) * C::EB + cb * C::SUB + crow * 128 +
                                             (cpart + c) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
@@ -562,7 +616,7 @@ __global__ void __launch_bounds__(384, 1)
         if (cut) {
           if (C::HAS_PV)
             for (int e = 0; ok && e < NE; ++e)
-              ok = wait_all(&x.full2[(n * NE + e) % N2], (uint32_t)(((n * NE + e) / N2) & 1));
+              ok = wait_all(&x.full2[(N * NE + e) % N2], (uint32_t)(((N * NE + e) / N2) & 1));
           if (!ok) break;
           if (crow < p.sht * p.stok && (tok0 + crow / p.sht >= blk.end || hc + crow % p.sht >= p.hpg))
             for (int e = 0; e < NE; ++e)
@@ -571,8 +625,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int c = 0; c < CPT; ++c) {
                   const uint32_t o = cb * C::SUB + crow * 128 + (cpart + c) * 16;
-                  if (C::HAS_DP) *reinterpret_cast<uint4*>(ring1 + ((n * NE + e) % N1) * C::EB + o) = make_uint4(0, 0, 0, 0);
-                  if (C::HAS_PV) *reinterpret_cast<uint4*>(ring2 + ((n * NE + e) % N2) * C::EB + o) = make_uint4(0, 0, 0, 0);
+                  if (C::HAS_DP) *reinterpret_cast<uint4*>(ring1 + ((N * NE + e) % N1) * C::EB + o) = make_uint4(0, 0, 0, 0);
+                  if (C::HAS_PV) *reinterpret_cast<uint4*>(ring2 + ((N * NE + e) % N2) * C::EB + o) = make_uint4(0, 0, 0, 0);
                 }
           fence_proxy_async_smem();
         }
@@ -635,7 +689,7 @@ __global__ void __launch_bounds__(384, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&x.p_full[NS == 2 ? n & 1 : 0]);
+        if (lane == 0) mbar_arrive(&x.p_full[NS == 2 ? N & 1 : 0]);
       }
       if (C::HAS_DP) {
         if (!(ok = wait_all(&x.dp_full, par))) break;
@@ -682,8 +736,8 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         if (!Q_STAYS || n >= pre) {
-          if constexpr (HC == 64) tmem_st_32x32b_x32(tl + ds_col(n), w);
-          else tmem_st_32x32b_x16(tl + ds_col(n), w);
+          if constexpr (HC == 64) tmem_st_32x32b_x32(tl + ds_col(N), w);
+          else tmem_st_32x32b_x16(tl + ds_col(N), w);
           tmem_st_wait();
         }
         tc_fence_before();
@@ -695,50 +749,53 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) mbar_arrive(&x.stat_empty[st]);
       }
     }
-    if (ok && (ok = wait_all(&x.acc_full, 0))) {
-      tc_fence_after();
-      // DKV: group 0 dV, group 1 dK; else each group half of the columns.  The warp's rows
-      // are turned in shared memory, which nothing uses any more.
-      constexpr int W = ROLE == DKV ? D : D / 2;
-      const uint32_t t_acc =
-          tmem_base + ((uint32_t)(q4 * 32) << 16) + C::T_ACC + (ROLE == DKV ? (grp ? 0 : D) : grp * W);
-      __nv_bfloat16* dst;
-      int64_t off;
-      if (Q_STAYS) {
-        dst = p.dq;
-        off = (int64_t)(blk.first + tk) * p.ld_dq + (int64_t)(h0 + hh) * D + grp * W;
-      } else if (ROLE == DV || (ROLE == DKV && grp == 0)) {
-        dst = p.dv;
-        off = (int64_t)(blk.first + tk) * p.ld_dv + (int64_t)g * D + (ROLE == DKV ? 0 : grp * W);
-      } else {
-        dst = p.dk;
-        off = (int64_t)(blk.first + tk) * p.ld_dk + (int64_t)g * D + (ROLE == DKV ? 0 : grp * W);
-      }
-      if (!stored) off = -1;
-      const float fin = ROLE == DV || (ROLE == DKV && grp == 0) ? 1.0f : p.scale;
-      constexpr int PITCH = W * 2 + 16;
-      uint8_t* stg = smem + (warp - 4) * (32 * PITCH);
+    done += nk;
+    if (!ok || !(ok = wait_all(&x.acc_full, (uint32_t)(t & 1)))) break;
+    tc_fence_after();
+    // DKV: group 0 dV, group 1 dK; else each group half of the columns
+    constexpr int W = ROLE == DKV ? D : D / 2;
+    const uint32_t t_acc =
+        tmem_base + ((uint32_t)(q4 * 32) << 16) + C::T_ACC + (ROLE == DKV ? (grp ? 0 : D) : grp * W);
+    __nv_bfloat16* dst = nullptr;
+    if (stored) {
+      const int64_t row = blk.first + tk;
+      if (Q_STAYS) dst = p.dq + row * p.ld_dq + (int64_t)(h0 + hh) * D + grp * W;
+      else if (ROLE == DV || (ROLE == DKV && grp == 0)) dst = p.dv + row * p.ld_dv + (int64_t)g * D + (ROLE == DKV ? 0 : grp * W);
+      else dst = p.dk + row * p.ld_dk + (int64_t)g * D + (ROLE == DKV ? 0 : grp * W);
+    }
+    const float fin = ROLE == DV || (ROLE == DKV && grp == 0) ? 1.0f : p.scale;
 #pragma unroll 1
-      for (int c = 0; c < W / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(t_acc + 32 * c, o);
-        tmem_ld_wait();
+    for (int c = 0; c < W; c += 32) {
+      uint32_t o[32];
+      tmem_ld_32x32b_x32(t_acc + c, o);
+      tmem_ld_wait();
+      uint4 u[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(stg + lane * PITCH + 64 * c + 16 * k) =
-              make_uint4(pack_bf16(__uint_as_float(o[8 * k]) * fin, __uint_as_float(o[8 * k + 1]) * fin),
-                         pack_bf16(__uint_as_float(o[8 * k + 2]) * fin, __uint_as_float(o[8 * k + 3]) * fin),
-                         pack_bf16(__uint_as_float(o[8 * k + 4]) * fin, __uint_as_float(o[8 * k + 5]) * fin),
-                         pack_bf16(__uint_as_float(o[8 * k + 6]) * fin, __uint_as_float(o[8 * k + 7]) * fin));
+      for (int q = 0; q < 4; ++q)
+        u[q] = make_uint4(pack_bf16(__uint_as_float(o[8 * q]) * fin, __uint_as_float(o[8 * q + 1]) * fin),
+                          pack_bf16(__uint_as_float(o[8 * q + 2]) * fin, __uint_as_float(o[8 * q + 3]) * fin),
+                          pack_bf16(__uint_as_float(o[8 * q + 4]) * fin, __uint_as_float(o[8 * q + 5]) * fin),
+                          pack_bf16(__uint_as_float(o[8 * q + 6]) * fin, __uint_as_float(o[8 * q + 7]) * fin));
+      if constexpr (C::STAGED) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = u[q];
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int y = 8 * q + lane / 4, piece = lane & 3;
+          const int64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(dst), y);
+          const uint4 w = *reinterpret_cast<const uint4*>(stg + y * 64 + ((piece ^ ((y >> 1) & 3)) << 4));
+          if (at) *reinterpret_cast<uint4*>(at + 2 * c + 16 * piece) = w;
+        }
+      } else if (dst) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(dst + c)[q] = u[q];
       }
       __syncwarp();
-      constexpr int CH = W / 8;
-#pragma unroll 4
-      for (int u = lane; u < 32 * CH; u += 32) {
-        const int rr = u / CH, c = u % CH;
-        const int64_t to = __shfl_sync(0xffffffffu, off, rr);
-        if (to >= 0) *reinterpret_cast<uint4*>(dst + to + 8 * c) = *reinterpret_cast<const uint4*>(stg + rr * PITCH + 16 * c);
-      }
+    }
+    // the accumulators may be overwritten: the next block's first product into them
+    // waits for these warps' P or dS
+    tc_fence_before();
     }
   }
 
@@ -748,6 +805,34 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// stats = (log2(e) lse, D = dO . O) of each row and head.  Bound by bytes: a
+// warp a row, D / 8 lanes a head, two loads of 16 bytes a lane and turn.
+template <int D>
+__global__ void __launch_bounds__(256) var_bwd_prep_kernel(const VarBwdArgs a) {
+  constexpr int LPR = D / 8, HPW = D == 192 ? 1 : 32 / LPR;  // lanes a head, heads a turn
+  const int lane = threadIdx.x & 31;
+  const int sub = HPW > 1 ? lane / LPR : 0, c = HPW > 1 ? lane % LPR : lane;
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.seq.rows; row += (int64_t)gridDim.x * 8) {
+    const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + row * a.ld_dout;
+    const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.out) + row * a.ld_out;
+#pragma unroll 4
+    for (int h0 = 0; h0 < a.nq; h0 += HPW) {
+      const int h = h0 + sub;
+      float s = 0.0f;
+      if (h < a.nq && c < LPR) {
+        float x[8], y[8];
+        Vec<__nv_bfloat16>::load(g + (int64_t)h * D + 8 * c, x);
+        Vec<__nv_bfloat16>::load(o + (int64_t)h * D + 8 * c, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+      }
+#pragma unroll
+      for (int k = (HPW > 1 ? LPR : 32) / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      if (c == 0 && h < a.nq) a.stats[row * a.nq + h] = make_float2(a.lse[row * a.nq + h] * 1.4426950408889634f, s);
+    }
   }
 }
 
@@ -766,6 +851,7 @@ cudaError_t launch_role(BwdParams p, const VarBwdArgs& a, int num_sms, cudaStrea
   p.slots = make_slots(a.seq, block_tok);
   const int64_t units = p.slots.count * p.heads;
   if (units > 0x7fffffff / 2) return cudaErrorInvalidConfiguration;
+  p.units = (int)units;
   p.by_length = units > num_sms && a.seq.batch <= LPT_BATCH;
   CUtensorMap r1, r2, x1, x2;
   const int64_t rows = a.seq.rows;
@@ -779,13 +865,16 @@ cudaError_t launch_role(BwdParams p, const VarBwdArgs& a, int num_sms, cudaStrea
   cudaError_t e = allow_smem<var_bwd_kernel<D, ROLE>>(SMEM);
   if (e == cudaSuccess) e = check_regs<var_bwd_kernel<D, ROLE>>(384, 128 * (ISSUE_REGS + 2 * ROW_REGS));
   if (e != cudaSuccess) return e;
-  var_bwd_kernel<D, ROLE><<<(unsigned)units, 384, SMEM, st>>>(r1, r2, x1, x2, p);
+  var_bwd_kernel<D, ROLE><<<p.units < num_sms ? p.units : num_sms, 384, SMEM, st>>>(r1, r2, x1, x2, p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const BwdParams& p, const VarBwdArgs& a, int num_sms, cudaStream_t st) {
-  cudaError_t e = launch_role<D, DQ>(p, a, num_sms, st);  // writes the statistics that the others read
+  const int64_t want = (a.seq.rows + 7) / 8, most = 8LL * num_sms;
+  var_bwd_prep_kernel<D><<<(unsigned)(want < most ? want : most), 256, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_role<D, DQ>(p, a, num_sms, st);  // corrects the statistics that the others read
   if (e != cudaSuccess) return e;
   if constexpr (D <= 128) {
     return launch_role<D, DKV>(p, a, num_sms, st);
@@ -800,11 +889,6 @@ cudaError_t launch_d(const BwdParams& p, const VarBwdArgs& a, int num_sms, cudaS
 cudaError_t launch_var_bwd(const VarBwdArgs& a, int num_sms, cudaStream_t st) {
   BwdParams p{};
   p.seq = a.seq;
-  p.out = static_cast<const __nv_bfloat16*>(a.out);
-  p.dout = static_cast<const __nv_bfloat16*>(a.dout);
-  p.ld_out = a.ld_out;
-  p.ld_dout = a.ld_dout;
-  p.lse = a.lse;
   p.stats = a.stats;
   p.dq = static_cast<__nv_bfloat16*>(a.dq);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
