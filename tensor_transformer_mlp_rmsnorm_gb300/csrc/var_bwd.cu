@@ -519,7 +519,6 @@ __global__ void __launch_bounds__(384, 1)
     const int tid = grp * 128 + r;
     const uint32_t tl = tmem_base + ((uint32_t)(q4 * 32) << 16) + grp * HC;
     const int tok_r = Q_STAYS ? r / p.ht : r, hh = Q_STAYS ? r - tok_r * p.ht : 0;  // token or key of the row, head
-    const uint32_t magic = 65536u / (uint32_t)p.sht + 1u;  // c / sht = c magic >> 16 for c < 128
     uint8_t* stg = ring2 + N2 * C::EB + (warp - 4) * 2048;
     uint32_t pres = 0;
     int ok = 1;
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr int CPT = 8 * KB / 256;  // 16-byte pieces of a tile's row for each thread
       const int crow = tid % KB, cpart = tid / KB * CPT;
       bool masked;
-      int t0 = 0, tok0 = 0, hc = 0;
+      int t0 = 0, c_lo = 0, c_hi = 0;  // columns c_lo to c_hi - 1 of this group's are seen
       if (Q_STAYS) {
         const int tile0 = tile_of(blk, n) * KB;
         t0 = tile0 + grp * HC;
@@ -608,8 +607,12 @@ __global__ void __launch_bounds__(384, 1)
           fence_proxy_async_smem();
         }
       } else {
-        tok0 = blk.at + n / p.schunks * p.stok;
-        hc = n % p.schunks * p.sht;
+        const int tok0 = blk.at + n / p.schunks * p.stok, hc = n % p.schunks * p.sht;
+        // a key is seen by tokens without a gap, whose heads lie together: with more than one
+        // chunk of heads a step has one token
+        const int w = p.window > 0 && tk >= p.sinks ? min(p.window, 0x7fffff00) : 0x7fffff00;
+        c_lo = min(max(tk - tok0, 0), p.stok) * p.sht - grp * HC;
+        c_hi = min(max(min(min(blk.end - tok0, p.stok), tk - tok0 + w), 0) * p.sht, p.schunks > 1 ? p.hpg - hc : KB) - grp * HC;
         const bool cut = tok0 + p.stok > blk.end || hc + p.sht > p.hpg;
         masked = cut || blk.at + 127 > tok0 ||
                  (p.window > 0 && tok0 + p.stok - 1 - blk.at >= p.window && blk.at + 128 > p.sinks);
@@ -649,10 +652,13 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (masked) {
             const int t = t0 + 32 * hf;
-            const int hi = tk - t, lo = p.window > 0 ? tk - p.window - t : -1, sk = p.window > 0 ? p.sinks - t : 0;
+            uint32_t bits = below(tk - t + 1);
+            if (p.window > 0) bits &= ~below(tk - p.window - t + 1) | below(p.sinks - t);
+            if (__any_sync(0xffffffffu, bits != ~0u)) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c > hi || (c <= lo && c >= sk)) u[c] = 0u;
+              for (int c = 0; c < 32; ++c)
+                if (!(bits & (1u << c))) u[c] = 0u;
+            }
           }
         } else {
           const ulonglong2* sp = reinterpret_cast<const ulonglong2*>(x.nlse2[st] + grp * HC + 32 * hf);
@@ -668,12 +674,11 @@ __global__ void __launch_bounds__(384, 1)
             u[c + 3] = __float_as_uint(ex2_fast(a3));
           }
           if (masked) {
-            const bool sink = p.window == 0 || tk < p.sinks;
+            const uint32_t bits = below(c_hi - 32 * hf) & ~below(c_lo - 32 * hf);
+            if (__any_sync(0xffffffffu, bits != ~0u)) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int cc = grp * HC + 32 * hf + c, dt = (int)((uint32_t)cc * magic >> 16), q = tok0 + dt;
-              const bool seen = tk <= q && q < blk.end && hc + cc - dt * p.sht < p.hpg && (sink || q - tk < p.window);
-              if (!seen) u[c] = 0u;
+              for (int c = 0; c < 32; ++c)
+                if (!(bits & (1u << c))) u[c] = 0u;
             }
           }
         }

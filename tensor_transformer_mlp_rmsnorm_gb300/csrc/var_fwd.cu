@@ -611,7 +611,6 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         if (t0 + KB - 1 > pos_first || (p.window > 0 && pos_last - t0 >= p.window && t0 + KB > p.sinks)) {
           // What the row sees as bits, 32 columns a word: two instructions a column, and
           // none for the words that every row of the warp sees whole.
-          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
           const int hi = pos - t0 + 1;                                // keys c < hi
           const int lo = p.window > 0 ? pos + 1 - p.window - t0 : 0;  // and c >= lo
           const int sk = p.window > 0 ? p.sinks - t0 : 0;             // or c < sk
