@@ -627,6 +627,7 @@ tpmlp_status kv_run_extend(tpkv_ctx* c, const SeqRows& seq, const void* q, int64
   a.scale = scale;
   a.window = window;
   a.sinks = sinks;
+  limit_window(&a.window, &a.sinks, (int64_t)max_pages * cf.page_size);
   a.status = c->status;
   a.paged = true;
   a.e4m3 = cf.cache_dtype == TPKV_E4M3;

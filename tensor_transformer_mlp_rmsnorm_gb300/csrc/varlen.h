@@ -50,6 +50,14 @@ struct VarFwdArgs {
   float* part;  // scratch of VAR_MAX_PARTS parts, or null: blocks are not split
 };
 
+// The kernels add to and subtract from `window` and `sinks` in 32 bits.  Where no
+// sequence is longer than `longest` tokens, a window of so many is none, and sinks
+// behind it are all alike.
+inline void limit_window(int* window, int* sinks, int64_t longest) {
+  if (*window >= longest) *window = 0;
+  if (*sinks > longest) *sinks = (int)longest;
+}
+
 // Backward over packed rows.
 struct VarBwdArgs {
   SeqRows seq;

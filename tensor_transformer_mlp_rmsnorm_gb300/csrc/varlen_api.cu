@@ -112,6 +112,7 @@ tpmlp_status tpattn_packed_forward(const tpattn_packed_desc* p, const void* q, i
   a.scale = p->scale;
   a.window = p->window;
   a.sinks = p->sinks;
+  limit_window(&a.window, &a.sinks, p->rows);
   a.status = status;
   const cudaError_t e = launch_var_fwd(a, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TPMLP_OK : bad(TPMLP_ERR_CUDA, cudaGetErrorString(e));
@@ -179,6 +180,7 @@ tpmlp_status tpattn_packed_backward(const tpattn_packed_desc* p, const void* q, 
   a.scale = p->scale;
   a.window = p->window;
   a.sinks = p->sinks;
+  limit_window(&a.window, &a.sinks, p->rows);
   a.status = status;
   const cudaError_t e = launch_var_bwd(a, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TPMLP_OK : bad(TPMLP_ERR_CUDA, cudaGetErrorString(e));
