@@ -46,7 +46,11 @@ struct Cfg {
   static constexpr int N1 = S1 * NE, N2 = S2 * NE;
   static constexpr uint32_t T_DP = KB == 128 && ROLE != DKV ? 256 : 128;
   static constexpr uint32_t T_ACC = KB == 128 && ROLE != DKV ? 384 : 256;
-  static constexpr int TWICE = 256 / KB;
+  // DQ: blocks of so many steps, and those under a window of few keys, take D from
+  // their own sums.  A single step's P and dP are still in registers then; more steps
+  // are run over twice.
+  static constexpr int EXACT = 128 / KB;
+  static constexpr bool HELD = EXACT == 1;
   // Results are turned in shared memory, 64 bytes of a row at a time, where there is room.
   static constexpr bool STAGED = !(D == 256 && HAS_DP) && D != 128;
   static constexpr uint32_t STAGE = STAGED ? 8 * 2048 : 0;
@@ -485,9 +489,9 @@ __global__ void __launch_bounds__(384, 1)
           // D = dO . O takes the output as it was rounded.  For tokens that see few
           // others D is as large as what it is taken from, and that rounding would be a
           // good part of a small gradient (dq off by 0.0026 of its norm where its own
-          // rounding is 0.0017).  Blocks of few steps run over their keys once more,
-          // before, for D = sum P dP: with 256 keys or more the rounding is averaged out.
-          if (k.n <= C::TWICE) k.pre = k.n;
+          // rounding is 0.0017): there D = sum P dP.  It shrinks with the root of the
+          // number of keys; behind 100 it is a tenth of the gradient's own rounding.
+          if (k.n <= C::EXACT ? !C::HELD : p.window > 0 && p.window + p.sinks < 128) k.pre = k.n;
           k.n += k.pre;
         } else {
           // the tokens [at, end) see keys of the block
@@ -530,43 +534,57 @@ __global__ void __launch_bounds__(384, 1)
     const bool stored = tk < blk.count && (!Q_STAYS || (r < p.ht * p.tok && hh < blk.nh));
     const int64_t stat_at = (int64_t)(blk.first + tk) * p.nq + h0 + hh;
     float lse2 = 0.0f, dsum = 0.0f;
+    // Over few keys: sum P, and sum P (dP - dref) with dref the dP of the first
+    // key that the row sees: exact where it sees no other.
+    const bool held = Q_STAYS && C::HELD && nk == 1, exact = held || pre > 0;
+    float l = 0.0f, dref = 0.0f;
     if (Q_STAYS) {
       if (stored) {
         const float2 z = p.stats[stat_at];
         lse2 = z.x;
-        if (!pre) dsum = z.y;
+        if (!exact) dsum = z.y;
       }
     }
-    // The first run over few keys: sum P, and sum P (dP - dref) with dref the
-    // dP of the first key that the row sees: exact where it sees no other.
-    float l = 0.0f, dref = 0.0f;
+    auto add = [&](float pr, uint32_t d) {
+      if (pr != 0.0f) {  // hidden values may be anything
+        if (l == 0.0f) dref = __uint_as_float(d);
+        l += pr;
+        dsum = fmaf(pr, __uint_as_float(d) - dref, dsum);
+      }
+    };
+    // The sums of both groups' halves: l becomes sum P, dsum becomes D.
+    auto settle = [&]() -> bool {
+      auto meet = [&](int i) -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.sums[i]);
+        return wait_all(&x.sums[i], pres & 1u);
+      };
+      if (grp == 1) {
+        x.row[r] = make_float2(l, dsum);
+        x.row_ref[r] = dref;
+      }
+      if (!meet(0)) return false;
+      if (grp == 0) {
+        const float2 o = x.row[r];
+        const float ref = x.row_ref[r], all = l + o.x;
+        const float d = l != 0.0f ? dref + (dsum + o.y + (o.x != 0.0f ? o.x * (ref - dref) : 0.0f)) / all
+                                  : ref + (o.y + dsum) / all;
+        x.row[r] = make_float2(all, d);
+      }
+      if (!meet(1)) return false;
+      ++pres;
+      l = x.row[r].x;
+      dsum = x.row[r].y;
+      lse2 += log2f(l);
+      if (stored && grp == 0) p.stats[stat_at] = make_float2(lse2, dsum);
+      return true;
+    };
     for (int n = 0; n < nk; ++n) {
       const int N = done + n;  // as rings and barriers count
       const uint32_t par = (uint32_t)(N & 1), par2 = (uint32_t)((N >> 1) & 1);
       const int st = N & 1;
-      if (Q_STAYS && pre && n == pre) {  // both groups' sums
-        auto meet = [&](int i) -> bool {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&x.sums[i]);
-          return wait_all(&x.sums[i], pres & 1u);
-        };
-        if (grp == 1) {
-          x.row[r] = make_float2(l, dsum);
-          x.row_ref[r] = dref;
-        }
-        if (!(ok = meet(0))) break;
-        if (grp == 0) {
-          const float2 o = x.row[r];
-          const float ref = x.row_ref[r], all = l + o.x;
-          const float d = l != 0.0f ? dref + (dsum + o.y + (o.x != 0.0f ? o.x * (ref - dref) : 0.0f)) / all
-                                    : ref + (o.y + dsum) / all;
-          x.row[r] = make_float2(all, d);
-        }
-        if (!(ok = meet(1))) break;
-        ++pres;
-        lse2 += log2f(x.row[r].x);
-        dsum = x.row[r].y;
-        if (stored && grp == 0) p.stats[stat_at] = make_float2(lse2, dsum);
+      if (Q_STAYS && pre && n == pre) {
+        if (!(ok = settle())) break;
       }
       if (!Q_STAYS && !(ok = wait_all(&x.stat_full[st], par2))) break;
       if (!(ok = wait_all(&x.s_full[NS == 2 ? N & 1 : 0], NS == 2 ? par2 : par))) break;
@@ -704,18 +722,22 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld_32x32b_x32(t_dp, *reinterpret_cast<uint32_t(*)[32]>(dd));
         tmem_ld_wait();
         if constexpr (HC == 64) tmem_ld_32x32b_x32(t_dp + 32, *reinterpret_cast<uint32_t(*)[32]>(dd + 32));
+        if (held) {
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < HC; ++c) add(__uint_as_float(v[c]), dd[c]);
+          if (!(ok = settle())) break;
+          const float inv = 1.0f / l;
+#pragma unroll
+          for (int c = 0; c < HC; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * inv);
+        }
 #pragma unroll
         for (int hf = 0; hf < HC / 32; ++hf) {
           uint32_t* d = dd + 32 * hf;
           if (hf == 1) tmem_ld_wait();
           if (Q_STAYS && n < pre) {  // the sums alone
 #pragma unroll
-            for (int c = 0; c < 32; ++c)  // hidden values may be anything
-              if (v[32 * hf + c] != 0u) {
-                if (l == 0.0f) dref = __uint_as_float(d[c]);
-                l += __uint_as_float(v[32 * hf + c]);
-                dsum = fmaf(__uint_as_float(v[32 * hf + c]), __uint_as_float(d[c]) - dref, dsum);
-              }
+            for (int c = 0; c < 32; ++c) add(__uint_as_float(v[32 * hf + c]), d[c]);
           } else {
             // P (dP - D); the scale comes in at the end
             const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(x.nd[Q_STAYS ? 0 : st] + (Q_STAYS ? 0 : grp * HC + 32 * hf));
