@@ -741,6 +741,40 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
           dst = reinterpret_cast<uint8_t*>(part + (size_t)rr * D);
         }
       }
+      if constexpr (C::STAGED) {
+        if (w.whole && !(NT == 2 && w.dual)) {  // 64 columns at a time, the next ones on their way
+          uint32_t o[64];
+          tmem_ld_32x32b_x32(t_o, *reinterpret_cast<uint32_t(*)[32]>(o));
+          tmem_ld_32x32b_x32(t_o + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+#pragma unroll 1
+          for (int c = 0; c < D; c += 64) {
+            uint32_t u[32];
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              u[e] = none ? 0u : pack_bf16(fa * __uint_as_float(o[2 * e]), fa * __uint_as_float(o[2 * e + 1]));
+            if (c + 64 < D) {
+              tmem_ld_32x32b_x32(t_o + c + 64, *reinterpret_cast<uint32_t(*)[32]>(o));
+              tmem_ld_32x32b_x32(t_o + c + 96, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                  make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+            __syncwarp();
+            const int64_t to = dst ? reinterpret_cast<int64_t>(dst) + 2 * c : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int y = 4 * k + lane / 8, piece = lane & 7;
+              const int64_t at = __shfl_sync(0xffffffffu, to, y);
+              const uint4 z = *reinterpret_cast<const uint4*>(stg + y * 128 + ((piece ^ (y & 7)) << 4));
+              if (at) *reinterpret_cast<uint4*>(at + 16 * piece) = z;
+            }
+            __syncwarp();
+          }
+          continue;
+        }
+      }
       // 32 columns at a time: a load from tensor memory takes some 300 cycles beside
       // the other tile's products whatever its size
 #pragma unroll 1
