@@ -387,9 +387,12 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         if constexpr (NT == 2) {
           const int na = w.na, nb = w.nb, nk = w.nk, most = max(na, nb);
           const bool dual = w.dual;
-          int seen = base;  // elements of the ring that are there
+          // Elements of the ring that are there.  With two tiles of rows each one is waited
+          // for in order, by the tile that comes first.  Turns at the steps go out of
+          // order, and copies land out of order: each is waited for by the one that uses it.
+          int seen = base;
           auto there = [&](int at) -> bool {
-            if (at < seen) return true;
+            if (!dual && at < seen) return true;
             if (!wait_elems(at)) return false;
             seen = at + NE;
             return true;

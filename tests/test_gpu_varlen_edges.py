@@ -108,3 +108,16 @@ def test_two_captured_steps_replayed_in_turn():
         torch.cuda.synchronize()
         for _, got, want, _ in jobs:
             assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("d,f8", [(64, False), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("new,past,nq,nkv", [([2] * 40, [4100] * 40, 16, 4), ([2] * 36, [4100] * 36, 16, 4),
+                                             ([5] * 48, [2500] * 48, 8, 2)])
+def test_values_that_arrive_after_later_keys(d, f8, new, past, nq, nkv):
+    """Many copies in flight land in any order: each is waited for, so that repeats give the same bits."""
+    c = Case(new, past, nq, nkv, d, 64, f8, seed=len(new))
+    out, lse = c.run()
+    c.check(out, lse)
+    for _ in range(20):
+        again, _ = c.run()
+        assert torch.equal(again, out)
