@@ -22,6 +22,7 @@ constexpr uint32_t SUB = 128 * 128;  // bytes of a [128 x 64] bf16 tile with the
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
 constexpr float MOVE_LOG2 = 8.0f;  // the running maximum is moved when it is off by more than 2^8
 constexpr int MIN_PART = 4;        // steps of a part at least
+constexpr int TAIL_PART = 12;      // and of one of a last turn's blocks
 
 enum Source { PACKED = 0, PAGED = 1, PAGED_F8 = 2 };
 
@@ -73,8 +74,10 @@ struct FwdParams {
   int tok;           // tokens of a tile
   Slots slots;
   int heads;  // block slots, key heads times chunks
-  int units;         // slots times heads times parts
-  int nsplit;
+  // Blocks in order (slots times heads): those from `tail` on are shared by
+  // nsplit CTAs each, in parts of at least min_part steps.
+  int units;         // blocks and parts
+  int tail, nsplit, min_part;
   bool by_length;
   float scale_log2;
   bool negate;
@@ -120,9 +123,29 @@ __device__ __forceinline__ void fill_block(Block* o, const SeqSpan& sp, int b, i
   o->n_a = o->sink_tiles + (end_a + KB - 1) / KB - o->win_tile;
 }
 
-// Steps of a part of a block of n steps that nsplit CTAs share.
-__device__ __forceinline__ int part_steps(int n, int nsplit) {
-  return nsplit == 1 ? n : max(MIN_PART, (n + nsplit - 1) / nsplit);
+// Steps of a part of a shared block of n steps.
+__device__ __forceinline__ int part_steps(const FwdParams& p, int n) {
+  return max(p.min_part, (n + p.nsplit - 1) / p.nsplit);
+}
+
+// Block `rank` of the order in which blocks are taken, by the lanes of one warp; false: none.
+__device__ __forceinline__ bool find_block(const FwdParams& p, ByLength<KB>& order, int rank, int block_tok, int64_t cap,
+                                           int lane, Block* k) {
+  int b, i = -1;
+  if (p.by_length) order.find(rank, lane, &b, &i);
+  else b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
+  if (b < 0) return false;
+  bool bad = false;  // reported elsewhere
+  const SeqSpan s = seq_span(p.seq, b, cap, &bad);
+  if (!p.by_length) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
+  if (i < 0 || (int64_t)i * block_tok >= s.count) return false;
+  fill_block(k, s, b, i, p.tok, block_tok, p.window, p.sinks);
+  return true;
+}
+__device__ __forceinline__ void start_order(const FwdParams& p, ByLength<KB>& order, int block_tok, int64_t cap, int lane) {
+  if (p.by_length)
+    order.init(p.seq, cap, block_tok,
+               p.window > 0 ? (p.window + block_tok) / KB + 2 + (p.sinks + KB - 1) / KB : 0x7fffffff, lane);
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -142,9 +165,9 @@ __device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t v, bool high) {
   return pack_bf16(f.x, f.y);
 }
 
-// A piece of work: a block, or with nsplit > 1 a part of its steps.
+// A piece of work: a block, or a part of its steps.
 struct Work : Block {
-  int hd, split;
+  int part;        // its place among the parts
   int g, h0, nh;   // key head, first query head, query heads
   int j0, nk;      // steps [j0, j0 + nk) of the block
   int na, nb;      // those of the first and the second tile
@@ -486,9 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
       }
       ByLength<KB> order;
-      if (p.by_length)
-        order.init(p.seq, cap, block_tok,
-                   p.window > 0 ? (p.window + block_tok) / KB + 2 + (p.sinks + KB - 1) / KB : 0x7fffffff, lane);
+      start_order(p, order, block_tok, cap, lane);
       bool ok = true;
       int t = 0;
       for (int k = 0; ok; ++k) {
@@ -498,30 +519,21 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         w.b = NONE;
         if (!end) {
           if (u >= p.units) continue;
-          const int unit = (int)u;
-          w.split = unit % p.nsplit;
-          w.hd = unit / p.nsplit % p.heads;
-          w.g = w.hd / p.chunks;
-          w.h0 = w.g * p.hpg + w.hd % p.chunks * p.ht;
-          w.nh = min(p.ht, (w.g + 1) * p.hpg - w.h0);
-          const int rank = unit / p.nsplit / p.heads;
-          int b, i = 0;
-          if (p.by_length) {
-            order.find(rank, lane, &b, &i);
-          } else {
-            const int slot = (int)p.slots.count - 1 - rank;
-            b = find_slot(p.seq, p.slots, slot, lane);
-            i = -1;  // below
+          int unit = (int)u, split = 0;
+          const bool shared = unit >= p.tail;
+          w.part = unit - p.tail;
+          if (shared) {
+            split = w.part % p.nsplit;
+            unit = p.tail + w.part / p.nsplit;
           }
-          if (b < 0) continue;
-          bool bad = false;
-          const SeqSpan s = seq_span(p.seq, b, cap, &bad);
-          if (i < 0) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
-          if (i < 0 || (int64_t)i * block_tok >= s.count) continue;
-          fill_block(&w, s, b, i, p.tok, block_tok, p.window, p.sinks);
-          const int per = part_steps(w.n, p.nsplit);
-          w.j0 = w.split * per;
-          if (w.split > 0 && w.j0 >= w.n) continue;
+          const int hd = unit % p.heads;
+          w.g = hd / p.chunks;
+          w.h0 = w.g * p.hpg + hd % p.chunks * p.ht;
+          w.nh = min(p.ht, (w.g + 1) * p.hpg - w.h0);
+          if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &w)) continue;
+          const int per = shared ? part_steps(p, w.n) : w.n;
+          w.j0 = split * per;
+          if (split > 0 && w.j0 >= w.n) continue;
           w.whole = per >= w.n;
           w.nk = min(w.n, w.j0 + per) - w.j0;
           w.dual = NT == 2 && (FEW || w.count <= p.tok) && w.nk > 1;
@@ -736,8 +748,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         fa *= inv;
         fb *= inv;
       } else {  // a part: weighted values, maximum and sum
-        const int64_t slot_b = slot_base(p.slots, w.first - w.i * block_tok, w.b) + w.i;
-        float* part = p.part + ((slot_b * p.heads + w.hd) * p.nsplit + w.split) * (C::QTILES * 128) * (D + 2);
+        float* part = p.part + (int64_t)w.part * (C::QTILES * 128) * (D + 2);
         if (stored) {
           part[(size_t)C::QTILES * 128 * D + rr] = m_run;
           part[(size_t)C::QTILES * 128 * (D + 1) + rr] = l;
@@ -891,30 +902,27 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
   }
 }
 
-// Joins the parts of split blocks, a warp a row and head, in the parts' order.
+// Joins the parts of shared blocks, a warp a row and head, in the parts' order.
 template <int D>
 __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p, int tiles) {
   constexpr int V = D / 64;
   const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (id >= p.seq.rows * p.nq) return;
-  const int row = (int)(id / p.nq), head = (int)(id % p.nq);
-  const int block_tok = tiles * p.tok;
-  const int b = find_row(p.seq, row, lane);
-  bool bad = false;
-  const SeqSpan s = seq_span(p.seq, b, (int64_t)p.max_pages * p.page_size, &bad);
-  if (row < s.first || row - s.first >= s.count) return;
-  const int i = (row - s.first) / block_tok, tk = row - s.first - i * block_tok;
+  const int block_tok = tiles * p.tok, at = (int)blockIdx.x / (16 * tiles);  // place among the shared blocks
+  const int rr = (int)blockIdx.x % (16 * tiles) * 8 + (threadIdx.x >> 5), r = rr & 127;
+  const int unit = p.tail + at, hd = unit % p.heads, g = hd / p.chunks;
+  const int tk = (rr >> 7) * p.tok + r / p.ht, head = g * p.hpg + hd % p.chunks * p.ht + r % p.ht;
+  if (r >= p.tok * p.ht || head >= (g + 1) * p.hpg) return;
+  const int64_t cap = (int64_t)p.max_pages * p.page_size;
+  ByLength<KB> order;
+  start_order(p, order, block_tok, cap, lane);
   Block k;
-  fill_block(&k, s, b, i, p.tok, block_tok, p.window, p.sinks);
-  const int per = part_steps(k.n, p.nsplit);
-  if (per >= k.n) return;  // not split
+  if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &k) || tk >= k.count) return;
+  const int per = part_steps(p, k.n);
+  if (per >= k.n) return;  // one CTA's
   const int parts = (k.n + per - 1) / per;
-  const int g = head / p.hpg, hc = (head - g * p.hpg) / p.ht, hh = head - g * p.hpg - hc * p.ht;
-  const int rr = tk / p.tok * 128 + tk % p.tok * p.ht + hh;
-  const int hd = g * p.chunks + hc;
+  const int64_t row = (int64_t)k.first + tk;
   const size_t size = (size_t)tiles * 128 * (D + 2);
-  const float* base = p.part + ((int64_t)(slot_base(p.slots, s.first, b) + i) * p.heads + hd) * p.nsplit * size;
+  const float* base = p.part + (int64_t)at * p.nsplit * size;
   // all lanes look at the parts' maxima, 32 at a time
   float top = -INFINITY;
   for (int q = lane; q < parts; q += 32) top = fmaxf(top, __ldcg(base + q * size + (size_t)tiles * 128 * D + rr));
@@ -938,10 +946,10 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p, int ti
     }
   }
   const float inv = (p.v_inv_scale ? p.v_inv_scale[g] : 1.0f) / sum;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + (int64_t)row * p.ld_out + (int64_t)head * D);
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + (int64_t)head * D);
 #pragma unroll
   for (int v = 0; v < V; ++v) out[lane + 32 * v] = pack_bf16(acc[v].x * inv, acc[v].y * inv);
-  if (p.lse && lane == 0) p.lse[id] = (top + log2f(sum)) * 0.69314718055994531f;
+  if (p.lse && lane == 0) p.lse[row * p.nq + head] = (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 // {64 columns, box slots} of a cache {d, page_size, nkv, pages}; E4M3 codes lie unswizzled, 64 bytes a row.
@@ -966,16 +974,26 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   p.slots = make_slots(a.seq, C::QTILES * p.tok);
   const int64_t units = p.slots.count * p.heads;
   if (units > 0x7fffffff / 2) return cudaErrorInvalidConfiguration;
+  // Few blocks: all are shared.  Many: the CTAs take them in turns, and a last turn
+  // with work for less than half of them shares its blocks out, which are the
+  // shortest.  (2 x 2048 tokens behind 30000, 512 blocks for 152 CTAs: 1651 us
+  // without, 1465 with; 4 x 1024 behind 7000 in E4M3: 493 and 458.)
+  p.tail = (int)units;
   p.nsplit = 1;
-  if (SRC != PACKED && a.part && units * 2 <= num_sms) {
+  p.min_part = MIN_PART;
+  if (SRC != PACKED && a.part) {
     const int most = num_sms < VAR_MAX_PARTS ? num_sms : VAR_MAX_PARTS;
     const int64_t steps = ((int64_t)a.max_pages * a.page_size + KB - 1) / KB;
-    const int64_t parts = (steps + MIN_PART - 1) / MIN_PART;
-    p.nsplit = (int)(most / units < parts ? most / units : parts);
-    if (p.nsplit < 1) p.nsplit = 1;
+    const int64_t left = units > num_sms ? units % num_sms : units;
+    if (units > num_sms) p.min_part = TAIL_PART;
+    const int64_t parts = (steps + p.min_part - 1) / p.min_part;
+    if (left > 0 && left * 2 <= most && parts > 1) {
+      p.tail = (int)(units - left);
+      p.nsplit = (int)(most / left < parts ? most / left : parts);
+    }
   }
   p.by_length = units > num_sms && a.seq.batch <= LPT_BATCH;
-  p.units = (int)(units * p.nsplit);
+  p.units = (int)(p.tail + (units - p.tail) * p.nsplit);
   CUtensorMap mq, mk, mv;
   bool ok = map3(&mq, a.q, D, a.nq, a.seq.rows, a.ld_q, p.ht, p.tok);
   if (SRC == PACKED) {
@@ -991,7 +1009,7 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   var_fwd_kernel<D, SRC, FEW><<<p.units < num_sms ? p.units : num_sms, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
-  var_join_kernel<D><<<(unsigned)((a.seq.rows * a.nq + 7) / 8), 256, 0, st>>>(p, C::QTILES);
+  var_join_kernel<D><<<(unsigned)((units - p.tail) * 16 * C::QTILES), 256, 0, st>>>(p, C::QTILES);
   return cudaGetLastError();
 }
 

@@ -110,6 +110,17 @@ def test_two_captured_steps_replayed_in_turn():
             assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("d,f8", [(64, False), (128, False), (128, True), (192, False), (192, True), (256, True)])
+@pytest.mark.parametrize("new,past,nq,nkv", [
+    ([256] * 20, [3900] * 20, 8, 8), ([128] * 22, [5000] + [3300] * 21, 16, 8),  # a last turn of 8 to 24 blocks
+    ([200, 300, 90, 256] * 5, [4000, 3500, 5100, -1] * 5, 8, 8), ([100] * 70, [3400, 10] * 35, 8, 8),
+    ([2] * 40, [4100] * 40, 16, 4)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2600, 100)])
+def test_last_turns_over_long_caches(d, f8, new, past, nq, nkv, window, sinks):
+    c = Case(new, past, nq, nkv, d, 64, f8, seed=len(new))
+    c.check(*c.run(window=window, sinks=sinks), window, sinks)
+
+
 @pytest.mark.parametrize("d,f8", [(64, False), (64, True), (128, False), (128, True)])
 @pytest.mark.parametrize("new,past,nq,nkv", [([2] * 40, [4100] * 40, 16, 4), ([2] * 36, [4100] * 36, 16, 4),
                                              ([5] * 48, [2500] * 48, 8, 2)])
