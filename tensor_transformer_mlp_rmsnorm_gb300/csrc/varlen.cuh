@@ -74,6 +74,20 @@ __device__ __forceinline__ int find_slot(const SeqRows& s, const Slots& t, int s
   return lo;
 }
 
+// The sequence that a row belongs to if to any: the last one that does not
+// begin behind it.  By the lanes of one warp.
+__device__ __forceinline__ int find_row(const SeqRows& s, int row, int lane) {
+  if (!s.cu_rows) return row / s.rows_per_seq;
+  int lo = 0, hi = s.batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, b < hi && s.cu_rows[b] <= row));
+    lo += max(n - 1, 0) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // Blocks are ordered by length up to this many sequences, two a lane; with
 // more there are many blocks, and the last ones count for little.
 constexpr int LPT_BATCH = 64;
