@@ -23,6 +23,7 @@ constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
 constexpr float MOVE_LOG2 = 8.0f;  // the running maximum is moved when it is off by more than 2^8
 constexpr int MIN_PART = 4;        // steps of a part at least
 constexpr int TAIL_PART = 12;      // and of one of a last turn's blocks
+constexpr int PART_STEPS = 5;      // steps in the time of a part's start and result
 
 enum Source { PACKED = 0, PAGED = 1, PAGED_F8 = 2 };
 
@@ -975,22 +976,29 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   const int64_t units = p.slots.count * p.heads;
   if (units > 0x7fffffff / 2) return cudaErrorInvalidConfiguration;
   // Few blocks: all are shared.  Many: the CTAs take them in turns, and a last turn
-  // with work for less than half of them shares its blocks out, which are the
-  // shortest.  (2 x 2048 tokens behind 30000, 512 blocks for 152 CTAs: 1651 us
-  // without, 1465 with; 4 x 1024 behind 7000 in E4M3: 493 and 458.)
+  // with work for less than half of them shares out its blocks, which are the shortest.
+  // (With more the parts' own time is what it costs: 48 x 5 tokens behind up to 8192 in
+  // E4M3, 80 blocks left, 169 us without and 185 with.)  A part takes its steps and the
+  // time of PART_STEPS more; the number of parts is the one that ends first.
+  // 2 x 2048 tokens behind 30000 (512 blocks for 152 CTAs): 1651 us without, 1431 with;
+  // 4 x 1024 behind 7000 in E4M3: 493 and 461.
   p.tail = (int)units;
   p.nsplit = 1;
-  p.min_part = MIN_PART;
+  p.min_part = units > num_sms ? TAIL_PART : MIN_PART;
   if (SRC != PACKED && a.part) {
-    const int most = num_sms < VAR_MAX_PARTS ? num_sms : VAR_MAX_PARTS;
     const int64_t steps = ((int64_t)a.max_pages * a.page_size + KB - 1) / KB;
-    const int64_t left = units > num_sms ? units % num_sms : units;
-    if (units > num_sms) p.min_part = TAIL_PART;
-    const int64_t parts = (steps + p.min_part - 1) / p.min_part;
-    if (left > 0 && left * 2 <= most && parts > 1) {
-      p.tail = (int)(units - left);
-      p.nsplit = (int)(most / left < parts ? most / left : parts);
+    const int64_t last = units % num_sms, left = units <= num_sms ? units : last * 2 <= num_sms ? last : 0;
+    const int64_t room = VAR_MAX_PARTS * var_part_floats(D) / ((size_t)C::QTILES * 128 * (D + 2));  // parts
+    const int64_t most = (steps + p.min_part - 1) / p.min_part;
+    int64_t best = steps + PART_STEPS;
+    for (int64_t n = 2; left > 0 && n <= most && n * left <= room; ++n) {
+      const int64_t turns = (n * left + num_sms - 1) / num_sms, time = turns * ((steps + n - 1) / n + PART_STEPS);
+      if (turns == 1 ? time < best : time * 20 < best * 19) {
+        best = time;
+        p.nsplit = (int)n;
+      }
     }
+    if (p.nsplit > 1) p.tail = (int)(units - left);
   }
   p.by_length = units > num_sms && a.seq.batch <= LPT_BATCH;
   p.units = (int)(p.tail + (units - p.tail) * p.nsplit);

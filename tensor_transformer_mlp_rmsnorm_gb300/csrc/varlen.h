@@ -11,7 +11,7 @@
 namespace tpmlp {
 
 // Parts of blocks that are split over the length of a cache, and the floats of one.
-constexpr int VAR_MAX_PARTS = 160;
+constexpr int VAR_MAX_PARTS = 320;
 inline size_t var_part_floats(int d) { return (size_t)(d <= 128 ? 256 : 128) * (d + 2); }
 
 // Which rows are whose.  Sequence b has `count` rows from `first` on, the i-th
