@@ -644,6 +644,7 @@ static tpmlp_status attn_run_forward(tpattn_ctx* c, int B, int S, int N, const i
     v.d = d;
     v.scale = 1.0f / std::sqrt((float)d);
     v.status = c->wsp<uint32_t>(c->L.status);
+    v.launches = &c->launches;
     ATTN_TRY(c->run(A_VAR_FWD, [&] { return launch_var_fwd(v, c->num_sms, c->stream); }));
   } else if (c->fwd_fused) {
     ATTN_TRY(c->run(A_FLASH_FWD, [&] {
@@ -799,6 +800,7 @@ tpmlp_status tpattn_backward(tpattn_ctx* c, const void* dy, void* dx, float* dno
     v.d = d;
     v.scale = 1.0f / std::sqrt((float)d);
     v.status = c->wsp<uint32_t>(c->L.status);
+    v.launches = &c->launches;
     ATTN_TRY(c->run(A_VAR_BWD, [&] { return launch_var_bwd(v, c->num_sms, c->stream); }));
   } else if (c->fwd_fused) {
     float* dq_acc = c->wsp<float>(c->L.dkv_head);

@@ -644,6 +644,7 @@ tpmlp_status kv_run_extend(tpkv_ctx* c, const SeqRows& seq, const void* q, int64
   a.k_inv_scale = c->k_inv_scale;
   a.v_inv_scale = c->v_inv_scale;
   a.part = c->part;
+  a.launches = &c->launches;
   OnDevice on(c->device);
   cudaError_t e = wait_for_clear(c, st);
   if (e == cudaSuccess) e = launch_var_fwd(a, c->num_sms, st);

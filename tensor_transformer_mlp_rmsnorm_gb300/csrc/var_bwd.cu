@@ -900,6 +900,7 @@ template <int D>
 cudaError_t launch_d(const BwdParams& p, const VarBwdArgs& a, int num_sms, cudaStream_t st) {
   const int64_t want = (a.seq.rows + 7) / 8, most = 8LL * num_sms;
   var_bwd_prep_kernel<D><<<(unsigned)(want < most ? want : most), 256, 0, st>>>(a);
+  if (a.launches) *a.launches += D <= 128 ? 2 : 3;
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = launch_role<D, DQ>(p, a, num_sms, st);  // corrects the statistics that the others read
   if (e != cudaSuccess) return e;

@@ -1017,6 +1017,7 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   var_fwd_kernel<D, SRC, FEW><<<p.units < num_sms ? p.units : num_sms, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
+  if (a.launches) ++*a.launches;
   var_join_kernel<D><<<(unsigned)((units - p.tail) * 16 * C::QTILES), 256, 0, st>>>(p, C::QTILES);
   return cudaGetLastError();
 }

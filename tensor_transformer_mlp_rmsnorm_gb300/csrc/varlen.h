@@ -48,6 +48,7 @@ struct VarFwdArgs {
   int64_t stride_page, stride_head, stride_slot;
   const float *k_inv_scale, *v_inv_scale;  // E4M3: [nkv] or null
   float* part;  // scratch of VAR_MAX_PARTS parts, or null: blocks are not split
+  uint64_t* launches;  // counts the kernels behind the first, or null
 };
 
 // The kernels add to and subtract from `window` and `sinks` in 32 bits.  Where no
@@ -71,6 +72,7 @@ struct VarBwdArgs {
   float scale;
   int window, sinks;
   uint32_t* status;
+  uint64_t* launches;  // as above
 };
 
 // For each row its position (pos, or null), and zeros in rows of z and dz (row
