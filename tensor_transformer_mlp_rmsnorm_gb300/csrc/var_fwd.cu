@@ -3,6 +3,44 @@
 // For the token at position p, over the tokens t that it sees (t <= p; with a
 // window, p - t < window or t < sinks):
 //   s_t = scale q . k_t,  lse = log sum exp s_t,  out = sum exp(s_t - lse) v_t
+//
+// Rows.  The query heads of a key head see the same keys, so a tile of 128 rows
+// holds the heads of one key head by 128 / heads tokens, and every key that is
+// read serves them all.  Heads of 64 and 128 have two tiles at work, whose
+// softmaxes hide under each other's products; heads of 192 and 256 leave room
+// for one, with two score buffers.  A step is 128 keys: the longest block whose
+// scores fit tensor memory beside the sums.
+//
+// Numbers.  S and O are 32-bit sums in tensor memory, m and l are 32 bits.  The
+// maximum that P = 2^(s - m) refers to is moved only when it is off by more than
+// 2^8: P stays below 2^8, l and O in range, and O is seldom rescaled.  P is
+// rounded once, to bf16, as the products want it, and l sums what was not
+// rounded: outputs are off by 0.0022 of their norm, where rounding the result
+// alone gives 0.0017.  Hidden scores are -inf before the maximum is taken, and
+// values that no row of the tile sees are cleared in shared memory, so nothing
+// that is not seen counts, whatever it holds.  E4M3 codes become bf16 exactly;
+// their scales go into the scores' scale and the result.
+//
+// Work.  One CTA an SM takes blocks (two tiles) by a static order, longest
+// first: times of causal blocks differ 100-fold.  The next block's copies, then
+// its scores, run under the end of the one before.  Few rows over a long cache
+// are cut along the cache: each part leaves its weighted sums, maximum and sum,
+// and a second kernel joins them in order, so repeats give the same bits.
+//
+// Measured (GB300; 1980 TFLOP/s and 6689 GB/s are its product and copy rates):
+//   one sequence of 16384 tokens, 32 + 8 heads of 128   1490 us, 1476 TFLOP/s
+//   2 x 2048 tokens behind 30000, the same heads        1431 us, 1452 TFLOP/s
+//   64 tokens behind 131000, the same heads              118 us, 4.6 TB/s and 1166 TFLOP/s
+//   4 x 1024 tokens behind 7000, E4M3                    461 us, 1118 TFLOP/s
+//   19 sequences, 8192 tokens                             75 us,  556 TFLOP/s of pairs that are seen
+//   48 x 5 tokens behind up to 8192, E4M3                169 us, 2.5 TB/s
+// What bounds them.  Long: a step of two tiles takes some 3000 cycles where its
+// products need 2080, the rest is the way between the issuing warp and the
+// softmax (a wait that is fulfilled costs 150 cycles, a load from tensor memory
+// beside products 300).  Short sequences: a block of one to four steps pays a
+// start and a result of some 4000 cycles, and up to half of a step's keys are
+// hidden.  E4M3: 16384 codes an operand are converted by 128 threads, about 1500
+// cycles, which few rows do not hide.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -143,7 +181,8 @@ __device__ __forceinline__ bool find_block(const FwdParams& p, ByLength<KB>& ord
   fill_block(k, s, b, i, p.tok, block_tok, p.window, p.sinks);
   return true;
 }
-__device__ __forceinline__ void start_order(const FwdParams& p, ByLength<KB>& order, int block_tok, int64_t cap, int lane) {
+__device__ __forceinline__ void start_order(const FwdParams& p, ByLength<KB>& order, int block_tok, int64_t cap,
+                                            int lane) {
   if (p.by_length)
     order.init(p.seq, cap, block_tok,
                p.window > 0 ? (p.window + block_tok) / KB + 2 + (p.sinks + KB - 1) / KB : 0x7fffffff, lane);
