@@ -26,7 +26,7 @@
 //   one sequence of 8192 tokens, 32 + 8 heads of 128    1371 us, 1003 TFLOP/s (1400 with all 7)
 //   19 sequences, 8192 tokens                            248 us,  421 TFLOP/s of pairs that are seen:
 //     lse and D 26 (bytes), dQ 116, dK and dV 107
-//   5 sequences, 333 tokens, 5 + 1 heads of 64            29 us (prep 5, dQ 9, dK and dV 16)
+//   5 sequences, 333 tokens, 5 + 1 heads of 64            29 us, three launches' latencies
 // What bounds them.  dK and dV: a step takes some 2950 cycles, its products 2560.
 // dQ: a step takes some 2650 cycles where its products need 1540; one buffer for
 // dP is all that tensor memory has left beside two for scores and dQ, so dP, the row

@@ -34,12 +34,12 @@
 //   4 x 1024 tokens behind 7000, E4M3                    461 us, 1118 TFLOP/s
 //   19 sequences, 8192 tokens                             75 us,  556 TFLOP/s of pairs that are seen
 //   48 x 5 tokens behind up to 8192, E4M3                169 us, 2.5 TB/s
-// What bounds them.  Long: a step of two tiles takes some 3000 cycles where its
-// products need 2080, the rest is the way between the issuing warp and the
-// softmax (a wait that is fulfilled costs 150 cycles, a load from tensor memory
-// beside products 300).  Short sequences: a block of one to four steps pays a
-// start and a result of some 4000 cycles, and up to half of a step's keys are
-// hidden.  E4M3: 16384 codes an operand are converted by 128 threads, about 1500
+// What bounds them.  Long: a step of two tiles takes some 2800 to 3300 cycles
+// where its products need 2080, the rest is the way between the issuing warp and
+// the softmax (a wait that is fulfilled costs 150 cycles, a load from tensor
+// memory beside products 300).  Short sequences: a block of one to four steps
+// pays some 7500 cycles for its result (5500) and the next one's start, in which
+// the tensor cores rest, and up to half of a step's keys are hidden.  E4M3: 16384 codes an operand are converted by 128 threads, about 1500
 // cycles, which few rows do not hide.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -120,6 +120,7 @@ struct FwdParams {
   bool by_length;
   float scale_log2;
   bool negate;
+  bool out_boxes;  // 32 rows of a tile are a box of out
   int window, sinks;
   uint32_t* status;
   const int32_t* table;
@@ -219,7 +220,7 @@ constexpr int NONE = -2;  // Work::b behind the last piece
 template <int D, int SRC, bool FEW>
 __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
     var_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v, const FwdParams p) {
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const FwdParams p) {
   using C = Cfg<D, SRC, FEW>;
   constexpr int NT = C::NT, NE = C::NE, EC = C::EC, NST = C::NST;
   constexpr bool F8 = C::F8, RAW_RING = C::RAW_RING;
@@ -266,6 +267,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
+    tma_prefetch_desc(&map_o);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_base_sh, 512);
@@ -606,6 +608,11 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
     const uint32_t t_o = tmem_base + lane_off + 256 + x * D;
     const int tok_r = r / p.ht, hh = r - tok_r * p.ht;  // token in the tile, head
     uint8_t* stg = raw + C::RAW + (FEW ? warp & 3 : warp - 4) * 4096;
+    // before the warp's staging space is written: what a bulk copy reads there
+    auto stage_free = [&]() {
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+    };
     uint32_t steps = 0, outs = 0, duals = 0;  // of this tile so far
     bool ok = true;
     const Work* wp;
@@ -795,8 +802,11 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
           dst = reinterpret_cast<uint8_t*>(part + (size_t)rr * D);
         }
       }
+      // A warp whose 32 rows are all results hands them to a bulk copy; the others' rows
+      // of other sequences, or of nobody, lie between theirs in memory.
       if constexpr (C::STAGED) {
         if (w.whole && !(NT == 2 && w.dual)) {  // 64 columns at a time, the next ones on their way
+          const bool bulk = p.out_boxes && __all_sync(0xffffffffu, stored);
           uint32_t o[64];
           tmem_ld_32x32b_x32(t_o, *reinterpret_cast<uint32_t(*)[32]>(o));
           tmem_ld_32x32b_x32(t_o + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
@@ -811,10 +821,20 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
               tmem_ld_32x32b_x32(t_o + c + 64, *reinterpret_cast<uint32_t(*)[32]>(o));
               tmem_ld_32x32b_x32(t_o + c + 96, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
             }
+            stage_free();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
                   make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+            if (bulk) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&map_o, stg, c, w.h0, w.first + xt * p.tok + q4 * 32 / p.ht);
+                bulk_commit_group();
+              }
+              continue;
+            }
             __syncwarp();
             const int64_t to = dst ? reinterpret_cast<int64_t>(dst) + 2 * c : 0;
 #pragma unroll
@@ -852,6 +872,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
           for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
         }
         if constexpr (C::STAGED) {
+          if (c == 0) stage_free();
           const int k0 = w.whole ? (c & 32) >> 3 : 0;  // piece of the 128 bytes
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -884,6 +905,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         if (lane == 0) mbar_arrive(&taken);
       }
     }
+    if (C::STAGED && lane == 0) bulk_wait_read_all();  // shared memory goes with the CTA
   } else {
     // ------------------------------------------------- E4M3 codes to bf16
     if constexpr (F8) {
@@ -1041,8 +1063,10 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   }
   p.by_length = units > num_sms && a.seq.batch <= LPT_BATCH;
   p.units = (int)(p.tail + (units - p.tail) * p.nsplit);
-  CUtensorMap mq, mk, mv;
-  bool ok = map3(&mq, a.q, D, a.nq, a.seq.rows, a.ld_q, p.ht, p.tok);
+  CUtensorMap mq, mk, mv, mo;
+  p.out_boxes = 32 % p.ht == 0;
+  bool ok = map3(&mo, a.out, D, a.nq, a.seq.rows, a.ld_out, p.out_boxes ? p.ht : 1, p.out_boxes ? 32 / p.ht : 32);
+  ok = ok && map3(&mq, a.q, D, a.nq, a.seq.rows, a.ld_q, p.ht, p.tok);
   if (SRC == PACKED) {
     ok = ok && map3(&mk, a.k, D, a.nkv, a.seq.rows, a.ld_k, 1, KB) && map3(&mv, a.v, D, a.nkv, a.seq.rows, a.ld_v, 1, KB);
   } else {
@@ -1053,7 +1077,7 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   cudaError_t e = allow_smem<var_fwd_kernel<D, SRC, FEW>>(C::SMEM);
   if (e == cudaSuccess) e = check_regs<var_fwd_kernel<D, SRC, FEW>>(C::THREADS, C::SOFTMAX_REGS > 0 ? C::REGS : 0);
   if (e != cudaSuccess) return e;
-  var_fwd_kernel<D, SRC, FEW><<<p.units < num_sms ? p.units : num_sms, C::THREADS, C::SMEM, st>>>(mq, mk, mv, p);
+  var_fwd_kernel<D, SRC, FEW><<<p.units < num_sms ? p.units : num_sms, C::THREADS, C::SMEM, st>>>(mq, mk, mv, mo, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
   if (a.launches) ++*a.launches;
