@@ -450,6 +450,7 @@ tpmlp_status tpkv_extend(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q
   if (!c) return TPMLP_ERR_ARG;
   KV_TRY(kv_check_call(c, batch, past_lens, table, ld_table, max_pages));
   KV_TRY(kv_check_rows(c, rows, batch, cu_rows, new_lens));
+  if (rows > (1 << 28)) return c->fail(TPMLP_ERR_SHAPE, "rows out of range (at most 2^28)");
   const int64_t Z = (int64_t)c->cfg.n_heads * c->cfg.head_dim;
   if (ld_q % 8 != 0 || ld_q < Z || ld_out % 8 != 0 || ld_out < Z)
     return c->fail(TPMLP_ERR_SHAPE, "row strides must be multiples of 8 and hold a row");

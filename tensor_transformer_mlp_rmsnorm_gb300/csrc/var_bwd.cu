@@ -50,6 +50,7 @@ namespace {
 // 88 + 2 x 208 = 3 x 168.
 constexpr int ISSUE_REGS = 88, ROW_REGS = 208;
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
+constexpr uint64_t BLOCK_NS = 60000000000ull;  // for a whole block: the largest that fits memory takes some 6 s
 
 // What a CTA accumulates.  DQ: 128 rows of (token, head) stay, their keys and
 // values stream by.  The others: 128 keys stay, the rows of (token, head) that
@@ -532,7 +533,8 @@ __global__ void __launch_bounds__(384, 1)
             k.n = (k.end - k.at + p.stok - 1) / p.stok * p.schunks;
           }
         }
-        ok = wait_all(&x.work_empty[t & 1], (uint32_t)((t >> 1) & 1) ^ 1u);
+        ok = __all_sync(0xffffffffu, mbar_wait(&x.work_empty[t & 1], (uint32_t)((t >> 1) & 1) ^ 1u, abort_flag, p.status,
+                                               STATUS_TIMEOUT, BLOCK_NS));
         if (ok && lane == 0) {
           x.work[t & 1] = k;
           mbar_arrive(&x.work_full[t & 1]);

@@ -58,6 +58,7 @@ namespace {
 constexpr int KB = 128;  // keys of a step
 constexpr uint32_t SUB = 128 * 128;  // bytes of a [128 x 64] bf16 tile with the 128-byte swizzle
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
+constexpr uint64_t BLOCK_NS = 60000000000ull;  // for a whole block: 2^30 keys take some 13 s
 constexpr float MOVE_LOG2 = 8.0f;  // the running maximum is moved when it is off by more than 2^8
 constexpr int MIN_PART = 4;        // steps of a part at least
 constexpr int TAIL_PART = 12;      // and of one of a last turn's blocks
@@ -588,7 +589,8 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
           }
         }
         const int q = t & 1;
-        ok = wait_all(&work_empty[q], (uint32_t)((t >> 1) & 1) ^ 1u);
+        ok = __all_sync(0xffffffffu, mbar_wait(&work_empty[q], (uint32_t)((t >> 1) & 1) ^ 1u, abort_flag, p.status,
+                                               STATUS_TIMEOUT, BLOCK_NS));
         if (ok && lane == 0) {
           work_sh[q] = w;
           mbar_arrive(&work_full[q]);

@@ -1,6 +1,10 @@
 """Attention over packed sequences and over new tokens with a cache, where blocks of different lengths follow one
 another on a multiprocessor and where arguments are as large as they may be: against float64 with derived bounds
 (tests/_varlen_ops.py)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -132,3 +136,52 @@ def test_values_that_arrive_after_later_keys(d, f8, new, past, nq, nkv):
     for _ in range(20):
         again, _ = c.run()
         assert torch.equal(again, out)
+
+
+def test_more_rows_than_there_may_be_are_refused():
+    T = _tp()
+    c = Case([3], [20], 4, 2, 128, 16)
+    q, out = c.q, torch.empty_like(c.q)
+    status = T.lib().tpkv_extend(c.kv.ctx, 2 ** 28 + 1, 1, q.data_ptr(), 512, c.cu.data_ptr(), None,
+                                 c.past_dev.data_ptr(), c.table.data_ptr(), c.table.shape[1], c.table.shape[1], 0.1, 0, 0,
+                                 out.data_ptr(), 512, None)
+    assert status == T.ERR_SHAPE
+
+
+FIRST_CALLS = """
+import torch, tensor_transformer_mlp_rmsnorm_gb300 as T
+g = torch.Generator(device="cuda").manual_seed(0)
+q, k, v, dout = (torch.randn(300, n * 64, generator=g, device="cuda").bfloat16() for n in (4, 2, 2, 4))
+cu = torch.tensor([0, 170, 300], dtype=torch.int32, device="cuda")
+past = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+table = torch.arange(24, dtype=torch.int32, device="cuda").view(2, 12)
+kc, vc = (torch.zeros(24, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+for b, (lo, hi) in enumerate(((0, 170), (170, 300))):
+    for cache, x in ((kc, k), (vc, v)):
+        pos = torch.arange(hi - lo, device="cuda")
+        cache[table[b][pos // 16].long(), :, pos % 16] = x[lo:hi].view(-1, 2, 64)
+kv = T.TPKV(kc, vc, 4, max_batch=2)
+word = torch.zeros(1, dtype=torch.int32, device="cuda")
+def step():
+    out, lse = T.packed_attention(q, k, v, cu, 4, 2, return_lse=True, status=word)
+    return (out, lse, *T.packed_attention_backward(dout, q, k, v, out, lse, cu, 4, 2, status=word),
+            kv.extend(q, past, table, cu_rows=cu))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert int(word) == 0
+print("same")
+"""
+
+
+def test_captured_before_any_other_call():
+    """A process whose first calls are captured: what a kernel's first launch sets up is no work of a stream."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
