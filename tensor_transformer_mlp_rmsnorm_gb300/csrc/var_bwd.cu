@@ -469,11 +469,6 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else {
       // ------------------------------------------------------------- scheduler
-      if (blockIdx.x == 0) {  // looks at every sequence, for the report
-        bool bad = false;
-        for (int b = lane; b < p.seq.batch; b += 32) seq_span(p.seq, b, -1, &bad);
-        if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
-      }
       ByLength<KB> order;
       if (p.by_length)
         order.init(p.seq, -1, block_tok,
@@ -543,6 +538,7 @@ __global__ void __launch_bounds__(384, 1)
         ++t;
         if (last) break;
       }
+      report_bad(p.seq, -1, p.status, lane);
     }
   } else {
     regs_inc<ROW_REGS>();

@@ -546,11 +546,6 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
       mbar_wait(&drain_bar, 0, &no_abort, p.status, STATUS_TIMEOUT, DRAIN_NS);
     } else if (warp == 2) {
       // ----------------------------------------------------------- scheduler
-      if (blockIdx.x == 0) {  // looks at every sequence, for the report
-        bool bad = false;
-        for (int b = lane; b < p.seq.batch; b += 32) seq_span(p.seq, b, cap, &bad);
-        if (bad) atomicOr(p.status, STATUS_BAD_INDEX);
-      }
       ByLength<KB> order;
       start_order(p, order, block_tok, cap, lane);
       bool ok = true;
@@ -599,6 +594,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         ++t;
         if (end) break;
       }
+      report_bad(p.seq, cap, p.status, lane);
     }
   } else if (warp < 4 + 4 * NT) {
     // --------------------------------------------------------------- softmax

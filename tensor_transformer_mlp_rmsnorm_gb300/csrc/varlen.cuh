@@ -38,6 +38,13 @@ __device__ __forceinline__ SeqSpan seq_span(const SeqRows& s, int b, int64_t cap
   return r;
 }
 
+// One warp a CTA, while the others work: every sequence is looked at, for the report.
+__device__ __forceinline__ void report_bad(const SeqRows& s, int64_t cap, uint32_t* status, int lane) {
+  bool bad = false;
+  for (int64_t b = (int64_t)blockIdx.x * 32 + lane; b < s.batch; b += (int64_t)gridDim.x * 32) seq_span(s, (int)b, cap, &bad);
+  if (bad) atomicOr(status, STATUS_BAD_INDEX);
+}
+
 // Block slots: every block of `tokens` rows of every sequence has one of its own,
 // slot(b) + i, found from either side without looking at the other sequences.
 // Sequences of the same number of rows, and a single one: per_seq slots each.
