@@ -23,16 +23,18 @@
 // and the next dP under P.
 //
 // Measured (GB300; 1980 TFLOP/s is its product rate, flops count 5 products):
-//   one sequence of 8192 tokens, 32 + 8 heads of 128    1371 us, 1003 TFLOP/s (1400 with all 7)
-//   19 sequences, 8192 tokens                            248 us,  421 TFLOP/s of pairs that are seen:
-//     lse and D 26 (bytes), dQ 116, dK and dV 107
+//   one sequence of 8192 tokens, 32 + 8 heads of 128    1365 us, 1007 TFLOP/s (1410 with all 7)
+//   19 sequences, 8192 tokens                            237 us,  440 TFLOP/s of pairs that are seen:
+//     lse and D 26 (bytes), dQ 110, dK and dV 104
 //   5 sequences, 333 tokens, 5 + 1 heads of 64            29 us, three launches' latencies
 // What bounds them.  dK and dV: a step takes some 2950 cycles, its products 2560.
 // dQ: a step takes some 2650 cycles where its products need 1540; one buffer for
 // dP is all that tensor memory has left beside two for scores and dQ, so dP, the row
 // groups' dS and the next dP follow one another.  Short sequences: a block of one to
-// four steps pays some 5000 cycles for its first copies, its statistics and its
-// result.
+// four steps pays some 4000 cycles for its first copies, its statistics and its
+// result.  Heads of 192 and 256: steps of 64 keys, as 128 would not leave room for
+// two in flight, pay the same chain for half the work (2 x 4096 tokens, 16 heads
+// of 192 on 4 key heads: 1435 us, 360 TFLOP/s; of 128: 391 us, 879 TFLOP/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -84,10 +86,7 @@ struct Cfg {
   // are run over twice.
   static constexpr int EXACT = 128 / KB;
   static constexpr bool HELD = EXACT == 1;
-  // Results are turned in shared memory, 64 bytes of a row at a time, where there is room.
-  static constexpr bool STAGED = !(D == 256 && HAS_DP) && D != 128;
-  static constexpr uint32_t STAGE = STAGED ? 8 * 2048 : 0;
-  static constexpr uint32_t TILES = NRES * RB + (N1 + N2) * EB + STAGE;
+  static constexpr uint32_t TILES = NRES * RB + (N1 + N2) * EB;
   static constexpr int READERS = ROLE == DQ ? 10 : 11;  // warps that a block is handed to
 };
 
@@ -289,18 +288,18 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t x1m = sw128_desc(smem_u32(ring1), C::SUB, 1024), x2m = sw128_desc(smem_u32(ring2), C::SUB, 1024);
       auto wait_elems = [&](uint64_t* bars, int stages, int n) -> int {
         int r = 1;
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < NE; ++e)
           r = r && wait_all(&bars[(n * NE + e) % stages], (uint32_t)(((n * NE + e) / stages) & 1));
         return r;
       };
       // scores: resident operand `o` times the streamed one
       auto product = [&](int o, int stages, uint64_t xk, int n, uint32_t col) {
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < NE; ++e) {
           const uint64_t b = desc_advance(xk, ((n * NE + e) % stages) * C::EB);
           const uint64_t a = desc_advance(r_desc, o * C::RB + e * (EC / 64) * C::RSUB);
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < EC / 16; ++kk)
             tc_mma_f16(tmem_base + col, desc_advance(a, (kk >> 2) * C::RSUB + (kk & 3) * 32),
                        desc_advance(b, (kk >> 2) * C::SUB + (kk & 3) * 32), IDESC_S, e > 0 || kk > 0 ? 1u : 0u);
@@ -309,17 +308,17 @@ __global__ void __launch_bounds__(384, 1)
       // accumulator at `acc` += (bf16 rows, each row group's half at the start of
       // its half of the columns from `a_col` on) times the streamed operand
       auto accumulate = [&](int stages, uint64_t xm, int n, uint32_t a_col, uint32_t acc, bool first) {
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < NE; ++e) {
           const uint64_t b = desc_advance(xm, ((n * NE + e) % stages) * C::EB);
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < KB / 16; ++kk)
             tc_mma_f16_ts(tmem_base + acc + e * EC, tmem_base + a_col + kk / (HC / 16) * HC + kk % (HC / 16) * 8,
                           desc_advance(b, kk * 2048), IDESC_A, !first || kk > 0 ? 1u : 0u);
         }
       };
       auto release = [&](uint64_t* bars, int stages, int n) {
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < NE; ++e) tc_commit(&bars[(n * NE + e) % stages]);
       };
       bool ok = true;
@@ -366,7 +365,7 @@ __global__ void __launch_bounds__(384, 1)
           if (elect_one()) put_s(1);
           __syncwarp();
         }
-  #pragma unroll 1
+#pragma unroll 1
         for (int n = 0; ok && n < nk; ++n) {
           const uint32_t par = (uint32_t)((c + n) & 1);
           const bool n1 = n + 1 < nk, n2 = n + 2 < nk;
@@ -450,14 +449,14 @@ __global__ void __launch_bounds__(384, 1)
           const int st = (c + n) & 1;
           const int tok0 = k.at + n / p.schunks * p.stok, hc = n % p.schunks * p.sht;
           float2 v[KB / 32];
-  #pragma unroll
+#pragma unroll
           for (int q = 0; q < KB / 32; ++q) {
             const int r = lane + 32 * q, tk = tok0 + r / p.sht, hh = hc + r % p.sht;
             const bool valid = r < p.sht * p.stok && tk < k.end && hh < p.hpg;
             v[q] = valid ? __ldg(p.stats + (int64_t)(k.first + tk) * p.nq + k.h0 + hh) : make_float2(INFINITY, 0.0f);
           }
           if (!(ok = wait_all(&x.stat_empty[st], (uint32_t)(((c + n) >> 1) & 1) ^ 1u))) break;
-  #pragma unroll
+#pragma unroll
           for (int q = 0; q < KB / 32; ++q) {
             x.nlse2[st][lane + 32 * q] = -v[q].x;
             x.nd[st][lane + 32 * q] = -v[q].y;
@@ -552,7 +551,6 @@ __global__ void __launch_bounds__(384, 1)
     const int tid = grp * 128 + r;
     const uint32_t tl = tmem_base + ((uint32_t)(q4 * 32) << 16) + grp * HC;
     const int tok_r = Q_STAYS ? r / p.ht : r, hh = Q_STAYS ? r - tok_r * p.ht : 0;  // token or key of the row, head
-    uint8_t* stg = ring2 + N2 * C::EB + (warp - 4) * 2048;
     uint32_t pres = 0;
     int ok = 1;
     const BwdBlock* kp;
@@ -645,9 +643,9 @@ __global__ void __launch_bounds__(384, 1)
             const int t = tile0 + crow;
             if (t >= blk.end || (t < blk.lo && t >= blk.sink_end))
               for (int e = 0; e < NE; ++e)
-  #pragma unroll
+#pragma unroll
                 for (int cb = 0; cb < EC / 64; ++cb)
-  #pragma unroll
+#pragma unroll
                   for (int c = 0; c < CPT; ++c)
                     *reinterpret_cast<uint4*>(ring1 + ((N * NE + e) % N1) * C::EB + cb * C::SUB + crow * 128 +
                                               (cpart + c) * 16) = make_uint4(0, 0, 0, 0);
@@ -671,9 +669,9 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             if (crow < p.sht * p.stok && (tok0 + crow / p.sht >= blk.end || hc + crow % p.sht >= p.hpg))
               for (int e = 0; e < NE; ++e)
-  #pragma unroll
+#pragma unroll
                 for (int cb = 0; cb < EC / 64; ++cb)
-  #pragma unroll
+#pragma unroll
                   for (int c = 0; c < CPT; ++c) {
                     const uint32_t o = cb * C::SUB + crow * 128 + (cpart + c) * 16;
                     if (C::HAS_DP) *reinterpret_cast<uint4*>(ring1 + ((N * NE + e) % N1) * C::EB + o) = make_uint4(0, 0, 0, 0);
@@ -684,14 +682,14 @@ __global__ void __launch_bounds__(384, 1)
         }
         // P, 32 columns at a time
         uint32_t w[HC / 2];
-  #pragma unroll
+#pragma unroll
         for (int hf = 0; hf < HC / 32; ++hf) {
           uint32_t* u = v + 32 * hf;
           if (hf == 1) tmem_ld_wait();
           const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
           if (Q_STAYS) {
             const uint64_t nl2 = f2_pack(-lse2, -lse2);
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 32; c += 2) {
               float a0, a1;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sc2, nl2), a0, a1);
@@ -703,14 +701,14 @@ __global__ void __launch_bounds__(384, 1)
               uint32_t bits = below(tk - t + 1);
               if (p.window > 0) bits &= ~below(tk - p.window - t + 1) | below(p.sinks - t);
               if (__any_sync(0xffffffffu, bits != ~0u)) {
-  #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 32; ++c)
                   if (!(bits & (1u << c))) u[c] = 0u;
               }
             }
           } else {
             const ulonglong2* sp = reinterpret_cast<const ulonglong2*>(x.nlse2[st] + grp * HC + 32 * hf);
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 32; c += 4) {
               const ulonglong2 z = sp[c >> 2];
               float a0, a1, a2, a3;
@@ -724,14 +722,14 @@ __global__ void __launch_bounds__(384, 1)
             if (masked) {
               const uint32_t bits = below(c_hi - 32 * hf) & ~below(c_lo - 32 * hf);
               if (__any_sync(0xffffffffu, bits != ~0u)) {
-  #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 32; ++c)
                   if (!(bits & (1u << c))) u[c] = 0u;
               }
             }
           }
           if (C::HAS_PV) {
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 32; c += 2)
               w[16 * hf + (c >> 1)] = pack_bf16(__uint_as_float(u[c]), __uint_as_float(u[c + 1]));
           }
@@ -754,24 +752,24 @@ __global__ void __launch_bounds__(384, 1)
           if constexpr (HC == 64) tmem_ld_32x32b_x32(t_dp + 32, *reinterpret_cast<uint32_t(*)[32]>(dd + 32));
           if (held) {
             tmem_ld_wait();
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < HC; ++c) add(__uint_as_float(v[c]), dd[c]);
             if (!(ok = settle())) break;
             const float inv = 1.0f / l;
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < HC; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * inv);
           }
-  #pragma unroll
+#pragma unroll
           for (int hf = 0; hf < HC / 32; ++hf) {
             uint32_t* d = dd + 32 * hf;
             if (hf == 1) tmem_ld_wait();
             if (Q_STAYS && n < pre) {  // the sums alone
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < 32; ++c) add(__uint_as_float(v[32 * hf + c]), d[c]);
             } else {
               // P (dP - D); the scale comes in at the end
               const ulonglong2* dp = reinterpret_cast<const ulonglong2*>(x.nd[Q_STAYS ? 0 : st] + (Q_STAYS ? 0 : grp * HC + 32 * hf));
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const int cc = 32 * hf + c;
                 ulonglong2 z;
@@ -783,7 +781,7 @@ __global__ void __launch_bounds__(384, 1)
                 f2_unpack(f2_mul(f2_pack(__uint_as_float(v[cc + 2]), __uint_as_float(v[cc + 3])),
                                  f2_add(f2_pack(__uint_as_float(d[c + 2]), __uint_as_float(d[c + 3])), z.y)), e[2], e[3]);
                 if (masked) {  // 0 whatever dP is
-  #pragma unroll
+#pragma unroll
                   for (int k = 0; k < 4; ++k)
                     if (v[cc + k] == 0u) e[k] = 0.0f;
                 }
@@ -820,34 +818,26 @@ __global__ void __launch_bounds__(384, 1)
         else if (ROLE == DV || (ROLE == DKV && grp == 0)) dst = p.dv + row * p.ld_dv + (int64_t)g * D + (ROLE == DKV ? 0 : grp * W);
         else dst = p.dk + row * p.ld_dk + (int64_t)g * D + (ROLE == DKV ? 0 : grp * W);
       }
+      int64_t row_at[4];  // of the four lanes that turn their pieces together
+#pragma unroll
+      for (int q = 0; q < 4; ++q) row_at[q] = __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(dst), (lane & ~3) + q);
       const float fin = ROLE == DV || (ROLE == DKV && grp == 0) ? 1.0f : p.scale;
-  #pragma unroll 1
+#pragma unroll 1
       for (int c = 0; c < W; c += 32) {
         uint32_t o[32];
         tmem_ld_32x32b_x32(t_acc + c, o);
         tmem_ld_wait();
         uint4 u[4];
-  #pragma unroll
+#pragma unroll
         for (int q = 0; q < 4; ++q)
           u[q] = make_uint4(pack_bf16(__uint_as_float(o[8 * q]) * fin, __uint_as_float(o[8 * q + 1]) * fin),
                             pack_bf16(__uint_as_float(o[8 * q + 2]) * fin, __uint_as_float(o[8 * q + 3]) * fin),
                             pack_bf16(__uint_as_float(o[8 * q + 4]) * fin, __uint_as_float(o[8 * q + 5]) * fin),
                             pack_bf16(__uint_as_float(o[8 * q + 6]) * fin, __uint_as_float(o[8 * q + 7]) * fin));
-        if constexpr (C::STAGED) {
-  #pragma unroll
-          for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = u[q];
-          __syncwarp();
-  #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int y = 8 * q + lane / 4, piece = lane & 3;
-            const int64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(dst), y);
-            const uint4 w = *reinterpret_cast<const uint4*>(stg + y * 64 + ((piece ^ ((y >> 1) & 3)) << 4));
-            if (at) *reinterpret_cast<uint4*>(at + 2 * c + 16 * piece) = w;
-          }
-        } else if (dst) {
-  #pragma unroll
-          for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(dst + c)[q] = u[q];
-        }
+        turn_pieces(u, lane);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (row_at[q]) *reinterpret_cast<uint4*>(row_at[q] + 2 * c + 16 * (lane & 3)) = u[q];
         __syncwarp();
       }
       // the accumulators may be overwritten: the next block's first product into them

@@ -197,6 +197,26 @@ template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// Four lanes (4 i to 4 i + 3) have four pieces of 16 bytes of a row each: afterwards
+// lane 4 i + j has piece j of the four rows, so that a store of the k-th fills 64
+// bytes of each of 8 rows.  (One of 16 bytes in each of 32 rows takes some 250 cycles.)
+__device__ __forceinline__ void turn_pieces(uint4 (&u)[4], int lane) {
+  auto swap = [&](uint4& a, uint4& b, int bit) {  // a lane without the bit gives b, one with it gives a
+    const bool has = lane & bit;
+    uint4 g = has ? a : b;
+    g.x = __shfl_xor_sync(0xffffffffu, g.x, bit);
+    g.y = __shfl_xor_sync(0xffffffffu, g.y, bit);
+    g.z = __shfl_xor_sync(0xffffffffu, g.z, bit);
+    g.w = __shfl_xor_sync(0xffffffffu, g.w, bit);
+    if (has) a = g;
+    else b = g;
+  };
+  swap(u[0], u[1], 1);
+  swap(u[2], u[3], 1);
+  swap(u[0], u[2], 2);
+  swap(u[1], u[3], 2);
+}
+
 // Bits 0 to n - 1 of a word.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
