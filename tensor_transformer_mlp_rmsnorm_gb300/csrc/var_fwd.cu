@@ -32,13 +32,13 @@
 //   2 x 2048 tokens behind 30000, the same heads        1431 us, 1452 TFLOP/s
 //   64 tokens behind 131000, the same heads              118 us, 4.6 TB/s and 1166 TFLOP/s
 //   4 x 1024 tokens behind 7000, E4M3                    461 us, 1118 TFLOP/s
-//   19 sequences, 8192 tokens                             75 us,  556 TFLOP/s of pairs that are seen
+//   19 sequences, 8192 tokens                             73 us,  570 TFLOP/s of pairs that are seen
 //   48 x 5 tokens behind up to 8192, E4M3                169 us, 2.5 TB/s
 // What bounds them.  Long: a step of two tiles takes some 2800 to 3300 cycles
 // where its products need 2080, the rest is the way between the issuing warp and
 // the softmax (a wait that is fulfilled costs 150 cycles, a load from tensor
 // memory beside products 300).  Short sequences: a block of one to four steps
-// pays some 7500 cycles for its result (5500) and the next one's start, in which
+// pays some 7000 cycles for its result (5000) and the next one's start, in which
 // the tensor cores rest, and up to half of a step's keys are hidden.  E4M3: 16384 codes an operand are converted by 128 threads, about 1500
 // cycles, which few rows do not hide.
 #include <cuda.h>
