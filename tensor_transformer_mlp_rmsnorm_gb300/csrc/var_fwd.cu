@@ -325,16 +325,19 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
       for (int t = 0, base = 0; ok && (wp = next(t)); give_back(t++)) {
         const Work& w = *wp;
         const int g = w.g, h0 = w.h0;
-        // page of this lane's box in a step: num_pages (nothing is read, zeros land) where no row sees it
-        auto look = [&](int j) -> int {
-          const int at = w.tile(w.j0 + j) * KB + row0, pi = at / p.page_size;
-          const bool seen = (at < w.end && at + p.box > w.lo) || at < w.sink_end;
-          if (!issues || !seen) return (int)p.num_pages;
-          return pi < p.max_pages ? __ldg(p.table + (int64_t)w.b * p.ld_table + pi) : -1;
+        // Whether any row sees this lane's box in a step.  Its page is asked for a step ahead,
+        // and looked at when it is used; num_pages there: nothing is read, zeros land.
+        auto seen = [&](int j) -> bool {
+          const int at = w.tile(w.j0 + j) * KB + row0;
+          return issues && ((at < w.end && at + p.box > w.lo) || at < w.sink_end);
         };
-        auto valid = [&](int page) -> int {
-          if (page >= 0 && page <= p.num_pages) return page;
-          atomicOr(p.status, STATUS_BAD_INDEX);
+        auto look = [&](int j) -> int {
+          const int pi = (w.tile(w.j0 + j) * KB + row0) / p.page_size;
+          return seen(j) && pi < p.max_pages ? __ldg(p.table + (int64_t)w.b * p.ld_table + pi) : -1;
+        };
+        auto valid = [&](int j, int page) -> int {
+          if (page >= 0 && page < p.num_pages) return page;
+          if (seen(j)) atomicOr(p.status, STATUS_BAD_INDEX);
           return (int)p.num_pages;
         };
         auto load = [&](int at, const CUtensorMap* map, int j, int page) -> bool {
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         int page = 0, page_n = 0, page_v = 0;
         if (w.nk > 0) {
           if constexpr (SRC != PACKED) {
-            page = valid(look(0));
+            page = valid(0, look(0));
             if (w.nk > 1) page_n = look(1);
           }
           ok = load(k_at(base, w, 0), &map_k, 0, page);
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         for (int j = 0; ok && j < w.nk; ++j) {
           if (j > 0) {
             if constexpr (SRC != PACKED) {
-              page = valid(page_n);
+              page = valid(j, page_n);
               if (j + 1 < w.nk) page_n = look(j + 1);
             }
             ok = load(k_at(base, w, j), &map_k, j, page);
