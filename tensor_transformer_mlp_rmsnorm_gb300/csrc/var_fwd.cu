@@ -697,7 +697,9 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         }
         const float mb =
             fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale_log2;
-        const bool move = __any_sync(0xffffffffu, mb > m_run + MOVE_LOG2);
+        // Lanes without a result have no say: their queries are other sequences', nobody's or
+        // no copy's, and the frame that P is rounded in must not depend on those.
+        const bool move = __any_sync(0xffffffffu, stored && mb > m_run + MOVE_LOG2);
         if (move) {
           const float m_new = fmaxf(m_run, mb);
           const float alpha = m_new == -INFINITY ? 1.0f : ex2_fast(m_run - m_new);  // 0 on the first step

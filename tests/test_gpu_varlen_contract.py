@@ -30,3 +30,76 @@ def test_the_first_page_past_the_end_is_reported(d, f8, new, past):
     assert all(torch.equal(a, b) for a, b in zip(c.run(), (want, wl)))
 
 
+
+
+def _steep(q, k, spans, hot):
+    """Scores whose maxima keep rising: keys grow along the rows; rows of q in `hot` are 40 times as large."""
+    for lo, hi in spans:
+        k[lo:hi] *= torch.linspace(0.5, 1.5, hi - lo, device="cuda")[:, None].to(k.dtype)
+    for lo, hi in hot:
+        q[lo:hi] *= 40.0
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("nq,nkv", [(4, 1), (3, 3), (6, 2), (5, 1)])
+def test_finite_rows_of_others_do_not_matter(d, nq, nkv):
+    """The bits of a sequence are the same whatever (finite) numbers its neighbours and rows of nobody hold: their
+    queries lie in the same tiles, and their scores against its keys rise by more than its own."""
+    T = _tp()
+    from tests.test_gpu_packed_attention import _inputs
+    lens = [701, 50, 943, 9]
+    q, k, v, dout, cu = _inputs(lens, nq, nkv, d, 5, extra=30)
+    _steep(q, k, ((0, 701), (751, 1694)), ())
+    run = lambda: T.packed_attention(q, k, v, cu, nq, nkv, return_lse=True)  # noqa: E731
+    out, lse = run()
+    gr = T.packed_attention_backward(dout, q, k, v, out, lse, cu, nq, nkv)
+    for lo, hi in ((701, 751), (1694, 1733)):
+        for t in (q, k, v, dout):
+            t[lo:hi] *= 40.0
+    out2, lse2 = run()
+    gr2 = T.packed_attention_backward(dout, q, k, v, out2, lse2, cu, nq, nkv)
+    T.packed_attention_check()
+    for a, b in zip((out, lse, *gr), (out2, lse2, *gr2)):
+        for lo, hi in ((0, 701), (751, 1694)):
+            assert torch.equal(a[lo:hi], b[lo:hi])
+
+
+@pytest.mark.parametrize("d,f8", [(64, False), (128, False), (128, True), (192, True), (256, False)])
+@pytest.mark.parametrize("per,new", [(70, [61, 5, 33]), (9, [5, 0, 3])])
+def test_queries_of_padding_do_not_matter(d, f8, per, new):
+    c = Case(new, [900, 500, 1300], 4, 2, d, 16, f8)
+    kv, n = c.kv, len(new) * per
+    q = torch.zeros(n, 4 * d, dtype=BF, device="cuda")
+    mine = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for b, m in enumerate(new):
+        q[b * per: b * per + m] = c.q[c.cul[b]: c.cul[b + 1]]
+        mine[b * per: b * per + m] = True
+    noise = torch.randn(n, 4 * d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF)
+    lens = torch.tensor(new, **I32)
+    got = []
+    for size in (0.0, 40.0):
+        x = torch.where(mine[:, None], q, noise * size)
+        got.append(kv.extend(x, c.past_dev, c.table, new_lens=lens, return_lse=True))
+    kv.sync()
+    for a, b in zip(*got):
+        assert torch.equal(a[mine], b[mine])
+    out, lse = (x[mine] for x in got[1])
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("nq", [3, 5, 7])
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+def test_shared_memory_of_earlier_kernels_does_not_matter(nq, d):
+    """Groups that do not fill a tile: the rest of its rows hold what was in shared memory before."""
+    T = _tp()
+    from tests.test_gpu_packed_attention import _inputs
+    q, k, v, _, cu = _inputs([700, 1100], nq, 1, d, 3)
+    _steep(q, k, ((0, 700), (700, 1800)), ())
+    fill, kf, vf, _, cf = _inputs([4096 * 4], 8, 4, d, 4)
+    want = None
+    for size in (0.0, 1.0, 30.0, 1000.0):
+        T.packed_attention(fill * size, kf, vf, cf, 8, 4)
+        got = T.packed_attention(q, k, v, cu, nq, 1, return_lse=True)
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), size
+    T.packed_attention_check()
