@@ -60,6 +60,9 @@ constexpr uint32_t SUB = 128 * 128;  // bytes of a [128 x 64] bf16 tile with the
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
 constexpr uint64_t BLOCK_NS = 60000000000ull;  // for a whole block: 2^30 keys take some 13 s
 constexpr float MOVE_LOG2 = 8.0f;  // the running maximum is moved when it is off by more than 2^8
+// In place of a scale of 0: the smallest number there is, which keeps hidden scores at -inf
+// and makes less than 10^-6 of the largest others.
+constexpr float NO_SCALE = 1.4e-45f;
 constexpr int MIN_PART = 4;        // steps of a part at least
 constexpr int TAIL_PART = 12;      // and of one of a last turn's blocks
 constexpr int PART_STEPS = 5;      // steps in the time of a part's start and result
@@ -628,6 +631,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
       float scale_log2 = p.scale_log2, vscale = 1.0f;
       if constexpr (F8) {
         if (p.k_inv_scale) scale_log2 *= p.k_inv_scale[w.g];
+        if (scale_log2 == 0.0f) scale_log2 = NO_SCALE;
         if (p.v_inv_scale) vscale = p.v_inv_scale[w.g];
       }
       float m_run = -INFINITY, l = 0.0f;
@@ -1114,10 +1118,9 @@ cudaError_t launch_var_fwd(const VarFwdArgs& a, int num_sms, cudaStream_t st) {
   p.chunks = (p.hpg + p.ht - 1) / p.ht;
   p.tok = 128 / p.ht;
   p.heads = a.nkv * p.chunks;
-  // a scale of 0 keeps hidden scores at -inf
   p.negate = a.scale < 0.0f;
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
-  if (p.scale_log2 < 1e-30f) p.scale_log2 = 1e-30f;
+  if (p.scale_log2 == 0.0f) p.scale_log2 = NO_SCALE;
   p.window = a.window;
   p.sinks = a.sinks;
   p.status = a.status;

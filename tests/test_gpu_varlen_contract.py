@@ -103,3 +103,34 @@ def test_shared_memory_of_earlier_kernels_does_not_matter(nq, d):
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(want, got)), size
     T.packed_attention_check()
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-38, -1e-40])
+@pytest.mark.parametrize("f8", [None, False, True])
+def test_a_scale_of_zero_with_large_scores(scale, f8):
+    """Products of up to 2^126 count as the scale says: nothing, so that every visible token weighs the same; inverse
+    scales of the cache that make it smaller still hide nothing and show nothing."""
+    T = _tp()
+    n, past, nq, nkv, d = 40, 200, 4, 2, 128
+    c = Case([n], [past], nq, nkv, d, 16, bool(f8))
+    c.q *= 2.0 ** 60
+    sc = torch.tensor(scale, dtype=torch.float32).item()
+    if f8 is None:
+        g = torch.Generator(device="cuda").manual_seed(2)
+        k, v = (torch.randn(n, nkv * d, generator=g, device="cuda").to(BF) for _ in "kv")
+        k *= 2.0 ** 60
+        out, lse = T.packed_attention(c.q, k, v, c.cu, nq, nkv, scale=scale, return_lse=True)
+        T.packed_attention_check()
+        K, V, past = k.double().unflatten(1, (nkv, d)), v.double().unflatten(1, (nkv, d)), 0
+    else:
+        if f8:
+            c.ks *= 2.0 ** -20
+            c.kd[0] *= 2.0 ** -20
+        else:
+            c.k *= 2.0 ** 60
+            c.kd[0] *= 2.0 ** 60
+        out, lse = c.run(scale=scale)
+        K, V = c.kd[0], c.vd[0]
+    o, z, ot, zt = R.forward(c.q.double().unflatten(1, (nq, d)), K, V, R.seen(n, past, 0, 0), sc)
+    R.close(out.unflatten(1, (nq, d)), o, ot, "out")
+    R.close(lse, z, zt, "lse")
