@@ -486,18 +486,12 @@ __global__ void __launch_bounds__(384, 1)
           k.g = Q_STAYS ? hd / p.chunks : hd;
           k.h0 = k.g * p.hpg + (Q_STAYS ? hd % p.chunks * p.ht : 0);
           k.nh = Q_STAYS ? min(p.ht, (k.g + 1) * p.hpg - k.h0) : p.hpg;
-          int b, i = 0;
-          if (p.by_length) {
-            order.find(rank, lane, &b, &i);
-          } else {
-            b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
-            i = -1;  // below
+          int b, i, next;  // next: the rank of the next one that there may be a block at
+          SeqSpan s;
+          if (!find_ranked(p.seq, p.slots, p.by_length, order, rank, block_tok, -1, lane, &b, &i, &s, &next)) {
+            turn = max(turn, (int)((int64_t)next * p.heads / gridDim.x) - 1);
+            continue;
           }
-          if (b < 0) continue;
-          bool bad = false;
-          const SeqSpan s = seq_span(p.seq, b, -1, &bad);
-          if (i < 0) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
-          if (i < 0 || (int64_t)i * block_tok >= s.count) continue;
           // key blocks from the first on are the long ones
           if (!Q_STAYS) i = (s.count - 1) / block_tok - i;
           k.b = b;

@@ -172,17 +172,11 @@ __device__ __forceinline__ int part_steps(const FwdParams& p, int n) {
   return max(p.min_part, (n + p.nsplit - 1) / p.nsplit);
 }
 
-// Block `rank` of the order in which blocks are taken, by the lanes of one warp; false: none.
 __device__ __forceinline__ bool find_block(const FwdParams& p, ByLength<KB>& order, int rank, int block_tok, int64_t cap,
-                                           int lane, Block* k) {
-  int b, i = -1;
-  if (p.by_length) order.find(rank, lane, &b, &i);
-  else b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
-  if (b < 0) return false;
-  bool bad = false;  // reported elsewhere
-  const SeqSpan s = seq_span(p.seq, b, cap, &bad);
-  if (!p.by_length) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
-  if (i < 0 || (int64_t)i * block_tok >= s.count) return false;
+                                           int lane, Block* k, int* next) {
+  int b, i;
+  SeqSpan s;
+  if (!find_ranked(p.seq, p.slots, p.by_length, order, rank, block_tok, cap, lane, &b, &i, &s, next)) return false;
   fill_block(k, s, b, i, p.tok, block_tok, p.window, p.sinks);
   return true;
 }
@@ -574,7 +568,12 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
           w.g = hd / p.chunks;
           w.h0 = w.g * p.hpg + hd % p.chunks * p.ht;
           w.nh = min(p.ht, (w.g + 1) * p.hpg - w.h0);
-          if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &w)) continue;
+          int rank;  // the next one that there may be a block at
+          if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &w, &rank)) {
+            const int64_t to = (int64_t)rank * p.heads, at = to <= p.tail ? to : p.tail + (to - p.tail) * p.nsplit;
+            k = max(k, (int)(at / gridDim.x) - 1);
+            continue;
+          }
           const int per = shared ? part_steps(p, w.n) : w.n;
           w.j0 = split * per;
           if (split > 0 && w.j0 >= w.n) continue;
@@ -985,7 +984,8 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p, int ti
   ByLength<KB> order;
   start_order(p, order, block_tok, cap, lane);
   Block k;
-  if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &k) || tk >= k.count) return;
+  int next;
+  if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &k, &next) || tk >= k.count) return;
   const int per = part_steps(p, k.n);
   if (per >= k.n) return;  // one CTA's
   const int parts = (k.n + per - 1) / per;

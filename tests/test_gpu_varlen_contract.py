@@ -134,3 +134,49 @@ def test_a_scale_of_zero_with_large_scores(scale, f8):
     o, z, ot, zt = R.forward(c.q.double().unflatten(1, (nq, d)), K, V, R.seen(n, past, 0, 0), sc)
     R.close(out.unflatten(1, (nq, d)), o, ot, "out")
     R.close(lse, z, zt, "lse")
+
+
+@pytest.mark.parametrize("at", [0, 1 << 19, (1 << 20) - 3])
+def test_many_empty_sequences_and_key_heads(at):
+    """2^20 sequences, three of them with rows, and 256 key heads: nobody waits too long for the blocks."""
+    T = _tp()
+    from tests.test_gpu_packed_attention import _inputs
+    heads, d = 256, 64
+    q, k, v, dout, cu = _inputs([70, 1, 229], heads, heads, d, 3)
+    out, lse = T.packed_attention(q, k, v, cu, heads, heads, return_lse=True)
+    gr = T.packed_attention_backward(dout, q, k, v, out, lse, cu, heads, heads)
+    wide = torch.full(((1 << 20) + 1,), 300, **I32)
+    wide[: at + 1] = 0
+    wide[at + 1: at + 4] = cu[1:]
+    out2, lse2 = T.packed_attention(q, k, v, wide, heads, heads, return_lse=True)
+    gr2 = T.packed_attention_backward(dout, q, k, v, out2, lse2, wide, heads, heads)
+    T.packed_attention_check()
+    for a, b in zip((out, lse, *gr), (out2, lse2, *gr2)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("padded", [False, True])
+def test_many_sequences_without_new_tokens(padded):
+    """2^20 sequences over a cache, few of them with new tokens, as row ranges and as padded rows."""
+    T = _tp()
+    n, nq, nkv, d = 1 << 20, 2, 2, 64
+    c = Case([1] * 4, [5, 17, 40, 0], nq, nkv, d, 16)
+    want, wl = c.run()
+    mine = torch.tensor([0, 7, n // 2, n - 1], device="cuda")
+    table = torch.zeros(n, c.table.shape[1], **I32)
+    past = torch.zeros(n, **I32)
+    table[mine], past[mine] = c.table, c.past_dev
+    new = torch.zeros(n, **I32)
+    new[mine] = 1
+    kv = T.TPKV(c.k, c.v, nq, max_batch=n)
+    if padded:
+        q = torch.zeros(n, nq * d, dtype=BF, device="cuda")
+        q[mine] = c.q
+        out, lse = kv.extend(q, past, table, new_lens=new, return_lse=True)
+        out, lse = out[mine], lse[mine]
+    else:
+        cu = torch.zeros(n + 1, **I32)
+        cu[1:] = new.cumsum(0)
+        out, lse = kv.extend(c.q, past, table, cu_rows=cu, return_lse=True)
+    kv.sync()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
