@@ -542,7 +542,7 @@ TPMLP_API tpmlp_status tpattn_qk_rope_backward(const tpattn_qk_desc* desc, const
  * tpmlp_last_error(NULL). */
 typedef struct {
   int64_t rows;        /* of every tensor, at most 2^28 */
-  int32_t batch;       /* sequences, at most 2^20 */
+  int32_t batch;       /* sequences, at most 2^20; batch max(n_kv_heads, n_heads / 64) + rows n_heads / 64 < 2^30 */
   int32_t n_heads, n_kv_heads;
   int32_t head_dim;    /* 64, 128, 192 or 256 */
   const int32_t* cu_rows; /* device [batch + 1], ascending: sequence b has the rows [cu_rows[b], cu_rows[b+1]) */
@@ -675,8 +675,9 @@ TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, 
  * window or t < sinks).
  *  q bf16 [rows, n_heads d] (row stride ld_q) -> out bf16 [rows, n_heads d]
  *  (row stride ld_out; may be q with the same stride), lse float [rows, n_heads]
- *  or NULL, as in tpkv_decode.  Rows of an inactive sequence get out 0 and lse
- *  -inf; rows of padding and of nobody are left as they were.  Nothing behind a
+ *  or NULL, as in tpkv_decode.  At most 2^28 rows; batch and rows times heads as
+ *  in tpattn_packed_desc.  Rows of an inactive sequence get out 0 and lse -inf;
+ *  rows of padding and of nobody are left as they were.  Nothing behind a
  *  sequence's last token, in pages or table, and no page that all of its rows'
  *  windows have left, influences the result.  Repeated calls give the same bits. */
 TPMLP_API tpmlp_status tpkv_extend(tpkv_ctx* ctx, int64_t rows, int32_t batch, const void* q, int64_t ld_q,

@@ -558,6 +558,8 @@ tpmlp_status tpattn_forward_packed(tpattn_ctx* c, int64_t tokens, int32_t batch,
   if (batch < 1 || batch > (1 << 20)) return c->fail(TPMLP_ERR_SHAPE, "batch out of range (1 to 2^20)");
   if (!cu_rows) return c->fail(TPMLP_ERR_ARG, "cu_rows is NULL");
   if (reinterpret_cast<uintptr_t>(cu_rows) & 3u) return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
+  if (!var_fits(SeqRows{cu_rows, nullptr, nullptr, batch, 0, tokens}, c->cfg.n_heads, c->cfg.n_kv_heads))
+    return c->fail(TPMLP_ERR_SHAPE, "too many blocks: sequences and rows times key heads");
   ATTN_TRY(attn_check_forward(c, x, norm_w, w_qkv, w_o, b_o, eps, t, y));
   return attn_run_forward(c, batch, 0, (int)tokens, cu_rows, x, norm_w, w_qkv, w_o, b_o, eps, y);
 }
@@ -1211,6 +1213,7 @@ tpmlp_status tpattn_extend(tpattn_ctx* c, tpkv_ctx* kv, int64_t rows, int32_t ba
   const tpattn_config& cf = c->cfg;
   const int N = (int)rows, d = cf.head_dim, W = (cf.n_heads + 2 * cf.n_kv_heads) * d, Zc = cf.n_heads * d;
   const SeqRows seq{cu_rows, new_lens, past_lens, batch, N / batch, rows};
+  if (const tpmlp_status s = kv_check_blocks(kv, seq)) return c->fail(s, kv->err);
   QkTransform tr;
   if (c->qk_on) tr = {&c->qk_freqs, c->qk.q_norm_w, c->qk.k_norm_w, c->qk.eps};
   return attn_answer(c, N, x, norm_w, w_qkv, w_o, b_o, eps, y, [&](void* qkv, void* z) {

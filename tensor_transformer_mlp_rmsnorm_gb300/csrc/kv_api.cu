@@ -462,6 +462,7 @@ tpmlp_status tpkv_extend(tpkv_ctx* c, int64_t rows, int32_t batch, const void* q
     return c->fail(TPMLP_ERR_ARG, "tensor not 16-byte aligned");
   if (q == out && ld_q != ld_out && rows > 1) return c->fail(TPMLP_ERR_ARG, "in place needs equal strides");
   const SeqRows seq{cu_rows, new_lens, past_lens, batch, (int)(rows / batch), rows};
+  KV_TRY(kv_check_blocks(c, seq));
   return kv_run_extend(c, seq, q, ld_q, table, ld_table, max_pages, scale, window, sinks, out, ld_out, lse, c->stream);
 }
 
@@ -519,6 +520,12 @@ tpmlp_status kv_check_rows(tpkv_ctx* c, int64_t rows, int32_t batch, const int32
   if ((reinterpret_cast<uintptr_t>(cu_rows) | reinterpret_cast<uintptr_t>(new_lens)) & 3u)
     return c->fail(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
   return TPMLP_OK;
+}
+
+tpmlp_status kv_check_blocks(tpkv_ctx* c, const SeqRows& s) {
+  return var_fits(s, c->cfg.n_heads, c->cfg.n_kv_heads)
+             ? TPMLP_OK
+             : c->fail(TPMLP_ERR_SHAPE, "too many blocks: sequences and rows times key heads");
 }
 
 tpmlp_status kv_check_append(tpkv_ctx* c) {

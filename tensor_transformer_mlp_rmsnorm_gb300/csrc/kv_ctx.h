@@ -57,6 +57,7 @@ tpmlp_status kv_check_call(tpkv_ctx* c, int64_t batch, const int32_t* lens, cons
                            int32_t max_pages);
 tpmlp_status kv_check_append(tpkv_ctx* c);
 tpmlp_status kv_check_rows(tpkv_ctx* c, int64_t rows, int32_t batch, const int32_t* cu_rows, const int32_t* new_lens);
+tpmlp_status kv_check_blocks(tpkv_ctx* c, const SeqRows& s);  // batch and rows > 0
 tpmlp_status kv_run_append(tpkv_ctx* c, int64_t rows, int32_t batch, const void* qkv, int64_t ld_qkv,
                            const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
                            const int32_t* table, int64_t ld_table, int32_t max_pages, const QkTransform& tr,

@@ -891,7 +891,7 @@ cudaError_t launch_role(BwdParams p, const VarBwdArgs& a, int num_sms, cudaStrea
   p.stok = C::KB / p.sht;
   p.slots = make_slots(a.seq, block_tok);
   const int64_t units = p.slots.count * p.heads;
-  if (units > 0x7fffffff / 2) return cudaErrorInvalidConfiguration;
+  if (units > VAR_MAX_BLOCKS) return cudaErrorInvalidConfiguration;  // var_fits
   p.units = (int)units;
   p.by_length = units > num_sms && a.seq.batch <= LPT_BATCH;
   CUtensorMap r1, r2, x1, x2;

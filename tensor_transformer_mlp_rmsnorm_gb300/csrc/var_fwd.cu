@@ -1042,7 +1042,7 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   static_assert(C::SMEM + 900 + (C::NT == 2 ? 1024 : 0) <= 232448, "shared memory");
   p.slots = make_slots(a.seq, C::QTILES * p.tok);
   const int64_t units = p.slots.count * p.heads;
-  if (units > 0x7fffffff / 2) return cudaErrorInvalidConfiguration;
+  if (units > VAR_MAX_BLOCKS) return cudaErrorInvalidConfiguration;  // var_fits
   // Few blocks: all are shared.  Many: the CTAs take them in turns, and a last turn
   // with work for less than half of them shares out its blocks, which are the shortest.
   // (With more the parts' own time is what it costs: 48 x 5 tokens behind up to 8192 in

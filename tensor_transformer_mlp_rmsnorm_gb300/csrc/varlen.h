@@ -25,6 +25,18 @@ struct SeqRows {
   int64_t rows;
 };
 
+// Blocks of a call (those of all sequences, times key heads) are numbered in 31 bits, with
+// room for the turn behind them.  A tile has 128 rows of (token, head): the bound counts
+// blocks of one tile; those of two are fewer.
+constexpr int64_t VAR_MAX_BLOCKS = 0x7fffffff / 2;
+inline bool var_fits(const SeqRows& s, int nq, int nkv) {
+  const int hpg = nq / nkv, ht = hpg < 128 ? hpg : 128, tok = 128 / ht;
+  const int64_t heads = (int64_t)nkv * ((hpg + ht - 1) / ht);
+  const int64_t slots = s.cu_rows && s.batch > 1 ? s.rows / tok + s.batch
+                        : (int64_t)((s.rows / s.batch + tok - 1) / tok) * s.batch;
+  return slots <= VAR_MAX_BLOCKS / heads;
+}
+
 // Forward: q, out [rows, >= nq d] bf16, lse [rows, nq] natural log or null.
 // Keys and values: rows of their own (packed), or a paged cache.
 struct VarFwdArgs {

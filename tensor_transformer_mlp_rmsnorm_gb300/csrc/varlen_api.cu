@@ -23,6 +23,14 @@ bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
     if (s_ != TPMLP_OK) return s_;  \
   } while (0)
 
+SeqRows rows_of(const tpattn_packed_desc* p) {
+  SeqRows s{};
+  s.cu_rows = p->cu_rows;
+  s.batch = p->batch;
+  s.rows = p->rows;
+  return s;
+}
+
 tpmlp_status check_desc(const tpattn_packed_desc* p) {
   if (!p) return bad(TPMLP_ERR_ARG, "descriptor is NULL");
   if (p->reserved != 0) return bad(TPMLP_ERR_ARG, "reserved must be 0");
@@ -36,6 +44,8 @@ tpmlp_status check_desc(const tpattn_packed_desc* p) {
   if (reinterpret_cast<uintptr_t>(p->cu_rows) & 3u) return bad(TPMLP_ERR_ARG, "index tensor not 4-byte aligned");
   if (!std::isfinite(p->scale)) return bad(TPMLP_ERR_ARG, "scale must be finite");
   if (p->window < 0 || p->sinks < 0) return bad(TPMLP_ERR_ARG, "window and sinks must be >= 0");
+  if (p->rows > 0 && p->batch > 0 && !var_fits(rows_of(p), p->n_heads, p->n_kv_heads))
+    return bad(TPMLP_ERR_SHAPE, "too many blocks: sequences and rows times key heads");
   return TPMLP_OK;
 }
 
@@ -64,14 +74,6 @@ tpmlp_status current_sms(int* sms) {
   if (dev >= 0 && dev < 64) cached[dev] = n;
   *sms = n;
   return TPMLP_OK;
-}
-
-SeqRows rows_of(const tpattn_packed_desc* p) {
-  SeqRows s{};
-  s.cu_rows = p->cu_rows;
-  s.batch = p->batch;
-  s.rows = p->rows;
-  return s;
 }
 
 }  // namespace

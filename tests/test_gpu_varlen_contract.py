@@ -180,3 +180,22 @@ def test_many_sequences_without_new_tokens(padded):
         out, lse = kv.extend(c.q, past, table, cu_rows=cu, return_lse=True)
     kv.sync()
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_extend_over_too_many_blocks_is_refused():
+    """2^20 sequences of 65536 key heads; nothing is launched, and the context goes on."""
+    T = _tp()
+    n, heads = 1 << 20, 65536
+    k = torch.zeros(1, heads, 8, 64, dtype=BF, device="cuda")
+    kv = T.TPKV(k, k.clone(), heads, max_batch=n)
+    q = torch.zeros(1, heads * 64, dtype=BF, device="cuda")
+    out = torch.full_like(q, 3.0)
+    zeros = torch.zeros(n + 1, **I32)
+    with pytest.raises(T.TPMLPError) as e:
+        kv.extend(q, zeros[:n], zeros[:n, None], cu_rows=zeros, out=out)
+    assert e.value.status == T.ERR_SHAPE
+    kv.sync()
+    assert bool((out == 3.0).all())
+    kv.extend(q, zeros[:1], zeros[:1, None], out=out)
+    kv.sync()
+    assert bool((out == 0.0).all())
