@@ -930,8 +930,6 @@ int kv_decode_workers(int num_sms) { return 2 * num_sms; }
 
 bool make_cache_map(CUtensorMap* m, const void* ptr, bool e4m3, int d, int page_size, int nkv, int64_t num_pages,
                     int64_t stride_page, int64_t stride_head, int64_t stride_slot, int box_tokens) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
   const uint64_t e = e4m3 ? 1 : 2;
   // {block of columns, slot, block, key head, page}: a box of all blocks lands
   // as [box_tokens][block] one behind the other (Cfg::BLOCK bytes a block's row)
@@ -939,10 +937,8 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, bool e4m3, int d, int page_
   cuuint64_t dims[5] = {blk / e, (cuuint64_t)page_size, row / blk, (cuuint64_t)nkv, (cuuint64_t)num_pages};
   cuuint64_t strides[4] = {(cuuint64_t)stride_slot * e, blk, (cuuint64_t)stride_head * e, (cuuint64_t)stride_page * e};
   cuuint32_t box[5] = {(cuuint32_t)(blk / e), (cuuint32_t)box_tokens, (cuuint32_t)(row / blk), 1, 1};
-  cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, blk == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, ptr, dims, strides, box,
+                      blk == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 cudaError_t launch_kv_decode(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int d, bool e4m3,

@@ -1023,17 +1023,12 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p, int ti
 
 // {64 columns, box slots} of a cache {d, page_size, nkv, pages}; E4M3 codes lie unswizzled, 64 bytes a row.
 bool map_cache(CUtensorMap* m, const void* ptr, const VarFwdArgs& a, int box_tokens) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
   const cuuint64_t e = a.e4m3 ? 1 : 2;
   cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.page_size, (cuuint64_t)a.nkv, (cuuint64_t)a.num_pages};
   cuuint64_t strides[3] = {(cuuint64_t)a.stride_slot * e, (cuuint64_t)a.stride_head * e, (cuuint64_t)a.stride_page * e};
   cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, 1, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
-             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             a.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, ptr, dims, strides,
+                      box, a.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D, int SRC, bool FEW>

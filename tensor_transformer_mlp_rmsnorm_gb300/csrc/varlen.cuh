@@ -258,15 +258,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 // {64 columns, mid, rows} boxes of a tensor {d, mid count, rows} with strides in elements.
 inline bool map3(CUtensorMap* m, const void* ptr, int d, int mid, int64_t rows, int64_t ld, int box_mid, int box_rows) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)mid, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)box_mid, (cuuint32_t)box_rows};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace tpmlp
