@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -964,35 +965,43 @@ def _lse(lse, wanted: bool, rows: int, heads: int, device, index: int):
 
 
 _packed_words = {}  # device index -> the status word of the calls on it that were given none
+_packed_lock = threading.Lock()  # held while one of them is launched, and while a word is read and cleared
 
 
-def _packed_status(status, device, index: int):
+def _packed_call(status, device, index: int, fn, *args):
+    """fn(*args, status word, stream): with the given word, or with the device's own."""
+    stream = _stream_of(device, index)
     if status is not None:
         if status.numel() < 1 or status.get_device() != index or status.dtype not in (torch.int32, torch.uint32):
             raise _bad(status, "status", f"a 32-bit integer tensor on cuda:{index}")
-        return status.data_ptr()
-    word = _packed_words.get(index)
-    if word is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise TPMLPError(ERR_ORDER, "call once outside a capture first, or give a status tensor")
-        word = torch.zeros(1, dtype=_I32T, device=device)
-        torch.cuda.current_stream(device).synchronize()  # calls on any stream find it cleared
-        _packed_words[index] = word
-    return word.data_ptr()
+        _on_device(index, fn, *args, status.data_ptr(), stream)
+        return
+    with _packed_lock:
+        word = _packed_words.get(index)
+        if word is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise TPMLPError(ERR_ORDER, "call once outside a capture first, or give a status tensor")
+            word = torch.zeros(1, dtype=_I32T, device=device)
+            torch.cuda.current_stream(device).synchronize()  # calls on any stream find it cleared
+            _packed_words[index] = word
+        _on_device(index, fn, *args, word.data_ptr(), stream)
 
 
 def packed_attention_check(device=None):
-    """Waits for the device's current stream and raises where a packed_attention call on the device (those without a
-    ``status`` of their own) met cu_rows that descend or leave the rows, or gave up a wait.  Clears the report."""
+    """Waits for the device and raises where a packed_attention call on it, on any stream (those without a ``status``
+    of their own), met cu_rows that descend or leave the rows, or gave up a wait.  Clears the report: graphs with such
+    calls must not be replayed meanwhile, and no stream be captured."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     index = torch.cuda.current_device() if dev.index is None else dev.index
     word = _packed_words.get(index)
     if word is None:
         return
-    with torch.cuda.device(index):
+    with _packed_lock, torch.cuda.device(index):
+        torch.cuda.synchronize(index)
         st = int(word.item())
         if st:
             word.zero_()
+            torch.cuda.current_stream(index).synchronize()
     if st & 1:
         raise TPMLPError(ERR_TIMEOUT, "a bounded device wait gave up")
     if st:
@@ -1035,8 +1044,8 @@ def packed_attention(q, k, v, cu_rows, n_heads: int, n_kv_heads: int, scale: flo
         out = q.new_empty((n, n_heads * d))
     op, _, ldo = _rows(out, n_heads * d, _BF, "out", index, n)
     lse = _lse(lse, return_lse, n, n_heads, q.device, index)
-    _on_device(index, lib().tpattn_packed_forward, desc, *ptrs, op, ldo, lse.data_ptr() if lse is not None else None,
-               _packed_status(status, q.device, index), _stream_of(q.device, index))
+    _packed_call(status, q.device, index, lib().tpattn_packed_forward, desc, *ptrs, op, ldo,
+                 lse.data_ptr() if lse is not None else None)
     return out if lse is None else (out, lse)
 
 
@@ -1068,9 +1077,8 @@ def packed_attention_backward(dout, q, k, v, out, lse, cu_rows, n_heads: int, n_
     dqp, _, ldq = _rows(dq, wq, _BF, "dq", index, n)
     dkp, _, ldk = _rows(dk, wk, _BF, "dk", index, n)
     dvp, _, ldv = _rows(dv, wk, _BF, "dv", index, n)
-    _on_device(index, lib().tpattn_packed_backward, desc, *ptrs, op, ldo, lse.data_ptr(), gp, ldg, dqp, ldq, dkp, ldk,
-               dvp, ldv, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-               _packed_status(status, q.device, index), _stream_of(q.device, index))
+    _packed_call(status, q.device, index, lib().tpattn_packed_backward, desc, *ptrs, op, ldo, lse.data_ptr(), gp, ldg,
+                 dqp, ldq, dkp, ldk, dvp, ldv, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv
 
 

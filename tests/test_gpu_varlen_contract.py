@@ -199,3 +199,63 @@ def test_extend_over_too_many_blocks_is_refused():
     kv.extend(q, zeros[:1], zeros[:1, None], out=out)
     kv.sync()
     assert bool((out == 0.0).all())
+
+
+def test_a_report_of_another_stream_is_waited_for():
+    """The check sees a call that is still to come on another stream, once."""
+    T = _tp()
+    from tests.test_gpu_packed_attention import _inputs
+    q, k, v, dout, cu = _inputs([40, 60], 2, 1, 64, 7)
+    bad = torch.tensor([0, 60, 40], **I32)
+    T.packed_attention(q, k, v, cu, 2, 1)
+    T.packed_attention_check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # some 0.1 s
+    T.packed_attention(q, k, v, bad, 2, 1, stream=side)
+    with pytest.raises(T.TPMLPError) as e:
+        T.packed_attention_check()
+    assert e.value.status == T.ERR_ARG
+    side.synchronize()
+    T.packed_attention_check()
+
+
+def test_first_calls_of_two_threads_share_one_word(monkeypatch):
+    import threading
+    import time
+    T = _tp()
+    from tests.test_gpu_packed_attention import _inputs
+    q, k, v, dout, cu = _inputs([40, 60], 2, 1, 64, 7)
+    T.packed_attention(q, k, v, cu, 2, 1)
+    torch.cuda.synchronize()
+    keep = dict(T.tpmlp._packed_words)
+    T.tpmlp._packed_words.clear()
+    made, zeros, start = [], torch.zeros, threading.Barrier(4)
+
+    def slow(*a, **kw):
+        made.append(1)
+        time.sleep(0.05)
+        return zeros(*a, **kw)
+
+    rows = [cu] + [torch.tensor([0, 60, 40], **I32) for _ in range(3)]
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "zeros", slow)
+
+    done = []
+
+    def call(r):
+        start.wait()
+        T.packed_attention(q, k, v, r, 2, 1)
+        done.append(1)
+
+    threads = [threading.Thread(target=call, args=(r,)) for r in rows]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(made) == 1 and len(done) == 4
+    with pytest.raises(T.TPMLPError):
+        T.packed_attention_check()
+    T.packed_attention_check()
+    T.tpmlp._packed_words.update(keep)
