@@ -611,9 +611,17 @@ typedef struct {
   int32_t reserved;   /* 0 */
 } tpkv_config;
 
+/* Bytes of device scratch; 0 if a field is out of range.  tpkv_extend cuts few
+ * rows over a long cache into parts of up to 133 KB (128 values a head), 320 of
+ * them with tpkv_workspace_bytes (43 MB), and with less as many as there is room
+ * for: results then differ by roundings, and long caches take longer.  Every
+ * other call needs tpkv_least_workspace_bytes (4 MB with up to 8 query heads a
+ * key head), which a context that never extends may be bound to. */
 TPMLP_API size_t tpkv_workspace_bytes(const tpkv_config* cfg);
+TPMLP_API size_t tpkv_least_workspace_bytes(const tpkv_config* cfg);
 TPMLP_API tpmlp_status tpkv_create(const tpkv_config* cfg, void* cuda_stream, tpkv_ctx** out);
-/* As tpmlp_bind_workspace (tpkv_workspace_bytes, 256-byte aligned).  It is
+/* As tpmlp_bind_workspace (256-byte aligned, tpkv_least_workspace_bytes at
+ * least; what is behind tpkv_workspace_bytes is left alone).  It is
  * cleared on the context's stream; launches on another stream (tpkv_set_stream,
  * the sublayer's calls) wait for that, captured ones by holding the host. */
 TPMLP_API tpmlp_status tpkv_bind_workspace(tpkv_ctx* ctx, void* dev, size_t bytes);

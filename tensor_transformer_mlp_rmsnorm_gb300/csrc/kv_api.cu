@@ -120,19 +120,20 @@ const char* kv_config_error(const tpkv_config* c, tpmlp_status* s) {
 }
 
 struct KvLayout {
-  size_t status, counters, part, total;
+  size_t status, counters, part, least, total;
 };
 // Sized for the largest worker count, so that it does not depend on the device.
+// least: the partial results of a decode; total: or of an extend, one call behind
+// the other.  What lies between decides how far an extend is cut along the cache.
 KvLayout kv_layout(const tpkv_config& c) {
   KvLayout L{};
   L.status = 0;
   L.counters = 256;
   L.part = al256(L.counters + 3 * (size_t)KV_MAX_WORKERS * sizeof(uint32_t));
-  // the partial results of a decode, or of an extend: one call behind the other
-  size_t floats = 2 * (size_t)KV_MAX_WORKERS * kv_decode_part_floats(c.head_dim, c.n_heads / c.n_kv_heads);
-  const size_t extend = (size_t)VAR_MAX_PARTS * var_part_floats(c.head_dim);
-  if (extend > floats) floats = extend;
-  L.total = al256(L.part + floats * sizeof(float));
+  L.least = al256(L.part + 2 * (size_t)KV_MAX_WORKERS * kv_decode_part_floats(c.head_dim, c.n_heads / c.n_kv_heads) *
+                               sizeof(float));
+  L.total = al256(L.part + VAR_MAX_PARTS * var_part_floats(c.head_dim) * sizeof(float));
+  if (L.total < L.least) L.total = L.least;
   return L;
 }
 
@@ -293,6 +294,11 @@ size_t tpkv_workspace_bytes(const tpkv_config* cfg) {
   return kv_config_error(cfg, &s) ? 0 : kv_layout(*cfg).total;
 }
 
+size_t tpkv_least_workspace_bytes(const tpkv_config* cfg) {
+  tpmlp_status s;
+  return kv_config_error(cfg, &s) ? 0 : kv_layout(*cfg).least;
+}
+
 tpmlp_status tpkv_create(const tpkv_config* cfg, void* stream, tpkv_ctx** out) {
   if (!out) return TPMLP_ERR_ARG;
   *out = nullptr;
@@ -336,7 +342,7 @@ tpmlp_status tpkv_bind_workspace(tpkv_ctx* c, void* dev, size_t bytes) {
   if (!dev || (reinterpret_cast<uintptr_t>(dev) & 255u))
     return c->fail(TPMLP_ERR_ARG, "workspace must be 256-byte aligned");
   const KvLayout L = kv_layout(c->cfg);
-  if (bytes < L.total) return c->fail(TPMLP_ERR_ARG, "workspace too small");
+  if (bytes < L.least) return c->fail(TPMLP_ERR_ARG, "workspace too small");
   OnDevice on(c->device);
   // the status word and the arrival counters; partial results need no initial contents
   const cudaError_t e = clear_workspace(c, dev, L.part);
@@ -345,6 +351,7 @@ tpmlp_status tpkv_bind_workspace(tpkv_ctx* c, void* dev, size_t bytes) {
   c->status = reinterpret_cast<uint32_t*>(w + L.status);
   c->counters = reinterpret_cast<uint32_t*>(w + L.counters);
   c->part = reinterpret_cast<float*>(w + L.part);
+  c->part_floats = ((bytes < L.total ? bytes : L.total) - L.part) / sizeof(float);
   return TPMLP_OK;
 }
 
@@ -652,6 +659,7 @@ tpmlp_status kv_run_extend(tpkv_ctx* c, const SeqRows& seq, const void* q, int64
   a.k_inv_scale = c->k_inv_scale;
   a.v_inv_scale = c->v_inv_scale;
   a.part = c->part;
+  a.part_floats = c->part_floats;
   a.launches = &c->launches;
   OnDevice on(c->device);
   cudaError_t e = wait_for_clear(c, st);

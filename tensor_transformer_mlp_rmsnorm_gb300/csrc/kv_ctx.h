@@ -20,6 +20,7 @@ struct tpkv_ctx {
   int device = 0, num_sms = 0, box_tokens = 64, workers = 0;
   uint32_t *status = nullptr, *counters = nullptr;
   float* part = nullptr;
+  size_t part_floats = 0;
   // The clears of status and counters: an event behind them until the host has
   // seen it, their stream, and the last other stream that waits for it.
   cudaEvent_t cleared = nullptr;

@@ -1051,7 +1051,7 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   if (SRC != PACKED && a.part) {
     const int64_t steps = ((int64_t)a.max_pages * a.page_size + KB - 1) / KB;
     const int64_t last = units % num_sms, left = units <= num_sms ? units : last * 2 <= num_sms ? last : 0;
-    const int64_t room = VAR_MAX_PARTS * var_part_floats(D) / ((size_t)C::QTILES * 128 * (D + 2));  // parts
+    const int64_t room = a.part_floats / ((size_t)C::QTILES * 128 * (D + 2));  // parts
     const int64_t most = (steps + p.min_part - 1) / p.min_part;
     int64_t best = steps + PART_STEPS;
     for (int64_t n = 2; left > 0 && n <= most && n * left <= room; ++n) {

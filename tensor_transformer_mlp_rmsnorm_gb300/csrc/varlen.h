@@ -10,7 +10,7 @@
 
 namespace tpmlp {
 
-// Parts of blocks that are split over the length of a cache, and the floats of one.
+// Parts of blocks that are split over the length of a cache at most, and the floats of one.
 constexpr int VAR_MAX_PARTS = 320;
 inline size_t var_part_floats(int d) { return (size_t)(d <= 128 ? 256 : 128) * (d + 2); }
 
@@ -59,7 +59,8 @@ struct VarFwdArgs {
   const void *k_cache, *v_cache;
   int64_t stride_page, stride_head, stride_slot;
   const float *k_inv_scale, *v_inv_scale;  // E4M3: [nkv] or null
-  float* part;  // scratch of VAR_MAX_PARTS parts, or null: blocks are not split
+  float* part;  // scratch for parts, or null: blocks are not split
+  size_t part_floats;
   uint64_t* launches;  // counts the kernels behind the first, or null
 };
 

@@ -178,6 +178,7 @@ _SIGNATURES = {
     "tpattn_append_kv": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32]),
     "tpattn_decode": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp]),
     "tpkv_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvConfig)]),
+    "tpkv_least_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvConfig)]),
     "tpkv_create": (_i32, [ctypes.POINTER(KvConfig), _vp, ctypes.POINTER(_vp)]),
     "tpkv_bind_workspace": (_i32, [_vp, _vp, ctypes.c_size_t]),
     "tpkv_set_stream": (_i32, [_vp, _vp]),
@@ -1088,11 +1089,12 @@ class TPKV:
     ``k_cache`` and ``v_cache``: [pages, n_kv_heads, page_size, head_dim], bfloat16 or float8_e4m3fn, with the same
     strides, the last one 1 (a [pages, page_size, n_kv_heads, head_dim] tensor is passed transposed).  E4M3 codes
     stand for code * inv_scale of their head.  The cache stays the caller's; the context's scratch is a torch
-    tensor.  Calls run on ``stream``, or on torch's current stream at each call where it is None; calls that may
+    tensor, of some 43 MB (128 values a head) or, with ``extend_scratch`` False, 4 MB: then ``extend`` is slower for
+    few tokens over long caches (tpkv_least_workspace_bytes).  Calls run on ``stream``, or on torch's current stream at each call where it is None; calls that may
     overlap on the GPU need a TPKV each."""
 
     def __init__(self, k_cache, v_cache, n_heads: int, max_batch: int = 1024, k_inv_scale=None, v_inv_scale=None,
-                 stream=None):
+                 stream=None, extend_scratch: bool = True):
         if k_cache.dim() != 4 or k_cache.get_device() < 0:
             raise TPMLPError(ERR_ARG, "k_cache must be a CUDA tensor [pages, n_kv_heads, page_size, head_dim]")
         kinds = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
@@ -1110,7 +1112,7 @@ class TPKV:
         self._scales = (k_inv_scale, v_inv_scale)
         self._norm = (None, None)
         self.index = k_cache.get_device()
-        self._fixed = stream
+        self._fixed, self._long = stream, bool(extend_scratch)
         if stream is not None:  # the scratch belongs to the stream that its first use runs on
             with torch.cuda.stream(stream):
                 self._create(pages, page, d)
@@ -1124,7 +1126,8 @@ class TPKV:
         with torch.cuda.device(dev):
             self._ck(lib().tpkv_create(ctypes.byref(self.cfg), self._stream, ctypes.byref(ctx)))
             self.ctx = ctx
-            nbytes = int(lib().tpkv_workspace_bytes(ctypes.byref(self.cfg)))
+            size = lib().tpkv_workspace_bytes if self._long else lib().tpkv_least_workspace_bytes
+            nbytes = int(size(ctypes.byref(self.cfg)))
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self._ck(lib().tpkv_bind_workspace(ctx, self.workspace.data_ptr(), nbytes))
         if self._fixed is not None:

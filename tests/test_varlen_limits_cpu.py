@@ -21,3 +21,18 @@ def test_as_many_as_there_may_be(T, batch, nq, nkv, rows):  # noqa: F811
     d = _desc(T, rows=rows, batch=batch, n_heads=nq, n_kv_heads=nkv)
     assert _forward(T, d, q=None, ld_q=nq * 64, ld_k=nkv * 64, ld_v=nkv * 64, ld_out=nq * 64) == T.ERR_ARG
     assert b"NULL" in T.lib().tpmlp_last_error(None)
+
+
+def test_sizes_of_the_cache_scratch(T):  # noqa: F811
+    """What append and decode need is as small as two partial results of a query-head tile for each of 512 workers."""
+    import ctypes
+    L = T.lib()
+    assert L.tpkv_least_workspace_bytes(None) == 0
+    for d in (64, 128, 192, 256):
+        for hpg, tile in ((1, 8), (8, 8), (16, 16), (32, 32), (200, 32)):
+            c = T.tpmlp.KvConfig(16, 16, 4, 2 * hpg, 2, d, 0, 0)
+            least, most = (f(ctypes.byref(c)) for f in (L.tpkv_least_workspace_bytes, L.tpkv_workspace_bytes))
+            need = 2 * 512 * tile * (d + 2) * 4
+            assert need <= least <= need + 8192 and least < most
+    c = T.tpmlp.KvConfig(16, 16, 4, 7, 2, 64, 0, 0)
+    assert L.tpkv_least_workspace_bytes(ctypes.byref(c)) == 0
