@@ -538,6 +538,11 @@ TPMLP_API tpmlp_status tpattn_qk_rope_backward(const tpattn_qk_desc* desc, const
  *     out = sum_t exp(s_t - lse) v_t,  s_t = scale q . k_t,  lse = log sum_t exp(s_t)
  * Query head h reads key head h / (n_heads / n_kv_heads).  bf16 rows, f32 sums.
  * A row depends on rows of its own sequence only, whatever the others hold.
+ * Within a sequence a token's value (v) that is not finite may make NaN of the
+ * out of tokens that do not see it, up to 255 before it and up to 255 behind the
+ * last one that does; queries and keys that are not finite reach nothing that
+ * does not see them.  Gradients of a sequence with anything that is not finite
+ * are unspecified.
  * Calls without a context run on the current device; their errors are in
  * tpmlp_last_error(NULL). */
 typedef struct {
@@ -687,7 +692,8 @@ TPMLP_API tpmlp_status tpkv_decode(tpkv_ctx* ctx, int32_t batch, const void* q, 
  *  in tpattn_packed_desc.  Rows of an inactive sequence get out 0 and lse -inf;
  *  rows of padding and of nobody are left as they were.  Nothing behind a
  *  sequence's last token, in pages or table, and no page that all of its rows'
- *  windows have left, influences the result.  Repeated calls give the same bits. */
+ *  windows have left, influences the result; values of its tokens that are not
+ *  finite as in tpattn_packed_forward.  Repeated calls give the same bits. */
 TPMLP_API tpmlp_status tpkv_extend(tpkv_ctx* ctx, int64_t rows, int32_t batch, const void* q, int64_t ld_q,
                                    const int32_t* cu_rows, const int32_t* new_lens, const int32_t* past_lens,
                                    const int32_t* block_table, int64_t ld_table, int32_t max_pages, float scale,

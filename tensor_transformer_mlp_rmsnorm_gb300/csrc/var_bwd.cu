@@ -16,7 +16,10 @@
 // memory, are the A operand of the second products as they are, and what streams
 // by is read as B both ways, along D and along its rows.  P and dS are each rounded
 // once (gradients off by 0.0024 of their norm, where rounding the results alone
-// gives 0.0017); S, dP, the statistics and all sums have 32 bits.
+// gives 0.0017); S, dP, the statistics and all sums have 32 bits.  Streamed rows
+// that none of the block's sees are cleared, and hidden P and dS are 0: other
+// sequences count nothing, whatever they hold.  Within a sequence a row that is
+// not finite may make any gradient NaN (0 times it, and D of the rows that see it).
 //
 // Both row groups work on every step, each on half of the columns, while the
 // tensor cores run the step's other products: dV and the next scores under dS, dK

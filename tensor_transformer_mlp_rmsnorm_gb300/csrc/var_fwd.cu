@@ -17,9 +17,11 @@
 // rounded once, to bf16, as the products want it, and l sums what was not
 // rounded: outputs are off by 0.0022 of their norm, where rounding the result
 // alone gives 0.0017.  Hidden scores are -inf before the maximum is taken, and
-// values that no row of the tile sees are cleared in shared memory, so nothing
-// that is not seen counts, whatever it holds.  E4M3 codes become bf16 exactly;
-// their scales go into the scores' scale and the result.
+// values that no row of the block sees are cleared in shared memory, so what a
+// block does not see counts nothing, whatever it holds.  A value that one row of
+// a block sees and another does not has the weight 0 for the other: one that is
+// not finite makes NaN of that.  Blocks have at most 256 tokens.  E4M3 codes
+// become bf16 exactly; their scales go into the scores' scale and the result.
 //
 // Work.  One CTA an SM takes blocks (two tiles) by a static order, longest
 // first: times of causal blocks differ 100-fold.  The next block's copies, then

@@ -259,3 +259,45 @@ def test_first_calls_of_two_threads_share_one_word(monkeypatch):
         T.packed_attention_check()
     T.packed_attention_check()
     T.tpmlp._packed_words.update(keep)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 0), (100, 9)])
+def test_how_far_a_value_that_is_not_finite_reaches(d, bad, window, sinks):
+    """A value (v) of one token: its own key head and column, and tokens that see it or are less than 256 away from one
+    that does; keys and queries: only tokens that see them, and their own."""
+    T = _tp()
+    from tests.test_gpu_packed_attention import _inputs
+    nq, nkv, t = 4, 2, 700
+    q, k, v, dout, cu = _inputs([300, 1500, 200], nq, nkv, d, 8)
+    run = lambda: T.packed_attention(q, k, v, cu, nq, nkv, window=window, sinks=sinks, return_lse=True)  # noqa: E731
+    want, wl = run()
+    row, col = 300 + t, d + 5  # of key head 1
+    last = 300 + t + window - 1 if window else 1799
+    keep = v[row, col].clone()
+    v[row, col] = bad
+    out, lse = run()
+    assert torch.equal(lse, wl)
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[row - 255: min(last + 256, 1800), torch.tensor([2 * d + 5, 3 * d + 5], device="cuda")] = False
+    assert torch.equal(out[same], want[same])
+    sees = out[row: last + 1].unflatten(1, (nq, d))[:, 2:, 5]
+    assert not bool(sees.isfinite().any())
+    v[row, col] = keep
+    for x, c in ((k, d + 5), (q, 2 * d + 5)):
+        keep = x[row, c].clone()
+        x[row, c] = bad
+        out, lse = run()
+        same = torch.ones(2000, nq, dtype=torch.bool, device="cuda")
+        if x is k:
+            same[row: last + 1, 2:] = False
+        else:
+            same[row, 2] = False
+        # a warp's rows share the moves of their maxima, so the last bits of its others may change: both are within half
+        # a step of every probability and of the result, and of the f32 sum of 1500 terms, of the same value
+        assert bool(((lse[same] - wl[same]).abs() <= 2 * 1500 * R.HALF_F32 * (1 + wl[same].abs())).all())
+        a, b = (y.double().unflatten(1, (nq, d))[same] for y in (out, want))
+        assert bool(((a - b).abs() <= 2 * R.HALF_BF16 * 1.01 * (b.abs() + float(v.abs().max()))).all())
+        x[row, c] = keep
+    T.packed_attention_check()
