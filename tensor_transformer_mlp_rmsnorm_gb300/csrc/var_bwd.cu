@@ -55,7 +55,9 @@ namespace {
 // 88 + 2 x 208 = 3 x 168.
 constexpr int ISSUE_REGS = 88, ROW_REGS = 208;
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
-constexpr uint64_t BLOCK_NS = 60000000000ull;  // for a whole block: the largest that fits memory takes some 6 s
+// For a whole block (the largest that fits memory takes some 6 s), and for the scheduler's
+// next one, which it may find behind 2^20 empty sequences.
+constexpr uint64_t BLOCK_NS = 60000000000ull;
 
 // What a CTA accumulates.  DQ: 128 rows of (token, head) stay, their keys and
 // values stream by.  The others: 128 keys stay, the rows of (token, head) that
@@ -213,7 +215,9 @@ __global__ void __launch_bounds__(384, 1)
   };
   // The t-th block of this CTA, in shared memory until it is given back; null behind the last.
   auto next = [&](int t) -> const BwdBlock* {
-    if (!wait_all(&x.work_full[t & 1], (uint32_t)((t >> 1) & 1))) return nullptr;
+    if (!__all_sync(0xffffffffu, mbar_wait(&x.work_full[t & 1], (uint32_t)((t >> 1) & 1), abort_flag, p.status,
+                                           STATUS_TIMEOUT, BLOCK_NS)))
+      return nullptr;
     return x.work[t & 1].b == NONE ? nullptr : &x.work[t & 1];
   };
   auto give_back = [&](int t) {
@@ -489,10 +493,19 @@ __global__ void __launch_bounds__(384, 1)
           k.g = Q_STAYS ? hd / p.chunks : hd;
           k.h0 = k.g * p.hpg + (Q_STAYS ? hd % p.chunks * p.ht : 0);
           k.nh = Q_STAYS ? min(p.ht, (k.g + 1) * p.hpg - k.h0) : p.hpg;
-          int b, i, next;  // next: the rank of the next one that there may be a block at
-          SeqSpan s;
-          if (!find_ranked(p.seq, p.slots, p.by_length, order, rank, block_tok, -1, lane, &b, &i, &s, &next)) {
-            turn = max(turn, (int)((int64_t)next * p.heads / gridDim.x) - 1);
+          int b, i = 0;
+          if (p.by_length) {
+            order.find(rank, lane, &b, &i);
+          } else {
+            b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
+            i = -1;  // below
+          }
+          if (b < 0) continue;
+          bool bad = false;
+          const SeqSpan s = seq_span(p.seq, b, -1, &bad);
+          if (i < 0) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
+          if (i < 0 || (int64_t)i * block_tok >= s.count) {
+            turn = max(turn, (rank + 1) * p.heads / (int)gridDim.x - 1);  // empty for all key heads
             continue;
           }
           // key blocks from the first on are the long ones

@@ -60,7 +60,9 @@ namespace {
 constexpr int KB = 128;  // keys of a step
 constexpr uint32_t SUB = 128 * 128;  // bytes of a [128 x 64] bf16 tile with the 128-byte swizzle
 constexpr uint64_t WAIT_NS = 1000000000ull, DRAIN_NS = 200000000ull;
-constexpr uint64_t BLOCK_NS = 60000000000ull;  // for a whole block: 2^30 keys take some 13 s
+// For a whole block (2^30 keys take some 13 s), and for the scheduler's next one, which it
+// may find behind 2^20 empty sequences.
+constexpr uint64_t BLOCK_NS = 60000000000ull;
 constexpr float MOVE_LOG2 = 8.0f;  // the running maximum is moved when it is off by more than 2^8
 // In place of a scale of 0: the smallest number there is, which keeps hidden scores at -inf
 // and makes less than 10^-6 of the largest others.
@@ -174,11 +176,17 @@ __device__ __forceinline__ int part_steps(const FwdParams& p, int n) {
   return max(p.min_part, (n + p.nsplit - 1) / p.nsplit);
 }
 
+// Block `rank` of the order in which blocks are taken, by the lanes of one warp; false: none.
 __device__ __forceinline__ bool find_block(const FwdParams& p, ByLength<KB>& order, int rank, int block_tok, int64_t cap,
-                                           int lane, Block* k, int* next) {
-  int b, i;
-  SeqSpan s;
-  if (!find_ranked(p.seq, p.slots, p.by_length, order, rank, block_tok, cap, lane, &b, &i, &s, next)) return false;
+                                           int lane, Block* k) {
+  int b, i = -1;
+  if (p.by_length) order.find(rank, lane, &b, &i);
+  else b = find_slot(p.seq, p.slots, (int)p.slots.count - 1 - rank, lane);
+  if (b < 0) return false;
+  bool bad = false;  // reported elsewhere
+  const SeqSpan s = seq_span(p.seq, b, cap, &bad);
+  if (!p.by_length) i = (int)p.slots.count - 1 - rank - slot_base(p.slots, s.first, b);
+  if (i < 0 || (int64_t)i * block_tok >= s.count) return false;
   fill_block(k, s, b, i, p.tok, block_tok, p.window, p.sinks);
   return true;
 }
@@ -283,7 +291,9 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
   // The t-th piece of this CTA's work, in shared memory until it is given back;
   // null behind the last.
   auto next = [&](int t) -> const Work* {
-    if (!wait_all(&work_full[t & 1], (uint32_t)((t >> 1) & 1))) return nullptr;
+    if (!__all_sync(0xffffffffu, mbar_wait(&work_full[t & 1], (uint32_t)((t >> 1) & 1), abort_flag, p.status,
+                                           STATUS_TIMEOUT, BLOCK_NS)))
+      return nullptr;
     return work_sh[t & 1].b == NONE ? nullptr : &work_sh[t & 1];
   };
   auto give_back = [&](int t) {
@@ -324,20 +334,20 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
       for (int t = 0, base = 0; ok && (wp = next(t)); give_back(t++)) {
         const Work& w = *wp;
         const int g = w.g, h0 = w.h0;
-        // Whether any row sees this lane's box in a step.  Its page is asked for a step ahead,
-        // and looked at when it is used; num_pages there: nothing is read, zeros land.
-        auto seen = [&](int j) -> bool {
-          const int at = w.tile(w.j0 + j) * KB + row0;
-          return issues && ((at < w.end && at + p.box > w.lo) || at < w.sink_end);
-        };
+        // Page of this lane's box in a step, asked for a step ahead and looked at when it is
+        // used; num_pages (nothing is read, zeros land) where no row sees the box.
+        const int no_page = (int)p.num_pages;
+        bool seen = false;  // of the page that was asked for last
         auto look = [&](int j) -> int {
-          const int pi = (w.tile(w.j0 + j) * KB + row0) / p.page_size;
-          return seen(j) && pi < p.max_pages ? __ldg(p.table + (int64_t)w.b * p.ld_table + pi) : -1;
+          const int at = w.tile(w.j0 + j) * KB + row0, pi = at / p.page_size;
+          seen = issues && ((at < w.end && at + p.box > w.lo) || at < w.sink_end);
+          if (!seen) return no_page;
+          return pi < p.max_pages ? __ldg(p.table + (int64_t)w.b * p.ld_table + pi) : -1;
         };
-        auto valid = [&](int j, int page) -> int {
-          if (page >= 0 && page < p.num_pages) return page;
-          if (seen(j)) atomicOr(p.status, STATUS_BAD_INDEX);
-          return (int)p.num_pages;
+        auto valid = [&](int page) -> int {
+          if ((uint32_t)page < (uint32_t)no_page) return page;
+          if (seen) atomicOr(p.status, STATUS_BAD_INDEX);
+          return no_page;
         };
         auto load = [&](int at, const CUtensorMap* map, int j, int page) -> bool {
           const int tile = w.tile(w.j0 + j);
@@ -361,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         int page = 0, page_n = 0, page_v = 0;
         if (w.nk > 0) {
           if constexpr (SRC != PACKED) {
-            page = valid(0, look(0));
+            page = valid(look(0));
             if (w.nk > 1) page_n = look(1);
           }
           ok = load(k_at(base, w, 0), &map_k, 0, page);
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
         for (int j = 0; ok && j < w.nk; ++j) {
           if (j > 0) {
             if constexpr (SRC != PACKED) {
-              page = valid(j, page_n);
+              page = valid(page_n);
               if (j + 1 < w.nk) page_n = look(j + 1);
             }
             ok = load(k_at(base, w, j), &map_k, j, page);
@@ -570,10 +580,10 @@ __global__ void __launch_bounds__(Cfg<D, SRC, FEW>::THREADS, 1)
           w.g = hd / p.chunks;
           w.h0 = w.g * p.hpg + hd % p.chunks * p.ht;
           w.nh = min(p.ht, (w.g + 1) * p.hpg - w.h0);
-          int rank;  // the next one that there may be a block at
-          if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &w, &rank)) {
-            const int64_t to = (int64_t)rank * p.heads, at = to <= p.tail ? to : p.tail + (to - p.tail) * p.nsplit;
-            k = max(k, (int)(at / gridDim.x) - 1);
+          if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &w)) {
+            // An empty slot is one of all key heads: on with the next slot.  (Sequences are not
+            // passed over many at a time: the code for that cost 1 to 2% of every call.)
+            k = max(k, (unit / p.heads + 1) * p.heads / (int)gridDim.x - 1);
             continue;
           }
           const int per = shared ? part_steps(p, w.n) : w.n;
@@ -986,8 +996,7 @@ __global__ void __launch_bounds__(256) var_join_kernel(const FwdParams p, int ti
   ByLength<KB> order;
   start_order(p, order, block_tok, cap, lane);
   Block k;
-  int next;
-  if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &k, &next) || tk >= k.count) return;
+  if (!find_block(p, order, unit / p.heads, block_tok, cap, lane, &k) || tk >= k.count) return;
   const int per = part_steps(p, k.n);
   if (per >= k.n) return;  // one CTA's
   const int parts = (k.n + per - 1) / per;

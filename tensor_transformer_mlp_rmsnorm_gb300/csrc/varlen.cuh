@@ -183,38 +183,6 @@ struct ByLength {
   }
 };
 
-// Block `rank` of the order in which blocks are taken (the longest first, or by place
-// from the end), by the lanes of one warp: block *i of sequence *b, whose rows are *sp.
-// False: there is none, and none before rank *next either.  Runs of slots without rows
-// are passed over 32 sequences at a time, in front of a block or the end: 2^20 empty
-// sequences take 2^15 steps a CTA and not as many for each key head.
-template <int KB>
-__device__ __forceinline__ bool find_ranked(const SeqRows& s, const Slots& t, bool by_length, ByLength<KB>& order,
-                                            int rank, int block_tok, int64_t cap, int lane, int* b, int* i, SeqSpan* sp,
-                                            int* next) {
-  bool bad = false;  // reported elsewhere
-  *next = (int)t.count;
-  if (by_length) {  // slots without rows come last
-    order.find(rank, lane, b, i);
-    if (*b >= 0) *sp = seq_span(s, *b, cap, &bad);
-    return *b >= 0;
-  }
-  const int slot = (int)t.count - 1 - rank;
-  *b = find_slot(s, t, slot, lane);
-  *sp = seq_span(s, *b, cap, &bad);
-  *i = slot - slot_base(t, sp->first, *b);
-  if (*i < 0) return false;  // in front of the first sequence
-  if ((int64_t)*i * block_tok < sp->count) return true;
-  int at = sp->count > 0 ? slot_base(t, sp->first, *b) + (sp->count - 1) / block_tok : -1;  // the next block's slot
-  for (int top = *b - 1; at < 0 && top >= 0; top -= 32) {
-    const SeqSpan o = top >= lane ? seq_span(s, top - lane, -1, &bad) : SeqSpan{0, 0, 0};
-    const uint32_t has = __ballot_sync(0xffffffffu, o.count > 0);
-    if (has) at = __shfl_sync(0xffffffffu, slot_base(t, o.first, top - lane) + (o.count - 1) / block_tok, __ffs(has) - 1);
-  }
-  if (at >= 0 && at < slot) *next = (int)t.count - 1 - at;  // not so: rows that descend, which are reported
-  return false;
-}
-
 // The unit of work of CTA c in its k-th turn among n CTAs: every other turn in
 // reverse, so that with units longest first nobody has the longer one each time.
 __device__ __forceinline__ int64_t snake(int k, int c, int n) {
