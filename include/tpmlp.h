@@ -387,9 +387,11 @@ TPMLP_API tpmlp_status tpattn_forward(tpattn_ctx* ctx, int64_t batch, int64_t se
  * x, y [tokens, H], tokens <= max_tokens, cu_rows device [batch + 1], ascending,
  * kept by pointer until the backward or tpattn_append_kv.  Positions count from
  * each sequence's first row; max_seq does not matter.  Rows outside every
- * sequence have attention output 0.  tpattn_backward, the updates and
- * tpattn_append_kv follow as after tpattn_forward.  A bad cu_rows is reported by
- * tpattn_sync (TPMLP_ERR_ARG). */
+ * sequence have attention output 0; for the rest of the sublayer they are rows
+ * like any other (y = x + b_o, their dy is in db_o), and have to be finite, or
+ * the weights' gradients are not.  batch as in tpattn_packed_desc.
+ * tpattn_backward, the updates and tpattn_append_kv follow as after
+ * tpattn_forward.  A bad cu_rows is reported by tpattn_sync (TPMLP_ERR_ARG). */
 TPMLP_API tpmlp_status tpattn_forward_packed(tpattn_ctx* ctx, int64_t tokens, int32_t batch, const int32_t* cu_rows,
                                              const void* x, const void* norm_w, const void* w_qkv, const void* w_o,
                                              const void* b_o, float eps, int32_t t, void* y);

@@ -25,11 +25,12 @@
 // tensor cores run the step's other products: dV and the next scores under dS, dK
 // and the next dP under P.
 //
-// Measured (GB300; 1980 TFLOP/s is its product rate, flops count 5 products):
-//   one sequence of 8192 tokens, 32 + 8 heads of 128    1365 us, 1007 TFLOP/s (1410 with all 7)
+// Measured (GB300; 1947 TFLOP/s is its product rate, flops count 5 products), in replays of
+// a captured graph; calls in a row take 1435, 245 and 37 to 44 us:
+//   one sequence of 8192 tokens, 32 + 8 heads of 128    1368 us, 1005 TFLOP/s (1407 with all 7)
 //   19 sequences, 8192 tokens                            237 us,  440 TFLOP/s of pairs that are seen:
 //     lse and D 26 (bytes), dQ 110, dK and dV 104
-//   5 sequences, 333 tokens, 5 + 1 heads of 64            29 us, three launches' latencies
+//   5 sequences, 333 tokens, 5 + 1 heads of 64            30 us, three launches' latencies
 // What bounds them.  dK and dV: a step takes some 2950 cycles, its products 2560.
 // dQ: a step takes some 2650 cycles where its products need 1540; one buffer for
 // dP is all that tensor memory has left beside two for scores and dQ, so dP, the row
@@ -37,7 +38,7 @@
 // four steps pays some 4000 cycles for its first copies, its statistics and its
 // result.  Heads of 192 and 256: steps of 64 keys, as 128 would not leave room for
 // two in flight, pay the same chain for half the work (2 x 4096 tokens, 16 heads
-// of 192 on 4 key heads: 1435 us, 360 TFLOP/s; of 128: 391 us, 879 TFLOP/s).
+// of 192 on 4 key heads: 1446 us, 357 TFLOP/s; of 128: 391 us, 879 TFLOP/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -29,20 +29,23 @@
 // are cut along the cache: each part leaves its weighted sums, maximum and sum,
 // and a second kernel joins them in order, so repeats give the same bits.
 //
-// Measured (GB300; 1980 TFLOP/s and 6689 GB/s are its product and copy rates):
-//   one sequence of 16384 tokens, 32 + 8 heads of 128   1490 us, 1476 TFLOP/s
-//   2 x 2048 tokens behind 30000, the same heads        1431 us, 1452 TFLOP/s
-//   64 tokens behind 131000, the same heads              118 us, 4.6 TB/s and 1166 TFLOP/s
-//   4 x 1024 tokens behind 7000, E4M3                    461 us, 1118 TFLOP/s
-//   19 sequences, 8192 tokens                             73 us,  570 TFLOP/s of pairs that are seen
-//   48 x 5 tokens behind up to 8192, E4M3                169 us, 2.5 TB/s
+// Measured (GB300; 1947 TFLOP/s and 6678 GB/s are its product and copy rates), in
+// replays of a captured graph; calls in a row, under the power cap, take 1586, 1540,
+// 126, 470, 74 and 171 us:
+//   one sequence of 16384 tokens, 32 + 8 heads of 128   1497 us, 1469 TFLOP/s
+//   2 x 2048 tokens behind 30000, the same heads        1432 us, 1451 TFLOP/s
+//   64 tokens behind 131000, the same heads              117 us, 4.6 TB/s and 1170 TFLOP/s
+//   4 x 1024 tokens behind 7000, E4M3                    466 us, 1106 TFLOP/s
+//   19 sequences, 8192 tokens                             73 us,  569 TFLOP/s of pairs that are seen
+//   48 x 5 tokens behind up to 8192, E4M3                170 us, 2.5 TB/s
 // What bounds them.  Long: a step of two tiles takes some 2800 to 3300 cycles
 // where its products need 2080, the rest is the way between the issuing warp and
 // the softmax (a wait that is fulfilled costs 150 cycles, a load from tensor
 // memory beside products 300).  Short sequences: a block of one to four steps
 // pays some 7000 cycles for its result (5000) and the next one's start, in which
-// the tensor cores rest, and up to half of a step's keys are hidden.  E4M3: 16384 codes an operand are converted by 128 threads, about 1500
-// cycles, which few rows do not hide.
+// the tensor cores rest, and up to half of a step's keys are hidden.  E4M3: 16384
+// codes an operand are converted by 128 threads, about 1500 cycles, which few rows
+// do not hide.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -67,9 +70,16 @@ constexpr float MOVE_LOG2 = 8.0f;  // the running maximum is moved when it is of
 // In place of a scale of 0: the smallest number there is, which keeps hidden scores at -inf
 // and makes less than 10^-6 of the largest others.
 constexpr float NO_SCALE = 1.4e-45f;
-constexpr int MIN_PART = 4;        // steps of a part at least
-constexpr int TAIL_PART = 12;      // and of one of a last turn's blocks
-constexpr int PART_STEPS = 5;      // steps in the time of a part's start and result
+// Steps of a part at least: 64 tokens behind 131000 take 117 us with 2, 4 and 8 alike; 16
+// behind 484, whose four steps are too few to cut, 16.6 with 2 (cut), 17.8 with 4 (not cut,
+// and a second kernel that finds nothing to join) and 15.5 with 8 (one kernel).
+constexpr int MIN_PART = 4;
+// And of one of a last turn's blocks: 13 prompts behind 300 tokens take 112 us with 4, 106
+// with 12 and with 24; 4 x 1024 behind 7000 in E4M3 463, 463 and 459.
+constexpr int TAIL_PART = 12;
+// Steps in the time of a part's start and result: 13 prompts 106 us with 2, 5 and 12;
+// 4 x 1024 in E4M3 464, 463 and 460.
+constexpr int PART_STEPS = 5;
 
 enum Source { PACKED = 0, PAGED = 1, PAGED_F8 = 2 };
 
@@ -1051,11 +1061,14 @@ cudaError_t launch_one(FwdParams& p, const VarFwdArgs& a, int num_sms, cudaStrea
   if (units > VAR_MAX_BLOCKS) return cudaErrorInvalidConfiguration;  // var_fits
   // Few blocks: all are shared.  Many: the CTAs take them in turns, and a last turn
   // with work for less than half of them shares out its blocks, which are the shortest.
+  // What is counted are slots: the lengths are on the device, and with sequences of
+  // different ones a last turn may be empty slots, with nothing to share.
   // (With more the parts' own time is what it costs: 48 x 5 tokens behind up to 8192 in
   // E4M3, 80 blocks left, 169 us without and 185 with.)  A part takes its steps and the
   // time of PART_STEPS more; the number of parts is the one that ends first.
   // 2 x 2048 tokens behind 30000 (512 blocks for 152 CTAs): 1651 us without, 1431 with;
-  // 4 x 1024 behind 7000 in E4M3: 493 and 461.
+  // 4 x 1024 behind 7000 in E4M3: 493 and 461.  More than one turn of parts has to be 5%
+  // better by that count; without the margin 13 prompts take 106 us as with it.
   p.tail = (int)units;
   p.nsplit = 1;
   p.min_part = units > num_sms ? TAIL_PART : MIN_PART;

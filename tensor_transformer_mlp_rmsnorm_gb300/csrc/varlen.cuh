@@ -95,8 +95,10 @@ __device__ __forceinline__ int find_row(const SeqRows& s, int row, int lane) {
   return lo;
 }
 
-// Blocks are ordered by length up to this many sequences, two a lane; with
-// more there are many blocks, and the last ones count for little.
+// Blocks are ordered by length up to this many sequences, two a lane, and by place
+// from the end with more.  That is worse where a long sequence lies first: 16384 tokens
+// before 64 x 100 take 1676 us, before 63 x 100 1530 (1626 by place); behind them 1600 and
+// 1550.  19 sequences of 8192 tokens: 72 us by length, 81 by place.
 constexpr int LPT_BATCH = 64;
 
 // Finds the blocks of units of work, longest first (more steps of KB tokens
