@@ -1090,8 +1090,8 @@ class TPKV:
     strides, the last one 1 (a [pages, page_size, n_kv_heads, head_dim] tensor is passed transposed).  E4M3 codes
     stand for code * inv_scale of their head.  The cache stays the caller's; the context's scratch is a torch
     tensor, of some 43 MB (128 values a head) or, with ``extend_scratch`` False, 4 MB: then ``extend`` is slower for
-    few tokens over long caches (tpkv_least_workspace_bytes).  Calls run on ``stream``, or on torch's current stream at each call where it is None; calls that may
-    overlap on the GPU need a TPKV each."""
+    few tokens over long caches (tpkv_least_workspace_bytes).  Calls run on ``stream``, or on torch's current stream
+    at each call where it is None; calls that may overlap on the GPU need a TPKV each."""
 
     def __init__(self, k_cache, v_cache, n_heads: int, max_batch: int = 1024, k_inv_scale=None, v_inv_scale=None,
                  stream=None, extend_scratch: bool = True):
